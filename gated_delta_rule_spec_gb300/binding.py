@@ -9,6 +9,10 @@ Names follow the C ABI: ``verify``, ``commit``, ``fold``, ``reset``,
 ``read_status`` wrap ``gdn_spec_verify`` ... ``gdn_spec_read_status``.
 ``SpecLayer`` and ``SpecCursors`` allocate the per-layer state and the shared
 cursors with torch and produce the C descriptors.
+
+The softmax-attention layers of a hybrid model: ``KvCache`` is the paged cache of
+all of them, ``kv_*`` its pages, ``RopePlan`` / ``rope`` / ``rope_append`` the
+rotary positions and ``tree_attn`` the attention of a drafted window.
 """
 from __future__ import annotations
 
@@ -23,6 +27,10 @@ GATE_SCALAR, GATE_PER_KEY = 0, 1
 DTYPE_BF16, DTYPE_FP32 = 0, 1
 ST_ACCEPT_RANGE, ST_SLOT_OOR, ST_RING_OVERFLOW, ST_CURSOR_CORRUPT, ST_TIMEOUT = 1, 2, 4, 8, 16
 ST_UNFOLDED = 32
+ST_NO_PAGES, ST_PAGE_OOR, ST_SLOT_BUSY = 64, 128, 256
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = 0, 1, 2, 3, 4
+TREE_MAX = 64                     # drafted tokens of a window (bits of a tree mask)
 
 _IO_TORCH = {DTYPE_BF16: torch.bfloat16, DTYPE_FP32: torch.float32}
 _NAME_TO_DTYPE = {"bf16": DTYPE_BF16, "fp32": DTYPE_FP32}
@@ -48,12 +56,37 @@ class CursorDesc(ctypes.Structure):
                 ("status", ctypes.c_void_p)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("HKV", ctypes.c_int32), ("P", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_void_p),
+                ("length", ctypes.c_void_p), ("ref", ctypes.c_void_p),
+                ("free_bits", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class RopeScalingDesc(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class RopePlanDesc(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int32), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("freq", ctypes.c_uint64 * 128)]
+
+
 _lib = None
 EXPORTS = ("gdn_spec_verify", "gdn_spec_verify_d", "gdn_spec_commit", "gdn_spec_fold",
            "gdn_spec_reset", "gdn_spec_prefill",
            "gdn_spec_snapshot_verify", "gdn_spec_snapshot_commit",
            "gdn_spec_read_status", "gdn_spec_strerror", "gdn_spec_abi_version",
-           "gdn_spec_verify_path", "gdn_spec_prefill_path", "gdn_spec_set_wait_limit")
+           "gdn_spec_verify_path", "gdn_spec_prefill_path", "gdn_spec_set_wait_limit",
+           "gdn_spec_kv_init", "gdn_spec_kv_reserve", "gdn_spec_kv_fork", "gdn_spec_kv_commit",
+           "gdn_spec_kv_free", "gdn_spec_kv_read_status", "gdn_spec_rope_init",
+           "gdn_spec_rope_init_freqs", "gdn_spec_rope", "gdn_spec_rope_append",
+           "gdn_spec_tree_attn", "gdn_spec_tree_attn_workspace", "gdn_spec_tree_attn_path")
 
 
 def library_path() -> str:
@@ -97,6 +130,28 @@ def load() -> ctypes.CDLL:
     lib.gdn_spec_prefill_path.restype = ctypes.c_char_p
     lib.gdn_spec_set_wait_limit.argtypes = [ctypes.c_uint32]
     lib.gdn_spec_set_wait_limit.restype = ctypes.c_uint32
+    KP, RP, I64, F64 = (ctypes.POINTER(KvCacheDesc), ctypes.POINTER(RopePlanDesc), ctypes.c_int64,
+                        ctypes.c_double)
+    lib.gdn_spec_kv_init.argtypes = [KP, P]
+    lib.gdn_spec_kv_reserve.argtypes = [KP, P, I32, I32, P, P, P]
+    lib.gdn_spec_kv_fork.argtypes = [KP, P, P, I32, P, P]
+    lib.gdn_spec_kv_commit.argtypes = [KP, P, I32, I32, P, P, P]
+    lib.gdn_spec_kv_free.argtypes = [KP, P, I32, P]
+    lib.gdn_spec_kv_read_status.argtypes = [KP, ctypes.POINTER(ctypes.c_uint32), I32, P]
+    lib.gdn_spec_rope_init.argtypes = [RP, I32, I32, I32, F64, ctypes.POINTER(RopeScalingDesc)]
+    lib.gdn_spec_rope_init_freqs.argtypes = [RP, I32, I32, I32, ctypes.POINTER(F64), F64]
+    lib.gdn_spec_rope.argtypes = [RP, I32, I32, I32, P, P, I64, P, I64, I32, P]
+    lib.gdn_spec_rope_append.argtypes = [RP, KP, I32, P, I32, I32, P, P, I32, P, I64, P, I64, P, I64, P, P]
+    lib.gdn_spec_tree_attn.argtypes = [KP, I32, P, I32, I32, I32, P, P, P, ctypes.c_float, P, P, P, I64, P]
+    lib.gdn_spec_tree_attn_workspace.argtypes = [KP, I32, I32, I32]
+    lib.gdn_spec_tree_attn_workspace.restype = I64
+    lib.gdn_spec_tree_attn_path.argtypes = [KP, I32, I32]
+    lib.gdn_spec_tree_attn_path.restype = ctypes.c_char_p
+    for name in ("gdn_spec_kv_init", "gdn_spec_kv_reserve", "gdn_spec_kv_fork", "gdn_spec_kv_commit",
+                 "gdn_spec_kv_free", "gdn_spec_kv_read_status", "gdn_spec_rope_init",
+                 "gdn_spec_rope_init_freqs", "gdn_spec_rope", "gdn_spec_rope_append",
+                 "gdn_spec_tree_attn"):
+        getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -350,3 +405,287 @@ def set_wait_limit(polls: int) -> int:
     each data copy gives up; WAIT_LIMIT_DEFAULT restores the default.  Returns
     the previous limit."""
     return int(load().gdn_spec_set_wait_limit(ctypes.c_uint32(polls & 0xFFFFFFFF)))
+
+
+# ------------------------------------------------ softmax-attention layers
+
+class KvCache:
+    """The paged key/value cache of all softmax-attention layers: ``k`` and ``v``
+    [n_layers, num_pages, HKV, P, D], the slots' page tables and lengths, the pages'
+    holders.  A new cache is empty (keys and values uninitialised); ``tensors`` gives
+    some or all of its tensors instead (as they are, nothing is reset)."""
+
+    def __init__(self, n_layers: int, num_pages: int, HKV: int, P: int, D: int, num_slots: int,
+                 max_pages: int, io_dtype: str = "bf16", device="cuda", tensors: dict | None = None):
+        self.n_layers, self.num_pages, self.HKV, self.P, self.D = n_layers, num_pages, HKV, P, D
+        self.num_slots, self.max_pages = num_slots, max_pages
+        self.io_code = _NAME_TO_DTYPE[io_dtype]
+        self.io_torch = _IO_TORCH[self.io_code]
+        t = dict(tensors or {})
+        shape, i32 = (n_layers, num_pages, HKV, P, D), torch.int32
+        words = (num_pages + 31) // 32
+        new = {"k": lambda: torch.empty(shape, dtype=self.io_torch, device=device),
+               "v": lambda: torch.empty(shape, dtype=self.io_torch, device=device),
+               "page_table": lambda: torch.full((num_slots, max_pages), -1, dtype=i32, device=device),
+               "n_pages": lambda: torch.zeros(num_slots, dtype=i32, device=device),
+               "length": lambda: torch.zeros(num_slots, dtype=i32, device=device),
+               "ref": lambda: torch.zeros(num_pages, dtype=i32, device=device),
+               "free_bits": lambda: self._all_free(num_pages, device),
+               "status": lambda: torch.zeros(4, dtype=i32, device=device)}
+        want = {"k": shape, "v": shape, "page_table": (num_slots, max_pages), "n_pages": (num_slots,),
+                "length": (num_slots,), "ref": (num_pages,), "free_bits": (words,), "status": None}
+        for name, make in new.items():
+            x = t.pop(name, None)
+            if x is None:
+                x = make()
+            elif name == "status":
+                _need(x, name, i32, x.shape)
+            else:
+                _need(x, name, self.io_torch if name in "kv" else i32, want[name])
+            setattr(self, name, x)
+        if t:
+            raise GdnSpecError(f"unknown cache tensors: {sorted(t)}")
+        self._desc = KvCacheDesc(n_layers, num_pages, HKV, P, D, self.io_code, num_slots, max_pages,
+                                 *(getattr(self, n).data_ptr() for n in new))
+        self._ref = ctypes.byref(self._desc)
+
+    @staticmethod
+    def _all_free(num_pages: int, device) -> torch.Tensor:
+        bits = torch.full(((num_pages + 31) // 32,), -1, dtype=torch.int32, device=device)
+        if num_pages % 32:
+            bits[-1] = (1 << num_pages % 32) - 1
+        return bits
+
+    def desc(self) -> KvCacheDesc:
+        return self._desc
+
+
+def kv_init(cache: KvCache, stream=None) -> None:
+    """gdn_spec_kv_init: every slot empty, every page free."""
+    _check(load().gdn_spec_kv_init(cache._ref, _stream(stream)), "gdn_spec_kv_init")
+
+
+def _done(done: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
+    if done is None:
+        done = torch.empty_like(like)
+    _need(done, "done", torch.int32, like.shape)
+    return done
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    if t.dim() != 1:
+        raise GdnSpecError(f"{name}: want one dimension, got {tuple(t.shape)}")
+    _need(t, name, torch.int32, t.shape)
+    return t.shape[0]
+
+
+def kv_reserve(cache: KvCache, slot_idx: torch.Tensor, T: int, n_tokens: torch.Tensor | None = None,
+               done: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gdn_spec_kv_reserve: pages for T (or n_tokens[b] <= T) more tokens of every row's
+    slot.  Returns int32 [B]: 1 where the row is served."""
+    B = _rows(slot_idx, "slot_idx")
+    done = _done(done, slot_idx)
+    if n_tokens is not None:
+        _need(n_tokens, "n_tokens", torch.int32, (B,))
+    rc = load().gdn_spec_kv_reserve(cache._ref, _ptr(slot_idx), B, T, _ptr(n_tokens), _ptr(done),
+                                    _stream(stream))
+    _check(rc, "gdn_spec_kv_reserve")
+    return done
+
+
+def kv_fork(cache: KvCache, src_idx: torch.Tensor, dst_idx: torch.Tensor,
+            done: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gdn_spec_kv_fork: slots dst_idx become copies of slots src_idx, full pages
+    shared.  Returns int32 [B]: 1 where the row is served."""
+    B = _rows(src_idx, "src_idx")
+    _need(dst_idx, "dst_idx", torch.int32, (B,))
+    done = _done(done, src_idx)
+    rc = load().gdn_spec_kv_fork(cache._ref, _ptr(src_idx), _ptr(dst_idx), B, _ptr(done),
+                                 _stream(stream))
+    _check(rc, "gdn_spec_kv_fork")
+    return done
+
+
+def kv_commit(cache: KvCache, slot_idx: torch.Tensor, accept_len: torch.Tensor, T: int,
+              path: torch.Tensor | None = None, stream=None) -> None:
+    """gdn_spec_kv_commit: the accepted drafts (nodes path[b, :accept_len[b]], or the first
+    accept_len[b]) become the slots' next committed tokens, in every layer."""
+    B = _rows(slot_idx, "slot_idx")
+    _need(accept_len, "accept_len", torch.int32, (B,))
+    if path is not None:
+        _need(path, "path", torch.int32, (B, T))
+    rc = load().gdn_spec_kv_commit(cache._ref, _ptr(slot_idx), B, T, _ptr(path), _ptr(accept_len),
+                                   _stream(stream))
+    _check(rc, "gdn_spec_kv_commit")
+
+
+def kv_free(cache: KvCache, slot_idx: torch.Tensor, stream=None) -> None:
+    """gdn_spec_kv_free: the slots become empty, pages that nobody holds free."""
+    B = _rows(slot_idx, "slot_idx")
+    _check(load().gdn_spec_kv_free(cache._ref, _ptr(slot_idx), B, _stream(stream)),
+           "gdn_spec_kv_free")
+
+
+def kv_read_status(cache: KvCache, clear: bool = True, stream=None) -> int:
+    v = ctypes.c_uint32(0)
+    rc = load().gdn_spec_kv_read_status(cache._ref, ctypes.byref(v), int(clear), _stream(stream))
+    _check(rc, "gdn_spec_kv_read_status")
+    return int(v.value)
+
+
+_ROPE_LAYOUT = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}
+_ROPE_KIND = {"none": ROPE_NONE, "linear": ROPE_LINEAR, "ntk": ROPE_NTK, "yarn": ROPE_YARN,
+              "bands": ROPE_BANDS}
+
+
+class RopePlan:
+    """gdn_spec_rope_init: the rotary positions of heads of D dims, the first ``rot`` of
+    them turned, frequencies base^(-2i/rot) scaled for long contexts by ``scaling``
+    ("none", "linear", "ntk", "yarn" with fast and slow, "bands" with low and high), or
+    given as ``freqs`` (radians a position, rot / 2 of them; then ``mscale`` is the
+    factor on cos and sin)."""
+
+    def __init__(self, D: int, rot: int | None = None, layout: str = "half", base: float = 1.0e4,
+                 scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+                 fast: float = 32.0, slow: float = 1.0, low: float = 1.0, high: float = 4.0,
+                 freqs=None, mscale: float = 1.0):
+        self.D, self.rot = D, D if rot is None else rot
+        if layout not in _ROPE_LAYOUT or scaling not in _ROPE_KIND:
+            raise GdnSpecError(f"rotary layout {layout!r} or scaling {scaling!r} is not known")
+        self._desc = RopePlanDesc()
+        self._ref = ctypes.byref(self._desc)
+        if freqs is not None:
+            f = [float(x) for x in freqs]
+            if len(f) != self.rot // 2:
+                raise GdnSpecError(f"freqs: want {self.rot // 2} values, got {len(f)}")
+            arr = (ctypes.c_double * max(len(f), 1))(*f)
+            rc = load().gdn_spec_rope_init_freqs(self._ref, D, self.rot, _ROPE_LAYOUT[layout], arr, mscale)
+            _check(rc, "gdn_spec_rope_init_freqs")
+            return
+        yarn = scaling == "yarn"
+        sc = RopeScalingDesc(_ROPE_KIND[scaling], 0, factor, original, fast if yarn else low,
+                             slow if yarn else high)
+        rc = load().gdn_spec_rope_init(self._ref, D, self.rot, _ROPE_LAYOUT[layout], base,
+                                       ctypes.byref(sc))
+        _check(rc, "gdn_spec_rope_init")
+
+    def desc(self) -> RopePlanDesc:
+        return self._desc
+
+
+def _token_stride(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """Elements between tokens of [..tokens.., heads, D] whose heads are dense and whose
+    tokens are evenly spaced."""
+    st, nd = t.stride(), len(shape)
+    ok = t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_cuda
+    ok = ok and (shape[-1] == 1 or st[-1] == 1) and (shape[-2] == 1 or st[-2] == shape[-1])
+    step, span = None, 1
+    for i in range(nd - 3, -1, -1):
+        if shape[i] != 1 and ok:
+            if step is None:
+                ok = st[i] % span == 0
+                step = st[i] // span
+            else:
+                ok = st[i] == step * span
+        span *= shape[i]
+    if not ok:
+        raise GdnSpecError(f"{name}: want CUDA {dtype} {tuple(shape)} with dense heads and evenly spaced "
+                           f"tokens, got {t.dtype} {tuple(t.shape)} strides={tuple(st)} device={t.device}")
+    return shape[-1] * shape[-2] if step is None else step
+
+
+def rope(plan: RopePlan, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None,
+         transpose: bool = False, stream=None) -> torch.Tensor:
+    """gdn_spec_rope: x [N, heads, D] (tokens may be strided) turned to positions pos
+    [N]; transpose gives the gradient of x from that of the result.  out may be x."""
+    N, heads, D = x.shape if x.dim() == 3 else (0, 0, 0)
+    if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float32) or D != plan.D:
+        raise GdnSpecError(f"x: want bf16 or fp32 [N, heads, {plan.D}], got {x.dtype} {tuple(x.shape)}")
+    _need(pos, "pos", torch.int32, (N,))
+    xs = _token_stride(x, "x", x.dtype, (N, heads, D))
+    if out is None:
+        out = torch.empty((N, heads, D), dtype=x.dtype, device=x.device)
+    os_ = _token_stride(out, "out", x.dtype, (N, heads, D))
+    code = DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_FP32
+    rc = load().gdn_spec_rope(plan._ref, N, heads, code, _ptr(pos), _ptr(x), xs, _ptr(out), os_,
+                              int(bool(transpose)), _stream(stream))
+    _check(rc, "gdn_spec_rope")
+    return out
+
+
+def rope_append(plan: RopePlan, cache: KvCache, layer: int, slot_idx: torch.Tensor, q, k, v,
+                pos: torch.Tensor | None = None, n_tokens: torch.Tensor | None = None,
+                q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gdn_spec_rope_append: rotated q [B, T, HQ, D]; rotated k and v [B, T, HKV, D] go
+    behind the slots' committed tokens in ``layer`` of the cache.  q, k, v may be
+    slices of one projection's output."""
+    B = _rows(slot_idx, "slot_idx")
+    if q.dim() != 4 or k.dim() != 4:
+        raise GdnSpecError(f"q, k: want [B, T, heads, D], got {tuple(q.shape)} and {tuple(k.shape)}")
+    T, HQ, io = q.shape[1], q.shape[2], cache.io_torch
+    qs = _token_stride(q, "q", io, (B, T, HQ, cache.D))
+    ks = _token_stride(k, "k", io, (B, T, cache.HKV, cache.D))
+    vs = _token_stride(v, "v", io, (B, T, cache.HKV, cache.D))
+    if pos is not None:
+        _need(pos, "pos", torch.int32, (B, T))
+    if n_tokens is not None:
+        _need(n_tokens, "n_tokens", torch.int32, (B,))
+    if q_out is None:
+        q_out = torch.empty((B, T, HQ, cache.D), dtype=io, device=q.device)
+    _need(q_out, "q_out", io, (B, T, HQ, cache.D))
+    rc = load().gdn_spec_rope_append(plan._ref, cache._ref, layer, _ptr(slot_idx), B, T,
+                                     _ptr(n_tokens), _ptr(pos), HQ, _ptr(q), qs, _ptr(k), ks,
+                                     _ptr(v), vs, _ptr(q_out), _stream(stream))
+    _check(rc, "gdn_spec_rope_append")
+    return q_out
+
+
+def tree_attn_path(cache: KvCache, T: int, HQ: int) -> str:
+    r = load().gdn_spec_tree_attn_path(cache._ref, T, HQ)
+    if r is None:
+        raise GdnSpecError("invalid cache descriptor, window or head count")
+    return r.decode()
+
+
+def tree_attn_workspace(cache: KvCache, B: int, T: int, HQ: int) -> int:
+    """gdn_spec_tree_attn_workspace: bytes that a call of this size needs on the current device."""
+    n = load().gdn_spec_tree_attn_workspace(cache._ref, B, T, HQ)
+    if n < 0:
+        _check(n, "gdn_spec_tree_attn_workspace")
+    return n
+
+
+def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tensor,
+              tree_mask: torch.Tensor | None = None, tree_len: torch.Tensor | None = None,
+              scale: float | None = None, out: torch.Tensor | None = None,
+              lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """gdn_spec_tree_attn: attention [B, T, HQ, D] of a window of drafted tokens over
+    ``layer`` of the cache.  tree_mask int64 [B, T]: bit n of a node's word lets it
+    attend to node n (None: a chain); tree_len int32 [B]: the rows' nodes (None: T);
+    scale: D^-0.5 by default; lse fp32 [B, T, HQ]: written when given; workspace: uint8,
+    at least ``tree_attn_workspace`` bytes (None: allocated)."""
+    B = _rows(slot_idx, "slot_idx")
+    if q.dim() != 4:
+        raise GdnSpecError(f"q: want [B, T, HQ, D], got {tuple(q.shape)}")
+    T, HQ = q.shape[1], q.shape[2]
+    _need(q, "q", cache.io_torch, (B, T, HQ, cache.D))
+    if tree_mask is not None:
+        _need(tree_mask, "tree_mask", torch.int64, (B, T))
+    if tree_len is not None:
+        _need(tree_len, "tree_len", torch.int32, (B,))
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", cache.io_torch, (B, T, HQ, cache.D))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, T, HQ))
+    if workspace is None:
+        workspace = torch.empty(max(16, tree_attn_workspace(cache, B, T, HQ)), dtype=torch.uint8,
+                                device=q.device)
+    _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    rc = load().gdn_spec_tree_attn(cache._ref, layer, _ptr(slot_idx), B, T, HQ, _ptr(q),
+                                   _ptr(tree_mask), _ptr(tree_len),
+                                   cache.D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
+                                   _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "gdn_spec_tree_attn")
+    return out

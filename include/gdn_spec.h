@@ -66,12 +66,15 @@
 extern "C" {
 #endif
 
-#define GDN_SPEC_ABI_VERSION 4   /* 2: adds gdn_spec_prefill and the snapshot comparison calls;
+#define GDN_SPEC_ABI_VERSION 5   /* 2: adds gdn_spec_prefill and the snapshot comparison calls;
                                     3: adds gdn_spec_verify_d, gdn_spec_set_wait_limit, commit's
                                        cursor check and the poisoning of rows a fold or prefill
                                        could not finish;
                                     4: adds gdn_spec_prefill_path, the chunk-parallel prefill and
-                                       the tensor-core KDA verify ("tc_kda") */
+                                       the tensor-core KDA verify ("tc_kda");
+                                    5: adds the softmax-attention layers' step: gdn_spec_tree_attn,
+                                       gdn_spec_rope and gdn_spec_rope_append, and the paged cache
+                                       gdn_spec_kv_* */
 
 /* host-side error codes (return values) */
 #define GDN_SPEC_OK            0
@@ -96,6 +99,11 @@ extern "C" {
                                               or partly prefilled, so the slot must be rebuilt:
                                               gdn_spec_reset, then gdn_spec_prefill. */
 #define GDN_SPEC_ST_UNFOLDED      32u  /* prefill: continuing from a checkpoint whose ring is not folded */
+#define GDN_SPEC_ST_NO_PAGES      64u  /* kv_reserve, kv_fork: not enough free pages or table columns for
+                                              the row; other calls: the slot's pages do not hold its tokens */
+#define GDN_SPEC_ST_PAGE_OOR     128u  /* a page table entry in use is outside [0, num_pages): the row's
+                                              outputs are not valid */
+#define GDN_SPEC_ST_SLOT_BUSY    256u  /* kv_fork: the destination slot holds tokens or pages */
 
 #define GDN_SPEC_GATE_SCALAR  0    /* GDN: one gate per (token, v-head)            */
 #define GDN_SPEC_GATE_PER_KEY 1    /* KDA: one gate per (token, v-head, key channel) */
@@ -323,6 +331,205 @@ const char *gdn_spec_verify_path(const gdn_spec_layer *layer);
  * CUDA-core path), or NULL if the layer is invalid.  Host only; launches
  * nothing. */
 const char *gdn_spec_prefill_path(const gdn_spec_layer *layer);
+
+/* ======================================================================
+ * The softmax-attention layers of a hybrid model: a speculative step over a
+ * paged key/value cache.  Per layer: gdn_spec_rope_append (rotary positions,
+ * the window's keys and values written behind the committed tokens), then
+ * gdn_spec_tree_attn (the window's attention; a window is a tree of drafted
+ * tokens).  Per step, over all layers: gdn_spec_kv_commit (the accepted path
+ * moves together behind the committed tokens) and gdn_spec_kv_reserve (pages
+ * for the next window).  gdn_spec_kv_fork and gdn_spec_kv_free start and end
+ * a sequence that shares another one's pages.
+ * ====================================================================== */
+
+/*
+ * The cache of all softmax-attention layers.  Slot s holds length[s] committed
+ * tokens; token i of slot s is row i % P of page page_table[s][i / P], in every
+ * layer.  The drafted tokens of a step follow the committed ones (position
+ * length[s] + node) in the same pages.  A page may be held by several slots
+ * (ref counts them); only full pages are ever shared, so no shared page is
+ * written.  Page p is free exactly when ref[p] == 0 and bit p % 32 of
+ * free_bits[p / 32] is set.
+ */
+typedef struct {
+    int32_t n_layers;     /* softmax-attention layers                                   */
+    int32_t num_pages;    /* pages in the pool                                          */
+    int32_t HKV;          /* key/value heads                                            */
+    int32_t P;            /* tokens per page: 16, 32, 64, 128 or 256                    */
+    int32_t D;            /* head dim: a multiple of 8, at most 256                     */
+    int32_t io_dtype;     /* dtype of k, v and of the calls' q, k, v, out               */
+    int32_t num_slots;    /* slots in the pool                                          */
+    int32_t max_pages;    /* columns of page_table: pages a slot can hold               */
+    void *k, *v;          /* io_dtype [n_layers, num_pages, HKV, P, D]                  */
+    int32_t *page_table;  /* [num_slots, max_pages], -1 where there is no page          */
+    int32_t *n_pages;     /* [num_slots] pages held                                     */
+    int32_t *length;      /* [num_slots] committed tokens                               */
+    int32_t *ref;         /* [num_pages] slots that hold the page                       */
+    uint32_t *free_bits;  /* [ceil(num_pages / 32)]                                     */
+    uint32_t *status;     /* [1], device status bits (GDN_SPEC_ST_*); may be the word of
+                             a gdn_spec_cursors                                         */
+} gdn_spec_kv_cache;
+
+/* gdn_spec_kv_init -- every slot empty, every page free.  k and v are not touched. */
+int gdn_spec_kv_init(const gdn_spec_kv_cache *cache, void *stream);
+
+/*
+ * gdn_spec_kv_reserve -- pages for up to T more tokens: row b's slot gets the
+ * pages it lacks to hold length + n tokens, n = n_tokens[b] (NULL: T).  The free
+ * pages of lowest number are handed out in row order, so the tables depend only
+ * on the calls made.  Row b is served when the pages that rows 0..b lack
+ * together are free (rows that are refused for another reason take none);
+ * otherwise it keeps what it has and NO_PAGES is set.
+ *   n_tokens  int32 [B], device, 0 <= n_tokens <= T, or NULL
+ *   done      int32 [B], device (written): 1 where the row is served, else 0
+ * Device status: SLOT_OOR, ACCEPT_RANGE (n_tokens), CURSOR_CORRUPT, NO_PAGES.
+ */
+int gdn_spec_kv_reserve(const gdn_spec_kv_cache *cache, const int32_t *slot_idx, int32_t B, int32_t T,
+                        const int32_t *n_tokens, int32_t *done, void *stream);
+
+/*
+ * gdn_spec_kv_fork -- slot dst_idx[b] becomes a copy of slot src_idx[b]: the
+ * full pages of its committed tokens are shared (ref + 1), the committed rows of
+ * a last, partly filled page are copied to a page of its own in every layer
+ * (pages that the source holds past them are not taken over).  A
+ * destination must be empty (SLOT_BUSY otherwise), and no destination may be
+ * named twice or be a source; a source may be named often.  Rows are served as
+ * by gdn_spec_kv_reserve.  A negative index on either side is a padding row.
+ *   done      int32 [B], device (written)
+ */
+int gdn_spec_kv_fork(const gdn_spec_kv_cache *cache, const int32_t *src_idx, const int32_t *dst_idx,
+                     int32_t B, int32_t *done, void *stream);
+
+/*
+ * gdn_spec_kv_commit -- after sampling: the accepted drafts of every row move
+ * together, row i of the window's committed tokens taken from drafted node
+ * path[b][i] (i < accept_len[b]), in every layer, in place; then
+ * length += accept_len.  Pages are kept for the next window.
+ *   path        int32 [B, T], device: strictly ascending nodes in [0, T) (a
+ *               parent is numbered before its children), or NULL: nodes 0, 1, ...
+ *   accept_len  int32 [B], device, 0 <= accept_len <= T
+ * Device status: ACCEPT_RANGE (accept_len, or a path that does not ascend in
+ * [0, T)), SLOT_OOR, CURSOR_CORRUPT, NO_PAGES, PAGE_OOR; such a row is left as
+ * it is.
+ */
+int gdn_spec_kv_commit(const gdn_spec_kv_cache *cache, const int32_t *slot_idx, int32_t B, int32_t T,
+                       const int32_t *path, const int32_t *accept_len, void *stream);
+
+/* gdn_spec_kv_free -- each row's slot becomes empty; a page that no slot holds any more is free. */
+int gdn_spec_kv_free(const gdn_spec_kv_cache *cache, const int32_t *slot_idx, int32_t B, void *stream);
+
+/* gdn_spec_kv_read_status -- as gdn_spec_read_status, for a cache's status word. */
+int gdn_spec_kv_read_status(const gdn_spec_kv_cache *cache, uint32_t *host_out, int32_t clear,
+                            void *stream);
+
+/* pairs of a rotated vector: (x[i], x[i + rot/2]) or (x[2i], x[2i + 1]) */
+#define GDN_SPEC_ROPE_HALF        0
+#define GDN_SPEC_ROPE_INTERLEAVED 1
+
+/* how the frequencies f_i = base^(-2i/rot) are scaled for contexts longer than trained on */
+#define GDN_SPEC_ROPE_NONE   0
+#define GDN_SPEC_ROPE_LINEAR 1  /* f_i / factor                                              */
+#define GDN_SPEC_ROPE_NTK    2  /* base * factor^(rot / (rot - 2)) in place of base          */
+#define GDN_SPEC_ROPE_YARN   3  /* f_i / factor and f_i mixed by a ramp over i between the pairs
+                                   that turn `low` (floor) and `high` (ceil) times in `original`
+                                   positions (low is the larger number: the faster pair); cos and
+                                   sin times 0.1 ln(factor) + 1                              */
+#define GDN_SPEC_ROPE_BANDS  4  /* f_i / factor and f_i mixed by (turns - low) / (high - low)
+                                   clamped to [0, 1], turns = original f_i / (2 pi)          */
+
+typedef struct {
+    int32_t kind;      /* GDN_SPEC_ROPE_NONE ...                  */
+    int32_t reserved;  /* 0                                       */
+    double factor;     /* >= 1                                    */
+    double original;   /* positions trained on (YARN, BANDS)      */
+    double low, high;  /* YARN: fast, slow (32, 1); BANDS: 1, 4   */
+} gdn_spec_rope_scaling;
+
+/* A rotary plan, filled once by gdn_spec_rope_init or gdn_spec_rope_init_freqs (host only) and then
+ * passed to the calls, which copy it into their launch. */
+typedef struct {
+    int32_t D;           /* head dim: a multiple of 8, at most 256                  */
+    int32_t rot;         /* leading dims that are rotated: even, 2 .. D             */
+    int32_t layout;      /* GDN_SPEC_ROPE_HALF or GDN_SPEC_ROPE_INTERLEAVED         */
+    float   mscale;      /* factor on cos and sin                                   */
+    uint64_t freq[128];  /* turns per position of pair i, as a fraction of 2^64     */
+} gdn_spec_rope_plan;
+
+/* gdn_spec_rope_init -- frequencies from a base and a scaling (NULL: none). */
+int gdn_spec_rope_init(gdn_spec_rope_plan *plan, int32_t D, int32_t rot, int32_t layout, double base,
+                       const gdn_spec_rope_scaling *scaling);
+
+/* gdn_spec_rope_init_freqs -- frequencies given in radians per position, rot / 2 of them (host). */
+int gdn_spec_rope_init_freqs(gdn_spec_rope_plan *plan, int32_t D, int32_t rot, int32_t layout,
+                             const double *freqs, double mscale);
+
+/*
+ * gdn_spec_rope -- out = R x: pair i of every head of token n turned by the
+ * angle pos[n] f_i and multiplied by mscale, the other dims copied.  transpose
+ * != 0 gives R^T x, the gradient of x from that of out.  The angle is taken
+ * modulo a turn in 64-bit fixed point, so it does not lose precision at long
+ * positions; the products are fp32 and rounded once.
+ *   pos   int32 [N], device
+ *   x     io_dtype [N, heads, D]: token n at x + n * x_stride elements, its heads dense
+ *   out   io_dtype [N, heads, D]: token stride out_stride; may be x itself with the same stride
+ * Strides are multiples of 8 elements, at least heads * D.
+ */
+int gdn_spec_rope(const gdn_spec_rope_plan *plan, int32_t N, int32_t heads, int32_t io_dtype,
+                  const int32_t *pos, const void *x, int64_t x_stride, void *out, int64_t out_stride,
+                  int32_t transpose, void *stream);
+
+/*
+ * gdn_spec_rope_append -- a window's rotary positions and its append to one
+ * layer of the cache: q_out = R q; R k and v are written behind the committed
+ * tokens of row b's slot, token t at length + t, t < n_tokens[b] (NULL: T).
+ * length is not changed (gdn_spec_kv_commit moves it; for a prompt, with
+ * path = NULL and accept_len = n_tokens).  The pages must have been reserved.
+ *   q      io_dtype [B, T, HQ, D], k, v io_dtype [B, T, HKV, D]: token (b, t) at
+ *          (b * T + t) * {q,k,v}_stride elements, its heads dense, so the three can be
+ *          slices of one projection's output.  Strides are multiples of 8 elements.
+ *   pos    int32 [B, T], device; NULL: length + t (a chain)
+ *   q_out  io_dtype [B, T, HQ, D], dense (written; zeros for padding rows and t >= n_tokens)
+ * T >= 1, any length.  Device status: SLOT_OOR, ACCEPT_RANGE (n_tokens),
+ * CURSOR_CORRUPT, NO_PAGES, PAGE_OOR; such a row writes zeros to q_out only.
+ */
+int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache *cache, int32_t layer,
+                         const int32_t *slot_idx, int32_t B, int32_t T, const int32_t *n_tokens,
+                         const int32_t *pos, int32_t HQ, const void *q, int64_t q_stride, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, void *q_out, void *stream);
+
+/*
+ * gdn_spec_tree_attn -- softmax attention of a window of drafted tokens over
+ * one layer of the cache.  Node t of row b attends to the length committed
+ * tokens of its slot and, of the window's tokens (cache positions length + n,
+ * n < tree_len[b]), to those whose bit n is set in tree_mask[b][t]:
+ *   out = sum_j p_j v_j,  p = softmax_j(scale <q, k_j>)
+ * A node that attends to nothing, a node t >= tree_len[b] and a padding row give
+ * zeros (lse: -inf).  What is masked has no effect, whatever its bits.
+ *   q          io_dtype [B, T, HQ, D]; HKV divides HQ, head h reads kv head h / (HQ / HKV)
+ *   tree_mask  uint64 [B, T], device; NULL: a chain (node t attends to nodes 0..t)
+ *   tree_len   int32 [B], device, 0 <= tree_len <= T; NULL: T
+ *   scale      > 0
+ *   out        io_dtype [B, T, HQ, D] (written)
+ *   lse        fp32 [B, T, HQ] (written), natural log of the softmax denominator; or NULL
+ *   workspace  device memory of workspace_bytes >= gdn_spec_tree_attn_workspace, 16-byte
+ *              aligned; its contents need not be kept or cleared, and calls that may run at
+ *              the same time need one each
+ * fp32 throughout on the CUDA cores ("generic", gdn_spec_tree_attn_path).  1 <= T <= 64.
+ * Device status: SLOT_OOR, ACCEPT_RANGE (tree_len), CURSOR_CORRUPT, NO_PAGES (the row
+ * gives zeros), PAGE_OOR, TIMEOUT.
+ */
+int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int32_t *slot_idx, int32_t B,
+                       int32_t T, int32_t HQ, const void *q, const uint64_t *tree_mask,
+                       const int32_t *tree_len, float scale, void *out, float *lse, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace for such a call on the current device, or a negative GDN_SPEC_E* code. */
+int64_t gdn_spec_tree_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, int32_t T, int32_t HQ);
+
+/* Name of the kernel gdn_spec_tree_attn would launch ("tc", "generic"), or NULL if the descriptor is
+ * invalid.  Host only. */
+const char *gdn_spec_tree_attn_path(const gdn_spec_kv_cache *cache, int32_t T, int32_t HQ);
 
 #ifdef __cplusplus
 }
