@@ -30,6 +30,9 @@ cudaError_t launch_rope_append(const gdn_spec_rope_plan *plan, const KvArgs &C, 
                                int64_t v_stride, void *q_out, cudaStream_t st);
 void tree_attn_cut(AttnArgs *A, int sms);
 cudaError_t launch_tree_attn(const AttnArgs &A, bool bf16, cudaStream_t st);
+bool tree_attn_tc_supported(const KvArgs &C, int G, bool bf16);
+void tree_attn_tc_cut(AttnArgs *A, int sms);
+cudaError_t launch_tree_attn_tc(const AttnArgs &A, cudaStream_t st);
 
 }  // namespace gdnspec
 
@@ -120,6 +123,10 @@ int device_sms(int *sms) {
     return cuda_rc(e);
 }
 
+bool attn_on_tc(const gdn_spec_kv_cache *c, int32_t HQ) {
+    return tree_attn_tc_supported(kv_args(c), HQ / c->HKV, c->io_dtype == GDN_SPEC_DTYPE_BF16);
+}
+
 int attn_args(const gdn_spec_kv_cache *c, int32_t B, int32_t T, int32_t HQ, AttnArgs *A) {
     A->C = kv_args(c);
     A->layer = 0;
@@ -130,7 +137,7 @@ int attn_args(const gdn_spec_kv_cache *c, int32_t B, int32_t T, int32_t HQ, Attn
     int sms;
     const int rc = device_sms(&sms);
     if (rc) return rc;
-    tree_attn_cut(A, sms);
+    if (attn_on_tc(c, HQ)) tree_attn_tc_cut(A, sms); else tree_attn_cut(A, sms);
     return GDN_SPEC_OK;
 }
 
@@ -298,7 +305,8 @@ int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache
 }
 
 const char *gdn_spec_tree_attn_path(const gdn_spec_kv_cache *cache, int32_t T, int32_t HQ) {
-    return check_attn(cache, 0, T, HQ) == GDN_SPEC_OK ? "generic" : nullptr;
+    if (check_attn(cache, 0, T, HQ) != GDN_SPEC_OK) return nullptr;
+    return attn_on_tc(cache, HQ) ? "tc" : "generic";
 }
 
 int64_t gdn_spec_tree_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, int32_t T, int32_t HQ) {
@@ -333,6 +341,7 @@ int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int3
     A.part_o = static_cast<float4 *>(workspace);
     A.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + rows * cache->D * 4);
     A.wait_limit = data_wait_limit();
+    if (attn_on_tc(cache, HQ)) return cuda_rc(launch_tree_attn_tc(A, as_stream(stream)));
     return cuda_rc(launch_tree_attn(A, cache->io_dtype == GDN_SPEC_DTYPE_BF16, as_stream(stream)));
 }
 
