@@ -141,7 +141,11 @@ int attn_args(const gdn_spec_kv_cache *c, int32_t B, int32_t T, int32_t HQ, Attn
     return GDN_SPEC_OK;
 }
 
+// Workspace: pieces' sums, their maxima and sums, the chunks' notes.
 int64_t part_rows(const AttnArgs &A) { return (int64_t)A.groups * A.NQT * 2 * A.MT; }
+int64_t workspace_bytes_of(const AttnArgs &A) {
+    return part_rows(A) * ((int64_t)A.C.D * 4 + 8) + (int64_t)A.groups * sizeof(AttnCut);
+}
 
 }  // namespace
 
@@ -314,7 +318,7 @@ int64_t gdn_spec_tree_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, 
     if (rc) return rc;
     AttnArgs A = {};
     if ((rc = attn_args(cache, B, T, HQ, &A))) return rc;
-    return part_rows(A) * ((int64_t)cache->D * 4 + 8);
+    return workspace_bytes_of(A);
 }
 
 int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int32_t *slot_idx, int32_t B, int32_t T,
@@ -329,7 +333,7 @@ int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int3
     AttnArgs A = {};
     if ((rc = attn_args(cache, B, T, HQ, &A))) return rc;
     const int64_t rows = part_rows(A);
-    if (workspace_bytes < rows * ((int64_t)cache->D * 4 + 8)) return GDN_SPEC_EINVAL;
+    if (workspace_bytes < workspace_bytes_of(A)) return GDN_SPEC_EINVAL;
     A.layer = layer;
     A.slot_idx = slot_idx;
     A.tree_mask = tree_mask;
@@ -340,6 +344,7 @@ int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int3
     A.lse = lse;
     A.part_o = static_cast<float4 *>(workspace);
     A.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + rows * cache->D * 4);
+    A.cuts = reinterpret_cast<AttnCut *>(static_cast<char *>(workspace) + rows * ((int64_t)cache->D * 4 + 8));
     A.wait_limit = data_wait_limit();
     if (attn_on_tc(cache, HQ)) return cuda_rc(launch_tree_attn_tc(A, as_stream(stream)));
     return cuda_rc(launch_tree_attn(A, cache->io_dtype == GDN_SPEC_DTYPE_BF16, as_stream(stream)));

@@ -31,6 +31,7 @@ struct AttnArgs {
     float *lse;
     float4 *part_o;            // [groups * NQT][2][D / 4][MT] unnormalised sums of a piece
     float2 *part_ml;           // [groups * NQT][2][MT] (maximum in log2 units, sum)
+    struct AttnCut *cuts;      // [groups] where each chunk starts, for the join
     int TN, MT, NQT, groups, min_chunk;
     uint32_t wait_limit;
 };
@@ -181,6 +182,16 @@ struct AttnWalk {
         }
     }
 };
+
+// Where a chunk starts, noted by the group's first block.
+struct __align__(16) AttnCut {
+    int b, h, t, tiles;        // row (-1: the chunk is empty), kv head, tile of the item's `tiles`
+    int cnt, chunk, pad[2];    // the row's tokens, tiles of a chunk
+};
+
+__device__ __forceinline__ void attn_note(const AttnArgs &A, int group, bool any, const AttnPiece &pc, int chunk) {
+    A.cuts[group] = any ? AttnCut{pc.b, pc.h, pc.t0, pc.tiles, pc.cnt, chunk, {0, 0}} : AttnCut{-1, 0, 0, 0, 0, chunk, {0, 0}};
+}
 
 __device__ __forceinline__ AttnWalk attn_walk(const AttnPlan &p, int group) {
     AttnWalk w;

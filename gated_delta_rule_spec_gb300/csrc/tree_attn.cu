@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(kAttnThreads) tree_attn_kernel(const __grid_co
     const AttnPlan plan = attn_plan<kAttnThreads>(A, group, blockIdx.x == 0, scratch);
     AttnWalk walk = attn_walk(plan, group);
     AttnPiece pc;
-    while (walk.next(A, &pc)) {
+    bool any = walk.next(A, &pc);
+    if (tid == 0 && qt == 0) attn_note(A, group, any, pc, plan.chunk);
+    for (; any; any = walk.next(A, &pc)) {
         const int live = min(MT, pc.cnt * A.G - qt * MT);   // rows of this query tile
         if (live <= 0) continue;
         const int kv = pc.len + pc.cnt, D8 = D >> 3;
@@ -216,70 +218,83 @@ __global__ void __launch_bounds__(kAttnThreads) tree_attn_kernel(const __grid_co
 // ------------------------------------------------------------------ join
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinLanes = 8;      // pieces taken side by side
+constexpr int kJoinLanes = 8;      // threads that share an element's pieces when they are many
+constexpr int kJoinMany = 16;      // from so many pieces on
+
+// (m, l, o) of a row's four dims, as (maximum in log2 units, sum, unnormalised sums)
+struct JoinSum {
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float2 ml, float4 po) {
+        if (ml.y == 0.0f) return;   // that piece saw nothing, its sums may be anything
+        const float mn = fmaxf(m, ml.x), wa = exp2f(m - mn), wb = exp2f(ml.x - mn);
+        l = l * wa + ml.y * wb;
+        o.x = o.x * wa + po.x * wb;
+        o.y = o.y * wa + po.y * wb;
+        o.z = o.z * wa + po.z * wb;
+        o.w = o.w * wa + po.w * wb;
+        m = mn;
+    }
+};
 
 template <typename IO>
+__device__ __forceinline__ void join_put(const AttnArgs &A, const JoinSum &j, int64_t row, int d4) {
+    const float inv = j.l == 0.0f ? 0.0f : 1.0f / j.l;
+    IO out[4] = {from_f32<IO>(j.o.x * inv), from_f32<IO>(j.o.y * inv), from_f32<IO>(j.o.z * inv), from_f32<IO>(j.o.w * inv)};
+    IO *op = static_cast<IO *>(A.out) + row * A.C.D + 4 * d4;
+    if (sizeof(IO) == 2) *reinterpret_cast<uint2 *>(op) = *reinterpret_cast<const uint2 *>(out);
+    else *reinterpret_cast<uint4 *>(op) = *reinterpret_cast<const uint4 *>(out);
+    if (A.lse && d4 == 0) A.lse[row] = attn_lse(j.m, j.l);
+}
+
+// Block (g, query tile, part).  A thread takes the same four dims of one row from
+// every piece, all loads of two pieces in flight before they are merged; where an
+// item has many pieces (few rows, long contexts) eight threads share an element.
+// Everything about the item is in the chunk's note, so a block starts with one load.
+template <typename IO>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs A) {
-    __shared__ int scratch[kAttnScratch];
     __shared__ float4 o_s[kJoinLanes][32];
     __shared__ float2 ml_s[kJoinLanes][32];
     grid_dep_wait();
     const int g = blockIdx.x + 1, qt = blockIdx.y, tid = threadIdx.x, lane = tid & 31, pl = tid >> 5;
-    const AttnPlan p = attn_plan<kJoinThreads>(A, g, false, scratch);
-    if (p.b < 0) return;
-    uint32_t bits;
-    const AttnRow row = attn_row(A, p.b, &bits);
-    const int tiles = attn_tiles(A, row), h = p.off / tiles, t = p.off - h * tiles;
-    const int64_t cut = (int64_t)g * p.chunk, s = cut - t;
-    if (t == 0 || s / p.chunk != g - 1) return;   // the cut is between items, or not the item's first
-    const int live = min(A.MT, row.cnt * A.G - qt * A.MT);
+    const AttnCut cut = A.cuts[g];
+    const int64_t s = (int64_t)g * cut.chunk - cut.t;                // the item's first tile in the line
+    if (cut.b < 0 || cut.t == 0 || s / cut.chunk != g - 1) return;   // a cut between items, or not the item's first
+    const int live = min(A.MT, cut.cnt * A.G - qt * A.MT);
     if (live <= 0) return;
-    const int last = (int)((s + tiles - 1) / p.chunk);
+    const int last = (int)((s + cut.tiles - 1) / cut.chunk);
     const int D4 = A.C.D >> 2, work = live * D4;
+    const auto part_of = [&](int c) { return ((int64_t)c * A.NQT + qt) * 2 + (s > (int64_t)c * cut.chunk ? 1 : 0); };
+    if (last - g + 2 < kJoinMany) {
+        for (int x = blockIdx.z * kJoinThreads + tid; x < work; x += gridDim.z * kJoinThreads) {
+            const int d4 = x / live, r = x - d4 * live;
+            JoinSum sum;
+            for (int c = g - 1; c <= last; c += 2) {
+                const int64_t p0 = part_of(c), p1 = part_of(min(c + 1, last));
+                const float2 ml0 = A.part_ml[p0 * A.MT + r], ml1 = A.part_ml[p1 * A.MT + r];
+                const float4 o0 = A.part_o[(p0 * D4 + d4) * A.MT + r], o1 = A.part_o[(p1 * D4 + d4) * A.MT + r];
+                sum.add(ml0, o0);
+                if (c < last) sum.add(ml1, o1);
+            }
+            join_put<IO>(A, sum, attn_out_row(A, cut.b, cut.h, qt * A.MT + r), d4);
+        }
+        return;
+    }
     for (int x0 = blockIdx.z * 32; x0 < work; x0 += gridDim.z * 32) {
         const int x = x0 + lane, d4 = x / live, r = x - d4 * live;
-        float m = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x < work) {
+        JoinSum sum;
+        if (x < work)
             for (int c = g - 1 + pl; c <= last; c += kJoinLanes) {
-                const int64_t part = ((int64_t)c * A.NQT + qt) * 2 + (s > (int64_t)c * p.chunk ? 1 : 0);
-                const float2 ml = A.part_ml[part * A.MT + r];
-                if (ml.y == 0.0f) continue;   // the piece saw nothing
-                const float4 po = A.part_o[(part * D4 + d4) * A.MT + r];
-                const float mn = fmaxf(m, ml.x), wa = exp2f(m - mn), wb = exp2f(ml.x - mn);
-                l = l * wa + ml.y * wb;
-                o.x = o.x * wa + po.x * wb;
-                o.y = o.y * wa + po.y * wb;
-                o.z = o.z * wa + po.z * wb;
-                o.w = o.w * wa + po.w * wb;
-                m = mn;
+                const int64_t part = part_of(c);
+                sum.add(A.part_ml[part * A.MT + r], A.part_o[(part * D4 + d4) * A.MT + r]);
             }
-        }
-        o_s[pl][lane] = o;
-        ml_s[pl][lane] = make_float2(m, l);
+        o_s[pl][lane] = sum.o;
+        ml_s[pl][lane] = make_float2(sum.m, sum.l);
         __syncthreads();
         if (pl == 0 && x < work) {
 #pragma unroll
-            for (int w = 1; w < kJoinLanes; ++w) {
-                const float2 ml = ml_s[w][lane];
-                if (ml.y == 0.0f) continue;
-                const float4 po = o_s[w][lane];
-                const float mn = fmaxf(m, ml.x), wa = exp2f(m - mn), wb = exp2f(ml.x - mn);
-                l = l * wa + ml.y * wb;
-                o.x = o.x * wa + po.x * wb;
-                o.y = o.y * wa + po.y * wb;
-                o.z = o.z * wa + po.z * wb;
-                o.w = o.w * wa + po.w * wb;
-                m = mn;
-            }
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const int64_t orow = attn_out_row(A, p.b, h, qt * A.MT + r);
-            IO *op = static_cast<IO *>(A.out) + orow * A.C.D + 4 * d4;
-            op[0] = from_f32<IO>(o.x * inv);
-            op[1] = from_f32<IO>(o.y * inv);
-            op[2] = from_f32<IO>(o.z * inv);
-            op[3] = from_f32<IO>(o.w * inv);
-            if (A.lse && d4 == 0) A.lse[orow] = attn_lse(m, l);
+            for (int w = 1; w < kJoinLanes; ++w) sum.add(ml_s[w][lane], o_s[w][lane]);
+            join_put<IO>(A, sum, attn_out_row(A, cut.b, cut.h, qt * A.MT + r), d4);
         }
         __syncthreads();
     }
@@ -287,9 +302,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 
 cudaError_t launch_attn_join(const AttnArgs &A, bool bf16, cudaStream_t stream) {
     if (A.groups < 2) return cudaSuccess;
-    // enough blocks along an item's rows and columns that each walks its pieces a few times at most
     const int rows = A.T * A.G < A.MT ? A.T * A.G : A.MT;
-    int parts = (rows * (A.C.D / 4) + 127) / 128;
+    int parts = (rows * (A.C.D / 4) + 2 * kJoinThreads - 1) / (2 * kJoinThreads);   // two elements a thread
+    if (parts < 4) parts = 4;
     if (parts > 16) parts = 16;
     const dim3 grid(A.groups - 1, A.NQT, parts);
     return bf16 ? launch_dependent(attn_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, stream, A)

@@ -7,7 +7,7 @@
 //   O += P V      tcgen05.mma kind::f16, P from TMEM, V as it lies in its pages
 //                 (token rows of 64-element runs: the MN-major operand), fp32 in TMEM
 // One producer warp copies the pages' rows by TMA (one box of min(P, TN) tokens by 64
-// dims per lane, the page numbers looked up a tile ahead), one thread issues the
+// dims per lane, the page numbers looked up a tile ahead), one warp issues the
 // MMAs, and a warpgroup of 128 threads, one query row each, does each tile's softmax.
 // Two arrangements keep the tensor core and the copies busy while a softmax runs:
 //   NQ = 1, D <= 128: the tiles of one query tile go to two warpgroups in turn, each
@@ -33,8 +33,9 @@
 //
 // Every wait is bounded.  One that runs out raises the block's abort flag, on which all
 // roles leave their loops; the producer then waits for the copies it has in flight and
-// the MMA thread for its MMAs, TMEM is freed, and the status word gets TIMEOUT.
+// the MMA warp for its MMAs, TMEM is freed, and the status word gets TIMEOUT.
 #include <mutex>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -55,12 +56,21 @@ struct Lay {
     static constexpr int TN = D == 256 ? 64 : 128;             // keys of a tile
     static constexpr int NWG = D == 256 ? 1 : 2;               // softmax warpgroups, streams of O
     static constexpr bool kShare = NQ == 2;                    // both streams use every tile
-    static constexpr int kThreads = NWG * 128 + 64;
+    static constexpr bool kTurns = NWG == 2 && !kShare;        // tiles go to the streams in turn
+    static constexpr int kStep = kTurns ? 2 : 1;               // from a stream's tile to its next
+    // two warpgroups: a third holds the producer and the MMA warp and gives registers up, so that a softmax thread
+    // can hold its row's 128 scores (168 x 384 = 208 x 256 + 88 x 128)
+    static constexpr int kThreads = NWG == 2 ? 384 : 192;
+    static constexpr int kRegsMore = 208, kRegsLess = 88;
     static constexpr uint32_t kBlocks = D / 64;                // 64-dim blocks of a row
     static constexpr uint32_t kQTile = kRows * D * 2;          // one query tile
-    static constexpr int QB = D == 256 || (D == 128 && NQ == 2) ? 1 : 2;   // buffers of NQ query tiles
+    static constexpr int QB = D == 64 ? 2 : 1;                 // buffers of NQ query tiles
     static constexpr uint32_t kStage = TN * D * 2;             // one K or V tile
-    static constexpr int NST = D == 64 ? 9 : 5;
+    // Stages stand in rings, one for each warp that uses them in order: with tiles in turn every stream has its
+    // own, so that each stage's barriers are met by the same warps in every phase.
+    static constexpr int kRings = kTurns ? 2 : 1;
+    static constexpr int NR = D == 64 ? (kTurns ? 5 : 9) : (kTurns ? 3 : 5);
+    static constexpr int NST = kRings * NR;
     static constexpr uint32_t kOffKV = QB * NQ * kQTile;
     static constexpr uint32_t kOffMisc = kOffKV + NST * kStage;
     // TMEM columns
@@ -71,7 +81,7 @@ struct Lay {
 
 // Shared memory behind the tiles.
 struct Misc {
-    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_full, o_empty, drain;
+    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], o_full, o_empty, drain[2], clean[2];
     float2 ml[2][kRows];                  // (m, l) of the two streams' rows, exchanged when they are merged
     unsigned long long bad[3];            // drafts whose values are not finite, by piece modulo 3
     int scratch[kAttnScratch];
@@ -89,6 +99,12 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     return false;
 }
 
+// The same by a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                         uint32_t limit = kWaitLimitDefault) {
+    return __all_sync(0xffffffffu, wait(bar, parity, abort, limit));
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -101,6 +117,41 @@ __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
     ptx::tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ void landed32(uint32_t *r) {
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -123,11 +174,14 @@ __device__ __forceinline__ bool any_at_barrier(int threads, bool bad) {
     return r != 0;
 }
 
-// Order in which the K and V tiles of a piece of n tiles are copied and used.
-// Shared tiles: K0 V0 K1 V1 ..; tiles in turn: K0 K1 V0 K2 V1 .. (the next scores are
-// formed before this tile's sums).
-template <bool SHARE> __device__ __forceinline__ int pos_v(int i, int n) {
-    return SHARE ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+// Place of tile i's values, of a piece of n tiles, in its ring's order: K V K V .., or, with one stream,
+// K0 K1 V0 K2 V1 .. (the next scores are formed before this tile's sums).
+template <class L> __device__ __forceinline__ int pos_v(int i, int n) {
+    return L::NWG == 2 ? 2 * (i / L::kStep) + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+}
+// Places that a piece of n tiles takes in ring r.
+template <class L> __device__ __forceinline__ int ring_places(int n, int r) {
+    return L::kTurns ? 2 * ((n + 1 - r) >> 1) : 2 * n;
 }
 
 // Which of a tile's keys a row attends to, as 128 bits: keys before `len` all, drafted
@@ -164,7 +218,7 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
     const int RT = A.MT / NQ, tokens_q = RT / A.G;             // rows and tokens of a query tile
     const uint32_t box_bytes = BR * 128u;
     const uint32_t q_bytes = 128u * A.G * min(tokens_q, A.T);   // one 64-dim block of one query tile
-    uint32_t issued = 0, q_issued = 0;
+    uint32_t issued[2] = {0, 0}, q_issued = 0;
     bool ok = true;
     AttnWalk walk = attn_walk(plan, group);
     AttnPiece pc;
@@ -184,8 +238,9 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
             return ((A.layer * A.C.num_pages + page) * A.C.HKV + pc.h) * A.C.P + ((int)tok & (A.C.P - 1));
         };
         const auto copy = [&](const CUtensorMap *map, int row, int t) {
-            const uint32_t st = issued % L::NST, ph = (issued / L::NST) & 1u;
-            if (!__all_sync(0xffffffffu, wait(ptx::smem_addr(&ms->empty[st]), ph ^ 1u, &ms->abort))) return false;
+            const int r = L::kTurns ? (t - pc.t0) & 1 : 0;
+            const uint32_t p = r ? issued[1] : issued[0], st = r * L::NR + p % L::NR, ph = (p / L::NR) & 1u;
+            if (!all_wait(ptx::smem_addr(&ms->empty[st]), ph ^ 1u, &ms->abort)) return false;
             const uint32_t bar = ptx::smem_addr(&ms->full[st]);
             const int left = kv - t * L::TN, live = min(chunks, (left + BR - 1) / BR);
             if (lane == 0) ptx::mbar_expect_tx(bar, box_bytes * live * L::kBlocks);
@@ -193,14 +248,14 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
             if (row >= 0)
                 ptx::tma_load_2d(base + L::kOffKV + st * L::kStage + my_blk * (L::TN * 128u) + my_chunk * box_bytes, map,
                                  bar, my_blk * 64, row);
-            ++issued;
+            if (r) ++issued[1]; else ++issued[0];
             return true;
         };
         int row = box_row(pc.t0), next = box_row(pc.t0 + 1);
         ok = copy(mk, row, pc.t0);
         if (ok) {   // the query tiles, behind the first keys
             const uint32_t qb = q_issued % L::QB, ph = (q_issued / L::QB) & 1u;
-            ok = __all_sync(0xffffffffu, wait(ptx::smem_addr(&ms->q_empty[qb]), ph ^ 1u, &ms->abort));
+            ok = all_wait(ptx::smem_addr(&ms->q_empty[qb]), ph ^ 1u, &ms->abort);
             if (ok) {
                 const uint32_t bar = ptx::smem_addr(&ms->q_full[qb]);
                 const int t0 = qt * NQ * tokens_q;
@@ -217,148 +272,206 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
                 ++q_issued;
             }
         }
-        for (int i = 0; ok && i < n; ++i) {
+        if (ok && !L::kShare && n > 1) ok = copy(mk, next, pc.t0 + 1);
+        for (int i = 0; ok && i < n; ++i) {   // values of tile i, then the keys that are used after them
             const int t = pc.t0 + i;
             const int after = box_row(t + 2);
-            if (!L::kShare && i + 1 < n) ok = copy(mk, next, t + 1);
-            if (ok) ok = copy(mv, row, t);
-            if (ok && L::kShare && i + 1 < n) ok = copy(mk, next, t + 1);
+            ok = copy(mv, row, t);
+            if (L::kShare) {
+                if (ok && i + 1 < n) ok = copy(mk, next, t + 1);
+            } else {
+                if (ok && i + 2 < n) ok = copy(mk, after, t + 2);
+            }
             row = next;
             next = after;
         }
     }
     if (!ok) {   // copies in flight land before the block's shared memory goes away
-        for (uint32_t p = issued > L::NST ? issued - L::NST : 0; p < issued; ++p)
-            ptx::mbar_wait(ptx::smem_addr(&ms->full[p % L::NST]), (p / L::NST) & 1u);
+        for (int r = 0; r < L::kRings; ++r)
+            for (uint32_t p = issued[r] > L::NR ? issued[r] - L::NR : 0; p < issued[r]; ++p)
+                ptx::mbar_wait(ptx::smem_addr(&ms->full[r * L::NR + p % L::NR]), (p / L::NR) & 1u);
         for (uint32_t p = q_issued > L::QB ? q_issued - L::QB : 0; p < q_issued; ++p)
             ptx::mbar_wait(ptx::smem_addr(&ms->q_full[p % L::QB]), (p / L::QB) & 1u);
     }
 }
 
-// ------------------------------------------------------------------ MMA thread
+// ------------------------------------------------------------------ MMA warp
 
+// A value that all lanes hold, from one of them: the tensor core's operands are uniform
+// registers, and values that come from memory or from a loop are only seen to be
+// uniform behind a shuffle (without it each MMA costs some 300 cycles to issue).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Stream w of the block: with two streams each has a warp of its own, so that one's wait for a softmax does not
+// hold up the other's products.
 template <int D, int NQ>
 __device__ __forceinline__ void multiply(const AttnArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const AttnPlan &plan,
-                                         int group, int qt) {
+                                         int group, int qt, int w) {
     using L = Lay<D, NQ>;
     constexpr uint32_t idesc_s = ptx::idesc_bf16(kRows, L::TN);
     constexpr uint32_t idesc_o = ptx::idesc_bf16(kRows, D) | ptx::kIdescBMn;
-    uint32_t used = 0, q_used = 0, pieces = 0;
+    const int ring = L::kTurns ? w * L::NR : 0;   // first stage of this warp's ring
+    const uint32_t d_o = uniform(tmem + L::col_o(w));
+    uint32_t q_used = 0, pieces = 0;
+    uint32_t c_ph = 0;                          // bit of a barrier: parity of the waits done on clean
     uint32_t p_ph = 0, pv_ph = 0, pv_any = 0;   // bit of a buffer: parity of the waits done on p_full, of the commits
                                                 // made on pv_done, whether there was one
     bool ok = true;
     const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
-    const auto wait_full = [&](uint32_t pos) {
-        return wait(bar(ms->full[pos % L::NST]), (pos / L::NST) & 1u, &ms->abort, A.wait_limit);
+    // Everything that a product needs is made uniform before the wait that it hangs on, so that nothing but the
+    // issue lies between the two.
+    struct Stage {
+        uint32_t at, ph;   // stage of the ring, parity of its phase
     };
-    // S of buffer `buf` = query tile `s` times the K tile at `pos`
-    const auto scores = [&](int buf, uint32_t q_addr, uint32_t pos) {
-        const uint32_t k_addr = base + L::kOffKV + (pos % L::NST) * L::kStage;
-        ptx::tc_fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-            ptx::mma_bf16(tmem + L::col_s(buf), ptx::smem_desc_sw128(q_addr + (ks >> 2) * (kRows * 128u) + (ks & 3) * 32u),
-                          ptx::smem_desc_sw128(k_addr + (ks >> 2) * (L::TN * 128u) + (ks & 3) * 32u), idesc_s, ks != 0);
+    const auto after = [](Stage s, int n) {
+        s.at += n;
+        if (s.at >= (uint32_t)L::NR) {
+            s.at -= L::NR;
+            s.ph ^= 1u;
+        }
+        return s;
     };
-    const auto sums = [&](int buf, int o, uint32_t pos, bool first) {
-        const uint32_t v_addr = base + L::kOffKV + (pos % L::NST) * L::kStage;
+    struct Op {
+        uint64_t a, b;
+        uint32_t p, empty, full, ph;
+    };
+    const auto op = [&](Stage s, bool values, uint32_t q_addr, int buf) {
+        Op o;
+        const uint32_t addr = uniform(base + L::kOffKV + (ring + s.at) * L::kStage);
+        o.a = ptx::smem_desc_sw128(uniform(q_addr));
+        o.b = values ? ptx::smem_desc_sw128_mn(addr, L::TN * 128u) : ptx::smem_desc_sw128(addr);
+        o.p = uniform(tmem + L::col_s(buf));
+        o.empty = uniform(bar(ms->empty[ring + s.at]));
+        o.full = bar(ms->full[ring + s.at]);
+        o.ph = s.ph;
+        return o;
+    };
+    const auto wait_full = [&](const Op &o) { return all_wait(o.full, o.ph, &ms->abort, A.wait_limit); };
+    // S of a buffer = query tile times K tile
+    const auto scores = [&](const Op &o, int buf, bool last) {
+        const uint32_t done = uniform(bar(ms->s_full[buf])), q_done = uniform(bar(ms->q_empty[q_used % L::QB]));
         ptx::tc_fence_after_sync();
+        if (ptx::elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < L::TN / 16; ++ks)
-            ptx::mma_bf16_tmem_a(tmem + L::col_o(o), tmem + L::col_s(buf) + ks * 8,
-                                 ptx::smem_desc_sw128_mn(v_addr + ks * 2048u, L::TN * 128u), idesc_o, !first || ks != 0);
+            for (int ks = 0; ks < D / 16; ++ks)   // descriptors count in 16 bytes
+                ptx::mma_bf16(o.p, o.a + ((ks >> 2) * (kRows * 128u) + (ks & 3) * 32u) / 16,
+                              o.b + ((ks >> 2) * (L::TN * 128u) + (ks & 3) * 32u) / 16, idesc_s, ks != 0);
+            ptx::mma_commit(done);
+            ptx::mma_commit(o.empty);
+            if (last) ptx::mma_commit(q_done);
+        }
+        __syncwarp();
+    };
+    // O of this stream (+)= steps [K0, K1) of P times the V tile
+    const auto sums = [&](const Op &o, int buf, auto k0, auto k1, uint32_t keep) {
+        constexpr int K0 = decltype(k0)::value, K1 = decltype(k1)::value;
+        const uint32_t done = uniform(bar(ms->pv_done[buf]));
+        ptx::tc_fence_after_sync();
+        if (ptx::elect_one()) {
+#pragma unroll
+            for (int ks = K0; ks < K1; ++ks)
+                ptx::mma_bf16_tmem_a(d_o, o.p + ks * 8, o.b + ks * 2048u / 16, idesc_o, ks != 0 ? 1u : keep);
+            if (K1 == L::TN / 16) {
+                ptx::mma_commit(done);
+                ptx::mma_commit(o.empty);
+            }
+        }
+        __syncwarp();
+        if (K1 == L::TN / 16) {
+            pv_ph ^= 1u << buf;
+            pv_any |= 1u << buf;
+        }
+    };
+    const auto commit = [&](uint64_t &b) {
+        if (ptx::elect_one()) ptx::mma_commit(bar(b));
+        __syncwarp();
     };
     // S buffer `buf` may be written again once the sums that read its P are done
     const auto wait_free = [&](int buf) {
-        return !((pv_any >> buf) & 1u) || wait(bar(ms->pv_done[buf]), ((pv_ph >> buf) & 1u) ^ 1u, &ms->abort);
+        return !((pv_any >> buf) & 1u) || all_wait(bar(ms->pv_done[buf]), ((pv_ph >> buf) & 1u) ^ 1u, &ms->abort);
     };
-    const auto wait_p = [&](int buf) {
-        const uint32_t ph = (p_ph >> buf) & 1u;
-        p_ph ^= 1u << buf;
-        return wait(bar(ms->p_full[buf]), ph, &ms->abort);
-    };
+    using Zero = std::integral_constant<int, 0>;
+    using Half = std::integral_constant<int, L::TN / 32>;
+    using All = std::integral_constant<int, L::TN / 16>;
+    Stage sk = {0, 0}, sv = {0, 0};   // of the next K and V tile
     AttnWalk walk = attn_walk(plan, group);
     AttnPiece pc;
-    while (ok && walk.next(A, &pc)) {
+    bool any = walk.next(A, &pc);
+    if (w == 0 && qt == 0 && ptx::elect_one()) attn_note(A, group, any, pc, plan.chunk);
+    __syncwarp();
+    for (; ok && any; any = walk.next(A, &pc)) {
         if (pc.cnt * A.G - qt * A.MT <= 0) continue;
         const int n = pc.t1 - pc.t0;
         const uint32_t qb = q_used % L::QB;
-        const uint32_t q_addr = base + qb * NQ * L::kQTile;
-        const auto o_free = [&] { return wait(bar(ms->o_empty), (pieces & 1u) ^ 1u, &ms->abort); };
-        ok = wait_full(used) && wait(bar(ms->q_full[qb]), (q_used / L::QB) & 1u, &ms->abort, A.wait_limit);
-        if (L::kShare) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                ok = ok && wait_free(s);
-                if (ok) {
-                    scores(s, q_addr + s * L::kQTile, used);
-                    ptx::mma_commit(bar(ms->s_full[s]));
-                }
-            }
-            if (ok) {
-                ptx::mma_commit(bar(ms->empty[used % L::NST]));
-                if (n == 1) ptx::mma_commit(bar(ms->q_empty[qb]));
-            }
-            for (int i = 0; ok && i < n; ++i) {
-                const uint32_t pv = used + 2 * i + 1, pk = pv + 1;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    ok = ok && wait_p(s) && (s || wait_full(pv)) && (i || s || o_free());
-                    if (!ok) break;
-                    sums(s, s, pv, i == 0);
-                    ptx::mma_commit(bar(ms->pv_done[s]));
-                    pv_ph ^= 1u << s;
-                    pv_any |= 1u << s;
-                    if (s == 1) ptx::mma_commit(bar(ms->empty[pv % L::NST]));
-                    if (i + 1 < n) {
-                        ok = (s || wait_full(pk)) && wait_free(s);
-                        if (!ok) break;
-                        scores(s, q_addr + s * L::kQTile, pk);
-                        ptx::mma_commit(bar(ms->s_full[s]));
-                        if (s == 1) {
-                            ptx::mma_commit(bar(ms->empty[pk % L::NST]));
-                            if (i + 2 == n) ptx::mma_commit(bar(ms->q_empty[qb]));
-                        }
+        const uint32_t q_addr = base + (qb * NQ + (L::kShare ? w : 0)) * L::kQTile;
+        const auto o_free = [&] { return all_wait(bar(ms->o_empty), (pieces & 1u) ^ 1u, &ms->abort); };
+        ok = all_wait(bar(ms->q_full[qb]), (q_used / L::QB) & 1u, &ms->abort, A.wait_limit);
+        if (L::NWG == 2) {
+            // one S buffer a stream: scores, softmax, sums, then the next scores over what the sums have read
+            const int first = L::kTurns ? w : 0;
+            for (int i = first; ok && i < n; i += L::kStep) {
+                const Op qk = op(sk, false, q_addr, w);
+                ok = wait_full(qk) && wait_free(w);
+                if (!ok) break;
+                scores(qk, w, i + L::kStep >= n);
+                sv = after(sk, 1);
+                sk = after(sk, 2);
+                const Op pv = op(sv, true, q_addr, w);
+                const uint32_t keep = uniform(i > first);
+                const uint32_t half = bar(ms->p_half[w]), full = bar(ms->p_full[w]), ph = p_ph & 1u;
+                p_ph ^= 1u;
+                ok = wait_full(pv) && (i > first || o_free());
+                if (L::kShare && w == 1) {
+                    // a shared tile with drafts is cleaned by the first warpgroup: the window lies in at most two tiles
+                    const int d = pc.t0 + i - pc.len / L::TN;
+                    if (d >= 0) {
+                        ok = ok && all_wait(bar(ms->clean[d]), (c_ph >> d) & 1u, &ms->abort);
+                        c_ph ^= 1u << d;
                     }
                 }
+                ok = ok && all_wait(half, ph, &ms->abort);
+                if (!ok) break;
+                sums(pv, w, Zero(), Half(), keep);
+                ok = all_wait(full, ph, &ms->abort);
+                if (!ok) break;
+                sums(pv, w, Half(), All(), 1u);
+            }
+            if (ok && first >= n) {   // no tile for this stream; every phase of o_empty is waited for all the same
+                commit(ms->q_empty[qb]);
+                ok = o_free();
             }
         } else {
-            ok = ok && wait_free(0);
-            if (ok) {
-                scores(0, q_addr, used);
-                ptx::mma_commit(bar(ms->empty[used % L::NST]));
-                ptx::mma_commit(bar(ms->s_full[0]));
-                if (n == 1) ptx::mma_commit(bar(ms->q_empty[qb]));
-            }
+            // two S buffers: the next scores are formed before this tile's sums; the ring goes K0 K1 V0 K2 V1 ..
+            Op qk = op(sk, false, q_addr, 0);
+            ok = ok && wait_full(qk) && wait_free(0);
+            if (ok) scores(qk, 0, n == 1);
+            sk = after(sk, 1);
             for (int i = 0; ok && i < n; ++i) {
-                const int buf = i & 1, o = L::NWG == 2 ? buf : 0;
+                const int buf = i & 1;
                 if (i + 1 < n) {
-                    const uint32_t pk = used + 2 * i + 1;
-                    ok = wait_full(pk) && wait_free(buf ^ 1);
+                    qk = op(sk, false, q_addr, buf ^ 1);
+                    ok = wait_full(qk) && wait_free(buf ^ 1);
                     if (!ok) break;
-                    scores(buf ^ 1, q_addr, pk);
-                    ptx::mma_commit(bar(ms->empty[pk % L::NST]));
-                    ptx::mma_commit(bar(ms->s_full[buf ^ 1]));
-                    if (i + 2 == n) ptx::mma_commit(bar(ms->q_empty[qb]));
+                    scores(qk, buf ^ 1, i + 2 == n);
+                    sk = after(sk, 1);
                 }
-                const uint32_t pv = used + pos_v<false>(i, n);
-                ok = wait_p(buf) && wait_full(pv) && (i || o_free());
+                const Op pv = op(sk, true, q_addr, buf);
+                sk = after(sk, 1);
+                const uint32_t keep = uniform(i > 0);
+                const uint32_t ph = (p_ph >> buf) & 1u;
+                p_ph ^= 1u << buf;
+                ok = wait_full(pv) && (i || o_free()) && all_wait(bar(ms->p_full[buf]), ph, &ms->abort);
                 if (!ok) break;
-                sums(buf, o, pv, i < L::NWG);
-                ptx::mma_commit(bar(ms->empty[pv % L::NST]));
-                ptx::mma_commit(bar(ms->pv_done[buf]));
-                pv_ph ^= 1u << buf;
-                pv_any |= 1u << buf;
+                sums(pv, buf, Zero(), All(), keep);
             }
         }
-        if (ok) ptx::mma_commit(bar(ms->o_full));
-        used += 2 * n;
+        if (ok) commit(ms->o_full);
         ++q_used;
         ++pieces;
     }
     if (!ok) {   // no MMA is running when TMEM is freed
-        ptx::mma_commit(bar(ms->drain));
-        ptx::mbar_wait(bar(ms->drain), 0);
+        commit(ms->drain[w]);
+        ptx::mbar_wait(bar(ms->drain[w]), 0);
     }
 }
 
@@ -448,90 +561,120 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
         float m = -INFINITY, l = 0.0f;
         // A thread whose wait ran out goes on without waiting or computing, so that the warpgroup's barriers are
         // met by all, until the barrier at the piece's end tells everybody.
-        for (int i = L::kShare || L::NWG == 1 ? 0 : w; i < n; i += L::kShare || L::NWG == 1 ? 1 : 2) {
-            const int buf = L::kShare ? w : i & 1, o = L::NWG == 2 ? w : 0;
+        const int first = L::kTurns ? w : 0;
+        for (int i = first; i < n; i += L::kStep) {
+            const int buf = L::NWG == 2 ? w : i & 1, o = w;
+            const bool drafts = (pc.t0 + i + 1) * L::TN > pc.len;   // the tile holds drafted tokens, or ends the row
             const int k0 = (pc.t0 + i) * L::TN;
             ok = __all_sync(0xffffffffu, ok && wait(bar(ms->s_full[buf]), (s_ph >> buf) & 1u, &ms->abort));
             s_ph ^= 1u << buf;
             ptx::tc_fence_after_sync();
+            const bool ok_half = ok;
             if (ok && warp_on) {
+                // eight chains of three-input maxima (one chain's latency would be the whole row's), taken of each 32
+                // scores while the next are on their way from TMEM
                 uint32_t s[L::TN];
+                float tops[8];
+                uint32_t bits[4];
+                if (drafts) visible_bits(k0, pc.len, mask, bits);
+                ptx::tmem_ld32_bits(lane_addr + L::col_s(buf), s);
 #pragma unroll
-                for (int x = 0; x < L::TN; x += 32) ptx::tmem_ld32_bits(lane_addr + L::col_s(buf) + x, s + x);
-                landed(s);
-                if (k0 + L::TN > pc.len) {
-                    uint32_t bits[4];
-                    visible_bits(k0, pc.len, mask, bits);
+                for (int x = 0; x < L::TN; x += 32) {
+                    landed32(s + x);
+                    if (x + 32 < L::TN) ptx::tmem_ld32_bits(lane_addr + L::col_s(buf) + x + 32, s + x + 32);
+                    if (drafts) {
 #pragma unroll
-                    for (int x = 0; x < L::TN; ++x)
-                        if (!((bits[x >> 5] >> (x & 31)) & 1u)) s[x] = 0xff800000u;
+                        for (int j = 0; j < 32; ++j)
+                            if (!((bits[x >> 5] >> j) & 1u)) s[x + j] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float a = __uint_as_float(s[x + j]), b = __uint_as_float(s[x + 8 + j]);
+                        const float d = __uint_as_float(s[x + 16 + j]), e = __uint_as_float(s[x + 24 + j]);
+                        tops[j] = x == 0 ? max3(a, b, d) : max3(max3(tops[j], a, b), d, e);
+                        if (x == 0) tops[j] = fmaxf(tops[j], e);
+                    }
                 }
-                float top = __uint_as_float(s[0]);
-#pragma unroll
-                for (int x = 1; x < L::TN; ++x) top = fmaxf(top, __uint_as_float(s[x]));
-                top *= c;
+                const float top = c * max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]),
+                                           fmaxf(tops[6], tops[7]));
                 const bool move = top > m + kGrow || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, move)) {
                     const float to = move ? top : m;
                     const float al = m == -INFINITY ? 0.0f : ex2(m - to);
                     l *= al;
                     m = to;
-                    const bool begun = L::kShare || L::NWG == 1 ? i > 0 : i > 1;
-                    if (begun) {
+                    if (i > first) {
                         // the sums so far, in O, are those of the stream's tile before this one
                         if (L::NWG == 1)
                             ok = __all_sync(0xffffffffu, wait(bar(ms->pv_done[buf ^ 1]), ((pv_ph >> (buf ^ 1)) & 1u) ^ 1u,
                                                               &ms->abort));
                         if (ok) {
                             ptx::tc_fence_after_sync();
-#pragma unroll
-                            for (int x = 0; x < D; x += 32) {
-                                uint32_t u[32];
-                                ptx::tmem_ld32_bits(lane_addr + L::col_o(o) + x, u);
+#pragma unroll 1
+                            for (int x = 0; x < D; x += 8) {   // few at a time: the row's scores are held as well
+                                uint32_t u[8];
+                                ptx::tmem_ld8_bits(lane_addr + L::col_o(o) + x, u);
                                 landed(u);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * al);
-                                ptx::tmem_st32_bits(lane_addr + L::col_o(o) + x, u);
+                                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * al);
+                                ptx::tmem_st8_bits(lane_addr + L::col_o(o) + x, u);
                             }
                         }
                     }
                 }
                 const float off = m == -INFINITY ? 0.0f : -m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
 #pragma unroll
                 for (int x = 0; x < L::TN; x += 32) {
                     uint32_t p[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float a = ex2(fmaf(__uint_as_float(s[x + 2 * j]), c, off));
-                        const float b = ex2(fmaf(__uint_as_float(s[x + 2 * j + 1]), c, off));
-                        sum[(2 * j) & 3] += a;
-                        sum[(2 * j + 1) & 3] += b;
+                        float a, b;
+                        unpair(fma2(pair(__uint_as_float(s[x + 2 * j]), __uint_as_float(s[x + 2 * j + 1])), c2, off2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[j & 3] = add2(sum[j & 3], pair(a, b));
                         p[j] = pack_bf16(a, b);
                     }
                     ptx::tmem_st16_bits(lane_addr + L::col_s(buf) + x / 2, p);
+                    if (L::NWG == 2 && x + 32 == L::TN / 2 && !drafts) {   // the sums begin on the first half
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->p_half[buf]));
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float s0, s1;
+                unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                l += s0 + s1;
                 ptx::tmem_st_wait();
             }
-            if (k0 + L::TN > pc.len && (!L::kShare || w == 0)) {
-                const uint32_t pos = used + pos_v<L::kShare>(i, n), st = pos % L::NST;
-                ok = __all_sync(0xffffffffu, ok && wait(bar(ms->full[st]), (pos / L::NST) & 1u, &ms->abort));
+            if (drafts && (!L::kShare || w == 0)) {
+                const uint32_t pos = used + pos_v<L>(i, n), st = (L::kTurns ? w * L::NR : 0) + pos % L::NR;
+                ok = __all_sync(0xffffffffu, ok && wait(bar(ms->full[st]), (pos / L::NR) & 1u, &ms->abort));
                 clean_values<D, NQ>(sm + L::kOffKV + st * L::kStage, k0, pc.len, kv, tid, &ms->bad[pieces % 3]);
+                if (L::kShare) {
+                    __syncwarp();
+                    if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->clean[pc.t0 + i - pc.len / L::TN]));
+                }
             }
             ptx::tc_fence_before_sync();
             __syncwarp();
-            if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->p_full[buf]));
+            if ((tid & 31) == 0) {
+                if (L::NWG == 2 && (drafts || !(ok_half && warp_on))) ptx::mbar_arrive(bar(ms->p_half[buf]));
+                ptx::mbar_arrive(bar(ms->p_full[buf]));
+            }
             pv_ph ^= 1u << buf;
         }
         ok = ok && wait(bar(ms->o_full), pieces & 1u, &ms->abort);
         ptx::tc_fence_after_sync();
         // ---- the piece's rows: merge the streams, put out or keep
-        if (L::NWG == 2 && !L::kShare) ms->ml[w][tid] = make_float2(m, l);
+        if (L::kTurns) ms->ml[w][tid] = make_float2(m, l);
         if (tid_all == 0) ms->bad[(pieces + 1) % 3] = 0;
         ok = !any_at_barrier(kBothThreads, !ok);
         float w0 = 1.0f, w1 = 0.0f;
-        if (L::NWG == 2 && !L::kShare) {
+        if (L::kTurns) {
             const float2 a = ms->ml[0][tid], b = ms->ml[1][tid];
             m = fmaxf(a.x, b.x);
             w0 = a.y == 0.0f ? 0.0f : ex2(a.x - m);
@@ -543,15 +686,15 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
             const int64_t row = attn_out_row(A, pc.b, pc.h, on ? r : qt * A.MT);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             // the two warpgroups of a shared query tile take half of the dims each
-            constexpr int kDims = L::NWG == 2 && !L::kShare ? D / 2 : D;
-            const int d_begin = L::NWG == 2 && !L::kShare ? w * kDims : 0;
+            constexpr int kDims = L::kTurns ? D / 2 : D;
+            const int d_begin = L::kTurns ? w * kDims : 0;
             const int64_t part = (int64_t)blockIdx.x * 2 + pc.side;
             const bool whole = pc.whole();
 #pragma unroll 1
             for (int x = 0; x < kDims; x += 32) {
                 const int d0 = d_begin + x;
                 float f[32];
-                if (L::NWG == 2 && !L::kShare) {
+                if (L::kTurns) {
                     uint32_t u[32], v[32];
                     ptx::tmem_ld32_bits(lane_addr + L::col_o(0) + d0, u);
                     ptx::tmem_ld32_bits(lane_addr + L::col_o(1) + d0, v);
@@ -601,7 +744,7 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
         ptx::tc_fence_before_sync();
         __syncwarp();
         if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->o_empty));
-        used += 2 * n;
+        used += ring_places<L>(n, w);
         ++pieces;
     }
 }
@@ -628,18 +771,22 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         const auto init = [](uint64_t &b, uint32_t n) { ptx::mbar_init(ptx::smem_addr(&b), n); };
         for (int i = 0; i < L::NST; ++i) {
             init(ms->full[i], 1);
-            init(ms->empty[i], 1);
+            init(ms->empty[i], NQ);            // streams that use a tile
         }
         for (int i = 0; i < 2; ++i) {
             init(ms->q_full[i], 1);
-            init(ms->q_empty[i], 1);
+            init(ms->q_empty[i], L::NWG);
             init(ms->s_full[i], 1);
+            init(ms->p_half[i], 4);
             init(ms->p_full[i], 4);
             init(ms->pv_done[i], 1);
         }
-        init(ms->o_full, 1);
+        init(ms->o_full, L::NWG);
         init(ms->o_empty, L::NWG * 4);
-        init(ms->drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            init(ms->drain[i], 1);
+            init(ms->clean[i], 4);
+        }
         ms->bad[0] = ms->bad[1] = ms->bad[2] = 0;
         ms->abort = 0;
         ptx::mbar_init_fence();
@@ -656,12 +803,12 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     const uint32_t tmem = ms->tmem;
 
     if (warp < L::NWG * 4) {
+        if (L::NWG == 2) more_registers<L::kRegsMore>();
         soften<D, NQ>(A, ms, sm, tmem, plan, group, qt, tid);
-    } else if (warp == L::NWG * 4) {
-        produce<D, NQ>(A, &mq, &mk, &mv, ms, base, plan, group, qt, lane);
     } else {
-        if (lane == 0) multiply<D, NQ>(A, ms, base, tmem, plan, group, qt);
-        __syncwarp();
+        if (L::NWG == 2) fewer_registers<L::kRegsLess>();
+        if (warp == L::NWG * 4) produce<D, NQ>(A, &mq, &mk, &mv, ms, base, plan, group, qt, lane);
+        if (warp > L::NWG * 4 && warp <= L::NWG * 5) multiply<D, NQ>(A, ms, base, tmem, plan, group, qt, warp - L::NWG * 4 - 1);
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
