@@ -266,7 +266,9 @@ __device__ __forceinline__ int commit_row(const KvArgs &C, int slot, int acc, in
 // of one layer's keys or values and walks the path upwards, eight loads before
 // their eight stores.  In place this is safe: a path ascends, so path[i] >= i, and
 // the rows written so far, all below i, are never the source of a later move.
-// Leading nodes with path[i] == i stay.
+// Leading nodes with path[i] == i stay.  ADVANCE: the launch has one block per row,
+// which moves the length as well once it has read it.
+template <bool ADVANCE>
 __global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(KvArgs C, const int32_t *__restrict__ slot_idx, int T,
                                                                const int32_t *__restrict__ path,
                                                                const int32_t *__restrict__ accept_len, int es) {
@@ -295,7 +297,10 @@ __global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(KvArgs C, const i
                 n += __popc(any);
             }
         }
-        if (tid == 0) n_s = n;
+        if (tid == 0) {
+            n_s = n;
+            if (ADVANCE && len >= 0 && acc > 0) C.length[slot] = len + acc;
+        }
     }
     __syncthreads();
     const int n = n_s;
@@ -419,8 +424,12 @@ cudaError_t launch_kv_commit(const KvArgs &C, const int32_t *slot_idx, int B, in
     if (path) {
         const int64_t units = (int64_t)C.n_layers * C.HKV * 2 * (C.D * es / 16);
         const int64_t need = (units + kCopyThreads - 1) / kCopyThreads;
+        // one block per row saves the second launch (some 2 us) where a thread then walks no more than four columns
+        if (need <= 4)
+            return launch_dependent(kv_move_kernel<true>, dim3(B, 1), dim3(kCopyThreads), 0, stream, C, slot_idx, T, path,
+                                    accept_len, es);
         const int parts = copy_parts(B, need > 8192 ? 8192 : (int)need);
-        cudaError_t e = launch_dependent(kv_move_kernel, dim3(B, parts), dim3(kCopyThreads), 0, stream, C, slot_idx, T,
+        cudaError_t e = launch_dependent(kv_move_kernel<false>, dim3(B, parts), dim3(kCopyThreads), 0, stream, C, slot_idx, T,
                                          path, accept_len, es);
         if (e != cudaSuccess) return e;
     }
