@@ -358,7 +358,7 @@ void tree_attn_cut(AttnArgs *A, int sms) {
     if (per_sm < 1) per_sm = 1;
     const int groups = sms * per_sm / A->NQT;
     A->groups = groups < 1 ? 1 : groups;
-    A->min_chunk = 2;
+    A->min_chunk = 1;
 }
 
 cudaError_t launch_tree_attn(const AttnArgs &A, bool bf16, cudaStream_t st) {

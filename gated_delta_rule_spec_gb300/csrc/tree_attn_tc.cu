@@ -795,6 +795,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         ptx::prefetch_tmap(&mv);
     }
     if (warp == 0) ptx::tmem_alloc(ptx::smem_addr(&ms->tmem), kTmemCols);
+    grid_dep_wait();   // nothing in global memory was touched so far
     attn_dead_rows<__nv_bfloat16>(A, blockIdx.x, gridDim.x, L::kThreads);
     const AttnPlan plan = attn_plan<L::kThreads>(A, group, blockIdx.x == 0, ms->scratch);
     ptx::tc_fence_before_sync();
@@ -872,8 +873,7 @@ cudaError_t run(const AttnArgs &A, cudaStream_t st) {
     if (!bf16_map(&mk, A.C.k, 2, kv_dims, kv_stride, kv_box) || !bf16_map(&mv, A.C.v, 2, kv_dims, kv_stride, kv_box) ||
         !bf16_map(&mq, A.q, 3, q_dims, q_stride, q_box))
         return cudaErrorInvalidValue;
-    tree_attn_tc_kernel<D, NQ><<<A.groups * A.NQT, L::kThreads, smem, st>>>(mq, mk, mv, A);
-    return cudaGetLastError();
+    return launch_dependent(tree_attn_tc_kernel<D, NQ>, dim3(A.groups * A.NQT), dim3(L::kThreads), smem, st, mq, mk, mv, A);
 }
 
 }  // namespace tat
@@ -893,7 +893,7 @@ void tree_attn_tc_cut(AttnArgs *A, int sms) {
     A->NQT = (R + A->MT - 1) / A->MT;
     const int groups = sms / A->NQT;
     A->groups = groups < 1 ? 1 : groups;
-    A->min_chunk = A->C.D == 256 ? 4 : 2;
+    A->min_chunk = 1;
 }
 
 cudaError_t launch_tree_attn_tc(const AttnArgs &A, cudaStream_t st) {
