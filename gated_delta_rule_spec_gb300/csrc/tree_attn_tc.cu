@@ -1,21 +1,28 @@
 // tree_attn_tc.cu -- attention of a window of drafted tokens over the paged cache on
 // the tensor cores (bf16, D = 64, 128 or 256).
 //
-// A block works through the pieces of its chunk (attn_common.cuh) tile by tile:
-//   S = Q K^T     tcgen05.mma kind::f16, 128 query rows x TN keys, fp32 in TMEM
+// A block works through the pieces of its chunk (attn_common.cuh) in tiles of 64 keys:
+//   S = Q K^T     tcgen05.mma kind::f16, 128 query rows x 64 keys, fp32 in TMEM
 //   P = 2^(S scale log2 e - m), rounded to bf16, back into TMEM over S
 //   O += P V      tcgen05.mma kind::f16, P from TMEM, V as it lies in its pages
 //                 (token rows of 64-element runs: the MN-major operand), fp32 in TMEM
-// One producer warp copies the pages' rows by TMA (one box of min(P, TN) tokens by 64
-// dims per lane, the page numbers looked up a tile ahead), one warp issues the
-// MMAs, and a warpgroup of 128 threads, one query row each, does each tile's softmax.
-// Two arrangements keep the tensor core and the copies busy while a softmax runs:
-//   NQ = 1, D <= 128: the tiles of one query tile go to two warpgroups in turn, each
-//     with its own S, running maximum and O; the two halves are merged at the end.
-//   NQ = 2, D <= 128: windows of more than 128 rows; each warpgroup has a query tile of
+// One producer warp copies the pages' rows by TMA (boxes of min(P, 64) tokens; all of a
+// tile's dims by one copy where a page holds the tile), one warp issues the first
+// products, and the tiles go through one or two streams, each with a warp that
+// issues its second products and a warpgroup of 128 threads, one query row each, for
+// its softmax.  A stream has two buffers of S, so its next scores are formed while a
+// softmax runs; its O stays in TMEM over the piece.  The products are issued by warps
+// of their own because every wait on a barrier costs some 150 cycles even where it is
+// ready: one warp that issued both products of a tile took longer than its softmax.
+//   NQ = 1, D <= 128: one query tile; its key/value tiles go to the two streams in turn,
+//     each with a running maximum and an O of its own, merged at the end.
+//   NQ = 2, D <= 128: windows of more than 128 rows; each stream has a query tile of
 //     its own and both use every key/value tile that is copied.
-//   NQ = 1, D = 256: O takes half of TMEM, so there is one warpgroup, and S has two
-//     buffers of 64 keys, so that the next scores are formed during a softmax.
+//   NQ = 1, D = 256: O takes half of TMEM, so there is one stream.
+// Tiles of 64 keys instead of 128 make the first product read its query tile twice as
+// often from shared memory, but 128 keys leave no room for a second buffer of S, and
+// then each stream's scores, softmax and sums wait for one another: that took 492 us where
+// this takes 381 us (32 rows of 64 drafts over up to 8192 tokens, 64 heads on 8 of 128).
 // The G query heads of a kv head are rows of the same tile, so every key and value is
 // copied once for all of them: decoding is bound by HBM as long as a row group is below
 // some 280 rows (the machine's products per byte).
@@ -51,37 +58,43 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kGrow = 8.0f;            // log2 of what the maximum may grow by before it is moved
 constexpr int kSmemMax = 232448;
 
+constexpr int kTile = 64;                // keys of a tile
+constexpr int kMaxStages = 12;
+constexpr uint32_t kPolls = 1u << 18;    // of a wait, before it gives up (half a second)
+
 template <int D, int NQ>
 struct Lay {
-    static constexpr int TN = D == 256 ? 64 : 128;             // keys of a tile
-    static constexpr int NWG = D == 256 ? 1 : 2;               // softmax warpgroups, streams of O
+    static constexpr int NWG = D == 256 ? 1 : 2;               // streams
     static constexpr bool kShare = NQ == 2;                    // both streams use every tile
-    static constexpr bool kTurns = NWG == 2 && !kShare;        // tiles go to the streams in turn
-    static constexpr int kStep = kTurns ? 2 : 1;               // from a stream's tile to its next
-    // two warpgroups: a third holds the producer and the MMA warp and gives registers up, so that a softmax thread
-    // can hold its row's 128 scores (168 x 384 = 208 x 256 + 88 x 128)
-    static constexpr int kThreads = NWG == 2 ? 384 : 192;
-    static constexpr int kRegsMore = 208, kRegsLess = 88;
+    static constexpr bool kTurns = NWG == 2 && !kShare;        // units of tiles go to the streams in turn
+    static constexpr int kThreads = NWG == 2 ? 384 : 256;      // softmax warpgroups; producer and MMA warps
+    static constexpr int kUnit = D == 256 ? 1 : 2;             // tiles that are copied together, one stage
     static constexpr uint32_t kBlocks = D / 64;                // 64-dim blocks of a row
+    static constexpr uint32_t kBlock = kTile * 128;            // one of them, of a tile
     static constexpr uint32_t kQTile = kRows * D * 2;          // one query tile
     static constexpr int QB = D == 64 ? 2 : 1;                 // buffers of NQ query tiles
-    static constexpr uint32_t kStage = TN * D * 2;             // one K or V tile
-    // Stages stand in rings, one for each warp that uses them in order: with tiles in turn every stream has its
-    // own, so that each stage's barriers are met by the same warps in every phase.
-    static constexpr int kRings = kTurns ? 2 : 1;
-    static constexpr int NR = D == 64 ? (kTurns ? 5 : 9) : (kTurns ? 3 : 5);
-    static constexpr int NST = kRings * NR;
+    static constexpr uint32_t kStage = kUnit * kTile * D * 2;
+    // Stages stand in rings: one for the keys and one for each user of values (with units in turn each stream has its
+    // own), so that a stage's barriers are met by the same warps in every phase.
+    static constexpr int NK = D == 64 ? 4 : 2;
+    static constexpr int NV = D == 64 ? (kTurns ? 4 : 6) : kTurns ? 2 : 3;
+    static constexpr int kRings = kTurns ? 3 : 2;
+    static constexpr int NST = NK + (kRings - 1) * NV;
     static constexpr uint32_t kOffKV = QB * NQ * kQTile;
     static constexpr uint32_t kOffMisc = kOffKV + NST * kStage;
-    // TMEM columns
-    static constexpr uint32_t kColO = 2 * TN > 256 ? 256 : (D == 256 ? 256 : 2 * TN);
-    __host__ __device__ static constexpr uint32_t col_s(int i) { return i * TN; }
-    __host__ __device__ static constexpr uint32_t col_o(int w) { return kColO + w * D; }
+    __host__ __device__ static constexpr int ring_of(int w) { return kTurns ? 1 + w : 1; }   // a stream's values
+    __host__ __device__ static constexpr int first(int ring) { return ring ? NK + (ring - 1) * NV : 0; }
+    __host__ __device__ static constexpr int size(int ring) { return ring ? NV : NK; }
+    // TMEM columns: four buffers of S, then O
+    __host__ __device__ static constexpr uint32_t col_s(int w, int buf) { return (2 * w + buf) * kTile; }
+    __host__ __device__ static constexpr uint32_t col_o(int w) { return 256 + w * D; }
 };
 
 // Shared memory behind the tiles.
 struct Misc {
-    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], o_full, o_empty, drain[2], clean[2];
+    uint64_t full[kMaxStages], empty[kMaxStages], q_full[2], q_empty[2];
+    uint64_t s_full[4], p_full[4], pv_done[4];   // by stream and buffer of S
+    uint64_t o_full, o_empty, drain[3], clean[2];
     float2 ml[2][kRows];                  // (m, l) of the two streams' rows, exchanged when they are merged
     unsigned long long bad[3];            // drafts whose values are not finite, by piece modulo 3
     int scratch[kAttnScratch];
@@ -89,21 +102,33 @@ struct Misc {
     int abort;
 };
 
-// Bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit = kWaitLimitDefault) {
-    for (uint32_t it = 0; it < limit; ++it) {
-        if (ptx::mbar_try_wait(bar, parity, 256u)) return true;
-        if ((it & 15u) == 15u && *abort) return false;
+// Bounded wait of a whole warp, which also ends when another role has given up; one
+// answer for all lanes.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit = kPolls) {
+    bool ok = false;
+    for (uint32_t it = 0; !ok && it < limit; ++it) {
+        ok = ptx::mbar_try_wait(bar, parity);
+        if (!ok && (it & 15u) == 15u && *abort) break;
     }
-    *abort = 1;
-    return false;
+    if (!ok) *abort = 1;
+    return __all_sync(0xffffffffu, ok);
 }
 
-// The same by a whole warp, with one answer for all lanes.
-__device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, volatile int *abort,
-                                         uint32_t limit = kWaitLimitDefault) {
-    return __all_sync(0xffffffffu, wait(bar, parity, abort, limit));
-}
+// A value that all lanes hold, from one of them: the tensor core's operands are uniform
+// registers, and values that come from memory or from a loop are only seen to be
+// uniform behind a shuffle (without it each MMA costs some 300 cycles to issue).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Place in a ring of `size` stages.
+struct Place {
+    uint32_t at = 0, ph = 0;
+    __device__ __forceinline__ void step(uint32_t size) {
+        if (++at == size) {
+            at = 0;
+            ph ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -118,9 +143,6 @@ __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-
-template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -174,51 +196,38 @@ __device__ __forceinline__ bool any_at_barrier(int threads, bool bad) {
     return r != 0;
 }
 
-// Place of tile i's values, of a piece of n tiles, in its ring's order: K V K V .., or, with one stream,
-// K0 K1 V0 K2 V1 .. (the next scores are formed before this tile's sums).
-template <class L> __device__ __forceinline__ int pos_v(int i, int n) {
-    return L::NWG == 2 ? 2 * (i / L::kStep) + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+// Tiles of a piece of n that stream w takes, and which tile of the piece its j-th is.
+template <class L> __device__ __forceinline__ int stream_tiles(int n, int w) {
+    if (!L::kTurns) return n;
+    const int whole = n >> 2, rest = n & 3;   // units of two tiles, w's and the other's
+    return 2 * whole + (w ? max(rest - 2, 0) : min(rest, 2));
 }
-// Places that a piece of n tiles takes in ring r.
-template <class L> __device__ __forceinline__ int ring_places(int n, int r) {
-    return L::kTurns ? 2 * ((n + 1 - r) >> 1) : 2 * n;
+template <class L> __device__ __forceinline__ int stream_tile(int j, int w) {
+    return L::kTurns ? 4 * (j >> 1) + 2 * w + (j & 1) : j;
 }
 
-// Which of a tile's keys a row attends to, as 128 bits: keys before `len` all, drafted
+// Which of a tile's keys a row attends to, as 64 bits: keys before `len` all, drafted
 // ones by the row's mask (already cut to the row's tokens).
-__device__ __forceinline__ void visible_bits(int k0, int len, uint64_t mask, uint32_t (&bits)[4]) {
-    uint64_t lo, hi;
+__device__ __forceinline__ uint64_t visible_bits(int k0, int len, uint64_t mask) {
     const int n = len - k0;   // committed keys of the tile
-    if (n <= 0) {
-        lo = n > -64 ? mask >> -n : 0;
-        hi = 0;
-    } else if (n < 64) {
-        lo = ((1ull << n) - 1) | (mask << n);
-        hi = mask >> (64 - n);
-    } else {
-        lo = ~0ull;
-        hi = n == 64 ? mask : n < 128 ? ((1ull << (n - 64)) - 1) | (mask << (n - 64)) : ~0ull;
-    }
-    bits[0] = (uint32_t)lo;
-    bits[1] = (uint32_t)(lo >> 32);
-    bits[2] = (uint32_t)hi;
-    bits[3] = (uint32_t)(hi >> 32);
+    if (n <= 0) return n > -64 ? mask >> -n : 0;
+    return n < 64 ? ((1ull << n) - 1) | (mask << n) : ~0ull;
 }
 
 // ------------------------------------------------------------------ producer warp
 
+// All lanes compute the same and one issues: a copy's operands are uniform registers, and lanes with
+// copies of their own would be served one after another.
 template <int D, int NQ>
 __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq, const CUtensorMap *mk,
                                         const CUtensorMap *mv, Misc *ms, uint32_t base, const AttnPlan &plan, int group,
-                                        int qt, int lane) {
+                                        int qt) {
     using L = Lay<D, NQ>;
-    const int BR = min(A.C.P, L::TN), chunks = L::TN / BR;    // tokens of a box, boxes of a 64-dim block
-    const int my_chunk = lane % chunks, my_blk = lane / chunks;
-    const bool mine = my_blk < (int)L::kBlocks;
+    const int BR = min(A.C.P, kTile);                          // tokens of a box: within a page and within a tile
     const int RT = A.MT / NQ, tokens_q = RT / A.G;             // rows and tokens of a query tile
-    const uint32_t box_bytes = BR * 128u;
     const uint32_t q_bytes = 128u * A.G * min(tokens_q, A.T);   // one 64-dim block of one query tile
-    uint32_t issued[2] = {0, 0}, q_issued = 0;
+    Place place[3];
+    uint32_t issued[3] = {0, 0, 0}, q_issued = 0;
     bool ok = true;
     AttnWalk walk = attn_walk(plan, group);
     AttnPiece pc;
@@ -226,253 +235,228 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
         if (pc.cnt * A.G - qt * A.MT <= 0) continue;
         const int kv = pc.len + pc.cnt, n = pc.t1 - pc.t0;
         const int32_t *table = A.C.page_table + (int64_t)pc.slot * A.C.max_pages;
-        // row of the pool where this lane's box of tile t starts, -1: no token of it is in use
-        const auto box_row = [&](int t) {
-            const int64_t tok = (int64_t)t * L::TN + my_chunk * BR;
-            if (!mine || t >= pc.t1 || tok >= kv) return -1;
+        const int units = (n + L::kUnit - 1) / L::kUnit;
+        const auto copy = [&](const CUtensorMap *map, auto ring_c, int u) {   // unit u of the piece
+            constexpr int ring = decltype(ring_c)::value;
+            constexpr bool rows128 = !ring && L::kShare;   // a block of 64 dims as 128 rows; all else tile by tile
+            const uint32_t st = L::first(ring) + place[ring].at;
+            const int tok = (pc.t0 + u * L::kUnit) * kTile;
+            const int live = min(min(L::kUnit, n - u * L::kUnit) * kTile, kv - tok), boxes = (live + BR - 1) / BR;
             int page = table[tok >> A.C.logP];
-            if (page < 0 || page >= A.C.num_pages) {
-                atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
-                page = 0;
+            if (!wait(ptx::smem_addr(&ms->empty[st]), place[ring].ph ^ 1u, &ms->abort)) return false;
+            const uint32_t bar = uniform(ptx::smem_addr(&ms->full[st]));
+            const uint32_t dst = uniform(base + L::kOffKV + st * L::kStage);
+            if (ptx::elect_one()) {
+                ptx::mbar_expect_tx(bar, BR * 128u * L::kBlocks * boxes);
+                for (int c = 0; c < boxes; ++c) {
+                    const int at = c * BR;   // row of the unit
+                    if (c) page = table[(tok + at) >> A.C.logP];
+                    if (page < 0 || page >= A.C.num_pages) {
+                        atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+                        page = 0;
+                    }
+                    const int row = ((A.layer * A.C.num_pages + page) * A.C.HKV + pc.h) * A.C.P +
+                                    ((tok + at) & (A.C.P - 1));
+                    if (!rows128 && BR == kTile) {   // all of a tile's blocks by one copy
+                        ptx::tma_load_3d(dst + at * 128u * L::kBlocks, map, bar, 0, row, 0);
+                    } else {
+                        const uint32_t to = rows128 ? dst + at * 128u
+                                                    : dst + (at / kTile) * kTile * 128u * L::kBlocks + (at % kTile) * 128u;
+#pragma unroll
+                        for (int blk = 0; blk < (int)L::kBlocks; ++blk)
+                            ptx::tma_load_3d(to + blk * (rows128 ? L::kUnit : 1) * L::kBlock, map, bar, 0, row, blk);
+                    }
+                }
             }
-            return ((A.layer * A.C.num_pages + page) * A.C.HKV + pc.h) * A.C.P + ((int)tok & (A.C.P - 1));
-        };
-        const auto copy = [&](const CUtensorMap *map, int row, int t) {
-            const int r = L::kTurns ? (t - pc.t0) & 1 : 0;
-            const uint32_t p = r ? issued[1] : issued[0], st = r * L::NR + p % L::NR, ph = (p / L::NR) & 1u;
-            if (!all_wait(ptx::smem_addr(&ms->empty[st]), ph ^ 1u, &ms->abort)) return false;
-            const uint32_t bar = ptx::smem_addr(&ms->full[st]);
-            const int left = kv - t * L::TN, live = min(chunks, (left + BR - 1) / BR);
-            if (lane == 0) ptx::mbar_expect_tx(bar, box_bytes * live * L::kBlocks);
             __syncwarp();
-            if (row >= 0)
-                ptx::tma_load_2d(base + L::kOffKV + st * L::kStage + my_blk * (L::TN * 128u) + my_chunk * box_bytes, map,
-                                 bar, my_blk * 64, row);
-            if (r) ++issued[1]; else ++issued[0];
+            ++issued[ring];
+            place[ring].step(L::size(ring));
             return true;
         };
-        int row = box_row(pc.t0), next = box_row(pc.t0 + 1);
-        ok = copy(mk, row, pc.t0);
+        const auto copy_k = [&](int u) { return copy(mk, std::integral_constant<int, 0>(), u); };
+        const auto copy_v = [&](int u) {
+            return L::kTurns && (u & 1) ? copy(mv, std::integral_constant<int, L::kRings - 1>(), u)
+                                        : copy(mv, std::integral_constant<int, 1>(), u);
+        };
+        ok = copy_k(0);
         if (ok) {   // the query tiles, behind the first keys
             const uint32_t qb = q_issued % L::QB, ph = (q_issued / L::QB) & 1u;
-            ok = all_wait(ptx::smem_addr(&ms->q_empty[qb]), ph ^ 1u, &ms->abort);
+            ok = wait(ptx::smem_addr(&ms->q_empty[qb]), ph ^ 1u, &ms->abort);
             if (ok) {
-                const uint32_t bar = ptx::smem_addr(&ms->q_full[qb]);
+                const uint32_t bar = uniform(ptx::smem_addr(&ms->q_full[qb]));
+                const uint32_t dst = uniform(base + qb * NQ * L::kQTile);
                 const int t0 = qt * NQ * tokens_q;
-                int tiles = 0;
+                if (ptx::elect_one()) {
+                    int tiles = 0;
 #pragma unroll
-                for (int s = 0; s < NQ; ++s) tiles += t0 + s * tokens_q < pc.cnt;
-                if (lane == 0) ptx::mbar_expect_tx(bar, q_bytes * L::kBlocks * tiles);
-                __syncwarp();
-                if (lane < (int)L::kBlocks * tiles) {
-                    const int s = lane / L::kBlocks, blk = lane - s * L::kBlocks;
-                    ptx::tma_load_3d(base + (qb * NQ + s) * L::kQTile + blk * (kRows * 128u), mq, bar, blk * 64,
-                                     pc.h * A.G, pc.b * A.T + t0 + s * tokens_q);
+                    for (int s = 0; s < NQ; ++s) tiles += t0 + s * tokens_q < pc.cnt;
+                    ptx::mbar_expect_tx(bar, q_bytes * L::kBlocks * tiles);
+                    for (int s = 0; s < tiles; ++s)
+#pragma unroll
+                        for (int blk = 0; blk < (int)L::kBlocks; ++blk)
+                            ptx::tma_load_3d(dst + s * L::kQTile + blk * (kRows * 128u), mq, bar, blk * 64, pc.h * A.G,
+                                             pc.b * A.T + t0 + s * tokens_q);
                 }
+                __syncwarp();
                 ++q_issued;
             }
         }
-        if (ok && !L::kShare && n > 1) ok = copy(mk, next, pc.t0 + 1);
-        for (int i = 0; ok && i < n; ++i) {   // values of tile i, then the keys that are used after them
-            const int t = pc.t0 + i;
-            const int after = box_row(t + 2);
-            ok = copy(mv, row, t);
-            if (L::kShare) {
-                if (ok && i + 1 < n) ok = copy(mk, next, t + 1);
-            } else {
-                if (ok && i + 2 < n) ok = copy(mk, after, t + 2);
-            }
-            row = next;
-            next = after;
+        if (ok && units > 1) ok = copy_k(1);
+        for (int u = 0; ok && u < units; ++u) {   // the keys run ahead of the values by two units
+            // the table's line of some tiles on, so that its latency is not waited for later
+            const int ahead = (pc.t0 + min((u + 8) * L::kUnit, n - 1)) * kTile >> A.C.logP;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(table + ahead));
+            ok = copy_v(u);
+            if (ok && u + 2 < units) ok = copy_k(u + 2);
         }
     }
     if (!ok) {   // copies in flight land before the block's shared memory goes away
+#pragma unroll
         for (int r = 0; r < L::kRings; ++r)
-            for (uint32_t p = issued[r] > L::NR ? issued[r] - L::NR : 0; p < issued[r]; ++p)
-                ptx::mbar_wait(ptx::smem_addr(&ms->full[r * L::NR + p % L::NR]), (p / L::NR) & 1u);
+            for (uint32_t size = L::size(r), p = issued[r] > size ? issued[r] - size : 0; p < issued[r]; ++p)
+                ptx::mbar_wait(ptx::smem_addr(&ms->full[L::first(r) + p % size]), (p / size) & 1u);
         for (uint32_t p = q_issued > L::QB ? q_issued - L::QB : 0; p < q_issued; ++p)
             ptx::mbar_wait(ptx::smem_addr(&ms->q_full[p % L::QB]), (p / L::QB) & 1u);
     }
 }
 
-// ------------------------------------------------------------------ MMA warp
+// ------------------------------------------------------------------ MMA warps
 
-// A value that all lanes hold, from one of them: the tensor core's operands are uniform
-// registers, and values that come from memory or from a loop are only seen to be
-// uniform behind a shuffle (without it each MMA costs some 300 cycles to issue).
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (ptx::elect_one()) ptx::mma_commit(bar);
+    __syncwarp();
+}
 
-// Stream w of the block: with two streams each has a warp of its own, so that one's wait for a softmax does not
-// hold up the other's products.
+// When a warp gives up, none of its MMAs is running when TMEM is freed.
+__device__ __forceinline__ void drain(Misc *ms, int who) {
+    commit(ptx::smem_addr(&ms->drain[who]));
+    ptx::mbar_wait(ptx::smem_addr(&ms->drain[who]), 0);
+}
+
+// The first products, S = Q K^T, of all streams.  What an MMA needs is made uniform
+// before the wait that it hangs on, so that only the issue is behind it.
 template <int D, int NQ>
-__device__ __forceinline__ void multiply(const AttnArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const AttnPlan &plan,
-                                         int group, int qt, int w) {
+__device__ __forceinline__ void multiply_scores(const AttnArgs &A, Misc *ms, uint32_t base, uint32_t tmem,
+                                                const AttnPlan &plan, int group, int qt) {
     using L = Lay<D, NQ>;
-    constexpr uint32_t idesc_s = ptx::idesc_bf16(kRows, L::TN);
-    constexpr uint32_t idesc_o = ptx::idesc_bf16(kRows, D) | ptx::kIdescBMn;
-    const int ring = L::kTurns ? w * L::NR : 0;   // first stage of this warp's ring
-    const uint32_t d_o = uniform(tmem + L::col_o(w));
-    uint32_t q_used = 0, pieces = 0;
-    uint32_t c_ph = 0;                          // bit of a barrier: parity of the waits done on clean
-    uint32_t p_ph = 0, pv_ph = 0, pv_any = 0;   // bit of a buffer: parity of the waits done on p_full, of the commits
-                                                // made on pv_done, whether there was one
-    bool ok = true;
+    // An MMA of 128 x 64 takes as long as one of 128 x 128 (the query rows' traffic from shared memory): where the
+    // products are the bound, with shared tiles, one forms the scores of both tiles of a unit.
+    constexpr int kN = L::kShare ? L::kUnit : 1;   // tiles of a product
+    constexpr uint32_t idesc = ptx::idesc_bf16(kRows, kN * kTile);
     const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
-    // Everything that a product needs is made uniform before the wait that it hangs on, so that nothing but the
-    // issue lies between the two.
-    struct Stage {
-        uint32_t at, ph;   // stage of the ring, parity of its phase
-    };
-    const auto after = [](Stage s, int n) {
-        s.at += n;
-        if (s.at >= (uint32_t)L::NR) {
-            s.at -= L::NR;
-            s.ph ^= 1u;
-        }
-        return s;
-    };
-    struct Op {
-        uint64_t a, b;
-        uint32_t p, empty, full, ph;
-    };
-    const auto op = [&](Stage s, bool values, uint32_t q_addr, int buf) {
-        Op o;
-        const uint32_t addr = uniform(base + L::kOffKV + (ring + s.at) * L::kStage);
-        o.a = ptx::smem_desc_sw128(uniform(q_addr));
-        o.b = values ? ptx::smem_desc_sw128_mn(addr, L::TN * 128u) : ptx::smem_desc_sw128(addr);
-        o.p = uniform(tmem + L::col_s(buf));
-        o.empty = uniform(bar(ms->empty[ring + s.at]));
-        o.full = bar(ms->full[ring + s.at]);
-        o.ph = s.ph;
-        return o;
-    };
-    const auto wait_full = [&](const Op &o) { return all_wait(o.full, o.ph, &ms->abort, A.wait_limit); };
-    // S of a buffer = query tile times K tile
-    const auto scores = [&](const Op &o, int buf, bool last) {
-        const uint32_t done = uniform(bar(ms->s_full[buf])), q_done = uniform(bar(ms->q_empty[q_used % L::QB]));
-        ptx::tc_fence_after_sync();
-        if (ptx::elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)   // descriptors count in 16 bytes
-                ptx::mma_bf16(o.p, o.a + ((ks >> 2) * (kRows * 128u) + (ks & 3) * 32u) / 16,
-                              o.b + ((ks >> 2) * (L::TN * 128u) + (ks & 3) * 32u) / 16, idesc_s, ks != 0);
-            ptx::mma_commit(done);
-            ptx::mma_commit(o.empty);
-            if (last) ptx::mma_commit(q_done);
-        }
-        __syncwarp();
-    };
-    // O of this stream (+)= steps [K0, K1) of P times the V tile
-    const auto sums = [&](const Op &o, int buf, auto k0, auto k1, uint32_t keep) {
-        constexpr int K0 = decltype(k0)::value, K1 = decltype(k1)::value;
-        const uint32_t done = uniform(bar(ms->pv_done[buf]));
-        ptx::tc_fence_after_sync();
-        if (ptx::elect_one()) {
-#pragma unroll
-            for (int ks = K0; ks < K1; ++ks)
-                ptx::mma_bf16_tmem_a(d_o, o.p + ks * 8, o.b + ks * 2048u / 16, idesc_o, ks != 0 ? 1u : keep);
-            if (K1 == L::TN / 16) {
-                ptx::mma_commit(done);
-                ptx::mma_commit(o.empty);
-            }
-        }
-        __syncwarp();
-        if (K1 == L::TN / 16) {
-            pv_ph ^= 1u << buf;
-            pv_any |= 1u << buf;
-        }
-    };
-    const auto commit = [&](uint64_t &b) {
-        if (ptx::elect_one()) ptx::mma_commit(bar(b));
-        __syncwarp();
-    };
-    // S buffer `buf` may be written again once the sums that read its P are done
-    const auto wait_free = [&](int buf) {
-        return !((pv_any >> buf) & 1u) || all_wait(bar(ms->pv_done[buf]), ((pv_ph >> buf) & 1u) ^ 1u, &ms->abort);
-    };
-    using Zero = std::integral_constant<int, 0>;
-    using Half = std::integral_constant<int, L::TN / 32>;
-    using All = std::integral_constant<int, L::TN / 16>;
-    Stage sk = {0, 0}, sv = {0, 0};   // of the next K and V tile
+    uint32_t q_used = 0, used_any = 0, used_ph = 0;   // bit of an S buffer: whether it was used, parity of its uses
+    Place key;
+    bool ok = true;
     AttnWalk walk = attn_walk(plan, group);
     AttnPiece pc;
     bool any = walk.next(A, &pc);
-    if (w == 0 && qt == 0 && ptx::elect_one()) attn_note(A, group, any, pc, plan.chunk);
+    if (qt == 0 && ptx::elect_one()) attn_note(A, group, any, pc, plan.chunk);
     __syncwarp();
     for (; ok && any; any = walk.next(A, &pc)) {
         if (pc.cnt * A.G - qt * A.MT <= 0) continue;
         const int n = pc.t1 - pc.t0;
-        const uint32_t qb = q_used % L::QB;
-        const uint32_t q_addr = base + (qb * NQ + (L::kShare ? w : 0)) * L::kQTile;
-        const auto o_free = [&] { return all_wait(bar(ms->o_empty), (pieces & 1u) ^ 1u, &ms->abort); };
-        ok = all_wait(bar(ms->q_full[qb]), (q_used / L::QB) & 1u, &ms->abort, A.wait_limit);
-        if (L::NWG == 2) {
-            // one S buffer a stream: scores, softmax, sums, then the next scores over what the sums have read
-            const int first = L::kTurns ? w : 0;
-            for (int i = first; ok && i < n; i += L::kStep) {
-                const Op qk = op(sk, false, q_addr, w);
-                ok = wait_full(qk) && wait_free(w);
+        const uint32_t qb = q_used % L::QB, q_addr = base + qb * NQ * L::kQTile;
+        ok = wait(bar(ms->q_full[qb]), (q_used / L::QB) & 1u, &ms->abort, A.wait_limit);
+        for (int i = 0; ok && i < n; i += L::kUnit) {
+            const uint32_t keys = uniform(base + L::kOffKV + key.at * L::kStage);
+            const uint32_t empty = uniform(bar(ms->empty[key.at])), q_done = uniform(bar(ms->q_empty[qb]));
+            ok = wait(bar(ms->full[key.at]), key.ph, &ms->abort, A.wait_limit);
+            key.step(L::NK);
+#pragma unroll
+            for (int s = 0; s < L::kUnit / kN * NQ; ++s) {   // the unit's products
+                const int w = L::kTurns ? (i >> 1) & 1 : L::kShare ? s : 0;   // stream
+                const int t = L::kTurns ? s : 0;                              // tile of the unit
+                const int x = 2 * w + (L::kTurns ? s : L::kShare ? 0 : i & 1);   // (first) S buffer
+                const bool here = i + t < n, two = kN == 2 && i + 1 < n;
+                const bool last = i + L::kUnit >= n && (L::kTurns ? s == 1 : s == NQ - 1);
+                const uint64_t a = ptx::smem_desc_sw128(uniform(q_addr + (L::kShare ? s : 0) * L::kQTile));
+                const uint64_t b = ptx::smem_desc_sw128(keys + t * L::kBlocks * L::kBlock);
+                const uint32_t d = uniform(tmem + x * kTile);
+                const uint32_t done = uniform(bar(ms->s_full[x])), done2 = uniform(bar(ms->s_full[x | 1]));
+                // a buffer is free once the sums that read its last P are done
+#pragma unroll
+                for (int y = 0; y < kN; ++y)
+                    if (ok && here && ((used_any >> (x + y)) & 1u))
+                        ok = wait(bar(ms->pv_done[x + y]), ((used_ph >> (x + y)) & 1u) ^ 1u, &ms->abort);
                 if (!ok) break;
-                scores(qk, w, i + L::kStep >= n);
-                sv = after(sk, 1);
-                sk = after(sk, 2);
-                const Op pv = op(sv, true, q_addr, w);
-                const uint32_t keep = uniform(i > first);
-                const uint32_t half = bar(ms->p_half[w]), full = bar(ms->p_full[w]), ph = p_ph & 1u;
-                p_ph ^= 1u;
-                ok = wait_full(pv) && (i > first || o_free());
-                if (L::kShare && w == 1) {
-                    // a shared tile with drafts is cleaned by the first warpgroup: the window lies in at most two tiles
-                    const int d = pc.t0 + i - pc.len / L::TN;
-                    if (d >= 0) {
-                        ok = ok && all_wait(bar(ms->clean[d]), (c_ph >> d) & 1u, &ms->abort);
-                        c_ph ^= 1u << d;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
+                    if (here) {
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)   // descriptors count in 16 bytes
+                            ptx::mma_bf16(d, a + ((ks >> 2) * (kRows * 128u) + (ks & 3) * 32u) / 16,
+                                          b + ((ks >> 2) * kN * L::kBlock + (ks & 3) * 32u) / 16, idesc, ks != 0);
+                        ptx::mma_commit(done);
+                        if (two) ptx::mma_commit(done2);
                     }
+                    if (s == L::kUnit / kN * NQ - 1) ptx::mma_commit(empty);
+                    if (last) ptx::mma_commit(q_done);
                 }
-                ok = ok && all_wait(half, ph, &ms->abort);
-                if (!ok) break;
-                sums(pv, w, Zero(), Half(), keep);
-                ok = all_wait(full, ph, &ms->abort);
-                if (!ok) break;
-                sums(pv, w, Half(), All(), 1u);
-            }
-            if (ok && first >= n) {   // no tile for this stream; every phase of o_empty is waited for all the same
-                commit(ms->q_empty[qb]);
-                ok = o_free();
-            }
-        } else {
-            // two S buffers: the next scores are formed before this tile's sums; the ring goes K0 K1 V0 K2 V1 ..
-            Op qk = op(sk, false, q_addr, 0);
-            ok = ok && wait_full(qk) && wait_free(0);
-            if (ok) scores(qk, 0, n == 1);
-            sk = after(sk, 1);
-            for (int i = 0; ok && i < n; ++i) {
-                const int buf = i & 1;
-                if (i + 1 < n) {
-                    qk = op(sk, false, q_addr, buf ^ 1);
-                    ok = wait_full(qk) && wait_free(buf ^ 1);
-                    if (!ok) break;
-                    scores(qk, buf ^ 1, i + 2 == n);
-                    sk = after(sk, 1);
-                }
-                const Op pv = op(sk, true, q_addr, buf);
-                sk = after(sk, 1);
-                const uint32_t keep = uniform(i > 0);
-                const uint32_t ph = (p_ph >> buf) & 1u;
-                p_ph ^= 1u << buf;
-                ok = wait_full(pv) && (i || o_free()) && all_wait(bar(ms->p_full[buf]), ph, &ms->abort);
-                if (!ok) break;
-                sums(pv, buf, Zero(), All(), keep);
+                __syncwarp();
+                const uint32_t taken = here ? (two ? 3u : 1u) << x : 0u;
+                used_any |= taken;
+                used_ph ^= taken;
             }
         }
-        if (ok) commit(ms->o_full);
         ++q_used;
+    }
+    if (!ok) drain(ms, 2);
+}
+
+// The second products, O += P V, of stream w.
+template <int D, int NQ>
+__device__ __forceinline__ void multiply_sums(const AttnArgs &A, Misc *ms, uint32_t base, uint32_t tmem,
+                                              const AttnPlan &plan, int group, int qt, int w) {
+    using L = Lay<D, NQ>;
+    constexpr uint32_t idesc = ptx::idesc_bf16(kRows, D) | ptx::kIdescBMn;
+    const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
+    const uint32_t d = uniform(tmem + L::col_o(w));
+    const int first = L::first(L::ring_of(w));
+    uint32_t pieces = 0, p_ph = 0, c_ph = 0;   // bit of a buffer or barrier: parity of the waits done on it
+    Place val;
+    bool ok = true;
+    AttnWalk walk = attn_walk(plan, group);
+    AttnPiece pc;
+    while (ok && walk.next(A, &pc)) {
+        if (pc.cnt * A.G - qt * A.MT <= 0) continue;
+        const int mine = stream_tiles<L>(pc.t1 - pc.t0, w);
+        const auto o_free = [&] { return wait(bar(ms->o_empty), (pieces & 1u) ^ 1u, &ms->abort); };
+        if (mine == 0) ok = o_free();   // every phase is waited for
+        for (int j = 0; ok && j < mine; ++j) {
+            const int x = 2 * w + (j & 1), st = first + val.at;
+            const int half = j & (L::kUnit - 1);   // tile of the unit
+            const bool end = half == L::kUnit - 1 || j == mine - 1;
+            const uint64_t b = ptx::smem_desc_sw128_mn(
+                uniform(base + L::kOffKV + st * L::kStage + half * L::kBlocks * L::kBlock), L::kBlock);
+            const uint32_t p = uniform(tmem + x * kTile), keep = uniform(j > 0);
+            const uint32_t empty = uniform(bar(ms->empty[st])), done = uniform(bar(ms->pv_done[x]));
+            if (half == 0) ok = wait(bar(ms->full[st]), val.ph, &ms->abort, A.wait_limit) && (j || o_free());
+            if (end) val.step(L::NV);
+            if (L::kShare && w == 1) {
+                // a shared tile with drafts is cleaned by the first warpgroup: the window lies in at most two tiles
+                const int c = pc.t0 + j - pc.len / kTile;
+                if (c >= 0) {
+                    ok = ok && wait(bar(ms->clean[c]), (c_ph >> c) & 1u, &ms->abort);
+                    c_ph ^= 1u << c;
+                }
+            }
+            ok = ok && wait(bar(ms->p_full[x]), (p_ph >> (j & 1)) & 1u, &ms->abort);
+            p_ph ^= 1u << (j & 1);
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    ptx::mma_bf16_tmem_a(d, p + ks * 8, b + ks * 2048u / 16, idesc, ks != 0 ? 1u : keep);
+                ptx::mma_commit(done);
+                if (end) ptx::mma_commit(empty);
+            }
+            __syncwarp();
+        }
+        if (ok) commit(bar(ms->o_full));
         ++pieces;
     }
-    if (!ok) {   // no MMA is running when TMEM is freed
-        commit(ms->drain[w]);
-        ptx::mbar_wait(bar(ms->drain[w]), 0);
-    }
+    if (!ok) drain(ms, w);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -485,9 +469,9 @@ __device__ __forceinline__ void clean_values(uint8_t *tile, int k0, int len, int
     constexpr int kPieces = D / 8;   // 16-byte pieces of a row
     const int first = max(len - k0, 0);
     unsigned long long mine = 0;
-    for (int i = first * kPieces + tid; i < L::TN * kPieces; i += 128) {
+    for (int i = first * kPieces + tid; i < kTile * kPieces; i += 128) {
         const int r = i / kPieces, c = i - r * kPieces;
-        uint4 *p = reinterpret_cast<uint4 *>(tile + (c >> 3) * (L::TN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        uint4 *p = reinterpret_cast<uint4 *>(tile + (c >> 3) * (L::kBlock) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
         if (k0 + r >= kv) {
             *p = make_uint4(0, 0, 0, 0);
         } else {
@@ -502,10 +486,10 @@ __device__ __forceinline__ void clean_values(uint8_t *tile, int k0, int len, int
     asm volatile("bar.sync %0, 128;" ::"r"(2 + (int)(threadIdx.x >> 7)) : "memory");
     const unsigned long long all = *reinterpret_cast<volatile unsigned long long *>(bad);
     if (all)
-        for (int i = first * kPieces + tid; i < min(L::TN, kv - k0) * kPieces; i += 128) {
+        for (int i = first * kPieces + tid; i < min(kTile, kv - k0) * kPieces; i += 128) {
             const int r = i / kPieces, c = i - r * kPieces;
             if ((all >> (k0 + r - len)) & 1)
-                *reinterpret_cast<uint4 *>(tile + (c >> 3) * (L::TN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                *reinterpret_cast<uint4 *>(tile + (c >> 3) * (L::kBlock) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
                     make_uint4(0, 0, 0, 0);
         }
     ptx::fence_proxy_async_smem();
@@ -541,7 +525,7 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
     const int my_row = (L::kShare ? w * RT : 0) + tid;      // row of the block's MT
     const float c = A.scale_log2;
     const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
-    uint32_t used = 0, pieces = 0;
+    uint32_t used = 0, pieces = 0;                          // places used of the values' ring
     uint32_t s_ph = 0, pv_ph = 0;                           // bit of a buffer: parity of the tiles taken, handed on
     bool ok = true;
     AttnWalk walk = attn_walk(plan, group);
@@ -561,63 +545,53 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
         float m = -INFINITY, l = 0.0f;
         // A thread whose wait ran out goes on without waiting or computing, so that the warpgroup's barriers are
         // met by all, until the barrier at the piece's end tells everybody.
-        const int first = L::kTurns ? w : 0;
-        for (int i = first; i < n; i += L::kStep) {
-            const int buf = L::NWG == 2 ? w : i & 1, o = w;
-            const bool drafts = (pc.t0 + i + 1) * L::TN > pc.len;   // the tile holds drafted tokens, or ends the row
-            const int k0 = (pc.t0 + i) * L::TN;
-            ok = __all_sync(0xffffffffu, ok && wait(bar(ms->s_full[buf]), (s_ph >> buf) & 1u, &ms->abort));
+        const int mine = stream_tiles<L>(n, w);
+        for (int j = 0; j < mine; ++j) {
+            const int buf = j & 1, tile = pc.t0 + stream_tile<L>(j, w), k0 = tile * kTile;
+            const bool drafts = k0 + kTile > pc.len;   // the tile holds drafted tokens, or ends the row
+            const uint32_t s_addr = lane_addr + L::col_s(w, buf);
+            ok = ok && wait(bar(ms->s_full[2 * w + buf]), (s_ph >> buf) & 1u, &ms->abort);
             s_ph ^= 1u << buf;
             ptx::tc_fence_after_sync();
-            const bool ok_half = ok;
             if (ok && warp_on) {
-                // eight chains of three-input maxima (one chain's latency would be the whole row's), taken of each 32
-                // scores while the next are on their way from TMEM
-                uint32_t s[L::TN];
+                uint32_t s[kTile];
+                ptx::tmem_ld32_bits(s_addr, s);
+                ptx::tmem_ld32_bits(s_addr + 32, s + 32);
+                landed(s);
+                if (drafts) {
+                    const uint64_t bits = visible_bits(k0, pc.len, mask);
+#pragma unroll
+                    for (int x = 0; x < kTile; ++x)
+                        if (!((uint32_t)(bits >> (x & 32)) >> (x & 31) & 1u)) s[x] = 0xff800000u;
+                }
+                // eight chains of three-input maxima: one chain's latency would be the whole row's
                 float tops[8];
-                uint32_t bits[4];
-                if (drafts) visible_bits(k0, pc.len, mask, bits);
-                ptx::tmem_ld32_bits(lane_addr + L::col_s(buf), s);
 #pragma unroll
-                for (int x = 0; x < L::TN; x += 32) {
-                    landed32(s + x);
-                    if (x + 32 < L::TN) ptx::tmem_ld32_bits(lane_addr + L::col_s(buf) + x + 32, s + x + 32);
-                    if (drafts) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((bits[x >> 5] >> j) & 1u)) s[x + j] = 0xff800000u;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float a = __uint_as_float(s[x + j]), b = __uint_as_float(s[x + 8 + j]);
-                        const float d = __uint_as_float(s[x + 16 + j]), e = __uint_as_float(s[x + 24 + j]);
-                        tops[j] = x == 0 ? max3(a, b, d) : max3(max3(tops[j], a, b), d, e);
-                        if (x == 0) tops[j] = fmaxf(tops[j], e);
-                    }
+                for (int x = 0; x < 8; ++x) {
+                    const auto f = [&](int y) { return __uint_as_float(s[x + 8 * y]); };
+                    tops[x] = max3(max3(max3(f(0), f(1), f(2)), f(3), f(4)), f(5), fmaxf(f(6), f(7)));
                 }
                 const float top = c * max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]),
                                            fmaxf(tops[6], tops[7]));
-                const bool move = top > m + kGrow || (m == -INFINITY && top > m);
+                const bool move = top > m + kGrow;
                 if (__any_sync(0xffffffffu, move)) {
                     const float to = move ? top : m;
                     const float al = m == -INFINITY ? 0.0f : ex2(m - to);
                     l *= al;
                     m = to;
-                    if (i > first) {
-                        // the sums so far, in O, are those of the stream's tile before this one
-                        if (L::NWG == 1)
-                            ok = __all_sync(0xffffffffu, wait(bar(ms->pv_done[buf ^ 1]), ((pv_ph >> (buf ^ 1)) & 1u) ^ 1u,
-                                                              &ms->abort));
+                    if (j > 0) {   // O holds the sums up to the stream's tile before this one
+                        ok = wait(bar(ms->pv_done[2 * w + (buf ^ 1)]), ((pv_ph >> (buf ^ 1)) & 1u) ^ 1u, &ms->abort);
                         if (ok) {
                             ptx::tc_fence_after_sync();
 #pragma unroll 1
-                            for (int x = 0; x < D; x += 8) {   // few at a time: the row's scores are held as well
-                                uint32_t u[8];
-                                ptx::tmem_ld8_bits(lane_addr + L::col_o(o) + x, u);
+                            for (int x = 0; x < D; x += 32) {
+                                uint32_t u[32];
+                                ptx::tmem_ld32_bits(lane_addr + L::col_o(w) + x, u);
                                 landed(u);
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * al);
-                                ptx::tmem_st8_bits(lane_addr + L::col_o(o) + x, u);
+                                for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(__uint_as_float(u[y]) * al);
+                                ptx::tmem_st16_bits(lane_addr + L::col_o(w) + x, u);
+                                ptx::tmem_st16_bits(lane_addr + L::col_o(w) + x + 16, u + 16);
                             }
                         }
                     }
@@ -626,24 +600,18 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
                 const uint64_t c2 = pair(c, c), off2 = pair(off, off);
                 uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
 #pragma unroll
-                for (int x = 0; x < L::TN; x += 32) {
+                for (int x = 0; x < kTile; x += 32) {
                     uint32_t p[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int y = 0; y < 16; ++y) {
                         float a, b;
-                        unpair(fma2(pair(__uint_as_float(s[x + 2 * j]), __uint_as_float(s[x + 2 * j + 1])), c2, off2), a, b);
+                        unpair(fma2(pair(__uint_as_float(s[x + 2 * y]), __uint_as_float(s[x + 2 * y + 1])), c2, off2), a, b);
                         a = ex2(a);
                         b = ex2(b);
-                        sum[j & 3] = add2(sum[j & 3], pair(a, b));
-                        p[j] = pack_bf16(a, b);
+                        sum[y & 3] = add2(sum[y & 3], pair(a, b));
+                        p[y] = pack_bf16(a, b);
                     }
-                    ptx::tmem_st16_bits(lane_addr + L::col_s(buf) + x / 2, p);
-                    if (L::NWG == 2 && x + 32 == L::TN / 2 && !drafts) {   // the sums begin on the first half
-                        ptx::tmem_st_wait();
-                        ptx::tc_fence_before_sync();
-                        __syncwarp();
-                        if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->p_half[buf]));
-                    }
+                    ptx::tmem_st16_bits(s_addr + x / 2, p);
                 }
                 float s0, s1;
                 unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
@@ -651,20 +619,18 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
                 ptx::tmem_st_wait();
             }
             if (drafts && (!L::kShare || w == 0)) {
-                const uint32_t pos = used + pos_v<L>(i, n), st = (L::kTurns ? w * L::NR : 0) + pos % L::NR;
-                ok = __all_sync(0xffffffffu, ok && wait(bar(ms->full[st]), (pos / L::NR) & 1u, &ms->abort));
-                clean_values<D, NQ>(sm + L::kOffKV + st * L::kStage, k0, pc.len, kv, tid, &ms->bad[pieces % 3]);
+                const uint32_t pos = used + j / L::kUnit, st = L::first(L::ring_of(w)) + pos % L::NV;
+                ok = ok && wait(bar(ms->full[st]), (pos / L::NV) & 1u, &ms->abort);
+                clean_values<D, NQ>(sm + L::kOffKV + st * L::kStage + (j & (L::kUnit - 1)) * L::kBlocks * L::kBlock, k0,
+                                    pc.len, kv, tid, &ms->bad[pieces % 3]);
                 if (L::kShare) {
                     __syncwarp();
-                    if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->clean[pc.t0 + i - pc.len / L::TN]));
+                    if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->clean[tile - pc.len / kTile]));
                 }
             }
             ptx::tc_fence_before_sync();
             __syncwarp();
-            if ((tid & 31) == 0) {
-                if (L::NWG == 2 && (drafts || !(ok_half && warp_on))) ptx::mbar_arrive(bar(ms->p_half[buf]));
-                ptx::mbar_arrive(bar(ms->p_full[buf]));
-            }
+            if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->p_full[2 * w + buf]));
             pv_ph ^= 1u << buf;
         }
         ok = ok && wait(bar(ms->o_full), pieces & 1u, &ms->abort);
@@ -744,7 +710,7 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
         ptx::tc_fence_before_sync();
         __syncwarp();
         if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->o_empty));
-        used += ring_places<L>(n, w);
+        used += (mine + L::kUnit - 1) / L::kUnit;
         ++pieces;
     }
 }
@@ -759,7 +725,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     uint8_t *sm = smem_raw + pad;
     Misc *ms = reinterpret_cast<Misc *>(sm + L::kOffMisc);
     const uint32_t base = raw + pad;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int group = blockIdx.x / A.NQT, qt = blockIdx.x - group * A.NQT;
     uint32_t have;
     asm("mov.u32 %0, %dynamic_smem_size;" : "=r"(have));
@@ -771,22 +737,21 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         const auto init = [](uint64_t &b, uint32_t n) { ptx::mbar_init(ptx::smem_addr(&b), n); };
         for (int i = 0; i < L::NST; ++i) {
             init(ms->full[i], 1);
-            init(ms->empty[i], NQ);            // streams that use a tile
+            init(ms->empty[i], i < L::NK ? 1 : NQ);   // streams that use the values
         }
         for (int i = 0; i < 2; ++i) {
             init(ms->q_full[i], 1);
-            init(ms->q_empty[i], L::NWG);
+            init(ms->q_empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             init(ms->s_full[i], 1);
-            init(ms->p_half[i], 4);
             init(ms->p_full[i], 4);
             init(ms->pv_done[i], 1);
         }
         init(ms->o_full, L::NWG);
         init(ms->o_empty, L::NWG * 4);
-        for (int i = 0; i < 2; ++i) {
-            init(ms->drain[i], 1);
-            init(ms->clean[i], 4);
-        }
+        for (int i = 0; i < 2; ++i) init(ms->clean[i], 4);
+        for (int i = 0; i < 3; ++i) init(ms->drain[i], 1);
         ms->bad[0] = ms->bad[1] = ms->bad[2] = 0;
         ms->abort = 0;
         ptx::mbar_init_fence();
@@ -804,12 +769,13 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     const uint32_t tmem = ms->tmem;
 
     if (warp < L::NWG * 4) {
-        if (L::NWG == 2) more_registers<L::kRegsMore>();
         soften<D, NQ>(A, ms, sm, tmem, plan, group, qt, tid);
     } else {
-        if (L::NWG == 2) fewer_registers<L::kRegsLess>();
-        if (warp == L::NWG * 4) produce<D, NQ>(A, &mq, &mk, &mv, ms, base, plan, group, qt, lane);
-        if (warp > L::NWG * 4 && warp <= L::NWG * 5) multiply<D, NQ>(A, ms, base, tmem, plan, group, qt, warp - L::NWG * 4 - 1);
+        const int role = warp - L::NWG * 4;
+        if (role == 0) produce<D, NQ>(A, &mq, &mk, &mv, ms, base, plan, group, qt);
+        else if (role == 1) multiply_scores<D, NQ>(A, ms, base, tmem, plan, group, qt);
+        else if (role < 2 + L::NWG) multiply_sums<D, NQ>(A, ms, base, tmem, plan, group, qt, role - 2);
+        __syncwarp();
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
@@ -863,14 +829,16 @@ cudaError_t run(const AttnArgs &A, cudaStream_t st) {
     cudaError_t e = kernel_setup(setup, (const void *)tree_attn_tc_kernel<D, NQ>, smem, &sms);
     if (e != cudaSuccess) return e;
     const cuuint64_t rows = (cuuint64_t)A.C.n_layers * A.C.num_pages * A.C.HKV * A.C.P;
-    const cuuint64_t kv_dims[2] = {(cuuint64_t)D, rows}, kv_stride[1] = {(cuuint64_t)D};
-    const cuuint32_t kv_box[2] = {64, (cuuint32_t)(A.C.P < L::TN ? A.C.P : L::TN)};
+    // (64 dims, token rows, blocks of 64 dims): a box that holds a whole tile has all of its blocks, one after another
+    const cuuint64_t kv_dims[3] = {64, rows, L::kBlocks}, kv_stride[2] = {(cuuint64_t)D, 64};
+    const cuuint32_t v_box[3] = {64, (cuuint32_t)(A.C.P < kTile ? A.C.P : kTile), A.C.P >= kTile ? L::kBlocks : 1u};
+    const cuuint32_t k_box[3] = {64, v_box[1], L::kShare ? 1u : v_box[2]};
     const int tokens_q = A.MT / NQ / A.G;
     const cuuint64_t q_dims[3] = {(cuuint64_t)D, (cuuint64_t)A.HQ, (cuuint64_t)A.B * A.T};
     const cuuint64_t q_stride[2] = {(cuuint64_t)D, (cuuint64_t)A.HQ * D};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)A.G, (cuuint32_t)(tokens_q < A.T ? tokens_q : A.T)};
     CUtensorMap mq, mk, mv;
-    if (!bf16_map(&mk, A.C.k, 2, kv_dims, kv_stride, kv_box) || !bf16_map(&mv, A.C.v, 2, kv_dims, kv_stride, kv_box) ||
+    if (!bf16_map(&mk, A.C.k, 3, kv_dims, kv_stride, k_box) || !bf16_map(&mv, A.C.v, 3, kv_dims, kv_stride, v_box) ||
         !bf16_map(&mq, A.q, 3, q_dims, q_stride, q_box))
         return cudaErrorInvalidValue;
     return launch_dependent(tree_attn_tc_kernel<D, NQ>, dim3(A.groups * A.NQT), dim3(L::kThreads), smem, st, mq, mk, mv, A);
@@ -888,7 +856,7 @@ bool tree_attn_tc_supported(const KvArgs &C, int G, bool bf16) {
 void tree_attn_tc_cut(AttnArgs *A, int sms) {
     const int R = A->T * A->G, tile = tat::kRows / A->G * A->G;
     const int nq = A->C.D <= 128 && R > tile ? 2 : 1;
-    A->TN = A->C.D == 256 ? 64 : 128;
+    A->TN = tat::kTile;
     A->MT = nq * tile;
     A->NQT = (R + A->MT - 1) / A->MT;
     const int groups = sms / A->NQT;

@@ -193,20 +193,22 @@ def test_long_contexts_are_split_and_joined(io):
 
 
 def test_many_rows_share_pages_and_layers():
-    """More rows than a block scans at once, slots that repeat pages, the last of three layers."""
-    c = Case(7, "bf16", T=2, HQ=4, HKV=2, D=64, P=16, lens=[40, 90, 3, 64, 17], slots=[i % 5 for i in range(700)],
-             layers=3, layer=2)
-    out, lse = c.call()
-    first, lf = out[:5].clone(), lse[:5].clone()
+    """More rows than a block scans at once, slots that repeat pages, the last of three layers.  Rows that
+    are alike may be cut at different places, so they agree within the bounds."""
+    lens = [40, 90, 3, 64, 17]
+    c = Case(7, "bf16", T=2, HQ=4, HKV=2, D=64, P=16, lens=lens, slots=[i % 5 for i in range(700)], layers=3, layer=2)
     c.q = c.q[:5].repeat(140, 1, 1, 1)
     c.masks = [c.masks[i % 5] for i in range(700)]
     out, lse = c.call()
-    assert torch.equal(out.view(140, 5, *out.shape[1:]), out[:5].expand(140, *out[:5].shape))
-    small = Case(7, "bf16", T=2, HQ=4, HKV=2, D=64, P=16, lens=[40, 90, 3, 64, 17], layers=3, layer=2)
-    small.k, small.v, small.table, small.n_pages = c.k, c.v, c.table, c.n_pages
-    small.q, small.masks = c.q[:5], c.masks[:5]
-    small.check()
-    assert first.shape == out[:5].shape and lf.shape == lse[:5].shape
+    assert binding.kv_read_status(c.cache) == 0
+    c.q, c.masks, c.slots, c.counts = c.q[:5], c.masks[:5], c.slots[:5], c.counts[:5]
+    want, want_lse, spread = (x[None] for x in c.expect())
+    got = out.double().cpu().numpy().reshape(140, 5, 2, 4, 64)
+    bound = HALF_ULP["bf16"] * np.abs(want) + (HALF_ULP["bf16"] + FP32_NOISE) * spread * (1 + 2.0 ** -8)
+    assert (np.abs(got - want) <= bound).all()
+    assert np.max(np.abs(lse.double().cpu().numpy().reshape(140, 5, 2, 4) - want_lse)) <= 2e-5
+    small, _ = c.call()
+    assert small.shape == (5, 2, 4, 64)
 
 
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 30.0])
