@@ -33,6 +33,7 @@ struct AttnArgs {
     float2 *part_ml;           // [groups * NQT][2][MT] (maximum in log2 units, sum)
     struct AttnCut *cuts;      // [groups] where each chunk starts, for the join
     int TN, MT, NQT, groups, min_chunk;
+    bool whole;                // tensor-core kernel: a copy holds all dims of a tile
     uint32_t wait_limit;
 };
 

@@ -1,5 +1,6 @@
 // tree_attn_tc.cu -- attention of a window of drafted tokens over the paged cache on
-// the tensor cores (bf16, D = 64, 128 or 256).
+// the tensor cores (bf16; heads of other than 64, 128 or 256 dims are filled up with
+// zeros to the next of them in shared memory).
 //
 // A block works through the pieces of its chunk (attn_common.cuh) in tiles of 64 keys:
 //   S = Q K^T     tcgen05.mma kind::f16, 128 query rows x 64 keys, fp32 in TMEM
@@ -216,13 +217,14 @@ __device__ __forceinline__ uint64_t visible_bits(int k0, int len, uint64_t mask)
 
 // ------------------------------------------------------------------ producer warp
 
-// All lanes compute the same and one issues: a copy's operands are uniform registers, and lanes with
-// copies of their own would be served one after another.
+// One lane issues: a copy's operands are uniform registers, and lanes with copies of their own would be served one
+// after another.  The lanes look up the pages of a unit's boxes side by side.
 template <int D, int NQ>
 __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq, const CUtensorMap *mk,
                                         const CUtensorMap *mv, Misc *ms, uint32_t base, const AttnPlan &plan, int group,
                                         int qt) {
     using L = Lay<D, NQ>;
+    const int lane = threadIdx.x & 31;
     const int BR = min(A.C.P, kTile);                          // tokens of a box: within a page and within a tile
     const int RT = A.MT / NQ, tokens_q = RT / A.G;             // rows and tokens of a query tile
     const uint32_t q_bytes = 128u * A.G * min(tokens_q, A.T);   // one 64-dim block of one query tile
@@ -242,29 +244,40 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
             const uint32_t st = L::first(ring) + place[ring].at;
             const int tok = (pc.t0 + u * L::kUnit) * kTile;
             const int live = min(min(L::kUnit, n - u * L::kUnit) * kTile, kv - tok), boxes = (live + BR - 1) / BR;
-            int page = table[tok >> A.C.logP];
+            // row of the pool where box `lane` starts
+            int row = 0;
+            if (lane < boxes) {
+                const int at = tok + lane * BR;
+                int page = table[at >> A.C.logP];
+                if (page < 0 || page >= A.C.num_pages) {
+                    atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+                    page = 0;
+                }
+                row = ((A.layer * A.C.num_pages + page) * A.C.HKV + pc.h) * A.C.P + (at & (A.C.P - 1));
+            }
             if (!wait(ptx::smem_addr(&ms->empty[st]), place[ring].ph ^ 1u, &ms->abort)) return false;
             const uint32_t bar = uniform(ptx::smem_addr(&ms->full[st]));
             const uint32_t dst = uniform(base + L::kOffKV + st * L::kStage);
+            constexpr int kMost = L::kUnit * kTile / 16;   // boxes of the smallest pages
+            int rows[kMost];
+#pragma unroll
+            for (int c = 0; c < kMost; ++c) rows[c] = __shfl_sync(0xffffffffu, row, c);
             if (ptx::elect_one()) {
                 ptx::mbar_expect_tx(bar, BR * 128u * L::kBlocks * boxes);
-                for (int c = 0; c < boxes; ++c) {
-                    const int at = c * BR;   // row of the unit
-                    if (c) page = table[(tok + at) >> A.C.logP];
-                    if (page < 0 || page >= A.C.num_pages) {
-                        atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
-                        page = 0;
-                    }
-                    const int row = ((A.layer * A.C.num_pages + page) * A.C.HKV + pc.h) * A.C.P +
-                                    ((tok + at) & (A.C.P - 1));
-                    if (!rows128 && BR == kTile) {   // all of a tile's blocks by one copy
-                        ptx::tma_load_3d(dst + at * 128u * L::kBlocks, map, bar, 0, row, 0);
-                    } else {
+                if (!rows128 && A.whole) {   // all of a tile's blocks by one copy
+#pragma unroll
+                    for (int c = 0; c < L::kUnit; ++c)
+                        if (c < boxes) ptx::tma_load_3d(dst + c * L::kBlocks * L::kBlock, map, bar, 0, rows[c], 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kMost; ++c) {
+                        if (c >= boxes) break;
+                        const int at = c * BR;   // row of the unit
                         const uint32_t to = rows128 ? dst + at * 128u
-                                                    : dst + (at / kTile) * kTile * 128u * L::kBlocks + (at % kTile) * 128u;
+                                                    : dst + (at / kTile) * L::kBlocks * L::kBlock + (at % kTile) * 128u;
 #pragma unroll
                         for (int blk = 0; blk < (int)L::kBlocks; ++blk)
-                            ptx::tma_load_3d(to + blk * (rows128 ? L::kUnit : 1) * L::kBlock, map, bar, 0, row, blk);
+                            ptx::tma_load_3d(to + blk * (rows128 ? L::kUnit : 1) * L::kBlock, map, bar, blk * 64, rows[c], 0);
                     }
                 }
             }
@@ -498,7 +511,7 @@ __device__ __forceinline__ void clean_values(uint8_t *tile, int k0, int len, int
 // The terms of drafts that are not finite, for the rows that attend to them: weight
 // and value from memory.  o: dims d0 .. d0 + 31 of this row's unnormalised sums over m.
 __device__ __noinline__ void add_bad(const AttnArgs &A, const AttnPiece &pc, unsigned long long bad, int64_t qrow, float m,
-                                     int d0, float *o) {
+                                     int d0, int dims, float *o) {
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(A.q) + qrow * A.C.D;
     while (bad) {
         const int j = __ffsll((long long)bad) - 1;
@@ -510,7 +523,7 @@ __device__ __noinline__ void add_bad(const AttnArgs &A, const AttnPiece &pc, uns
         float s = 0.0f;
         for (int d = 0; d < A.C.D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
         const float p = __bfloat162float(__float2bfloat16_rn(ex2(s * A.scale_log2 - m)));
-        for (int d = 0; d < 32; ++d) o[d] = fmaf(p, __bfloat162float(v[d0 + d]), o[d]);
+        for (int d = 0; d < dims; ++d) o[d] = fmaf(p, __bfloat162float(v[d0 + d]), o[d]);
     }
 }
 
@@ -652,13 +665,13 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
             const int64_t row = attn_out_row(A, pc.b, pc.h, on ? r : qt * A.MT);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             // the two warpgroups of a shared query tile take half of the dims each
-            constexpr int kDims = L::kTurns ? D / 2 : D;
+            constexpr int kDims = L::kTurns ? D / 2 : D;   // of D, the head's dims filled up to 64, 128 or 256
             const int d_begin = L::kTurns ? w * kDims : 0;
             const int64_t part = (int64_t)blockIdx.x * 2 + pc.side;
             const bool whole = pc.whole();
 #pragma unroll 1
-            for (int x = 0; x < kDims; x += 32) {
-                const int d0 = d_begin + x;
+            for (int x = 0; x < kDims && d_begin + x < A.C.D; x += 32) {
+                const int d0 = d_begin + x, dims = min(32, A.C.D - d0);
                 float f[32];
                 if (L::kTurns) {
                     uint32_t u[32], v[32];
@@ -682,23 +695,23 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
                         float g[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) g[j] = f[j];
-                        add_bad(A, pc, bad, row, m, d0, g);
+                        add_bad(A, pc, bad, row, m, d0, dims, g);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = g[j];
                     }
                     if (whole) {
-                        uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) + row * D + d0);
+                        uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) + row * A.C.D + d0);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            out[j] = make_uint4(pack_bf16(f[8 * j] * inv, f[8 * j + 1] * inv),
+                            if (8 * j < dims) out[j] = make_uint4(pack_bf16(f[8 * j] * inv, f[8 * j + 1] * inv),
                                                 pack_bf16(f[8 * j + 2] * inv, f[8 * j + 3] * inv),
                                                 pack_bf16(f[8 * j + 4] * inv, f[8 * j + 5] * inv),
                                                 pack_bf16(f[8 * j + 6] * inv, f[8 * j + 7] * inv));
                     } else {
-                        float4 *po = A.part_o + (part * (D / 4) + d0 / 4) * A.MT + my_row;
+                        float4 *po = A.part_o + (part * (A.C.D / 4) + d0 / 4) * A.MT + my_row;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            po[(int64_t)j * A.MT] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                            if (4 * j < dims) po[(int64_t)j * A.MT] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
                     }
                 }
             }
@@ -829,16 +842,20 @@ cudaError_t run(const AttnArgs &A, cudaStream_t st) {
     cudaError_t e = kernel_setup(setup, (const void *)tree_attn_tc_kernel<D, NQ>, smem, &sms);
     if (e != cudaSuccess) return e;
     const cuuint64_t rows = (cuuint64_t)A.C.n_layers * A.C.num_pages * A.C.HKV * A.C.P;
-    // (64 dims, token rows, blocks of 64 dims): a box that holds a whole tile has all of its blocks, one after another
-    const cuuint64_t kv_dims[3] = {64, rows, L::kBlocks}, kv_stride[2] = {(cuuint64_t)D, 64};
-    const cuuint32_t v_box[3] = {64, (cuuint32_t)(A.C.P < kTile ? A.C.P : kTile), A.C.P >= kTile ? L::kBlocks : 1u};
-    const cuuint32_t k_box[3] = {64, v_box[1], L::kShare ? 1u : v_box[2]};
+    // Keys and values as (64 dims, token rows, blocks of 64 dims) where a box can hold all of a tile's blocks (they land
+    // one after another), else as (dims, token rows, 1) with a box for each block; dims past the head's are filled
+    // with zeros.
+    const cuuint64_t dims = A.C.D;
+    const cuuint64_t kv_dims[3] = {A.whole ? 64 : dims, rows, A.whole ? dims / 64 : 1}, kv_stride[2] = {dims, 64};
+    const cuuint32_t v_box[3] = {64, (cuuint32_t)(A.C.P < kTile ? A.C.P : kTile), A.whole ? (cuuint32_t)(dims / 64) : 1u};
+    const cuuint64_t k_dims[3] = {dims, rows, 1};
+    const cuuint32_t k_box[3] = {64, v_box[1], 1};
     const int tokens_q = A.MT / NQ / A.G;
-    const cuuint64_t q_dims[3] = {(cuuint64_t)D, (cuuint64_t)A.HQ, (cuuint64_t)A.B * A.T};
-    const cuuint64_t q_stride[2] = {(cuuint64_t)D, (cuuint64_t)A.HQ * D};
+    const cuuint64_t q_dims[3] = {dims, (cuuint64_t)A.HQ, (cuuint64_t)A.B * A.T};
+    const cuuint64_t q_stride[2] = {dims, (cuuint64_t)A.HQ * dims};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)A.G, (cuuint32_t)(tokens_q < A.T ? tokens_q : A.T)};
     CUtensorMap mq, mk, mv;
-    if (!bf16_map(&mk, A.C.k, 3, kv_dims, kv_stride, k_box) || !bf16_map(&mv, A.C.v, 3, kv_dims, kv_stride, v_box) ||
+    if (!(L::kShare ? bf16_map(&mk, A.C.k, 3, k_dims, kv_stride, k_box) : bf16_map(&mk, A.C.k, 3, kv_dims, kv_stride, v_box)) || !bf16_map(&mv, A.C.v, 3, kv_dims, kv_stride, v_box) ||
         !bf16_map(&mq, A.q, 3, q_dims, q_stride, q_box))
         return cudaErrorInvalidValue;
     return launch_dependent(tree_attn_tc_kernel<D, NQ>, dim3(A.groups * A.NQT), dim3(L::kThreads), smem, st, mq, mk, mv, A);
@@ -847,8 +864,7 @@ cudaError_t run(const AttnArgs &A, cudaStream_t st) {
 }  // namespace tat
 
 bool tree_attn_tc_supported(const KvArgs &C, int G, bool bf16) {
-    return bf16 && (C.D == 64 || C.D == 128 || C.D == 256) && G <= tat::kRows &&
-           (int64_t)C.n_layers * C.num_pages * C.HKV * C.P <= INT32_MAX;
+    return bf16 && G <= tat::kRows && (int64_t)C.n_layers * C.num_pages * C.HKV * C.P <= INT32_MAX;
 }
 
 // The cut of the work: a query tile holds whole tokens, as many as fit in 128 rows;
@@ -856,6 +872,7 @@ bool tree_attn_tc_supported(const KvArgs &C, int G, bool bf16) {
 void tree_attn_tc_cut(AttnArgs *A, int sms) {
     const int R = A->T * A->G, tile = tat::kRows / A->G * A->G;
     const int nq = A->C.D <= 128 && R > tile ? 2 : 1;
+    A->whole = A->C.P >= tat::kTile && A->C.D % 64 == 0 && A->C.D != 192;
     A->TN = tat::kTile;
     A->MT = nq * tile;
     A->NQT = (R + A->MT - 1) / A->MT;
@@ -867,8 +884,8 @@ void tree_attn_tc_cut(AttnArgs *A, int sms) {
 cudaError_t launch_tree_attn_tc(const AttnArgs &A, cudaStream_t st) {
     const bool two = A.MT > tat::kRows;
     cudaError_t e;
-    if (A.C.D == 64) e = two ? tat::run<64, 2>(A, st) : tat::run<64, 1>(A, st);
-    else if (A.C.D == 128) e = two ? tat::run<128, 2>(A, st) : tat::run<128, 1>(A, st);
+    if (A.C.D <= 64) e = two ? tat::run<64, 2>(A, st) : tat::run<64, 1>(A, st);
+    else if (A.C.D <= 128) e = two ? tat::run<128, 2>(A, st) : tat::run<128, 1>(A, st);
     else e = tat::run<256, 1>(A, st);
     return e != cudaSuccess ? e : launch_attn_join(A, true, st);
 }

@@ -515,9 +515,9 @@ int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache
  *   workspace  device memory of workspace_bytes >= gdn_spec_tree_attn_workspace, 16-byte
  *              aligned; its contents need not be kept or cleared, and calls that may run at
  *              the same time need one each
- * Two kernels (gdn_spec_tree_attn_path): "tc" -- bf16, D in {64, 128, 256}: TMA and
- * tcgen05, the probabilities rounded to bf16 for the second product; "generic" --
- * fp32 or another D, fp32 throughout on the CUDA cores.  1 <= T <= 64.
+ * Two kernels (gdn_spec_tree_attn_path): "tc" -- bf16, at most 128 query heads a kv
+ * head: TMA and tcgen05, the probabilities rounded to bf16 for the second
+ * product; "generic" -- otherwise: fp32 throughout on the CUDA cores.  1 <= T <= 64.
  * Device status: SLOT_OOR, ACCEPT_RANGE (tree_len), CURSOR_CORRUPT, NO_PAGES (the row
  * gives zeros), PAGE_OOR, TIMEOUT.
  */

@@ -93,7 +93,8 @@ def test_attention_call(lib):
         assert attn(lib, c, **kw) == want, kw
     assert lib.gdn_spec_tree_attn_path(ctypes.byref(c), 65, 8) is None
     assert lib.gdn_spec_tree_attn_path(ctypes.byref(cache(io_dtype=1)), 4, 8) == b"generic"
-    assert lib.gdn_spec_tree_attn_path(ctypes.byref(cache(D=96)), 4, 8) == b"generic"
+    assert lib.gdn_spec_tree_attn_path(ctypes.byref(cache(D=96)), 4, 8) == b"tc"
+    assert lib.gdn_spec_tree_attn_path(ctypes.byref(cache()), 4, 2 * 129) == b"generic"
 
 
 def plan(D=128, rot=128, layout="half", **kw):
