@@ -149,38 +149,42 @@ struct AttnPiece {
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
+// Keeps the row between its heads: a row's counts are three dependent loads.
 struct AttnWalk {
-    int b, off, left;
+    AttnRow row;
+    int b, h, t, tiles, left;   // next tile; left: tiles of the chunk not yet handed out
     bool first;
-    __device__ __forceinline__ void start(const AttnPlan &p) {
-        b = p.b;
-        off = p.off;
-        first = true;
-        left = 0;
+    __device__ __forceinline__ void load(const AttnArgs &A) {
+        uint32_t bits;
+        row = attn_row(A, b, &bits);
+        tiles = attn_tiles(A, row);
     }
-    // left: tiles of the chunk not yet handed out
     __device__ __forceinline__ bool next(const AttnArgs &A, AttnPiece *piece) {
         if (left <= 0) return false;
-        for (;; ++b, off = 0) {
-            if (b >= A.B) return false;
-            uint32_t bits;
-            const AttnRow r = attn_row(A, b, &bits);
-            const int tiles = attn_tiles(A, r);
-            if (off >= tiles * A.C.HKV) continue;
-            piece->b = b;
-            piece->slot = r.slot;
-            piece->len = r.len;
-            piece->cnt = r.cnt;
-            piece->h = off / tiles;
-            piece->t0 = off - piece->h * tiles;
-            piece->t1 = min(tiles, piece->t0 + left);
-            piece->tiles = tiles;
-            piece->side = first ? 0 : 1;
-            first = false;
-            off += piece->t1 - piece->t0;
-            left -= piece->t1 - piece->t0;
-            return true;
+        if (t == tiles) {
+            t = 0;
+            ++h;
         }
+        if (h >= A.C.HKV) {
+            h = 0;
+            do {
+                if (++b >= A.B) return false;
+                load(A);
+            } while (tiles == 0);
+        }
+        piece->b = b;
+        piece->slot = row.slot;
+        piece->len = row.len;
+        piece->cnt = row.cnt;
+        piece->h = h;
+        piece->t0 = t;
+        piece->t1 = min(tiles, t + left);
+        piece->tiles = tiles;
+        piece->side = first ? 0 : 1;
+        first = false;
+        left -= piece->t1 - t;
+        t = piece->t1;
+        return true;
     }
 };
 
@@ -194,10 +198,16 @@ __device__ __forceinline__ void attn_note(const AttnArgs &A, int group, bool any
     A.cuts[group] = any ? AttnCut{pc.b, pc.h, pc.t0, pc.tiles, pc.cnt, chunk, {0, 0}} : AttnCut{-1, 0, 0, 0, 0, chunk, {0, 0}};
 }
 
-__device__ __forceinline__ AttnWalk attn_walk(const AttnPlan &p, int group) {
+__device__ __forceinline__ AttnWalk attn_walk(const AttnArgs &A, const AttnPlan &p, int group) {
     AttnWalk w;
-    w.start(p);
-    w.left = p.b < 0 ? 0 : (int)min((int64_t)p.chunk, (int64_t)p.total - (int64_t)group * p.chunk);
+    w.first = true;
+    w.left = 0;
+    if (p.b < 0) return w;
+    w.b = p.b;
+    w.load(A);
+    w.h = p.off / w.tiles;
+    w.t = p.off - w.h * w.tiles;
+    w.left = (int)min((int64_t)p.chunk, (int64_t)p.total - (int64_t)group * p.chunk);
     return w;
 }
 

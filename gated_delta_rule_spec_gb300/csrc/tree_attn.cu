@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kAttnThreads) tree_attn_kernel(const __grid_co
 
     attn_dead_rows<IO>(A, blockIdx.x, gridDim.x, kAttnThreads);
     const AttnPlan plan = attn_plan<kAttnThreads>(A, group, blockIdx.x == 0, scratch);
-    AttnWalk walk = attn_walk(plan, group);
+    AttnWalk walk = attn_walk(A, plan, group);
     AttnPiece pc;
     bool any = walk.next(A, &pc);
     if (tid == 0 && qt == 0) attn_note(A, group, any, pc, plan.chunk);

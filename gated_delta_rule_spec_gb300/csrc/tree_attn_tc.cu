@@ -231,7 +231,7 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
     Place place[3];
     uint32_t issued[3] = {0, 0, 0}, q_issued = 0;
     bool ok = true;
-    AttnWalk walk = attn_walk(plan, group);
+    AttnWalk walk = attn_walk(A, plan, group);
     AttnPiece pc;
     while (ok && walk.next(A, &pc)) {
         if (pc.cnt * A.G - qt * A.MT <= 0) continue;
@@ -360,7 +360,7 @@ __device__ __forceinline__ void multiply_scores(const AttnArgs &A, Misc *ms, uin
     uint32_t q_used = 0, used_any = 0, used_ph = 0;   // bit of an S buffer: whether it was used, parity of its uses
     Place key;
     bool ok = true;
-    AttnWalk walk = attn_walk(plan, group);
+    AttnWalk walk = attn_walk(A, plan, group);
     AttnPiece pc;
     bool any = walk.next(A, &pc);
     if (qt == 0 && ptx::elect_one()) attn_note(A, group, any, pc, plan.chunk);
@@ -428,7 +428,7 @@ __device__ __forceinline__ void multiply_sums(const AttnArgs &A, Misc *ms, uint3
     uint32_t pieces = 0, p_ph = 0, c_ph = 0;   // bit of a buffer or barrier: parity of the waits done on it
     Place val;
     bool ok = true;
-    AttnWalk walk = attn_walk(plan, group);
+    AttnWalk walk = attn_walk(A, plan, group);
     AttnPiece pc;
     while (ok && walk.next(A, &pc)) {
         if (pc.cnt * A.G - qt * A.MT <= 0) continue;
@@ -509,7 +509,7 @@ __device__ __forceinline__ void clean_values(uint8_t *tile, int k0, int len, int
 }
 
 // The terms of drafts that are not finite, for the rows that attend to them: weight
-// and value from memory.  o: dims d0 .. d0 + 31 of this row's unnormalised sums over m.
+// and value from memory.  o: dims from d0 on of this row's unnormalised sums over m.
 __device__ __noinline__ void add_bad(const AttnArgs &A, const AttnPiece &pc, unsigned long long bad, int64_t qrow, float m,
                                      int d0, int dims, float *o) {
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(A.q) + qrow * A.C.D;
@@ -541,7 +541,7 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
     uint32_t used = 0, pieces = 0;                          // places used of the values' ring
     uint32_t s_ph = 0, pv_ph = 0;                           // bit of a buffer: parity of the tiles taken, handed on
     bool ok = true;
-    AttnWalk walk = attn_walk(plan, group);
+    AttnWalk walk = attn_walk(A, plan, group);
     AttnPiece pc;
     while (ok && walk.next(A, &pc)) {
         const int live = min(A.MT, pc.cnt * A.G - qt * A.MT);
@@ -669,49 +669,50 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
             const int d_begin = L::kTurns ? w * kDims : 0;
             const int64_t part = (int64_t)blockIdx.x * 2 + pc.side;
             const bool whole = pc.whole();
+            constexpr int kBatch = 32;   // a short body: it is fetched anew for every piece
 #pragma unroll 1
-            for (int x = 0; x < kDims && d_begin + x < A.C.D; x += 32) {
-                const int d0 = d_begin + x, dims = min(32, A.C.D - d0);
-                float f[32];
-                if (L::kTurns) {
-                    uint32_t u[32], v[32];
-                    ptx::tmem_ld32_bits(lane_addr + L::col_o(0) + d0, u);
-                    ptx::tmem_ld32_bits(lane_addr + L::col_o(1) + d0, v);
-                    landed(u);
-                    landed(v);
+            for (int x = 0; x < kDims && d_begin + x < A.C.D; x += kBatch) {
+                const int d0 = d_begin + x, dims = min(kBatch, A.C.D - d0);
+                uint32_t u[kBatch], v[L::kTurns ? kBatch : 1];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)   // a stream that saw nothing may hold anything
-                        f[j] = (w0 != 0.0f ? __uint_as_float(u[j]) * w0 : 0.0f) +
-                               (w1 != 0.0f ? __uint_as_float(v[j]) * w1 : 0.0f);
-                } else {
-                    uint32_t u[32];
-                    ptx::tmem_ld32_bits(lane_addr + L::col_o(L::kShare ? w : 0) + d0, u);
-                    landed(u);
+                for (int y = 0; y < kBatch; y += 32) {
+                    ptx::tmem_ld32_bits(lane_addr + L::col_o(L::kTurns ? 0 : w) + d0 + y, u + y);
+                    if (L::kTurns) ptx::tmem_ld32_bits(lane_addr + L::col_o(1) + d0 + y, v + (L::kTurns ? y : 0));
+                }
+                landed(u);
+                if (L::kTurns) landed(v);
+                float f[kBatch];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) f[j] = l != 0.0f ? __uint_as_float(u[j]) : 0.0f;
+                for (int y = 0; y < kBatch; ++y) {   // a stream that saw nothing may hold anything
+                    if (L::kTurns)
+                        f[y] = (w0 != 0.0f ? __uint_as_float(u[y]) * w0 : 0.0f) +
+                               (w1 != 0.0f ? __uint_as_float(v[L::kTurns ? y : 0]) * w1 : 0.0f);
+                    else
+                        f[y] = l != 0.0f ? __uint_as_float(u[y]) : 0.0f;
                 }
                 if (on) {
                     if (bad) {   // rare: a copy of its own, so that f stays in registers
-                        float g[32];
+                        float g[kBatch];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) g[j] = f[j];
+                        for (int y = 0; y < kBatch; ++y) g[y] = f[y];
                         add_bad(A, pc, bad, row, m, d0, dims, g);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = g[j];
+                        for (int y = 0; y < kBatch; ++y) f[y] = g[y];
                     }
                     if (whole) {
                         uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) + row * A.C.D + d0);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (8 * j < dims) out[j] = make_uint4(pack_bf16(f[8 * j] * inv, f[8 * j + 1] * inv),
-                                                pack_bf16(f[8 * j + 2] * inv, f[8 * j + 3] * inv),
-                                                pack_bf16(f[8 * j + 4] * inv, f[8 * j + 5] * inv),
-                                                pack_bf16(f[8 * j + 6] * inv, f[8 * j + 7] * inv));
+                        for (int y = 0; y < kBatch; y += 8)
+                            if (y < dims)
+                                out[y / 8] = make_uint4(pack_bf16(f[y] * inv, f[y + 1] * inv),
+                                                        pack_bf16(f[y + 2] * inv, f[y + 3] * inv),
+                                                        pack_bf16(f[y + 4] * inv, f[y + 5] * inv),
+                                                        pack_bf16(f[y + 6] * inv, f[y + 7] * inv));
                     } else {
                         float4 *po = A.part_o + (part * (A.C.D / 4) + d0 / 4) * A.MT + my_row;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (4 * j < dims) po[(int64_t)j * A.MT] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                        for (int y = 0; y < kBatch; y += 4)
+                            if (y < dims) po[(int64_t)(y / 4) * A.MT] = make_float4(f[y], f[y + 1], f[y + 2], f[y + 3]);
                     }
                 }
             }
