@@ -28,7 +28,7 @@ cudaError_t launch_rope_append(const gdn_spec_rope_plan *plan, const KvArgs &C, 
                                const int32_t *slot_idx, int B, int T, const int32_t *n_tokens, const int32_t *pos, int HQ,
                                const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                                int64_t v_stride, void *q_out, cudaStream_t st);
-void tree_attn_cut(AttnArgs *A, int sms);
+void tree_attn_cut(AttnArgs *A, int sms, int es);
 cudaError_t launch_tree_attn(const AttnArgs &A, bool bf16, cudaStream_t st);
 bool tree_attn_tc_supported(const KvArgs &C, int G, bool bf16);
 void tree_attn_tc_cut(AttnArgs *A, int sms);
@@ -137,7 +137,7 @@ int attn_args(const gdn_spec_kv_cache *c, int32_t B, int32_t T, int32_t HQ, Attn
     int sms;
     const int rc = device_sms(&sms);
     if (rc) return rc;
-    if (attn_on_tc(c, HQ)) tree_attn_tc_cut(A, sms); else tree_attn_cut(A, sms);
+    if (attn_on_tc(c, HQ)) tree_attn_tc_cut(A, sms); else tree_attn_cut(A, sms, elem_size(c->io_dtype));
     return GDN_SPEC_OK;
 }
 

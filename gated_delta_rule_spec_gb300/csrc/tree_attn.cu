@@ -1,68 +1,70 @@
 // tree_attn.cu -- attention of a window of drafted tokens over the paged cache on
-// the CUDA cores (fp32, and head dims that the tensor-core kernel does not take),
-// and the join of split items for both kernels.
+// the CUDA cores (fp32, and groups of more than 128 heads), and the join of split
+// items for both kernels.
 //
 // Per query row, one pass over the keys with a running maximum m and sum l in
 // powers of two: for a tile's scores s (times scale log2 e),
 //   m' = max(m, max s),  l' = l 2^(m-m') + sum 2^(s-m'),  o' = o 2^(m-m') + sum 2^(s-m') v,
 // and the row's output is o / l.  A row that has seen nothing yet has m = -inf, l = 0.
 //
-// A block of 256 threads holds MT = 4 RPT query rows and walks tiles of 64 keys
-// held in shared memory in fp32.  Scores: thread (i, c) forms those of key c with
-// its RPT rows, the key read once and the query rows broadcast, so a key's 16 bytes
-// serve RPT rows; the key rows are padded by 16 bytes so that eight keys' pieces
-// fall in different banks.  Sums: the same thread layout over output columns.
-// Shared-memory reads bound it (12 wavefronts for the 8 cycles of FMA that 32
-// multiply-adds take at RPT = 8); with few rows it is bound by the loads.
+// A block of four warps holds 4 RPT query rows and walks tiles of 32 keys, copied
+// asynchronously into one of two buffers while the other is worked on.  A warp owns RPT
+// rows: lane k forms their scores with key k (the key row is read once for all of
+// them, the query rows are broadcast; key rows are padded by 16 bytes, so eight
+// lanes' pieces fall in different banks), the maximum is a shuffle reduction, and
+// the sums run over output columns, VEC consecutive ones per lane.  Only the buffers
+// are shared between the warps.  With few rows it is bound by HBM, with 32 rows by
+// shared-memory reads (12 wavefronts for the 8 cycles that 32 multiply-adds take).
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
 
 namespace gdnspec {
 
-constexpr int kAttnThreads = 256;
-constexpr int kAttnTile = 64;     // keys of a tile
+constexpr int kAttnThreads = 128;
+constexpr int kAttnTile = 32;     // keys of a tile
 
-__host__ __device__ constexpr int attn_key_ld(int D) { return D + 4; }
-
-size_t tree_attn_smem(int D, int MT) {
-    return sizeof(float) * ((size_t)MT * D + kAttnTile * attn_key_ld(D) + kAttnTile * D + MT * (kAttnTile + 4) + 3 * MT);
+size_t tree_attn_smem(int D, int MT, int es) {
+    const size_t rows = (size_t)kAttnTile * ((D * es + 16) + D * es);          // a tile's keys and values
+    return 2 * rows + sizeof(float) * ((size_t)MT * D + MT * (kAttnTile + 4));  // and queries, probabilities
 }
 
-template <typename IO> __device__ __forceinline__ void load8(const IO *p, float (&x)[8]);
-template <> __device__ __forceinline__ void load8<float>(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+template <typename IO> __device__ __forceinline__ float4 load4(const IO *p);
+template <> __device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 r = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
 }
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+template <typename IO> __device__ __forceinline__ float2 load2(const IO *p);
+template <> __device__ __forceinline__ float2 load2<float>(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+template <> __device__ __forceinline__ float2 load2<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
 }
 
-// RPT rows per thread (MT = 4 RPT), COLS = ceil(D / 64) output columns per thread.
-template <typename IO, int RPT, int COLS>
-__global__ void __launch_bounds__(kAttnThreads) tree_attn_kernel(const __grid_constant__ AttnArgs A) {
-    constexpr int MT = 4 * RPT, SLD = kAttnTile + 4;
-    extern __shared__ float sm[];
+// Sixteen bytes from global to shared memory; zeros where !live.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+
+// RPT rows per warp (MT = 4 RPT); NG groups of 32 VEC output columns.
+template <typename IO, int RPT, int VEC, int NG>
+__global__ void __launch_bounds__(kAttnThreads, RPT == 8 ? 2 : 4) tree_attn_kernel(const __grid_constant__ AttnArgs A) {
+    constexpr int MT = 4 * RPT, PLD = kAttnTile + 4, kPiece = 16 / sizeof(IO);   // elements of 16 bytes
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int scratch[kAttnScratch];
-    const int D = A.C.D, KLD = attn_key_ld(D);
-    float *const Qs = sm;                        // [MT][D], times scale log2 e
-    float *const Ks = Qs + MT * D;               // [64][D + 4]
-    float *const Vs = Ks + kAttnTile * KLD;      // [64][D]
-    float *const Ss = Vs + kAttnTile * D;        // [MT][68] scores, then probabilities
-    float *const m_s = Ss + MT * SLD, *const l_s = m_s + MT, *const a_s = l_s + MT;
+    const int D = A.C.D, KLD = D + kPiece;
+    IO *const Ks = reinterpret_cast<IO *>(smem);                              // [2][32][D + 16 bytes]
+    IO *const Vs = Ks + 2 * kAttnTile * KLD;                                  // [2][32][D]
+    float *const Qs = reinterpret_cast<float *>(Vs + 2 * kAttnTile * D);      // [MT][D], times scale log2 e
+    float *const Ps = Qs + MT * D;                                            // [MT][36]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rg = tid >> 6, c64 = tid & 63;     // rows rg * RPT .., key or column c64
     const int group = blockIdx.x / A.NQT, qt = blockIdx.x - group * A.NQT;
+    float *const my_p = Ps + warp * RPT * PLD;
+    const float *const my_q = Qs + warp * RPT * D;
+    grid_dep_wait();
 
     attn_dead_rows<IO>(A, blockIdx.x, gridDim.x, kAttnThreads);
     const AttnPlan plan = attn_plan<kAttnThreads>(A, group, blockIdx.x == 0, scratch);
@@ -73,142 +75,140 @@ __global__ void __launch_bounds__(kAttnThreads) tree_attn_kernel(const __grid_co
     for (; any; any = walk.next(A, &pc)) {
         const int live = min(MT, pc.cnt * A.G - qt * MT);   // rows of this query tile
         if (live <= 0) continue;
-        const int kv = pc.len + pc.cnt, D8 = D >> 3;
+        const int kv = pc.len + pc.cnt, pieces = D / kPiece;
+        // four threads copy a token's key and value
+        const auto fetch = [&](int t, int buf) {
+            const int r = tid >> 2, tok = t * kAttnTile + r;
+            int64_t row = -1;
+            if (tok < kv) {
+                row = kv_token_row(A.C, pc.slot, tok);
+                if (row < 0) atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+            }
+            const bool there = row >= 0;   // rows past the end are zeros, whatever the page holds there
+            const int64_t e = there ? kv_elem(A.C, A.layer, pc.h, row) : 0;
+            const IO *k = static_cast<const IO *>(A.C.k) + e, *v = static_cast<const IO *>(A.C.v) + e;
+            IO *kd = Ks + (buf * kAttnTile + r) * KLD, *vd = Vs + (buf * kAttnTile + r) * D;
+            for (int c = tid & 3; c < pieces; c += 4) {
+                copy16(kd + c * kPiece, k + c * kPiece, there);
+                copy16(vd + c * kPiece, v + c * kPiece, there);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
         __syncthreads();   // the piece before is done with shared memory
-        for (int i = tid; i < MT * D8; i += kAttnThreads) {
-            const int r = i / D8, c = (i - r * D8) * 8;
-            float x[8] = {};
+        fetch(pc.t0, 0);
+        for (int i = tid; i < MT * D / 4; i += kAttnThreads) {
+            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < live) {
-                load8<IO>(static_cast<const IO *>(A.q) + attn_out_row(A, pc.b, pc.h, qt * MT + r) * D + c, x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= A.scale_log2;
+                x = load4<IO>(static_cast<const IO *>(A.q) + attn_out_row(A, pc.b, pc.h, qt * MT + r) * D + c);
+                x.x *= A.scale_log2, x.y *= A.scale_log2, x.z *= A.scale_log2, x.w *= A.scale_log2;
             }
-            store8(Qs + r * D + c, x);
+            *reinterpret_cast<float4 *>(Qs + r * D + c) = x;
         }
-        if (tid < MT) {
-            m_s[tid] = -INFINITY;
-            l_s[tid] = 0.0f;
+        uint64_t mask[RPT];
+        float m[RPT], l[RPT];   // l: this lane's keys only, until the end
+        float acc[RPT][NG * VEC] = {};
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const int r = warp * RPT + i;
+            mask[i] = r < live ? attn_mask(A, pc.b, (qt * MT + r) / A.G) : 0;
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
         }
-        float acc[RPT][COLS] = {};
         for (int t = pc.t0; t < pc.t1; ++t) {
-            const int k0 = t * kAttnTile, n = min(kAttnTile, kv - k0);
-            __syncthreads();
-            for (int i = tid; i < kAttnTile * D8; i += kAttnThreads) {
-                const int r = i / D8, c = (i - r * D8) * 8;
-                float kx[8] = {}, vx[8] = {};
-                if (r < n) {   // rows past the end are zeros, whatever the page holds there
-                    const int64_t row = kv_token_row(A.C, pc.slot, k0 + r);
-                    if (row >= 0) {
-                        const int64_t e = kv_elem(A.C, A.layer, pc.h, row) + c;
-                        load8<IO>(static_cast<const IO *>(A.C.k) + e, kx);
-                        load8<IO>(static_cast<const IO *>(A.C.v) + e, vx);
-                    } else if (c == 0) {
-                        atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
-                    }
-                }
-                store8(Ks + r * KLD + c, kx);
-                store8(Vs + r * D + c, vx);
+            const int buf = (t - pc.t0) & 1, k0 = t * kAttnTile;
+            if (t + 1 < pc.t1) {
+                fetch(t + 1, buf ^ 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             __syncthreads();
-            {   // scores of key c64
-                float s[RPT] = {};
-                const float *kp = Ks + c64 * KLD, *qp = Qs + rg * RPT * D;
-                for (int d = 0; d < D; d += 4) {
-                    const float4 kx = *reinterpret_cast<const float4 *>(kp + d);
-#pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const float4 qx = *reinterpret_cast<const float4 *>(qp + i * D + d);
-                        s[i] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, s[i]))));
-                    }
-                }
-                const int node = k0 + c64 - pc.len;
+            const IO *kp = Ks + (buf * kAttnTile + lane) * KLD, *vp = Vs + buf * kAttnTile * D;
+            float s[RPT] = {};
+#pragma unroll 2
+            for (int d = 0; d < D; d += 4) {
+                const float4 kx = load4<IO>(kp + d);
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    const int r = rg * RPT + i;
-                    bool seen = c64 < n && r < live;
-                    if (seen && node >= 0) seen = (attn_mask(A, pc.b, (qt * MT + r) / A.G) >> node) & 1;
-                    Ss[r * SLD + c64] = seen ? s[i] : -INFINITY;
+                    const float4 qx = *reinterpret_cast<const float4 *>(my_q + i * D + d);
+                    s[i] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, s[i]))));
                 }
             }
-            __syncthreads();
-            for (int r = warp; r < MT; r += kAttnThreads / 32) {
-                float *sp = Ss + r * SLD;
-                const float x0 = sp[lane], x1 = sp[lane + 32], m = m_s[r];
-                float mx = fmaxf(x0, x1);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.0f : mn;
-                const float p0 = exp2f(x0 - base), p1 = exp2f(x1 - base);
-                const float sum = warp_sum(p0 + p1), al = exp2f(m - base);
-                sp[lane] = p0;
-                sp[lane + 32] = p1;
-                if (lane == 0) {
-                    m_s[r] = mn;
-                    l_s[r] = l_s[r] * al + sum;
-                    a_s[r] = al;
-                }
-            }
-            __syncthreads();
+            const int node = k0 + lane - pc.len;   // < 0: committed
+            const bool drafts = k0 + kAttnTile > pc.len;
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
-                const float al = a_s[rg * RPT + i];
+                float x = s[i];
+                if (drafts && !(k0 + lane < kv && (node < 0 || ((mask[i] >> node) & 1)))) x = -INFINITY;
+                float top = x;
 #pragma unroll
-                for (int j = 0; j < COLS; ++j) acc[i][j] *= al;
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float mn = fmaxf(m[i], top), base = mn == -INFINITY ? 0.0f : mn;
+                const float p = exp2f(x - base);
+                if (mn > m[i]) {   // the same in all lanes
+                    const float al = exp2f(m[i] - base);
+                    l[i] *= al;
+#pragma unroll
+                    for (int j = 0; j < NG * VEC; ++j) acc[i][j] *= al;
+                    m[i] = mn;
+                }
+                l[i] += p;
+                my_p[i * PLD + lane] = p;
             }
-            // A tile that holds drafted tokens leaves masked ones out by a test, so that an infinity or
-            // NaN there stays without effect; committed tokens are seen by every row.
-            const bool drafts = k0 + n > pc.len;
-            for (int c = 0; c < kAttnTile; c += 4) {
+            __syncwarp();
+            // A tile that holds drafted tokens leaves masked ones out by a test, so that an infinity or NaN there stays
+            // without effect; committed tokens are seen by every row.
+#pragma unroll 1
+            for (int k = 0; k < kAttnTile; k += 4) {
                 float4 p[RPT];
 #pragma unroll
-                for (int i = 0; i < RPT; ++i) p[i] = *reinterpret_cast<const float4 *>(Ss + (rg * RPT + i) * SLD + c);
+                for (int i = 0; i < RPT; ++i) p[i] = *reinterpret_cast<const float4 *>(my_p + i * PLD + k);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float v[COLS];
+                    float v[NG * VEC];
 #pragma unroll
-                    for (int j = 0; j < COLS; ++j) {
-                        const int d = c64 + 64 * j;
-                        v[j] = d < D ? Vs[(c + e) * D + d] : 0.0f;
+                    for (int g = 0; g < NG; ++g) {
+                        const int d = (g * 32 + lane) * VEC;
+                        if (VEC == 4) {
+                            const float4 x = d < D ? load4<IO>(vp + (k + e) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            v[g * VEC] = x.x, v[g * VEC + 1] = x.y, v[g * VEC + 2] = x.z, v[g * VEC + 3] = x.w;
+                        } else {
+                            const float2 x = d < D ? load2<IO>(vp + (k + e) * D + d) : make_float2(0.f, 0.f);
+                            v[g * VEC] = x.x, v[g * VEC + 1] = x.y;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < RPT; ++i) {
                         const float x = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-                        if (drafts) {
-                            if (x != 0.0f)
+                        if (!drafts || x != 0.0f) {
 #pragma unroll
-                                for (int j = 0; j < COLS; ++j) acc[i][j] = fmaf(x, v[j], acc[i][j]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < COLS; ++j) acc[i][j] = fmaf(x, v[j], acc[i][j]);
+                            for (int j = 0; j < NG * VEC; ++j) acc[i][j] = fmaf(x, v[j], acc[i][j]);
                         }
                     }
                 }
             }
+            __syncthreads();   // the buffer may be filled again
         }
-        // l_s and m_s were written before the barrier in front of the last sums
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            const int r = rg * RPT + i;
+            const int r = warp * RPT + i;
+            const float sum = warp_sum(l[i]);
             if (r >= live) continue;
-            const float l = l_s[r];
-            if (pc.whole()) {
-                const int64_t row = attn_out_row(A, pc.b, pc.h, qt * MT + r);
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int64_t row = attn_out_row(A, pc.b, pc.h, qt * MT + r), part = (int64_t)blockIdx.x * 2 + pc.side;
+            const float inv = pc.whole() ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+            IO *out = static_cast<IO *>(A.out) + row * D;
+            float *po = reinterpret_cast<float *>(A.part_o) + part * MT * D;
 #pragma unroll
-                for (int j = 0; j < COLS; ++j) {
-                    const int d = c64 + 64 * j;
-                    if (d < D) static_cast<IO *>(A.out)[row * D + d] = from_f32<IO>(acc[i][j] * inv);
-                }
-                if (A.lse && c64 == 0) A.lse[row] = attn_lse(m_s[r], l);
-            } else {
-                const int64_t part = (int64_t)blockIdx.x * 2 + pc.side;
-                float *po = reinterpret_cast<float *>(A.part_o) + part * MT * D;
-#pragma unroll
-                for (int j = 0; j < COLS; ++j) {
-                    const int d = c64 + 64 * j;
-                    if (d < D) po[((d >> 2) * MT + r) * 4 + (d & 3)] = acc[i][j];
-                }
-                if (c64 == 0) A.part_ml[part * MT + r] = make_float2(m_s[r], l);
+            for (int j = 0; j < NG * VEC; ++j) {
+                const int d = (j / VEC * 32 + lane) * VEC + j % VEC;
+                if (d >= D) continue;
+                if (pc.whole()) out[d] = from_f32<IO>(acc[i][j] * inv);
+                else po[((d >> 2) * MT + r) * 4 + (d & 3)] = acc[i][j];
+            }
+            if (lane == 0) {
+                if (!pc.whole()) A.part_ml[part * MT + r] = make_float2(m[i], sum);
+                else if (A.lse) A.lse[row] = attn_lse(m[i], sum);
             }
         }
     }
@@ -313,28 +313,24 @@ cudaError_t launch_attn_join(const AttnArgs &A, bool bf16, cudaStream_t stream) 
 
 // ------------------------------------------------------------------ launch
 
-// Rows of a block's query tile: the fewest that hold the window, at most 32.
-static int rows_per_thread(int R) { return R <= 4 ? 1 : R <= 8 ? 2 : R <= 16 ? 4 : 8; }
+// Rows of a warp: the fewest that hold the window, at most 8.
+static int rows_per_warp(int R) { return R <= 4 ? 1 : R <= 8 ? 2 : R <= 16 ? 4 : 8; }
 
-template <typename IO, int RPT, int COLS>
+template <typename IO, int RPT, int VEC, int NG>
 static cudaError_t run_tree_attn(const AttnArgs &A, cudaStream_t st) {
     static KernelSetup setup;
-    const size_t smem = tree_attn_smem(A.C.D, 4 * RPT);
+    const size_t smem = tree_attn_smem(A.C.D, 4 * RPT, sizeof(IO));
     int sms;
-    cudaError_t e = kernel_setup(setup, (const void *)tree_attn_kernel<IO, RPT, COLS>, smem, &sms);
+    cudaError_t e = kernel_setup(setup, (const void *)tree_attn_kernel<IO, RPT, VEC, NG>, smem, &sms);
     if (e != cudaSuccess) return e;
-    tree_attn_kernel<IO, RPT, COLS><<<A.groups * A.NQT, kAttnThreads, smem, st>>>(A);
-    return cudaGetLastError();
+    return launch_dependent(tree_attn_kernel<IO, RPT, VEC, NG>, dim3(A.groups * A.NQT), dim3(kAttnThreads), smem, st, A);
 }
 
 template <typename IO, int RPT>
 static cudaError_t run_cols(const AttnArgs &A, cudaStream_t st) {
-    switch ((A.C.D + 63) / 64) {
-        case 1: return run_tree_attn<IO, RPT, 1>(A, st);
-        case 2: return run_tree_attn<IO, RPT, 2>(A, st);
-        case 3: return run_tree_attn<IO, RPT, 3>(A, st);
-        default: return run_tree_attn<IO, RPT, 4>(A, st);
-    }
+    if (A.C.D <= 64) return run_tree_attn<IO, RPT, 2, 1>(A, st);
+    if (A.C.D <= 128) return run_tree_attn<IO, RPT, 4, 1>(A, st);
+    return run_tree_attn<IO, RPT, 4, 2>(A, st);
 }
 
 template <typename IO>
@@ -348,17 +344,17 @@ static cudaError_t run_rows(const AttnArgs &A, cudaStream_t st) {
 }
 
 // The cut of the work on a machine of `sms` SMs (MT, TN, NQT, groups).
-void tree_attn_cut(AttnArgs *A, int sms) {
+void tree_attn_cut(AttnArgs *A, int sms, int es) {
     const int R = A->T * A->G;
     A->TN = kAttnTile;
-    A->MT = 4 * rows_per_thread(R);
+    A->MT = 4 * rows_per_warp(R);
     A->NQT = (R + A->MT - 1) / A->MT;
-    int per_sm = (int)((size_t)(228 * 1024) / (tree_attn_smem(A->C.D, A->MT) + 1024));
+    int per_sm = (int)((size_t)(227 * 1024) / (tree_attn_smem(A->C.D, A->MT, es) + 2048));
     if (per_sm > 4) per_sm = 4;
     if (per_sm < 1) per_sm = 1;
     const int groups = sms * per_sm / A->NQT;
     A->groups = groups < 1 ? 1 : groups;
-    A->min_chunk = 1;
+    A->min_chunk = 2;
 }
 
 cudaError_t launch_tree_attn(const AttnArgs &A, bool bf16, cudaStream_t st) {
