@@ -13,7 +13,7 @@
 // one or four tokens: its threads first form the tokens' cos and sin
 // (rot / 2 pairs a token, shared by all heads) in shared memory, then turn 16
 // elements of one head each (two runs of 8, a pair's halves in the half
-// layout).  Eight blocks an SM cover each other's set-up; loading a thread's next
+// layout).  The SM's other blocks cover a block's set-up; loading a thread's next
 // unit before this one's arithmetic took the registers for that: 146 us against
 // 134 us (8 x 4096 tokens, 32 + 2 x 8 heads of 128, bf16: 0.88 of the copy bandwidth).
 #include "kv_common.cuh"

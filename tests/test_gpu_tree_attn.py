@@ -287,3 +287,34 @@ def test_binding_refuses():
                 lambda: binding.tree_attn(cache, 0, s.cpu(), q)):
         with pytest.raises(binding.GdnSpecError):
             bad()
+
+
+@pytest.mark.parametrize("T,HQ,HKV,D,lens", [(4, 8, 2, 128, [700, 90]), (64, 8, 2, 128, [700, 90]),
+                                             (4, 8, 2, 256, [700, 90]), (33, 8, 1, 64, [5, 3000, 0])])
+def test_a_wait_that_runs_out_is_reported(T, HQ, HKV, D, lens):
+    """With the wait limit at zero the first wait on copied data gives up: the copies in flight
+    are drained, the call returns with TIMEOUT, and the next call is right."""
+    c = Case(12, "bf16", T=T, HQ=HQ, HKV=HKV, D=D, P=32, lens=lens)
+    cache = c.upload()
+    prev = binding.set_wait_limit(0)
+    try:
+        c.call()
+        st = binding.kv_read_status(cache)
+    finally:
+        binding.set_wait_limit(binding.WAIT_LIMIT_DEFAULT)
+    assert prev == 1 << 20 and st == binding.ST_TIMEOUT
+    c.check()
+
+
+def test_the_same_call_gives_the_same_bits():
+    """Forty calls of each layout of streams, other work between them."""
+    other = torch.zeros(1 << 22, device="cuda")
+    for T, HQ, HKV, D, lens in ((2, 8, 2, 128, [3000, 17, 900, 64]), (64, 16, 2, 128, [1500, 130]),
+                                (7, 8, 1, 256, [2000, 333, 1]), (40, 8, 2, 64, [800, 65])):
+        c = Case(13, "bf16", T=T, HQ=HQ, HKV=HKV, D=D, P=64, lens=lens)
+        a, la = c.call()
+        for _ in range(40):
+            other.add_(1.0)
+            b, lb = c.call()
+            assert torch.equal(a, b) and torch.equal(la, lb)
+        assert binding.kv_read_status(c.cache) == 0
