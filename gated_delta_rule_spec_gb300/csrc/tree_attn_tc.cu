@@ -49,7 +49,7 @@
 
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
-#include "ptx_sm100.cuh"
+#include "ptx_attn.cuh"
 
 namespace gdnspec {
 namespace tat {
@@ -163,12 +163,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-
-__device__ __forceinline__ void landed32(uint32_t *r) {
-    ptx::tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
