@@ -172,8 +172,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch._C._cuda_getDevice())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -473,16 +473,17 @@ def kv_init(cache: KvCache, stream=None) -> None:
 
 def _done(done: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
     if done is None:
-        done = torch.empty_like(like)
+        return torch.empty_like(like)
     _need(done, "done", torch.int32, like.shape)
     return done
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
-    if t.dim() != 1:
-        raise GdnSpecError(f"{name}: want one dimension, got {tuple(t.shape)}")
-    _need(t, name, torch.int32, t.shape)
-    return t.shape[0]
+    shape = t.shape
+    if len(shape) != 1:
+        raise GdnSpecError(f"{name}: want one dimension, got {tuple(shape)}")
+    _need(t, name, torch.int32, shape)
+    return shape[0]
 
 
 def kv_reserve(cache: KvCache, slot_idx: torch.Tensor, T: int, n_tokens: torch.Tensor | None = None,
@@ -615,8 +616,9 @@ def rope(plan: RopePlan, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor |
     _need(pos, "pos", torch.int32, (N,))
     xs = _token_stride(x, "x", x.dtype, (N, heads, D))
     if out is None:
-        out = torch.empty((N, heads, D), dtype=x.dtype, device=x.device)
-    os_ = _token_stride(out, "out", x.dtype, (N, heads, D))
+        out, os_ = torch.empty((N, heads, D), dtype=x.dtype, device=x.device), heads * D
+    else:
+        os_ = _token_stride(out, "out", x.dtype, (N, heads, D))
     code = DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_FP32
     rc = load().gdn_spec_rope(plan._ref, N, heads, code, _ptr(pos), _ptr(x), xs, _ptr(out), os_,
                               int(bool(transpose)), _stream(stream))
@@ -631,19 +633,21 @@ def rope_append(plan: RopePlan, cache: KvCache, layer: int, slot_idx: torch.Tens
     behind the slots' committed tokens in ``layer`` of the cache.  q, k, v may be
     slices of one projection's output."""
     B = _rows(slot_idx, "slot_idx")
-    if q.dim() != 4 or k.dim() != 4:
-        raise GdnSpecError(f"q, k: want [B, T, heads, D], got {tuple(q.shape)} and {tuple(k.shape)}")
-    T, HQ, io = q.shape[1], q.shape[2], cache.io_torch
+    if q.dim() != 4:
+        raise GdnSpecError(f"q: want [B, T, heads, D], got {tuple(q.shape)}")
+    _, T, HQ, _ = q.shape
+    io, kv_shape = cache.io_torch, (B, T, cache.HKV, cache.D)
     qs = _token_stride(q, "q", io, (B, T, HQ, cache.D))
-    ks = _token_stride(k, "k", io, (B, T, cache.HKV, cache.D))
-    vs = _token_stride(v, "v", io, (B, T, cache.HKV, cache.D))
+    ks = _token_stride(k, "k", io, kv_shape)
+    vs = _token_stride(v, "v", io, kv_shape)
     if pos is not None:
         _need(pos, "pos", torch.int32, (B, T))
     if n_tokens is not None:
         _need(n_tokens, "n_tokens", torch.int32, (B,))
     if q_out is None:
         q_out = torch.empty((B, T, HQ, cache.D), dtype=io, device=q.device)
-    _need(q_out, "q_out", io, (B, T, HQ, cache.D))
+    else:
+        _need(q_out, "q_out", io, (B, T, HQ, cache.D))
     rc = load().gdn_spec_rope_append(plan._ref, cache._ref, layer, _ptr(slot_idx), B, T,
                                      _ptr(n_tokens), _ptr(pos), HQ, _ptr(q), qs, _ptr(k), ks,
                                      _ptr(v), vs, _ptr(q_out), _stream(stream))
@@ -679,7 +683,7 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
     B = _rows(slot_idx, "slot_idx")
     if q.dim() != 4:
         raise GdnSpecError(f"q: want [B, T, HQ, D], got {tuple(q.shape)}")
-    T, HQ = q.shape[1], q.shape[2]
+    _, T, HQ, _ = q.shape
     _need(q, "q", cache.io_torch, (B, T, HQ, cache.D))
     if tree_mask is not None:
         _need(tree_mask, "tree_mask", torch.int64, (B, T))
@@ -687,13 +691,15 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
         _need(tree_len, "tree_len", torch.int32, (B,))
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", cache.io_torch, (B, T, HQ, cache.D))
+    else:
+        _need(out, "out", cache.io_torch, (B, T, HQ, cache.D))
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, T, HQ))
     if workspace is None:
         workspace = torch.empty(max(16, tree_attn_workspace(cache, B, T, HQ)), dtype=torch.uint8,
                                 device=q.device)
-    _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    else:
+        _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
     rc = load().gdn_spec_tree_attn(cache._ref, layer, _ptr(slot_idx), B, T, HQ, _ptr(q),
                                    _ptr(tree_mask), _ptr(tree_len),
                                    cache.D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
