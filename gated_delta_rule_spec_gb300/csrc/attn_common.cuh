@@ -222,18 +222,18 @@ __device__ __forceinline__ int64_t attn_out_row(const AttnArgs &A, int b, int h,
 }
 
 // Rows that nothing computes (tokens past cnt, rows that were refused): zeros, and
-// an lse of -inf.  By all threads, batch row b of the launch's blocks in turn.
+// an lse of -inf.  By `threads` threads of each block, the batch rows in turn.
 template <typename IO>
-__device__ __forceinline__ void attn_dead_rows(const AttnArgs &A, int block, int blocks, int threads) {
+__device__ __forceinline__ void attn_dead_rows(const AttnArgs &A, int block, int blocks, int thread, int threads) {
     for (int b = block; b < A.B; b += blocks) {
         uint32_t bits;
         const AttnRow r = attn_row(A, b, &bits);
         const int64_t row0 = ((int64_t)b * A.T + r.cnt) * A.HQ, rows = (int64_t)(A.T - r.cnt) * A.HQ;
         float4 *o = reinterpret_cast<float4 *>(static_cast<IO *>(A.out) + row0 * A.C.D);
         const int64_t n = rows * A.C.D * sizeof(IO) / 16;
-        for (int64_t i = threadIdx.x; i < n; i += threads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int64_t i = thread; i < n; i += threads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (A.lse)
-            for (int64_t i = threadIdx.x; i < rows; i += threads) A.lse[row0 + i] = -INFINITY;
+            for (int64_t i = thread; i < rows; i += threads) A.lse[row0 + i] = -INFINITY;
     }
 }
 

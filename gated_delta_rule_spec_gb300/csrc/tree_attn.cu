@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kAttnThreads, RPT == 8 ? 2 : 4) tree_attn_kern
     const float *const my_q = Qs + warp * RPT * D;
     grid_dep_wait();
 
-    attn_dead_rows<IO>(A, blockIdx.x, gridDim.x, kAttnThreads);
+    attn_dead_rows<IO>(A, blockIdx.x, gridDim.x, tid, kAttnThreads);
     const AttnPlan plan = attn_plan<kAttnThreads>(A, group, blockIdx.x == 0, scratch);
     AttnWalk walk = attn_walk(A, plan, group);
     AttnPiece pc;

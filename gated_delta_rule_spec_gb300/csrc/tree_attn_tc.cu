@@ -663,9 +663,27 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
             const int d_begin = L::kTurns ? w * kDims : 0;
             const int64_t part = (int64_t)blockIdx.x * 2 + pc.side;
             const bool whole = pc.whole();
+            // a piece to be joined is kept as it is (a lane with a draft that is not finite takes the long way)
+            const bool kept = !L::kTurns && !whole && !__any_sync(0xffffffffu, bad != 0);
+            if (kept) {
+#pragma unroll 1
+                for (int x = 0; x < kDims && x < A.C.D; x += 64) {
+                    uint32_t u[64];
+                    ptx::tmem_ld32_bits(lane_addr + L::col_o(w) + x, u);
+                    ptx::tmem_ld32_bits(lane_addr + L::col_o(w) + x + 32, u + 32);
+                    landed(u);
+                    float4 *po = A.part_o + (part * (A.C.D / 4) + x / 4) * A.MT + my_row;
+#pragma unroll
+                    for (int y = 0; y < 64; y += 4)
+                        if (on && x + y < A.C.D)
+                            po[(int64_t)(y / 4) * A.MT] =
+                                make_float4(__uint_as_float(u[y]), __uint_as_float(u[y + 1]), __uint_as_float(u[y + 2]),
+                                            __uint_as_float(u[y + 3]));
+                }
+            }
             constexpr int kBatch = 32;   // a short body: it is fetched anew for every piece
 #pragma unroll 1
-            for (int x = 0; x < kDims && d_begin + x < A.C.D; x += kBatch) {
+            for (int x = kept ? kDims : 0; x < kDims && d_begin + x < A.C.D; x += kBatch) {
                 const int d0 = d_begin + x, dims = min(kBatch, A.C.D - d0);
                 uint32_t u[kBatch], v[L::kTurns ? kBatch : 1];
 #pragma unroll
@@ -769,7 +787,6 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     }
     if (warp == 0) ptx::tmem_alloc(ptx::smem_addr(&ms->tmem), kTmemCols);
     grid_dep_wait();   // nothing in global memory was touched so far
-    attn_dead_rows<__nv_bfloat16>(A, blockIdx.x, gridDim.x, L::kThreads);
     const AttnPlan plan = attn_plan<L::kThreads>(A, group, blockIdx.x == 0, ms->scratch);
     ptx::tc_fence_before_sync();
     __syncthreads();
@@ -777,6 +794,8 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     const uint32_t tmem = ms->tmem;
 
     if (warp < L::NWG * 4) {
+        // while the first tile is on its way
+        attn_dead_rows<__nv_bfloat16>(A, blockIdx.x, gridDim.x, tid, L::NWG * 128);
         soften<D, NQ>(A, ms, sm, tmem, plan, group, qt, tid);
     } else {
         const int role = warp - L::NWG * 4;
