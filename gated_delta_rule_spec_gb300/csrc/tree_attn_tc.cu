@@ -95,7 +95,7 @@ struct Lay {
 struct Misc {
     uint64_t full[kMaxStages], empty[kMaxStages], q_full[2], q_empty[2];
     uint64_t s_full[4], p_full[4], pv_done[4];   // by stream and buffer of S
-    uint64_t o_full, o_empty, drain[3], clean[2];
+    uint64_t o_full, o_empty, drain[3];
     float2 ml[2][kRows];                  // (m, l) of the two streams' rows, exchanged when they are merged
     unsigned long long bad[3];            // drafts whose values are not finite, by piece modulo 3
     int scratch[kAttnScratch];
@@ -234,7 +234,6 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
         const int units = (n + L::kUnit - 1) / L::kUnit;
         const auto copy = [&](const CUtensorMap *map, auto ring_c, int u) {   // unit u of the piece
             constexpr int ring = decltype(ring_c)::value;
-            constexpr bool rows128 = !ring && L::kShare;   // a block of 64 dims as 128 rows; all else tile by tile
             const uint32_t st = L::first(ring) + place[ring].at;
             const int tok = (pc.t0 + u * L::kUnit) * kTile;
             const int live = min(min(L::kUnit, n - u * L::kUnit) * kTile, kv - tok), boxes = (live + BR - 1) / BR;
@@ -258,7 +257,7 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
             for (int c = 0; c < kMost; ++c) rows[c] = __shfl_sync(0xffffffffu, row, c);
             if (ptx::elect_one()) {
                 ptx::mbar_expect_tx(bar, BR * 128u * L::kBlocks * boxes);
-                if (!rows128 && A.whole) {   // all of a tile's blocks by one copy
+                if (A.whole) {   // all of a tile's blocks by one copy
 #pragma unroll
                     for (int c = 0; c < L::kUnit; ++c)
                         if (c < boxes) ptx::tma_load_3d(dst + c * L::kBlocks * L::kBlock, map, bar, 0, rows[c], 0);
@@ -267,11 +266,10 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
                     for (int c = 0; c < kMost; ++c) {
                         if (c >= boxes) break;
                         const int at = c * BR;   // row of the unit
-                        const uint32_t to = rows128 ? dst + at * 128u
-                                                    : dst + (at / kTile) * L::kBlocks * L::kBlock + (at % kTile) * 128u;
+                        const uint32_t to = dst + (at / kTile) * L::kBlocks * L::kBlock + (at % kTile) * 128u;
 #pragma unroll
                         for (int blk = 0; blk < (int)L::kBlocks; ++blk)
-                            ptx::tma_load_3d(to + blk * (rows128 ? L::kUnit : 1) * L::kBlock, map, bar, blk * 64, rows[c], 0);
+                            ptx::tma_load_3d(to + blk * L::kBlock, map, bar, blk * 64, rows[c], 0);
                     }
                 }
             }
@@ -340,16 +338,15 @@ __device__ __forceinline__ void drain(Misc *ms, int who) {
     ptx::mbar_wait(ptx::smem_addr(&ms->drain[who]), 0);
 }
 
-// The first products, S = Q K^T, of all streams.  What an MMA needs is made uniform
-// before the wait that it hangs on, so that only the issue is behind it.
+// The first products, S = Q K^T: of stream w where the streams share tiles (an issue
+// blocks while the tensor core is busy, and one warp for both streams left it idle
+// during its waits), else of all streams.  What an MMA needs is made uniform before
+// the wait that it hangs on, so that only the issue is behind it.
 template <int D, int NQ>
 __device__ __forceinline__ void multiply_scores(const AttnArgs &A, Misc *ms, uint32_t base, uint32_t tmem,
-                                                const AttnPlan &plan, int group, int qt) {
+                                                const AttnPlan &plan, int group, int qt, int w) {
     using L = Lay<D, NQ>;
-    // An MMA of 128 x 64 takes as long as one of 128 x 128 (the query rows' traffic from shared memory): where the
-    // products are the bound, with shared tiles, one forms the scores of both tiles of a unit.
-    constexpr int kN = L::kShare ? L::kUnit : 1;   // tiles of a product
-    constexpr uint32_t idesc = ptx::idesc_bf16(kRows, kN * kTile);
+    constexpr uint32_t idesc = ptx::idesc_bf16(kRows, kTile);
     const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
     uint32_t q_used = 0, used_any = 0, used_ph = 0;   // bit of an S buffer: whether it was used, parity of its uses
     Place key;
@@ -357,12 +354,12 @@ __device__ __forceinline__ void multiply_scores(const AttnArgs &A, Misc *ms, uin
     AttnWalk walk = attn_walk(A, plan, group);
     AttnPiece pc;
     bool any = walk.next(A, &pc);
-    if (qt == 0 && ptx::elect_one()) attn_note(A, group, any, pc, plan.chunk);
+    if (qt == 0 && w == 0 && ptx::elect_one()) attn_note(A, group, any, pc, plan.chunk);
     __syncwarp();
     for (; ok && any; any = walk.next(A, &pc)) {
         if (pc.cnt * A.G - qt * A.MT <= 0) continue;
         const int n = pc.t1 - pc.t0;
-        const uint32_t qb = q_used % L::QB, q_addr = base + qb * NQ * L::kQTile;
+        const uint32_t qb = q_used % L::QB, q_addr = base + (qb * NQ + (L::kShare ? w : 0)) * L::kQTile;
         ok = wait(bar(ms->q_full[qb]), (q_used / L::QB) & 1u, &ms->abort, A.wait_limit);
         for (int i = 0; ok && i < n; i += L::kUnit) {
             const uint32_t keys = uniform(base + L::kOffKV + key.at * L::kStage);
@@ -370,21 +367,16 @@ __device__ __forceinline__ void multiply_scores(const AttnArgs &A, Misc *ms, uin
             ok = wait(bar(ms->full[key.at]), key.ph, &ms->abort, A.wait_limit);
             key.step(L::NK);
 #pragma unroll
-            for (int s = 0; s < L::kUnit / kN * NQ; ++s) {   // the unit's products
-                const int w = L::kTurns ? (i >> 1) & 1 : L::kShare ? s : 0;   // stream
-                const int t = L::kTurns ? s : 0;                              // tile of the unit
-                const int x = 2 * w + (L::kTurns ? s : L::kShare ? 0 : i & 1);   // (first) S buffer
-                const bool here = i + t < n, two = kN == 2 && i + 1 < n;
-                const bool last = i + L::kUnit >= n && (L::kTurns ? s == 1 : s == NQ - 1);
-                const uint64_t a = ptx::smem_desc_sw128(uniform(q_addr + (L::kShare ? s : 0) * L::kQTile));
+            for (int t = 0; t < L::kUnit; ++t) {   // the unit's tiles
+                const int stream = L::kTurns ? (i >> 1) & 1 : w;
+                const int x = 2 * stream + (L::kUnit == 2 ? t : i & 1);   // S buffer
+                const bool here = i + t < n, last = i + L::kUnit >= n;
+                const uint64_t a = ptx::smem_desc_sw128(uniform(q_addr));
                 const uint64_t b = ptx::smem_desc_sw128(keys + t * L::kBlocks * L::kBlock);
-                const uint32_t d = uniform(tmem + x * kTile);
-                const uint32_t done = uniform(bar(ms->s_full[x])), done2 = uniform(bar(ms->s_full[x | 1]));
-                // a buffer is free once the sums that read its last P are done
-#pragma unroll
-                for (int y = 0; y < kN; ++y)
-                    if (ok && here && ((used_any >> (x + y)) & 1u))
-                        ok = wait(bar(ms->pv_done[x + y]), ((used_ph >> (x + y)) & 1u) ^ 1u, &ms->abort);
+                const uint32_t d = uniform(tmem + x * kTile), done = uniform(bar(ms->s_full[x]));
+                // the buffer is free once the sums that read its last P are done
+                if (ok && here && ((used_any >> x) & 1u))
+                    ok = wait(bar(ms->pv_done[x]), ((used_ph >> x) & 1u) ^ 1u, &ms->abort);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 if (ptx::elect_one()) {
@@ -392,34 +384,35 @@ __device__ __forceinline__ void multiply_scores(const AttnArgs &A, Misc *ms, uin
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)   // descriptors count in 16 bytes
                             ptx::mma_bf16(d, a + ((ks >> 2) * (kRows * 128u) + (ks & 3) * 32u) / 16,
-                                          b + ((ks >> 2) * kN * L::kBlock + (ks & 3) * 32u) / 16, idesc, ks != 0);
+                                          b + ((ks >> 2) * L::kBlock + (ks & 3) * 32u) / 16, idesc, ks != 0);
                         ptx::mma_commit(done);
-                        if (two) ptx::mma_commit(done2);
                     }
-                    if (s == L::kUnit / kN * NQ - 1) ptx::mma_commit(empty);
-                    if (last) ptx::mma_commit(q_done);
+                    if (t == L::kUnit - 1) {
+                        ptx::mma_commit(empty);
+                        if (last) ptx::mma_commit(q_done);
+                    }
                 }
                 __syncwarp();
-                const uint32_t taken = here ? (two ? 3u : 1u) << x : 0u;
-                used_any |= taken;
-                used_ph ^= taken;
+                if (here) {
+                    used_any |= 1u << x;
+                    used_ph ^= 1u << x;
+                }
             }
         }
         ++q_used;
     }
-    if (!ok) drain(ms, 2);
+    if (!ok) drain(ms, w);
 }
 
-// The second products, O += P V, of stream w.
+// The second products, O += P V, of stream w, or of both where they share tiles.
 template <int D, int NQ>
 __device__ __forceinline__ void multiply_sums(const AttnArgs &A, Misc *ms, uint32_t base, uint32_t tmem,
                                               const AttnPlan &plan, int group, int qt, int w) {
     using L = Lay<D, NQ>;
     constexpr uint32_t idesc = ptx::idesc_bf16(kRows, D) | ptx::kIdescBMn;
     const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
-    const uint32_t d = uniform(tmem + L::col_o(w));
     const int first = L::first(L::ring_of(w));
-    uint32_t pieces = 0, p_ph = 0, c_ph = 0;   // bit of a buffer or barrier: parity of the waits done on it
+    uint32_t pieces = 0, p_ph = 0;   // bit of a buffer: parity of the waits done on p_full
     Place val;
     bool ok = true;
     AttnWalk walk = attn_walk(A, plan, group);
@@ -430,40 +423,38 @@ __device__ __forceinline__ void multiply_sums(const AttnArgs &A, Misc *ms, uint3
         const auto o_free = [&] { return wait(bar(ms->o_empty), (pieces & 1u) ^ 1u, &ms->abort); };
         if (mine == 0) ok = o_free();   // every phase is waited for
         for (int j = 0; ok && j < mine; ++j) {
-            const int x = 2 * w + (j & 1), st = first + val.at;
+            const int st = first + val.at;
             const int half = j & (L::kUnit - 1);   // tile of the unit
             const bool end = half == L::kUnit - 1 || j == mine - 1;
             const uint64_t b = ptx::smem_desc_sw128_mn(
                 uniform(base + L::kOffKV + st * L::kStage + half * L::kBlocks * L::kBlock), L::kBlock);
-            const uint32_t p = uniform(tmem + x * kTile), keep = uniform(j > 0);
-            const uint32_t empty = uniform(bar(ms->empty[st])), done = uniform(bar(ms->pv_done[x]));
+            const uint32_t keep = uniform(j > 0), empty = uniform(bar(ms->empty[st]));
             if (half == 0) ok = wait(bar(ms->full[st]), val.ph, &ms->abort, A.wait_limit) && (j || o_free());
             if (end) val.step(L::NV);
-            if (L::kShare && w == 1) {
-                // a shared tile with drafts is cleaned by the first warpgroup: the window lies in at most two tiles
-                const int c = pc.t0 + j - pc.len / kTile;
-                if (c >= 0) {
-                    ok = ok && wait(bar(ms->clean[c]), (c_ph >> c) & 1u, &ms->abort);
-                    c_ph ^= 1u << c;
-                }
-            }
-            ok = ok && wait(bar(ms->p_full[x]), (p_ph >> (j & 1)) & 1u, &ms->abort);
-            p_ph ^= 1u << (j & 1);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            if (ptx::elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                    ptx::mma_bf16_tmem_a(d, p + ks * 8, b + ks * 2048u / 16, idesc, ks != 0 ? 1u : keep);
-                ptx::mma_commit(done);
-                if (end) ptx::mma_commit(empty);
+            for (int s = 0; s < NQ; ++s) {
+                const int stream = L::kShare ? s : w, x = 2 * stream + (j & 1);
+                const uint32_t d = uniform(tmem + L::col_o(stream)), p = uniform(tmem + x * kTile);
+                const uint32_t done = uniform(bar(ms->pv_done[x]));
+                // (a shared tile with drafts is cleaned by the first warpgroup before it hands its P on)
+                ok = ok && wait(bar(ms->p_full[x]), (p_ph >> x) & 1u, &ms->abort);
+                p_ph ^= 1u << x;
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        ptx::mma_bf16_tmem_a(d, p + ks * 8, b + ks * 2048u / 16, idesc, ks != 0 ? 1u : keep);
+                    ptx::mma_commit(done);
+                    if (end && s == NQ - 1) ptx::mma_commit(empty);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         if (ok) commit(bar(ms->o_full));
         ++pieces;
     }
-    if (!ok) drain(ms, w);
+    if (!ok) drain(ms, 1 + w + (L::kShare ? 1 : 0));
 }
 
 // ------------------------------------------------------------------ softmax
@@ -630,10 +621,6 @@ __device__ __forceinline__ void soften(const AttnArgs &A, Misc *ms, uint8_t *sm,
                 ok = ok && wait(bar(ms->full[st]), (pos / L::NV) & 1u, &ms->abort);
                 clean_values<D, NQ>(sm + L::kOffKV + st * L::kStage + (j & (L::kUnit - 1)) * L::kBlocks * L::kBlock, k0,
                                     pc.len, kv, tid, &ms->bad[pieces % 3]);
-                if (L::kShare) {
-                    __syncwarp();
-                    if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->clean[tile - pc.len / kTile]));
-                }
             }
             ptx::tc_fence_before_sync();
             __syncwarp();
@@ -763,20 +750,19 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         const auto init = [](uint64_t &b, uint32_t n) { ptx::mbar_init(ptx::smem_addr(&b), n); };
         for (int i = 0; i < L::NST; ++i) {
             init(ms->full[i], 1);
-            init(ms->empty[i], i < L::NK ? 1 : NQ);   // streams that use the values
+            init(ms->empty[i], i < L::NK ? NQ : 1);   // warps that use the stage
         }
         for (int i = 0; i < 2; ++i) {
             init(ms->q_full[i], 1);
-            init(ms->q_empty[i], 1);
+            init(ms->q_empty[i], NQ);
         }
         for (int i = 0; i < 4; ++i) {
             init(ms->s_full[i], 1);
             init(ms->p_full[i], 4);
             init(ms->pv_done[i], 1);
         }
-        init(ms->o_full, L::NWG);
+        init(ms->o_full, L::kTurns ? 2 : 1);
         init(ms->o_empty, L::NWG * 4);
-        for (int i = 0; i < 2; ++i) init(ms->clean[i], 4);
         for (int i = 0; i < 3; ++i) init(ms->drain[i], 1);
         ms->bad[0] = ms->bad[1] = ms->bad[2] = 0;
         ms->abort = 0;
@@ -800,8 +786,8 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     } else {
         const int role = warp - L::NWG * 4;
         if (role == 0) produce<D, NQ>(A, &mq, &mk, &mv, ms, base, plan, group, qt);
-        else if (role == 1) multiply_scores<D, NQ>(A, ms, base, tmem, plan, group, qt);
-        else if (role < 2 + L::NWG) multiply_sums<D, NQ>(A, ms, base, tmem, plan, group, qt, role - 2);
+        else if (role <= NQ) multiply_scores<D, NQ>(A, ms, base, tmem, plan, group, qt, role - 1);
+        else if (role <= NQ + (L::kTurns ? 2 : 1)) multiply_sums<D, NQ>(A, ms, base, tmem, plan, group, qt, role - NQ - 1);
         __syncwarp();
     }
     ptx::tc_fence_before_sync();
@@ -861,15 +847,13 @@ cudaError_t run(const AttnArgs &A, cudaStream_t st) {
     // with zeros.
     const cuuint64_t dims = A.C.D;
     const cuuint64_t kv_dims[3] = {A.whole ? 64 : dims, rows, A.whole ? dims / 64 : 1}, kv_stride[2] = {dims, 64};
-    const cuuint32_t v_box[3] = {64, (cuuint32_t)(A.C.P < kTile ? A.C.P : kTile), A.whole ? (cuuint32_t)(dims / 64) : 1u};
-    const cuuint64_t k_dims[3] = {dims, rows, 1};
-    const cuuint32_t k_box[3] = {64, v_box[1], 1};
+    const cuuint32_t kv_box[3] = {64, (cuuint32_t)(A.C.P < kTile ? A.C.P : kTile), A.whole ? (cuuint32_t)(dims / 64) : 1u};
     const int tokens_q = A.MT / NQ / A.G;
     const cuuint64_t q_dims[3] = {dims, (cuuint64_t)A.HQ, (cuuint64_t)A.B * A.T};
     const cuuint64_t q_stride[2] = {dims, (cuuint64_t)A.HQ * dims};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)A.G, (cuuint32_t)(tokens_q < A.T ? tokens_q : A.T)};
     CUtensorMap mq, mk, mv;
-    if (!(L::kShare ? bf16_map(&mk, A.C.k, 3, k_dims, kv_stride, k_box) : bf16_map(&mk, A.C.k, 3, kv_dims, kv_stride, v_box)) || !bf16_map(&mv, A.C.v, 3, kv_dims, kv_stride, v_box) ||
+    if (!bf16_map(&mk, A.C.k, 3, kv_dims, kv_stride, kv_box) || !bf16_map(&mv, A.C.v, 3, kv_dims, kv_stride, kv_box) ||
         !bf16_map(&mq, A.q, 3, q_dims, q_stride, q_box))
         return cudaErrorInvalidValue;
     return launch_dependent(tree_attn_tc_kernel<D, NQ>, dim3(A.groups * A.NQT), dim3(L::kThreads), smem, st, mq, mk, mv, A);
