@@ -7,26 +7,28 @@
 //   P = 2^(S scale log2 e - m), rounded to bf16, back into TMEM over S
 //   O += P V      tcgen05.mma kind::f16, P from TMEM, V as it lies in its pages
 //                 (token rows of 64-element runs: the MN-major operand), fp32 in TMEM
-// One producer warp copies the pages' rows by TMA (boxes of min(P, 64) tokens; all of a
-// tile's dims by one copy where a page holds the tile), one warp issues the first
-// products, and the tiles go through one or two streams, each with a warp that
-// issues its second products and a warpgroup of 128 threads, one query row each, for
-// its softmax.  A stream has two buffers of S, so its next scores are formed while a
-// softmax runs; its O stays in TMEM over the piece.  The products are issued by warps
-// of their own because every wait on a barrier costs some 150 cycles even where it is
-// ready: one warp that issued both products of a tile took longer than its softmax.
+// The tiles go through one or two streams.  A stream is a warpgroup of 128 threads, one
+// query row each, for the softmax, two buffers of S in TMEM, so that its next scores
+// are formed while a softmax runs, and an O that stays in TMEM over the piece.
 //   NQ = 1, D <= 128: one query tile; its key/value tiles go to the two streams in turn,
 //     each with a running maximum and an O of its own, merged at the end.
 //   NQ = 2, D <= 128: windows of more than 128 rows; each stream has a query tile of
 //     its own and both use every key/value tile that is copied.
 //   NQ = 1, D = 256: O takes half of TMEM, so there is one stream.
-// Tiles of 64 keys instead of 128 make the first product read its query tile twice as
-// often from shared memory, but 128 keys leave no room for a second buffer of S, and
-// then each stream's scores, softmax and sums wait for one another: that took 492 us where
-// this takes 381 us (32 rows of 64 drafts over up to 8192 tokens, 64 heads on 8 of 128).
+// One producer warp copies the pages' rows by TMA, two tiles to a stage where D <= 128
+// (boxes of min(P, 64) tokens; all of a tile's dims by one copy where a page holds the
+// tile), and the products are issued by warps of their own, first and second ones
+// apart: a wait on a barrier costs some 150 cycles even where it is ready, and an issue
+// blocks while the tensor core is busy, so one warp that issued both products of a
+// tile took longer than its softmax (32 rows of 64 drafts over up to 8192 tokens, 64
+// heads on 8 of 128: 466 us; with tiles of 128 keys and one buffer of S, where scores,
+// softmax and sums wait for one another, 492 us; as it is 340 us, 0.52 of the bf16 rate).
+// There the first product bounds it: an MMA of 128 x 64 takes as long as one of
+// 128 x 128, because the query rows come from shared memory.
 // The G query heads of a kv head are rows of the same tile, so every key and value is
-// copied once for all of them: decoding is bound by HBM as long as a row group is below
-// some 280 rows (the machine's products per byte).
+// copied once for all of them, and with fewer rows the copies are the bound: 4 rows of
+// 131072 tokens, 32 heads on 8 of 128: 252 us, 0.99 of the copy bandwidth; 128 rows of 8
+// drafts over up to 4096 tokens, 16 heads on 2 of 256: 130 us, 0.82.
 //
 // The running maximum is only moved when a row's maximum has grown by more than 2^8
 // over it: until then the probabilities are taken against the old one, which is exact
@@ -38,6 +40,8 @@
 // and drafted tokens with a value that is not finite are zeroed in the V tile before
 // the second product, since 0 times NaN is not 0; such a draft's term is added to the
 // rows that attend to it at the end.  Only tiles that hold drafted tokens are looked at.
+// Where two streams share a tile the first one cleans it; the warp that issues the sums
+// takes the first stream's before the second's.
 //
 // Every wait is bounded.  One that runs out raises the block's abort flag, on which all
 // roles leave their loops; the producer then waits for the copies it has in flight and
