@@ -141,8 +141,8 @@ int attn_args(const gdn_spec_kv_cache *c, int32_t B, int32_t T, int32_t HQ, Attn
     return GDN_SPEC_OK;
 }
 
-// Workspace: pieces' sums, their maxima and sums, the chunks' notes.
-int64_t part_rows(const AttnArgs &A) { return (int64_t)A.groups * A.NQT * 2 * A.MT; }
+// Workspace: pieces' sums, their maxima and sums (one group cuts nothing), the chunks' notes.
+int64_t part_rows(const AttnArgs &A) { return A.groups < 2 ? 0 : (int64_t)A.groups * A.NQT * 2 * A.MT; }
 int64_t workspace_bytes_of(const AttnArgs &A) {
     return part_rows(A) * ((int64_t)A.C.D * 4 + 8) + (int64_t)A.groups * sizeof(AttnCut);
 }

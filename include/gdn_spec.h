@@ -350,7 +350,7 @@ const char *gdn_spec_prefill_path(const gdn_spec_layer *layer);
  * length[s] + node) in the same pages.  A page may be held by several slots
  * (ref counts them); only full pages are ever shared, so no shared page is
  * written.  Page p is free exactly when ref[p] == 0 and bit p % 32 of
- * free_bits[p / 32] is set.
+ * free_bits[p / 32] is set.  num_pages * P and max_pages * P are below 2^31.
  */
 typedef struct {
     int32_t n_layers;     /* softmax-attention layers                                   */
@@ -378,9 +378,9 @@ int gdn_spec_kv_init(const gdn_spec_kv_cache *cache, void *stream);
  * gdn_spec_kv_reserve -- pages for up to T more tokens: row b's slot gets the
  * pages it lacks to hold length + n tokens, n = n_tokens[b] (NULL: T).  The free
  * pages of lowest number are handed out in row order, so the tables depend only
- * on the calls made.  Row b is served when the pages that rows 0..b lack
- * together are free (rows that are refused for another reason take none);
- * otherwise it keeps what it has and NO_PAGES is set.
+ * on the calls made.  Row b is served when it lacks none or when the pages that
+ * rows 0..b lack together are free (rows that are refused for another reason
+ * lack none); otherwise it keeps what it has and NO_PAGES is set.  B <= 8192.
  *   n_tokens  int32 [B], device, 0 <= n_tokens <= T, or NULL
  *   done      int32 [B], device (written): 1 where the row is served, else 0
  * Device status: SLOT_OOR, ACCEPT_RANGE (n_tokens), CURSOR_CORRUPT, NO_PAGES.
@@ -396,6 +396,7 @@ int gdn_spec_kv_reserve(const gdn_spec_kv_cache *cache, const int32_t *slot_idx,
  * destination must be empty (SLOT_BUSY otherwise), and no destination may be
  * named twice or be a source; a source may be named often.  Rows are served as
  * by gdn_spec_kv_reserve.  A negative index on either side is a padding row.
+ * B <= 8192.
  *   done      int32 [B], device (written)
  */
 int gdn_spec_kv_fork(const gdn_spec_kv_cache *cache, const int32_t *src_idx, const int32_t *dst_idx,
@@ -405,7 +406,8 @@ int gdn_spec_kv_fork(const gdn_spec_kv_cache *cache, const int32_t *src_idx, con
  * gdn_spec_kv_commit -- after sampling: the accepted drafts of every row move
  * together, row i of the window's committed tokens taken from drafted node
  * path[b][i] (i < accept_len[b]), in every layer, in place; then
- * length += accept_len.  Pages are kept for the next window.
+ * length += accept_len.  Pages are kept for the next window.  With a path,
+ * T <= 1024.
  *   path        int32 [B, T], device: strictly ascending nodes in [0, T) (a
  *               parent is numbered before its children), or NULL: nodes 0, 1, ...
  *   accept_len  int32 [B], device, 0 <= accept_len <= T
