@@ -236,22 +236,24 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
         const int kv = pc.len + pc.cnt, n = pc.t1 - pc.t0;
         const int32_t *table = A.C.page_table + (int64_t)pc.slot * A.C.max_pages;
         const int units = (n + L::kUnit - 1) / L::kUnit;
-        const auto copy = [&](const CUtensorMap *map, auto ring_c, int u) {   // unit u of the piece
+        // Tokens of unit u of the piece that lie before the end, and the page of its box `lane`.  A page is looked up
+        // some units before it is used, so that the table's latency is not waited for.
+        const auto live_of = [&](int u) {
+            return min(min(L::kUnit, n - u * L::kUnit) * kTile, kv - (pc.t0 + u * L::kUnit) * kTile);
+        };
+        const auto page_of = [&](int u) {
+            return u < units && lane * BR < live_of(u) ? table[((pc.t0 + u * L::kUnit) * kTile + lane * BR) >> A.C.logP] : 0;
+        };
+        const auto copy = [&](const CUtensorMap *map, auto ring_c, int u, int page) {
             constexpr int ring = decltype(ring_c)::value;
             const uint32_t st = L::first(ring) + place[ring].at;
-            const int tok = (pc.t0 + u * L::kUnit) * kTile;
-            const int live = min(min(L::kUnit, n - u * L::kUnit) * kTile, kv - tok), boxes = (live + BR - 1) / BR;
-            // row of the pool where box `lane` starts
-            int row = 0;
-            if (lane < boxes) {
-                const int at = tok + lane * BR;
-                int page = table[at >> A.C.logP];
-                if (page < 0 || page >= A.C.num_pages) {
-                    atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
-                    page = 0;
-                }
-                row = ((A.layer * A.C.num_pages + page) * A.C.HKV + pc.h) * A.C.P + (at & (A.C.P - 1));
+            const int tok = (pc.t0 + u * L::kUnit) * kTile, boxes = (live_of(u) + BR - 1) / BR;
+            if (lane < boxes && (page < 0 || page >= A.C.num_pages)) {
+                atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+                page = 0;
             }
+            // row of the pool where box `lane` starts
+            const int row = ((A.layer * A.C.num_pages + page) * A.C.HKV + pc.h) * A.C.P + ((tok + lane * BR) & (A.C.P - 1));
             if (!wait(ptx::smem_addr(&ms->empty[st]), place[ring].ph ^ 1u, &ms->abort)) return false;
             const uint32_t bar = uniform(ptx::smem_addr(&ms->full[st]));
             const uint32_t dst = uniform(base + L::kOffKV + st * L::kStage);
@@ -282,12 +284,13 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
             place[ring].step(L::size(ring));
             return true;
         };
-        const auto copy_k = [&](int u) { return copy(mk, std::integral_constant<int, 0>(), u); };
-        const auto copy_v = [&](int u) {
-            return L::kTurns && (u & 1) ? copy(mv, std::integral_constant<int, L::kRings - 1>(), u)
-                                        : copy(mv, std::integral_constant<int, 1>(), u);
+        const auto copy_k = [&](int u, int page) { return copy(mk, std::integral_constant<int, 0>(), u, page); };
+        const auto copy_v = [&](int u, int page) {
+            return L::kTurns && (u & 1) ? copy(mv, std::integral_constant<int, L::kRings - 1>(), u, page)
+                                        : copy(mv, std::integral_constant<int, 1>(), u, page);
         };
-        ok = copy_k(0);
+        int pages[4] = {page_of(0), page_of(1), page_of(2), 0};   // of units u .. u + 3
+        ok = copy_k(0, pages[0]);
         if (ok) {   // the query tiles, behind the first keys
             const uint32_t qb = q_issued % L::QB, ph = (q_issued / L::QB) & 1u;
             ok = wait(ptx::smem_addr(&ms->q_empty[qb]), ph ^ 1u, &ms->abort);
@@ -310,13 +313,13 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
                 ++q_issued;
             }
         }
-        if (ok && units > 1) ok = copy_k(1);
+        if (ok && units > 1) ok = copy_k(1, pages[1]);
         for (int u = 0; ok && u < units; ++u) {   // the keys run ahead of the values by two units
-            // the table's line of some tiles on, so that its latency is not waited for later
-            const int ahead = (pc.t0 + min((u + 8) * L::kUnit, n - 1)) * kTile >> A.C.logP;
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(table + ahead));
-            ok = copy_v(u);
-            if (ok && u + 2 < units) ok = copy_k(u + 2);
+            pages[3] = page_of(u + 3);
+            ok = copy_v(u, pages[0]);
+            if (ok && u + 2 < units) ok = copy_k(u + 2, pages[2]);
+#pragma unroll
+            for (int x = 0; x < 3; ++x) pages[x] = pages[x + 1];
         }
     }
     if (!ok) {   // copies in flight land before the block's shared memory goes away
