@@ -223,7 +223,7 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
                                         int qt) {
     using L = Lay<D, NQ>;
     const int lane = threadIdx.x & 31;
-    const int BR = min(A.C.P, kTile);                          // tokens of a box: within a page and within a tile
+    const int log_br = min(A.C.logP, 6), BR = 1 << log_br;     // tokens of a box: within a page and within a tile
     const int RT = A.MT / NQ, tokens_q = RT / A.G;             // rows and tokens of a query tile
     const uint32_t q_bytes = 128u * A.G * min(tokens_q, A.T);   // one 64-dim block of one query tile
     Place place[3];
@@ -247,7 +247,7 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
         const auto copy = [&](const CUtensorMap *map, auto ring_c, int u, int page) {
             constexpr int ring = decltype(ring_c)::value;
             const uint32_t st = L::first(ring) + place[ring].at;
-            const int tok = (pc.t0 + u * L::kUnit) * kTile, boxes = (live_of(u) + BR - 1) / BR;
+            const int tok = (pc.t0 + u * L::kUnit) * kTile, boxes = (live_of(u) + BR - 1) >> log_br;
             if (lane < boxes && (page < 0 || page >= A.C.num_pages)) {
                 atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
                 page = 0;
@@ -257,17 +257,23 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
             if (!wait(ptx::smem_addr(&ms->empty[st]), place[ring].ph ^ 1u, &ms->abort)) return false;
             const uint32_t bar = uniform(ptx::smem_addr(&ms->full[st]));
             const uint32_t dst = uniform(base + L::kOffKV + st * L::kStage);
-            constexpr int kMost = L::kUnit * kTile / 16;   // boxes of the smallest pages
-            int rows[kMost];
+            if (A.whole) {   // all of a tile's blocks by one copy
+                int rows[L::kUnit];
 #pragma unroll
-            for (int c = 0; c < kMost; ++c) rows[c] = __shfl_sync(0xffffffffu, row, c);
-            if (ptx::elect_one()) {
-                ptx::mbar_expect_tx(bar, BR * 128u * L::kBlocks * boxes);
-                if (A.whole) {   // all of a tile's blocks by one copy
+                for (int c = 0; c < L::kUnit; ++c) rows[c] = __shfl_sync(0xffffffffu, row, c);
+                if (ptx::elect_one()) {
+                    ptx::mbar_expect_tx(bar, L::kBlocks * L::kBlock * boxes);
 #pragma unroll
                     for (int c = 0; c < L::kUnit; ++c)
                         if (c < boxes) ptx::tma_load_3d(dst + c * L::kBlocks * L::kBlock, map, bar, 0, rows[c], 0);
-                } else {
+                }
+            } else {
+                constexpr int kMost = L::kUnit * kTile / 16;   // boxes of the smallest pages
+                int rows[kMost];
+#pragma unroll
+                for (int c = 0; c < kMost; ++c) rows[c] = __shfl_sync(0xffffffffu, row, c);
+                if (ptx::elect_one()) {
+                    ptx::mbar_expect_tx(bar, BR * 128u * L::kBlocks * boxes);
 #pragma unroll
                     for (int c = 0; c < kMost; ++c) {
                         if (c >= boxes) break;
@@ -840,7 +846,7 @@ bool bf16_map(CUtensorMap *map, const void *p, int rank, const cuuint64_t *dims,
 template <int D, int NQ>
 cudaError_t run(const AttnArgs &A, cudaStream_t st) {
     using L = Lay<D, NQ>;
-    static_assert(L::kOffMisc + sizeof(Misc) <= kSmemMax, "shared memory");
+    static_assert(L::kOffMisc + sizeof(Misc) <= kSmemMax && kTile == 1 << 6, "shared memory, tile");
     // room to reach a 1024-byte boundary (the dynamic segment starts on one: there is no static one)
     constexpr size_t need = L::kOffMisc + sizeof(Misc) + 1024;
     constexpr size_t smem = need < (size_t)kSmemMax ? need : (size_t)kSmemMax;
