@@ -7,20 +7,20 @@
 //   m' = max(m, max s),  l' = l 2^(m-m') + sum 2^(s-m'),  o' = o 2^(m-m') + sum 2^(s-m') v,
 // and the row's output is o / l.  A row that has seen nothing yet has m = -inf, l = 0.
 //
-// A block of four warps holds 4 RPT query rows and walks tiles of 32 keys, copied
-// asynchronously into one of two buffers while the other is worked on.  A warp owns RPT
-// rows: lane k forms their scores with key k (the key row is read once for all of
-// them, the query rows are broadcast; key rows are padded by 16 bytes, so eight
-// lanes' pieces fall in different banks), the maximum is a shuffle reduction, and
-// the sums run over output columns, VEC consecutive ones per lane.  Only the buffers
-// are shared between the warps.  With few rows it is bound by HBM, with 32 rows by
-// shared-memory reads (12 wavefronts for the 8 cycles that 32 multiply-adds take).
+// A block of four or eight warps holds RPT query rows a warp and walks tiles of 32
+// keys, copied asynchronously into one of two buffers while the other is worked on.
+// For a warp's rows lane k forms the scores with key k (the key row is read once for
+// all of them, the query rows are broadcast; key rows are padded by 16 bytes, so
+// eight lanes' pieces fall in different banks), the maximum is a shuffle reduction,
+// and the sums run over output columns, VEC consecutive ones per lane.  Only the
+// buffers are shared between the warps.  It is bound by shared-memory reads: every
+// warp reads the whole tile, 8 wavefronts of a key and four query rows for 16
+// multiply-adds a lane.
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
 
 namespace gdnspec {
 
-constexpr int kAttnThreads = 128;
 constexpr int kAttnTile = 32;     // keys of a tile
 
 size_t tree_attn_smem(int D, int MT, int es) {
@@ -49,10 +49,11 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
                  : "memory");
 }
 
-// RPT rows per warp (MT = 4 RPT); NG groups of 32 VEC output columns.
-template <typename IO, int RPT, int VEC, int NG>
-__global__ void __launch_bounds__(kAttnThreads, RPT == 8 ? 2 : 4) tree_attn_kernel(const __grid_constant__ AttnArgs A) {
-    constexpr int MT = 4 * RPT, PLD = kAttnTile + 4, kPiece = 16 / sizeof(IO);   // elements of 16 bytes
+// W warps of RPT rows (MT = W RPT); NG groups of 32 VEC output columns.
+template <typename IO, int W, int RPT, int VEC, int NG>
+__global__ void __launch_bounds__(32 * W, 2) tree_attn_kernel(const __grid_constant__ AttnArgs A) {
+    constexpr int kAttnThreads = 32 * W, kEach = kAttnThreads / kAttnTile;   // threads that copy a token
+    constexpr int MT = W * RPT, PLD = kAttnTile + 4, kPiece = 16 / sizeof(IO);   // elements of 16 bytes
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int scratch[kAttnScratch];
     const int D = A.C.D, KLD = D + kPiece;
@@ -76,9 +77,8 @@ __global__ void __launch_bounds__(kAttnThreads, RPT == 8 ? 2 : 4) tree_attn_kern
         const int live = min(MT, pc.cnt * A.G - qt * MT);   // rows of this query tile
         if (live <= 0) continue;
         const int kv = pc.len + pc.cnt, pieces = D / kPiece;
-        // four threads copy a token's key and value
         const auto fetch = [&](int t, int buf) {
-            const int r = tid >> 2, tok = t * kAttnTile + r;
+            const int r = tid / kEach, tok = t * kAttnTile + r;
             int64_t row = -1;
             if (tok < kv) {
                 row = kv_token_row(A.C, pc.slot, tok);
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kAttnThreads, RPT == 8 ? 2 : 4) tree_attn_kern
             const int64_t e = there ? kv_elem(A.C, A.layer, pc.h, row) : 0;
             const IO *k = static_cast<const IO *>(A.C.k) + e, *v = static_cast<const IO *>(A.C.v) + e;
             IO *kd = Ks + (buf * kAttnTile + r) * KLD, *vd = Vs + (buf * kAttnTile + r) * D;
-            for (int c = tid & 3; c < pieces; c += 4) {
+            for (int c = tid % kEach; c < pieces; c += kEach) {
                 copy16(kd + c * kPiece, k + c * kPiece, there);
                 copy16(vd + c * kPiece, v + c * kPiece, there);
             }
@@ -313,33 +313,36 @@ cudaError_t launch_attn_join(const AttnArgs &A, bool bf16, cudaStream_t stream) 
 
 // ------------------------------------------------------------------ launch
 
-// Rows of a warp: the fewest that hold the window, at most 8.
-static int rows_per_warp(int R) { return R <= 4 ? 1 : R <= 8 ? 2 : R <= 16 ? 4 : 8; }
+// Rows of a block's query tile: the fewest of 4, 8, 16 and 32 that hold the window.  Sixteen and 32 rows take eight
+// warps, which read the tile from shared memory twice as often as four would and cover that latency better: 8
+// sequences of 5000 tokens, 4 shared heads of 128 fp32, 8 drafts are 71 us with 16 rows and 108 with 32, against 84
+// and 131 with four warps.  Eight rows keep four: 16 of those sequences are 91 us, 100 with eight.
+static int tile_rows(int R) { return R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32; }
 
-template <typename IO, int RPT, int VEC, int NG>
+template <typename IO, int W, int RPT, int VEC, int NG>
 static cudaError_t run_tree_attn(const AttnArgs &A, cudaStream_t st) {
     static KernelSetup setup;
-    const size_t smem = tree_attn_smem(A.C.D, 4 * RPT, sizeof(IO));
+    const size_t smem = tree_attn_smem(A.C.D, W * RPT, sizeof(IO));
     int sms;
-    cudaError_t e = kernel_setup(setup, (const void *)tree_attn_kernel<IO, RPT, VEC, NG>, smem, &sms);
+    cudaError_t e = kernel_setup(setup, (const void *)tree_attn_kernel<IO, W, RPT, VEC, NG>, smem, &sms);
     if (e != cudaSuccess) return e;
-    return launch_dependent(tree_attn_kernel<IO, RPT, VEC, NG>, dim3(A.groups * A.NQT), dim3(kAttnThreads), smem, st, A);
+    return launch_dependent(tree_attn_kernel<IO, W, RPT, VEC, NG>, dim3(A.groups * A.NQT), dim3(32 * W), smem, st, A);
 }
 
-template <typename IO, int RPT>
+template <typename IO, int W, int RPT>
 static cudaError_t run_cols(const AttnArgs &A, cudaStream_t st) {
-    if (A.C.D <= 64) return run_tree_attn<IO, RPT, 2, 1>(A, st);
-    if (A.C.D <= 128) return run_tree_attn<IO, RPT, 4, 1>(A, st);
-    return run_tree_attn<IO, RPT, 4, 2>(A, st);
+    if (A.C.D <= 64) return run_tree_attn<IO, W, RPT, 2, 1>(A, st);
+    if (A.C.D <= 128) return run_tree_attn<IO, W, RPT, 4, 1>(A, st);
+    return run_tree_attn<IO, W, RPT, 4, 2>(A, st);
 }
 
 template <typename IO>
 static cudaError_t run_rows(const AttnArgs &A, cudaStream_t st) {
     switch (A.MT) {
-        case 4: return run_cols<IO, 1>(A, st);
-        case 8: return run_cols<IO, 2>(A, st);
-        case 16: return run_cols<IO, 4>(A, st);
-        default: return run_cols<IO, 8>(A, st);
+        case 4: return run_cols<IO, 4, 1>(A, st);
+        case 8: return run_cols<IO, 4, 2>(A, st);
+        case 16: return run_cols<IO, 8, 2>(A, st);
+        default: return run_cols<IO, 8, 4>(A, st);
     }
 }
 
@@ -347,10 +350,11 @@ static cudaError_t run_rows(const AttnArgs &A, cudaStream_t st) {
 void tree_attn_cut(AttnArgs *A, int sms, int es) {
     const int R = A->T * A->G;
     A->TN = kAttnTile;
-    A->MT = 4 * rows_per_warp(R);
+    A->MT = tile_rows(R);
     A->NQT = (R + A->MT - 1) / A->MT;
     int per_sm = (int)((size_t)(227 * 1024) / (tree_attn_smem(A->C.D, A->MT, es) + 2048));
-    if (per_sm > 4) per_sm = 4;
+    const int most = A->MT <= 8 ? 4 : 2;
+    if (per_sm > most) per_sm = most;
     if (per_sm < 1) per_sm = 1;
     const int groups = sms * per_sm / A->NQT;
     A->groups = groups < 1 ? 1 : groups;
