@@ -7,219 +7,37 @@
 //   m' = max(m, max s),  l' = l 2^(m-m') + sum 2^(s-m'),  o' = o 2^(m-m') + sum 2^(s-m') v,
 // and the row's output is o / l.  A row that has seen nothing yet has m = -inf, l = 0.
 //
-// A block of four or eight warps holds RPT query rows a warp and walks tiles of 32
-// keys, copied asynchronously into one of two buffers while the other is worked on.
-// For a warp's rows lane k forms the scores with key k (the key row is read once for
-// all of them, the query rows are broadcast; key rows are padded by 16 bytes, so
-// eight lanes' pieces fall in different banks), the maximum is a shuffle reduction,
-// and the sums run over output columns, VEC consecutive ones per lane.  Only the
-// buffers are shared between the warps.  It is bound by shared-memory reads: every
-// warp reads the whole tile, 8 wavefronts of a key and four query rows for 16
-// multiply-adds a lane.
+// A block holds MT query rows and walks tiles of 32 keys, copied asynchronously into
+// one of two buffers while the other is worked on.  Four warps share a tile, eight
+// keys each, and with 16 or 32 rows two such fours halve the rows: every warp keeps
+// a running maximum and sum of its own for its rows and keys, and the four are
+// merged in shared memory at the end of a piece.  So a key or value is read from
+// shared memory by one or two warps only.  Of a warp's scores lane (g, k) forms rows
+// g, g + 4, ... with key k; the maximum is a shuffle over eight lanes, and the sums
+// run over output columns, VEC consecutive ones per lane.  Rows of keys and queries
+// are padded by 16 bytes, so that the pieces read together fall in different banks.
+// 16 sequences of 5000 tokens, 4 heads of 128 fp32, 8 drafts: 71 us, 3.5 TB/s, half of
+// HBM's rate, with the issue slots 58% and the shared-memory pipe 53% busy; 8 of them
+// with 32 rows a head: 109 us, where a warp's 16 multiply-adds for 5 wide reads take
+// 8.7 wavefronts and the pipe is busy 72% of a tile.
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
 
 namespace gdnspec {
 
 constexpr int kAttnTile = 32;     // keys of a tile
+constexpr int kSplit = 4;         // warps that share a tile
+constexpr int kWarpKeys = kAttnTile / kSplit;
 
-size_t tree_attn_smem(int D, int MT, int es) {
-    const size_t rows = (size_t)kAttnTile * ((D * es + 16) + D * es);          // a tile's keys and values
-    return 2 * rows + sizeof(float) * ((size_t)MT * D + MT * (kAttnTile + 4));  // and queries, probabilities
+// Bytes at the front: the two buffers of keys and values, and at a piece's end the four warps' sums in their place.
+__host__ __device__ constexpr size_t attn_front_bytes(int D, int MT, int es) {
+    const size_t tiles = (size_t)2 * kAttnTile * (2 * D * es + 16), sums = (size_t)kSplit * MT * (D + 4) * sizeof(float);
+    return tiles > sums ? tiles : sums;
 }
 
-template <typename IO> __device__ __forceinline__ float4 load4(const IO *p);
-template <> __device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 r = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
-                       __uint_as_float(r.y & 0xffff0000u));
+size_t tree_attn_smem(int D, int MT, int es) {   // and queries, probabilities, (maximum, sum)
+    return attn_front_bytes(D, MT, es) + (size_t)MT * (D * es + 16) + sizeof(float) * (size_t)kSplit * MT * (kWarpKeys + 2);
 }
-template <typename IO> __device__ __forceinline__ float2 load2(const IO *p);
-template <> __device__ __forceinline__ float2 load2<float>(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-template <> __device__ __forceinline__ float2 load2<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
-    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
-}
-
-// Sixteen bytes from global to shared memory; zeros where !live.
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
-}
-
-// W warps of RPT rows (MT = W RPT); NG groups of 32 VEC output columns.
-template <typename IO, int W, int RPT, int VEC, int NG>
-__global__ void __launch_bounds__(32 * W, 2) tree_attn_kernel(const __grid_constant__ AttnArgs A) {
-    constexpr int kAttnThreads = 32 * W, kEach = kAttnThreads / kAttnTile;   // threads that copy a token
-    constexpr int MT = W * RPT, PLD = kAttnTile + 4, kPiece = 16 / sizeof(IO);   // elements of 16 bytes
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int scratch[kAttnScratch];
-    const int D = A.C.D, KLD = D + kPiece;
-    IO *const Ks = reinterpret_cast<IO *>(smem);                              // [2][32][D + 16 bytes]
-    IO *const Vs = Ks + 2 * kAttnTile * KLD;                                  // [2][32][D]
-    float *const Qs = reinterpret_cast<float *>(Vs + 2 * kAttnTile * D);      // [MT][D], times scale log2 e
-    float *const Ps = Qs + MT * D;                                            // [MT][36]
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = blockIdx.x / A.NQT, qt = blockIdx.x - group * A.NQT;
-    float *const my_p = Ps + warp * RPT * PLD;
-    const float *const my_q = Qs + warp * RPT * D;
-    grid_dep_wait();
-
-    attn_dead_rows<IO>(A, blockIdx.x, gridDim.x, tid, kAttnThreads);
-    const AttnPlan plan = attn_plan<kAttnThreads>(A, group, blockIdx.x == 0, scratch);
-    AttnWalk walk = attn_walk(A, plan, group);
-    AttnPiece pc;
-    bool any = walk.next(A, &pc);
-    if (tid == 0 && qt == 0) attn_note(A, group, any, pc, plan.chunk);
-    for (; any; any = walk.next(A, &pc)) {
-        const int live = min(MT, pc.cnt * A.G - qt * MT);   // rows of this query tile
-        if (live <= 0) continue;
-        const int kv = pc.len + pc.cnt, pieces = D / kPiece;
-        const auto fetch = [&](int t, int buf) {
-            const int r = tid / kEach, tok = t * kAttnTile + r;
-            int64_t row = -1;
-            if (tok < kv) {
-                row = kv_token_row(A.C, pc.slot, tok);
-                if (row < 0) atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
-            }
-            const bool there = row >= 0;   // rows past the end are zeros, whatever the page holds there
-            const int64_t e = there ? kv_elem(A.C, A.layer, pc.h, row) : 0;
-            const IO *k = static_cast<const IO *>(A.C.k) + e, *v = static_cast<const IO *>(A.C.v) + e;
-            IO *kd = Ks + (buf * kAttnTile + r) * KLD, *vd = Vs + (buf * kAttnTile + r) * D;
-            for (int c = tid % kEach; c < pieces; c += kEach) {
-                copy16(kd + c * kPiece, k + c * kPiece, there);
-                copy16(vd + c * kPiece, v + c * kPiece, there);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        __syncthreads();   // the piece before is done with shared memory
-        fetch(pc.t0, 0);
-        for (int i = tid; i < MT * D / 4; i += kAttnThreads) {
-            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < live) {
-                x = load4<IO>(static_cast<const IO *>(A.q) + attn_out_row(A, pc.b, pc.h, qt * MT + r) * D + c);
-                x.x *= A.scale_log2, x.y *= A.scale_log2, x.z *= A.scale_log2, x.w *= A.scale_log2;
-            }
-            *reinterpret_cast<float4 *>(Qs + r * D + c) = x;
-        }
-        uint64_t mask[RPT];
-        float m[RPT], l[RPT];   // l: this lane's keys only, until the end
-        float acc[RPT][NG * VEC] = {};
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int r = warp * RPT + i;
-            mask[i] = r < live ? attn_mask(A, pc.b, (qt * MT + r) / A.G) : 0;
-            m[i] = -INFINITY;
-            l[i] = 0.0f;
-        }
-        for (int t = pc.t0; t < pc.t1; ++t) {
-            const int buf = (t - pc.t0) & 1, k0 = t * kAttnTile;
-            if (t + 1 < pc.t1) {
-                fetch(t + 1, buf ^ 1);
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            }
-            __syncthreads();
-            const IO *kp = Ks + (buf * kAttnTile + lane) * KLD, *vp = Vs + buf * kAttnTile * D;
-            float s[RPT] = {};
-#pragma unroll 2
-            for (int d = 0; d < D; d += 4) {
-                const float4 kx = load4<IO>(kp + d);
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    const float4 qx = *reinterpret_cast<const float4 *>(my_q + i * D + d);
-                    s[i] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, s[i]))));
-                }
-            }
-            const int node = k0 + lane - pc.len;   // < 0: committed
-            const bool drafts = k0 + kAttnTile > pc.len;
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                float x = s[i];
-                if (drafts && !(k0 + lane < kv && (node < 0 || ((mask[i] >> node) & 1)))) x = -INFINITY;
-                float top = x;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float mn = fmaxf(m[i], top), base = mn == -INFINITY ? 0.0f : mn;
-                const float p = exp2f(x - base);
-                if (mn > m[i]) {   // the same in all lanes
-                    const float al = exp2f(m[i] - base);
-                    l[i] *= al;
-#pragma unroll
-                    for (int j = 0; j < NG * VEC; ++j) acc[i][j] *= al;
-                    m[i] = mn;
-                }
-                l[i] += p;
-                my_p[i * PLD + lane] = p;
-            }
-            __syncwarp();
-            // A tile that holds drafted tokens leaves masked ones out by a test, so that an infinity or NaN there stays
-            // without effect; committed tokens are seen by every row.
-#pragma unroll 1
-            for (int k = 0; k < kAttnTile; k += 4) {
-                float4 p[RPT];
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) p[i] = *reinterpret_cast<const float4 *>(my_p + i * PLD + k);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v[NG * VEC];
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const int d = (g * 32 + lane) * VEC;
-                        if (VEC == 4) {
-                            const float4 x = d < D ? load4<IO>(vp + (k + e) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            v[g * VEC] = x.x, v[g * VEC + 1] = x.y, v[g * VEC + 2] = x.z, v[g * VEC + 3] = x.w;
-                        } else {
-                            const float2 x = d < D ? load2<IO>(vp + (k + e) * D + d) : make_float2(0.f, 0.f);
-                            v[g * VEC] = x.x, v[g * VEC + 1] = x.y;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const float x = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-                        if (!drafts || x != 0.0f) {
-#pragma unroll
-                            for (int j = 0; j < NG * VEC; ++j) acc[i][j] = fmaf(x, v[j], acc[i][j]);
-                        }
-                    }
-                }
-            }
-            __syncthreads();   // the buffer may be filled again
-        }
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const int r = warp * RPT + i;
-            const float sum = warp_sum(l[i]);
-            if (r >= live) continue;
-            const int64_t row = attn_out_row(A, pc.b, pc.h, qt * MT + r), part = (int64_t)blockIdx.x * 2 + pc.side;
-            const float inv = pc.whole() ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-            IO *out = static_cast<IO *>(A.out) + row * D;
-            float *po = reinterpret_cast<float *>(A.part_o) + part * MT * D;
-#pragma unroll
-            for (int j = 0; j < NG * VEC; ++j) {
-                const int d = (j / VEC * 32 + lane) * VEC + j % VEC;
-                if (d >= D) continue;
-                if (pc.whole()) out[d] = from_f32<IO>(acc[i][j] * inv);
-                else po[((d >> 2) * MT + r) * 4 + (d & 3)] = acc[i][j];
-            }
-            if (lane == 0) {
-                if (!pc.whole()) A.part_ml[part * MT + r] = make_float2(m[i], sum);
-                else if (A.lse) A.lse[row] = attn_lse(m[i], sum);
-            }
-        }
-    }
-    grid_dep_launch();
-}
-
-// ------------------------------------------------------------------ join
-
-constexpr int kJoinThreads = 256;
-constexpr int kJoinLanes = 8;      // threads that share an element's pieces when they are many
-constexpr int kJoinMany = 16;      // from so many pieces on
 
 // (m, l, o) of a row's four dims, as (maximum in log2 units, sum, unnormalised sums)
 struct JoinSum {
@@ -246,6 +64,247 @@ __device__ __forceinline__ void join_put(const AttnArgs &A, const JoinSum &j, in
     else *reinterpret_cast<uint4 *>(op) = *reinterpret_cast<const uint4 *>(out);
     if (A.lse && d4 == 0) A.lse[row] = attn_lse(j.m, j.l);
 }
+
+template <typename IO> __device__ __forceinline__ float4 load4(const IO *p);
+template <> __device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 r = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
+}
+template <typename IO> __device__ __forceinline__ float2 load2(const IO *p);
+template <> __device__ __forceinline__ float2 load2<float>(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+template <> __device__ __forceinline__ float2 load2<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+}
+
+// Sixteen bytes from global to shared memory; zeros where !live.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+
+// Blocks of an SM that the registers leave room for.
+__host__ __device__ constexpr int attn_blocks(int WR, int RW, int NG) {
+    return WR == 2 ? (NG == 2 ? 1 : 2) : NG == 2 ? 2 : 4;
+}
+
+// acc += p v over a warp's keys; TEST: a probability of zero takes nothing from its value.
+template <typename IO, int RW, int VEC, int NG, bool TEST>
+__device__ __forceinline__ void add_values(float (&acc)[RW][NG * VEC], const float *p_s, const IO *v_s, int D, int lane) {
+#pragma unroll 1
+    for (int k = 0; k < kWarpKeys; k += 4) {
+        float v[4][NG * VEC];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int d = (g * 32 + lane) * VEC;
+                if (VEC == 4) {
+                    const float4 x = d < D ? load4<IO>(v_s + (k + e) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[e][g * VEC] = x.x, v[e][g * VEC + 1] = x.y, v[e][g * VEC + 2] = x.z, v[e][g * VEC + 3] = x.w;
+                } else {
+                    const float2 x = d < D ? load2<IO>(v_s + (k + e) * D + d) : make_float2(0.f, 0.f);
+                    v[e][g * VEC] = x.x, v[e][g * VEC + 1] = x.y;
+                }
+            }
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const float4 p = *reinterpret_cast<const float4 *>(p_s + r * kWarpKeys + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = e == 0 ? p.x : e == 1 ? p.y : e == 2 ? p.z : p.w;
+                if (!TEST || x != 0.0f) {
+#pragma unroll
+                    for (int j = 0; j < NG * VEC; ++j) acc[r][j] = fmaf(x, v[e][j], acc[r][j]);
+                }
+            }
+        }
+    }
+}
+
+// WR fours of warps with RW rows each (MT = WR RW); NG groups of 32 VEC output columns.
+template <typename IO, int WR, int RW, int VEC, int NG>
+__global__ void __launch_bounds__(32 * kSplit * WR, attn_blocks(WR, RW, NG)) tree_attn_kernel(const __grid_constant__ AttnArgs A) {
+    constexpr int kThreads = 32 * kSplit * WR, MT = WR * RW, R = RW / 4;
+    constexpr int kPiece = 16 / sizeof(IO);                                     // elements of 16 bytes
+    constexpr int kCopied = kAttnTile * 32 / kThreads;                          // tokens that a warp copies
+    constexpr int kLanes = NG * 32 * VEC / kPiece < 32 ? NG * 32 * VEC / kPiece : 32;   // lanes that copy a token
+    constexpr int kChains = R == 1 ? 4 : R == 2 ? 2 : 1;   // sums of a score, so that their additions overlap
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int scratch[kAttnScratch];
+    const int D = A.C.D, D4 = D >> 2, KLD = D + kPiece, QLD = D + 4;
+    IO *const Ks = reinterpret_cast<IO *>(smem);                              // [2][32][D + 16 bytes]
+    IO *const Vs = Ks + 2 * kAttnTile * KLD;                                  // [2][32][D]
+    float *const Os = reinterpret_cast<float *>(smem);                        // [4][MT][D + 4], at a piece's end
+    IO *const Qs = reinterpret_cast<IO *>(smem + attn_front_bytes(D, MT, sizeof(IO)));   // [MT][D + 16 bytes]
+    float *const Ps = reinterpret_cast<float *>(Qs + MT * KLD);                                          // [warps][RW][8]
+    float2 *const MLs = reinterpret_cast<float2 *>(Ps + kSplit * MT * kWarpKeys);   // [4][MT]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wk = warp % kSplit, r0 = warp / kSplit * RW;   // the warp's keys and first row
+    const int kl = lane & 7, rg = lane >> 3;                 // the lane's key and first row of them
+    const int group = blockIdx.x / A.NQT, qt = blockIdx.x - group * A.NQT;
+    float *const my_p = Ps + warp * RW * kWarpKeys;
+    const IO *const my_q = Qs + (r0 + rg) * KLD;
+    grid_dep_wait();
+
+    attn_dead_rows<IO>(A, blockIdx.x, gridDim.x, tid, kThreads);
+    const AttnPlan plan = attn_plan<kThreads>(A, group, blockIdx.x == 0, scratch);
+    AttnWalk walk = attn_walk(A, plan, group);
+    AttnPiece pc;
+    bool any = walk.next(A, &pc);
+    if (tid == 0 && qt == 0) attn_note(A, group, any, pc, plan.chunk);
+    for (; any; any = walk.next(A, &pc)) {
+        const int live = min(MT, pc.cnt * A.G - qt * MT);   // rows of this query tile
+        if (live <= 0) continue;
+        const int kv = pc.len + pc.cnt, pieces = D / kPiece;
+        const int fr = warp * kCopied + lane % kCopied;   // this lane looks up that token of a tile
+        const auto page_of = [&](int t) {   // of this thread's token of tile t
+            const int tok = t * kAttnTile + fr;
+            return t < pc.t1 && tok < kv ? A.C.page_table[(int64_t)pc.slot * A.C.max_pages + (tok >> A.C.logP)] : 0;
+        };
+        const auto fetch = [&](int t, int buf, int page) {
+            const int tok = t * kAttnTile + fr;
+            const bool ok = page >= 0 && page < A.C.num_pages, there = tok < kv && ok;
+            if (tok < kv && !ok) atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+            const int64_t mine = there ? kv_elem(A.C, A.layer, pc.h, ((int64_t)page << A.C.logP) + (tok & (A.C.P - 1))) : -1;
+#pragma unroll
+            for (int i = 0; i < kCopied; i += 32 / kLanes) {
+                const int r = i + lane / kLanes;
+                int64_t e = __shfl_sync(0xffffffffu, mine, r);
+                const bool live_row = e >= 0;   // rows past the end are zeros, whatever the page holds there
+                if (!live_row) e = 0;
+                const IO *k = static_cast<const IO *>(A.C.k) + e, *v = static_cast<const IO *>(A.C.v) + e;
+                IO *kd = Ks + (buf * kAttnTile + warp * kCopied + r) * KLD, *vd = Vs + (buf * kAttnTile + warp * kCopied + r) * D;
+                for (int c = lane % kLanes; c < pieces; c += kLanes) {
+                    copy16(kd + c * kPiece, k + c * kPiece, live_row);
+                    copy16(vd + c * kPiece, v + c * kPiece, live_row);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int page = page_of(pc.t0);
+        __syncthreads();   // the piece before is done with shared memory
+        for (int r = warp * (32 / kLanes) + lane / kLanes; r < MT; r += kThreads / kLanes) {
+            const IO *q = static_cast<const IO *>(A.q) + (r < live ? attn_out_row(A, pc.b, pc.h, qt * MT + r) * D : 0);
+            for (int c = lane % kLanes; c < pieces; c += kLanes) copy16(Qs + r * KLD + c * kPiece, q + c * kPiece, r < live);
+        }
+        fetch(pc.t0, 0, page);
+        page = page_of(pc.t0 + 1);   // always a tile ahead of its copy
+        uint64_t mask[R];
+        float m[R], l[R];   // of the warp's keys; l: this lane's only, until the end
+        float acc[RW][NG * VEC] = {};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = r0 + rg + 4 * i;
+            mask[i] = r < live ? attn_mask(A, pc.b, (qt * MT + r) / A.G) : 0;
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+        }
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            const int buf = (t - pc.t0) & 1, k0 = t * kAttnTile + wk * kWarpKeys;
+            if (t + 1 < pc.t1) {
+                fetch(t + 1, buf ^ 1, page);
+                page = page_of(t + 2);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncthreads();
+            const IO *kp = Ks + (buf * kAttnTile + wk * kWarpKeys + kl) * KLD;
+            const IO *vp = Vs + (buf * kAttnTile + wk * kWarpKeys) * D;
+            float s[R][kChains] = {};
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                const float4 kx = load4<IO>(kp + d);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float4 qx = load4<IO>(my_q + i * 4 * KLD + d);
+                    s[i][0] = fmaf(qx.x, kx.x, s[i][0]);
+                    s[i][1 % kChains] = fmaf(qx.y, kx.y, s[i][1 % kChains]);
+                    s[i][2 % kChains] = fmaf(qx.z, kx.z, s[i][2 % kChains]);
+                    s[i][3 % kChains] = fmaf(qx.w, kx.w, s[i][3 % kChains]);
+                }
+            }
+            const int node = k0 + kl - pc.len;   // < 0: committed
+            const bool drafts = k0 + kWarpKeys > pc.len;
+            float al[R];
+            bool up = false;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float x = kChains == 4 ? (s[i][0] + s[i][1 % kChains]) + (s[i][2 % kChains] + s[i][3 % kChains])
+                          : kChains == 2 ? s[i][0] + s[i][1 % kChains] : s[i][0];
+                x *= A.scale_log2;
+                if (drafts && !(k0 + kl < kv && (node < 0 || ((mask[i] >> node) & 1)))) x = -INFINITY;
+                float top = x;
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float mn = fmaxf(m[i], top), base = mn == -INFINITY ? 0.0f : mn;
+                const float p = exp2f(x - base);
+                al[i] = exp2f(m[i] - base);
+                up |= mn > m[i];
+                m[i] = mn;
+                l[i] = l[i] * al[i] + p;
+                my_p[(rg + 4 * i) * kWarpKeys + kl] = p;
+            }
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int r = 0; r < RW; ++r) {
+                    const float a = __shfl_sync(0xffffffffu, al[r / 4], (r & 3) * 8);
+#pragma unroll
+                    for (int j = 0; j < NG * VEC; ++j) acc[r][j] *= a;
+                }
+            }
+            __syncwarp();
+            // Keys that hold drafted tokens leave masked ones out by a test, so that an infinity or NaN there stays
+            // without effect; committed tokens are seen by every row.
+            if (drafts) add_values<IO, RW, VEC, NG, true>(acc, my_p, vp, D, lane);
+            else add_values<IO, RW, VEC, NG, false>(acc, my_p, vp, D, lane);
+            __syncthreads();   // the buffer may be filled again
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+            if (kl == 0) MLs[wk * MT + r0 + rg + 4 * i] = make_float2(m[i], l[i]);
+        }
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int d = (g * 32 + lane) * VEC;
+                float *o = Os + (wk * MT + r0 + r) * QLD + d;
+                if (d >= D) continue;
+                if (VEC == 4) *reinterpret_cast<float4 *>(o) = make_float4(acc[r][g * VEC], acc[r][g * VEC + 1], acc[r][g * VEC + 2], acc[r][g * VEC + 3]);
+                else *reinterpret_cast<float2 *>(o) = make_float2(acc[r][g * VEC], acc[r][g * VEC + 1]);
+            }
+        __syncthreads();
+        const int64_t part = (int64_t)blockIdx.x * 2 + pc.side;
+        for (int x = tid; x < MT * D4; x += kThreads) {
+            // in the order of where it goes: along a row of the output, or along the rows of a piece
+            const int r = pc.whole() ? x / D4 : x % MT, d4 = pc.whole() ? x - r * D4 : x / MT;
+            if (r >= live) continue;
+            JoinSum sum;
+#pragma unroll
+            for (int w = 0; w < kSplit; ++w) sum.add(MLs[w * MT + r], *reinterpret_cast<const float4 *>(Os + (w * MT + r) * QLD + 4 * d4));
+            if (pc.whole()) {
+                join_put<IO>(A, sum, attn_out_row(A, pc.b, pc.h, qt * MT + r), d4);
+            } else {
+                A.part_o[(part * D4 + d4) * MT + r] = sum.o;
+                if (d4 == 0) A.part_ml[part * MT + r] = make_float2(sum.m, sum.l);
+            }
+        }
+    }
+    grid_dep_launch();
+}
+
+// ------------------------------------------------------------------ join
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinLanes = 8;      // threads that share an element's pieces when they are many
+constexpr int kJoinMany = 16;      // from so many pieces on
 
 // Block (g, query tile, part).  A thread takes the same four dims of one row from
 // every piece, all loads of two pieces in flight before they are merged; where an
@@ -313,36 +372,37 @@ cudaError_t launch_attn_join(const AttnArgs &A, bool bf16, cudaStream_t stream) 
 
 // ------------------------------------------------------------------ launch
 
-// Rows of a block's query tile: the fewest of 4, 8, 16 and 32 that hold the window.  Sixteen and 32 rows take eight
-// warps, which read the tile from shared memory twice as often as four would and cover that latency better: 8
-// sequences of 5000 tokens, 4 shared heads of 128 fp32, 8 drafts are 71 us with 16 rows and 108 with 32, against 84
-// and 131 with four warps.  Eight rows keep four: 16 of those sequences are 91 us, 100 with eight.
+// Rows of a block's query tile: the fewest of 4, 8, 16 and 32 that hold the window.  Sixteen rows take two fours of
+// warps: with one four of sixteen rows a warp, 8 sequences of 5000 tokens, 4 shared heads of 128 fp32, 8 drafts were
+// 80 us against 66.
 static int tile_rows(int R) { return R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32; }
+static constexpr int fours(int MT) { return MT <= 8 ? 1 : 2; }
 
-template <typename IO, int W, int RPT, int VEC, int NG>
+template <typename IO, int MT, int VEC, int NG>
 static cudaError_t run_tree_attn(const AttnArgs &A, cudaStream_t st) {
+    constexpr int WR = fours(MT);
     static KernelSetup setup;
-    const size_t smem = tree_attn_smem(A.C.D, W * RPT, sizeof(IO));
+    const size_t smem = tree_attn_smem(A.C.D, MT, sizeof(IO));
     int sms;
-    cudaError_t e = kernel_setup(setup, (const void *)tree_attn_kernel<IO, W, RPT, VEC, NG>, smem, &sms);
+    cudaError_t e = kernel_setup(setup, (const void *)tree_attn_kernel<IO, WR, MT / WR, VEC, NG>, smem, &sms);
     if (e != cudaSuccess) return e;
-    return launch_dependent(tree_attn_kernel<IO, W, RPT, VEC, NG>, dim3(A.groups * A.NQT), dim3(32 * W), smem, st, A);
+    return launch_dependent(tree_attn_kernel<IO, WR, MT / WR, VEC, NG>, dim3(A.groups * A.NQT), dim3(32 * kSplit * WR), smem, st, A);
 }
 
-template <typename IO, int W, int RPT>
+template <typename IO, int MT>
 static cudaError_t run_cols(const AttnArgs &A, cudaStream_t st) {
-    if (A.C.D <= 64) return run_tree_attn<IO, W, RPT, 2, 1>(A, st);
-    if (A.C.D <= 128) return run_tree_attn<IO, W, RPT, 4, 1>(A, st);
-    return run_tree_attn<IO, W, RPT, 4, 2>(A, st);
+    if (A.C.D <= 64) return run_tree_attn<IO, MT, 2, 1>(A, st);
+    if (A.C.D <= 128) return run_tree_attn<IO, MT, 4, 1>(A, st);
+    return run_tree_attn<IO, MT, 4, 2>(A, st);
 }
 
 template <typename IO>
 static cudaError_t run_rows(const AttnArgs &A, cudaStream_t st) {
     switch (A.MT) {
-        case 4: return run_cols<IO, 4, 1>(A, st);
-        case 8: return run_cols<IO, 4, 2>(A, st);
-        case 16: return run_cols<IO, 8, 2>(A, st);
-        default: return run_cols<IO, 8, 4>(A, st);
+        case 4: return run_cols<IO, 4>(A, st);
+        case 8: return run_cols<IO, 8>(A, st);
+        case 16: return run_cols<IO, 16>(A, st);
+        default: return run_cols<IO, 32>(A, st);
     }
 }
 
@@ -352,10 +412,9 @@ void tree_attn_cut(AttnArgs *A, int sms, int es) {
     A->TN = kAttnTile;
     A->MT = tile_rows(R);
     A->NQT = (R + A->MT - 1) / A->MT;
-    int per_sm = (int)((size_t)(227 * 1024) / (tree_attn_smem(A->C.D, A->MT, es) + 2048));
-    const int most = A->MT <= 8 ? 4 : 2;
-    if (per_sm > most) per_sm = most;
-    if (per_sm < 1) per_sm = 1;
+    const int fit = (int)((size_t)(227 * 1024) / (tree_attn_smem(A->C.D, A->MT, es) + 2048));
+    const int most = attn_blocks(fours(A->MT), A->MT / fours(A->MT), A->C.D > 128 ? 2 : 1);
+    const int per_sm = fit < 1 ? 1 : fit < most ? fit : most;
     const int groups = sms * per_sm / A->NQT;
     A->groups = groups < 1 ? 1 : groups;
     A->min_chunk = 2;
