@@ -22,7 +22,7 @@
 // blocks while the tensor core is busy, so one warp that issued both products of a
 // tile took longer than its softmax (32 rows of 64 drafts over up to 8192 tokens, 64
 // heads on 8 of 128: 466 us; with tiles of 128 keys and one buffer of S, where scores,
-// softmax and sums wait for one another, 492 us; as it is 340 us, 0.52 of the bf16 rate).
+// softmax and sums wait for one another, 492 us; as it is 333 us, 0.53 of the bf16 rate).
 // There the first product bounds it: an MMA of 128 x 64 takes as long as one of
 // 128 x 128, because the query rows come from shared memory.
 // The G query heads of a kv head are rows of the same tile, so every key and value is
