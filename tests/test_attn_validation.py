@@ -97,6 +97,14 @@ def test_attention_call(lib):
     assert lib.gdn_spec_tree_attn_path(ctypes.byref(cache()), 4, 2 * 129) == b"generic"
 
 
+def test_attention_counts_in_31_bits(lib):
+    short = cache(HKV=1, P=16, max_pages=1)
+    assert attn(lib, short, B=1 << 25, T=64) == EUNSUP          # tokens
+    assert attn(lib, short, B=(1 << 31) - 1, T=1) == EUNSUP     # tiles: one of 16 tokens is a tile too
+    assert attn(lib, cache(max_pages=1 << 20), B=1 << 12) == EUNSUP
+    assert lib.gdn_spec_tree_attn_workspace(ctypes.byref(short), 1 << 25, 64, 8) == EUNSUP
+
+
 def plan(D=128, rot=128, layout="half", **kw):
     return binding.RopePlan(D, rot, layout=layout, **kw).desc()
 
