@@ -318,3 +318,75 @@ def test_the_same_call_gives_the_same_bits():
             b, lb = c.call()
             assert torch.equal(a, b) and torch.equal(la, lb)
         assert binding.kv_read_status(c.cache) == 0
+
+
+@pytest.mark.parametrize("io,T,HQ,HKV,D,P", [
+    ("fp32", 1, 4, 1, 128, 64), ("fp32", 2, 4, 2, 256, 16), ("fp32", 4, 1, 1, 136, 32),      # 4 rows a tile
+    ("fp32", 2, 8, 2, 64, 16), ("fp32", 7, 2, 2, 128, 128),                                  # 8
+    ("fp32", 16, 2, 2, 200, 64), ("fp32", 3, 10, 2, 64, 16),                                 # 16
+    ("fp32", 9, 8, 2, 256, 32), ("fp32", 64, 3, 1, 128, 256), ("fp32", 17, 2, 1, 24, 16),    # 32, several tiles
+    ("bf16", 2, 130, 1, 128, 32), ("bf16", 1, 300, 2, 64, 16), ("bf16", 3, 129, 1, 256, 64)])
+def test_the_cuda_core_kernel(io, T, HQ, HKV, D, P):
+    """Every size of its query tiles, and bf16 with more than 128 heads a kv head."""
+    c = Case(14, io, T, HQ, HKV, D, P, lens=[33, 0, 500, 31, 7])
+    c.check()
+    assert binding.tree_attn_path(c.cache, T, HQ) == "generic"
+
+
+@pytest.mark.parametrize("T,HQ,HKV,D", [(8, 4, 2, 128), (2, 2, 1, 64), (40, 8, 2, 256), (3, 4, 1, 72)])
+def test_infinite_values_in_fp32(T, HQ, HKV, D):
+    """As with bf16: a draft's infinite values reach the nodes below it, in their dims, and no other."""
+    c = Case(15, "fp32", T=T, HQ=HQ, HKV=HKV, D=D, P=64, lens=[61, 200, 30])
+    dims = torch.arange(0, D, 3)
+    for s in range(3):
+        i = int(c.lens[s]) + 1
+        c.v[0, int(c.table[s, i // 64]), :, i % 64, dims] = math.inf
+    out, _ = c.call()
+    want, _, spread = c.expect()
+    got = out.double().cpu().numpy()
+    fin = np.isfinite(want)
+    assert fin.any() and (~fin).any()
+    assert np.array_equal(np.isposinf(got), np.isposinf(want))
+    sp = np.where(np.isfinite(spread), spread, 0)
+    err = np.abs(np.where(fin, got, 0) - np.where(fin, want, 0))
+    assert (err <= 2.0 ** -24 * np.abs(np.where(fin, want, 0)) + FP32_NOISE * sp).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_a_pool_past_32_bits(io):
+    """Pages whose elements and bytes lie past 2^31 and 2^32: the same bits as from a small pool."""
+    T, HQ, HKV, D, P = 5, 4, 2, 256, 256
+    c = Case(16, io, T, HQ, HKV, D, P, lens=[700, 3, 256], layers=2, layer=1, poison=False)
+    want, wl = c.call()
+    small, big_pages = c.cache, 10000                        # 2 layers of 10000 pages: 2.6e9 elements
+    to = np.linspace(0, big_pages - 1, c.num_pages).astype(np.int32)[::-1].copy()   # first pages to the top
+    table = np.where(c.table >= 0, to[np.maximum(c.table, 0)], -1).astype(np.int32)
+    where = torch.from_numpy(to).long().cuda()
+    pool = [torch.empty(2, big_pages, HKV, P, D, dtype=ref.TORCH[io], device="cuda") for _ in range(2)]
+    assert pool[0].numel() > 2 ** 31
+    for x, y in zip(pool, (small.k, small.v)):
+        x[:, where] = y
+    slots = torch.from_numpy(c.slots).cuda()
+
+    def cache():
+        return binding.KvCache(2, big_pages, HKV, P, D, len(c.lens), table.shape[1], io, tensors={
+            "k": pool[0], "v": pool[1], "page_table": torch.from_numpy(table).cuda(),
+            "n_pages": torch.from_numpy(c.n_pages).cuda(), "length": torch.from_numpy(c.lens).cuda()})
+
+    big = cache()
+    c.cache = big
+    got, gl = c.call()
+    assert binding.kv_read_status(big) == 0 and torch.equal(got, want) and torch.equal(gl, wl)
+    # the window's append and the move of an accepted path, in both pools
+    plan = binding.RopePlan(D, 64)
+    r = np.random.default_rng(16)
+    qkv = ref.draw(r, (3, T, HQ + 2 * HKV, D), io).cuda()
+    path = torch.tensor([[0, 2, 4, 0, 0], [1, 3, 0, 0, 0], [0, 1, 2, 4, 0]], dtype=torch.int32, device="cuda")
+    acc = torch.tensor([3, 2, 4], dtype=torch.int32, device="cuda")
+    for cc in (small, big):
+        binding.rope_append(plan, cc, 1, slots, qkv[:, :, :HQ], qkv[:, :, HQ:HQ + HKV], qkv[:, :, HQ + HKV:])
+        binding.kv_commit(cc, slots, acc, T, path)
+        assert binding.kv_read_status(cc) == 0
+    for x, y in zip(pool, (small.k, small.v)):
+        assert torch.equal(x[:, where], y)
+    assert torch.equal(big.length, small.length)
