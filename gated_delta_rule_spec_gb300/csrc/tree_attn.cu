@@ -306,10 +306,11 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinLanes = 8;      // threads that share an element's pieces when they are many
 constexpr int kJoinMany = 16;      // from so many pieces on
 
-// Block (g, query tile, part).  A thread takes the same four dims of one row from
-// every piece, all loads of two pieces in flight before they are merged; where an
-// item has many pieces (few rows, long contexts) eight threads share an element.
-// Everything about the item is in the chunk's note, so a block starts with one load.
+// Block (g, query tile, part), for the item that chunk g starts inside of.  The blocks of all chunks that do share the
+// item's elements, so an item of many pieces has as many more blocks (3 rows of 7698 tokens, 28 rows of 256 fp32 each:
+// 107 us where the first of them took all, 36 so).  A thread takes the same four dims of one row from every piece, all
+// loads of two pieces in flight before they are merged; where an item has many pieces eight threads share an
+// element.  Everything about the item is in the chunk's note, so a block starts with one load.
 template <typename IO>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs A) {
     __shared__ float4 o_s[kJoinLanes][32];
@@ -318,17 +319,19 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int g = blockIdx.x + 1, qt = blockIdx.y, tid = threadIdx.x, lane = tid & 31, pl = tid >> 5;
     const AttnCut cut = A.cuts[g];
     const int64_t s = (int64_t)g * cut.chunk - cut.t;                // the item's first tile in the line
-    if (cut.b < 0 || cut.t == 0 || s / cut.chunk != g - 1) return;   // a cut between items, or not the item's first
+    if (cut.b < 0 || cut.t == 0) return;   // a cut between items
+    const int first = (int)(s / cut.chunk);
     const int live = min(A.MT, cut.cnt * A.G - qt * A.MT);
     if (live <= 0) return;
     const int last = (int)((s + cut.tiles - 1) / cut.chunk);
     const int D4 = A.C.D >> 2, work = live * D4;
+    const int block = (g - 1 - first) * gridDim.z + blockIdx.z, blocks = (last - first) * gridDim.z;   // of the item
     const auto part_of = [&](int c) { return ((int64_t)c * A.NQT + qt) * 2 + (s > (int64_t)c * cut.chunk ? 1 : 0); };
-    if (last - g + 2 < kJoinMany) {
-        for (int x = blockIdx.z * kJoinThreads + tid; x < work; x += gridDim.z * kJoinThreads) {
+    if (last - first + 1 < kJoinMany) {
+        for (int x = block * kJoinThreads + tid; x < work; x += blocks * kJoinThreads) {
             const int d4 = x / live, r = x - d4 * live;
             JoinSum sum;
-            for (int c = g - 1; c <= last; c += 2) {
+            for (int c = first; c <= last; c += 2) {
                 const int64_t p0 = part_of(c), p1 = part_of(min(c + 1, last));
                 const float2 ml0 = A.part_ml[p0 * A.MT + r], ml1 = A.part_ml[p1 * A.MT + r];
                 const float4 o0 = A.part_o[(p0 * D4 + d4) * A.MT + r], o1 = A.part_o[(p1 * D4 + d4) * A.MT + r];
@@ -339,11 +342,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         }
         return;
     }
-    for (int x0 = blockIdx.z * 32; x0 < work; x0 += gridDim.z * 32) {
+    for (int x0 = block * 32; x0 < work; x0 += blocks * 32) {
         const int x = x0 + lane, d4 = x / live, r = x - d4 * live;
         JoinSum sum;
         if (x < work)
-            for (int c = g - 1 + pl; c <= last; c += kJoinLanes) {
+            for (int c = first + pl; c <= last; c += kJoinLanes) {
                 const int64_t part = part_of(c);
                 sum.add(A.part_ml[part * A.MT + r], A.part_o[(part * D4 + d4) * A.MT + r]);
             }
