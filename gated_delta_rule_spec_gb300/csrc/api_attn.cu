@@ -112,8 +112,9 @@ int check_attn(const gdn_spec_kv_cache *c, int32_t B, int32_t T, int32_t HQ) {
     if (rc) return rc;
     if (B < 0 || T <= 0 || HQ <= 0 || HQ % c->HKV != 0) return GDN_SPEC_EINVAL;
     if (T > kTreeMax || HQ / c->HKV > 4096) return GDN_SPEC_EUNSUPPORTED;
-    // the line of key/value tiles (of 32 tokens, a row's last one begun) and the tokens are counted in 31 bits
-    if ((double)B * (((int64_t)c->max_pages * c->P + 31) / 32) * c->HKV > 2.0e9) return GDN_SPEC_EUNSUPPORTED;
+    // the line of key/value tiles (of 32 tokens, a row's last one begun, and gaps of at most 8) and the tokens are
+    // counted in 31 bits
+    if ((double)B * (((int64_t)c->max_pages * c->P + 31) / 32 + 8) * c->HKV > 2.0e9) return GDN_SPEC_EUNSUPPORTED;
     if ((int64_t)B * T > INT32_MAX) return GDN_SPEC_EUNSUPPORTED;
     return GDN_SPEC_OK;
 }

@@ -4,12 +4,13 @@
 // An item is one (batch row, kv head): its query rows are the row's cnt drafted
 // tokens times the G heads of the group (row r is token r / G, head r % G), cut into
 // query tiles of MT rows, and it is a run of `tiles` key/value tiles of TN tokens.
-// Items stand in one line, rows first, and the line of W tiles is cut into equal
-// chunks, one for each group of NQT blocks (one block per query tile of the
-// item, so the blocks that read the same keys and values run side by side and share
-// them in L2).  So ragged rows, few rows with long contexts and many short ones all
-// spread evenly over the machine, and every block finds its chunk from the
-// lengths on the device: nothing about them is known on the host.  A chunk that
+// Items stand in one line, rows first, each behind a gap of as many tiles as an item
+// costs besides its tiles, and the line is cut into equal chunks, one for each group
+// of NQT blocks (one block per query tile of the item, so the blocks that read the
+// same keys and values run side by side and share them in L2).  So ragged rows, few
+// rows with long contexts and many short ones all spread evenly over the machine,
+// and every block finds its chunk from the lengths on the device: nothing about
+// them is known on the host.  A chunk that
 // starts or ends inside an item leaves an unnormalised piece in the workspace (at
 // most two a block), and the join kernel merges an item's pieces in order, so the
 // result does not depend on timing.
@@ -32,7 +33,7 @@ struct AttnArgs {
     float4 *part_o;            // [groups * NQT][2][D / 4][MT] unnormalised sums of a piece
     float2 *part_ml;           // [groups * NQT][2][MT] (maximum in log2 units, sum)
     struct AttnCut *cuts;      // [groups] where each chunk starts, for the join
-    int TN, MT, NQT, groups, min_chunk;
+    int TN, MT, NQT, groups, min_chunk, gap;
     bool whole;                // tensor-core kernel: a copy holds all dims of a tile
     uint32_t wait_limit;
 };
@@ -54,9 +55,15 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs &A, const AttnRow &r) {
     return r.cnt > 0 ? (int)(((int64_t)r.len + r.cnt + A.TN - 1) / A.TN) : 0;
 }
 
-// Place of a tile of the line: the row it is in, and which of the row's tiles.
+// Length of a row's part of the line.
+__device__ __forceinline__ int attn_span(const AttnArgs &A, const AttnRow &r) {
+    const int tiles = attn_tiles(A, r);
+    return tiles > 0 ? (tiles + A.gap) * A.C.HKV : 0;
+}
+
+// A place of the line: the row it is in, and where in the row's part.
 struct AttnPlan {
-    int total, chunk;          // W, tiles of a chunk
+    int total, chunk;          // length of the line and of a chunk
     int b, off;                // of the asked place (b = -1: past the end)
 };
 
@@ -86,7 +93,7 @@ __device__ __forceinline__ int attn_scan(int x, int *scratch, int *before) {
     return sum;
 }
 
-// By all threads of a block: the line's length and the place of tile
+// By all threads of a block: the line's length and the place
 // group * chunk.  `report`: record the rows' status bits.
 template <int THREADS>
 __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &A, int group, bool report, int *scratch) {
@@ -101,7 +108,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &A, int group, bool
             uint32_t bits;
             const AttnRow r = attn_row(A, b0 + tid, &bits);
             if (bits && report) atomicOr(A.C.status, bits);
-            x = attn_tiles(A, r) * A.C.HKV;
+            x = attn_span(A, r);
         }
         const int sum = attn_scan<THREADS>(x, scratch, &ex);
         if (b0 == 0) { mine = x; before = ex; }
@@ -119,7 +126,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &A, int group, bool
                 x = 0;
                 if (b0 + tid < A.B) {
                     uint32_t bits;
-                    x = attn_tiles(A, attn_row(A, b0 + tid, &bits)) * A.C.HKV;
+                    x = attn_span(A, attn_row(A, b0 + tid, &bits));
                 }
             }
             int sum = 0;
@@ -145,15 +152,14 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &A, int group, bool
 struct AttnPiece {
     int b, slot, len, cnt, h;
     int t0, t1, tiles;         // key/value tiles [t0, t1) of the item's `tiles`
-    int side;                  // which of the block's two pieces it would be kept as
+    int side;                  // which of the block's two pieces it would be kept as: 1 if it starts its item
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
 // Keeps the row between its heads: a row's counts are three dependent loads.
 struct AttnWalk {
     AttnRow row;
-    int b, h, t, tiles, left;   // next tile; left: tiles of the chunk not yet handed out
-    bool first;
+    int b, h, t, tiles, left;   // next tile; left: what is left of the chunk
     __device__ __forceinline__ void load(const AttnArgs &A) {
         uint32_t bits;
         row = attn_row(A, b, &bits);
@@ -164,6 +170,8 @@ struct AttnWalk {
         if (t == tiles) {
             t = 0;
             ++h;
+            left -= A.gap;
+            if (left <= 0) return false;
         }
         if (h >= A.C.HKV) {
             h = 0;
@@ -180,8 +188,7 @@ struct AttnWalk {
         piece->t0 = t;
         piece->t1 = min(tiles, t + left);
         piece->tiles = tiles;
-        piece->side = first ? 0 : 1;
-        first = false;
+        piece->side = t == 0;
         left -= piece->t1 - t;
         t = piece->t1;
         return true;
@@ -200,14 +207,14 @@ __device__ __forceinline__ void attn_note(const AttnArgs &A, int group, bool any
 
 __device__ __forceinline__ AttnWalk attn_walk(const AttnArgs &A, const AttnPlan &p, int group) {
     AttnWalk w;
-    w.first = true;
     w.left = 0;
     if (p.b < 0) return w;
     w.b = p.b;
     w.load(A);
-    w.h = p.off / w.tiles;
-    w.t = p.off - w.h * w.tiles;
-    w.left = (int)min((int64_t)p.chunk, (int64_t)p.total - (int64_t)group * p.chunk);
+    w.h = p.off / (w.tiles + A.gap);
+    const int in_item = p.off - w.h * (w.tiles + A.gap) - A.gap;   // < 0: in the gap before the item
+    w.t = max(in_item, 0);
+    w.left = min(in_item, 0) + (int)min((int64_t)p.chunk, (int64_t)p.total - (int64_t)group * p.chunk);
     return w;
 }
 

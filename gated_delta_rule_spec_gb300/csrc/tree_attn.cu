@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     grid_dep_wait();
     const int g = blockIdx.x + 1, qt = blockIdx.y, tid = threadIdx.x, lane = tid & 31, pl = tid >> 5;
     const AttnCut cut = A.cuts[g];
-    const int64_t s = (int64_t)g * cut.chunk - cut.t;                // the item's first tile in the line
+    const int64_t s = (int64_t)g * cut.chunk - cut.t;   // the place of the item's first tile
     if (cut.b < 0 || cut.t == 0) return;   // a cut between items
     const int first = (int)(s / cut.chunk);
     const int live = min(A.MT, cut.cnt * A.G - qt * A.MT);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int last = (int)((s + cut.tiles - 1) / cut.chunk);
     const int D4 = A.C.D >> 2, work = live * D4;
     const int block = (g - 1 - first) * gridDim.z + blockIdx.z, blocks = (last - first) * gridDim.z;   // of the item
-    const auto part_of = [&](int c) { return ((int64_t)c * A.NQT + qt) * 2 + (s > (int64_t)c * cut.chunk ? 1 : 0); };
+    const auto part_of = [&](int c) { return ((int64_t)c * A.NQT + qt) * 2 + (c == first ? 1 : 0); };
     if (last - first + 1 < kJoinMany) {
         for (int x = block * kJoinThreads + tid; x < work; x += blocks * kJoinThreads) {
             const int d4 = x / live, r = x - d4 * live;
@@ -421,6 +421,7 @@ void tree_attn_cut(AttnArgs *A, int sms, int es) {
     const int groups = sms * per_sm / A->NQT;
     A->groups = groups < 1 ? 1 : groups;
     A->min_chunk = 2;
+    A->gap = 1;   // an item's queries, merge and way out take about as long as a tile
 }
 
 cudaError_t launch_tree_attn(const AttnArgs &A, bool bf16, cudaStream_t st) {

@@ -520,7 +520,7 @@ int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache
  * Two kernels (gdn_spec_tree_attn_path): "tc" -- bf16, at most 128 query heads a kv
  * head: TMA and tcgen05, the probabilities rounded to bf16 for the second
  * product; "generic" -- otherwise: fp32 throughout on the CUDA cores.  1 <= T <= 64; B * T is
- * below 2^31, and B * HKV times the tiles of 32 tokens that a slot can hold is at most 2e9.
+ * below 2^31, and B * HKV times (8 + the tiles of 32 tokens that a slot can hold) at most 2e9.
  * Device status: SLOT_OOR, ACCEPT_RANGE (tree_len), CURSOR_CORRUPT, NO_PAGES (the row
  * gives zeros), PAGE_OOR, TIMEOUT.
  */
