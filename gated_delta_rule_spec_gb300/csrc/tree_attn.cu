@@ -9,16 +9,16 @@
 //
 // A block holds MT query rows and walks tiles of 32 keys, copied asynchronously into
 // one of two buffers while the other is worked on.  Four warps share a tile, eight
-// keys each, and with 16 or 32 rows two such fours halve the rows: every warp keeps
+// keys each, and from 16 rows on two such fours halve the rows: every warp keeps
 // a running maximum and sum of its own for its rows and keys, and the four are
 // merged in shared memory at the end of a piece.  So a key or value is read from
 // shared memory by one or two warps only.  Of a warp's scores lane (g, k) forms rows
 // g, g + 4, ... with key k; the maximum is a shuffle over eight lanes, and the sums
 // run over output columns, VEC consecutive ones per lane.  Rows of keys and queries
 // are padded by 16 bytes, so that the pieces read together fall in different banks.
-// 16 sequences of 5000 tokens, 4 heads of 128 fp32, 8 drafts: 71 us, 3.5 TB/s, half of
+// 16 sequences of 5000 tokens, 4 heads of 128 fp32, 8 drafts: 69 us, 3.6 TB/s, half of
 // HBM's rate, with the issue slots 58% and the shared-memory pipe 53% busy; 8 of them
-// with 32 rows a head: 109 us, where a warp's 16 multiply-adds for 5 wide reads take
+// with 32 rows a head: 86 us, where a warp's 16 multiply-adds for 5 wide reads take
 // 8.7 wavefronts and the pipe is busy 72% of a tile.
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
@@ -375,11 +375,14 @@ cudaError_t launch_attn_join(const AttnArgs &A, bool bf16, cudaStream_t stream) 
 
 // ------------------------------------------------------------------ launch
 
-// Rows of a block's query tile: the fewest of 4, 8, 16 and 32 that hold the window.  Sixteen rows take two fours of
-// warps: with one four of sixteen rows a warp, 8 sequences of 5000 tokens, 4 shared heads of 128 fp32, 8 drafts were
-// 80 us against 66.
-static int tile_rows(int R) { return R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32; }
-static constexpr int fours(int MT) { return MT <= 8 ? 1 : 2; }
+// Rows of a block's query tile: the fewest of 4, 8, 12, 16, 24 and 32 that hold the window; longer windows take tiles of
+// 32, or two of 24 (against the next larger tile, geometric means of fp32 shapes: 12 rows 33.7 and 41.1 us, 24 rows
+// 34.3 and 40.0 us).  From 16 rows on there are two fours of warps: with one of sixteen rows a warp, 8 sequences of 5000
+// tokens, 4 shared heads of 128 fp32, 8 drafts x 2 heads were 80 us against 66.
+static int tile_rows(int R) {
+    return R <= 4 ? 4 : R <= 8 ? 8 : R <= 12 ? 12 : R <= 16 ? 16 : R <= 24 || (R > 32 && R <= 48) ? 24 : 32;
+}
+static constexpr int fours(int MT) { return MT <= 12 ? 1 : 2; }
 
 template <typename IO, int MT, int VEC, int NG>
 static cudaError_t run_tree_attn(const AttnArgs &A, cudaStream_t st) {
@@ -404,7 +407,9 @@ static cudaError_t run_rows(const AttnArgs &A, cudaStream_t st) {
     switch (A.MT) {
         case 4: return run_cols<IO, 4>(A, st);
         case 8: return run_cols<IO, 8>(A, st);
+        case 12: return run_cols<IO, 12>(A, st);
         case 16: return run_cols<IO, 16>(A, st);
+        case 24: return run_cols<IO, 24>(A, st);
         default: return run_cols<IO, 32>(A, st);
     }
 }

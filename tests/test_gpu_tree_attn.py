@@ -323,7 +323,9 @@ def test_the_same_call_gives_the_same_bits():
 @pytest.mark.parametrize("io,T,HQ,HKV,D,P", [
     ("fp32", 1, 4, 1, 128, 64), ("fp32", 2, 4, 2, 256, 16), ("fp32", 4, 1, 1, 136, 32),      # 4 rows a tile
     ("fp32", 2, 8, 2, 64, 16), ("fp32", 7, 2, 2, 128, 128),                                  # 8
+    ("fp32", 3, 8, 2, 128, 16), ("fp32", 6, 4, 2, 256, 64), ("fp32", 11, 1, 1, 64, 32),      # 12
     ("fp32", 16, 2, 2, 200, 64), ("fp32", 3, 10, 2, 64, 16),                                 # 16
+    ("fp32", 6, 4, 1, 64, 16), ("fp32", 8, 3, 1, 256, 64), ("fp32", 5, 18, 2, 128, 32),      # 24, once and twice
     ("fp32", 9, 8, 2, 256, 32), ("fp32", 64, 3, 1, 128, 256), ("fp32", 17, 2, 1, 24, 16),    # 32, several tiles
     ("bf16", 2, 130, 1, 128, 32), ("bf16", 1, 300, 2, 64, 16), ("bf16", 3, 129, 1, 256, 64)])
 def test_the_cuda_core_kernel(io, T, HQ, HKV, D, P):
