@@ -10,12 +10,15 @@
 // fp32 accuracy.  No table of positions is kept.
 //
 // Bound by HBM: every q, k, v element is read once and written once.  A block takes
-// one or four tokens: its threads first form the tokens' cos and sin
+// one to sixteen tokens: its threads first form the tokens' cos and sin
 // (rot / 2 pairs a token, shared by all heads) in shared memory, then turn 16
 // elements of one head each (two runs of 8, a pair's halves in the half
-// layout).  The SM's other blocks cover a block's set-up; loading a thread's next
-// unit before this one's arithmetic took the registers for that: 146 us against
-// 134 us (8 x 4096 tokens, 32 + 2 x 8 heads of 128, bf16: 0.88 of the copy bandwidth).
+// layout).  The SM's other blocks cover a block's set-up, so registers are held to
+// eight blocks an SM in bf16 (128 windows of 8 tokens, 16 + 2 x 2 heads of 256: 5.8 us,
+// 7.3 with five) and six in fp32; loading a thread's next unit before this one's
+// arithmetic took the registers for that and was slower.  8 x 4096 tokens, 32 + 2 x 8
+// heads of 128, bf16: 124 us, 0.96 of the copy bandwidth (134 us with a token's cos
+// and sin in the order of the pairs, where a warp's reads met in the same banks).
 #include "kv_common.cuh"
 #include "launch_setup.cuh"
 
@@ -23,7 +26,8 @@ namespace gdnspec {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxPairs = 128;
-constexpr int kRopeTokens = 4;   // tokens of a block when there are many
+constexpr int kRopeTokens = 16;   // tokens of a block at most
+__host__ __device__ constexpr int rope_blocks(size_t es) { return es == 2 ? 8 : 6; }   // of an SM
 
 struct RopeArgs {
     int D, rot, pairs;
@@ -86,31 +90,36 @@ template <> struct Run8<float> {
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
 };
 
+// Where pair i's cos and sin stand among a token's: units of eight pairs are spread so that a warp's lanes, which turn
+// neighbouring units, read neighbouring 16 bytes (two pairs).
+template <bool UNITS> __device__ __forceinline__ int turn_place(int i, int pairs) {
+    return UNITS ? ((i & 7) >> 1) * (pairs >> 2) + (i >> 3) * 2 + (i & 1) : i;
+}
+
 // One unit of a head: the two runs at offsets o0 and o1, turned by the pairs
-// from `pair` on when `turn` (interleaved: run 0 holds pairs pair..pair+3, run 1
-// the next four; half: pairs pair..pair+7 across the runs).
+// of unit u (interleaved: run 0 holds its first four pairs, run 1 the others;
+// half: all of them across the runs).
 template <typename IO, bool HALF>
-__device__ __forceinline__ void turn_unit(Run8<IO> &r0, Run8<IO> &r1, const float2 *cs, float sign) {
+__device__ __forceinline__ void turn_unit(Run8<IO> &r0, Run8<IO> &r1, const float2 *cs, int u, int pairs, float sign) {
     float x[8], y[8];
     r0.get(x);
     r1.get(y);
-    if (HALF) {
+    const auto turn = [sign](float &a, float &b, float c, float s) {
+        s *= sign;
+        const float a0 = a, b0 = b;
+        a = a0 * c - b0 * s;
+        b = a0 * s + b0 * c;
+    };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = cs[i].x, s = cs[i].y * sign, a = x[i], b = y[i];
-            x[i] = a * c - b * s;
-            y[i] = a * s + b * c;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float c = cs[i].x, s = cs[i].y * sign, c2 = cs[i + 4].x, s2 = cs[i + 4].y * sign;
-            float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * c - b * s;
-            x[2 * i + 1] = a * s + b * c;
-            a = y[2 * i], b = y[2 * i + 1];
-            y[2 * i] = a * c2 - b * s2;
-            y[2 * i + 1] = a * s2 + b * c2;
+    for (int k = 0; k < 4; ++k) {
+        const float4 t = *reinterpret_cast<const float4 *>(cs + k * (pairs >> 2) + u * 2);
+        if (HALF) {
+            turn(x[2 * k], y[2 * k], t.x, t.y);
+            turn(x[2 * k + 1], y[2 * k + 1], t.z, t.w);
+        } else {
+            float *const z = k < 2 ? x + 4 * k : y + 4 * (k - 2);
+            turn(z[0], z[1], t.x, t.y);
+            turn(z[2], z[3], t.z, t.w);
         }
     }
     r0.put(x);
@@ -145,16 +154,16 @@ __device__ __forceinline__ void turn_scalar(const IO *x, IO *y, const float2 *cs
 // x and out may be the same memory (each unit reads what it writes, before it
 // writes), so neither is __restrict__.
 template <typename IO, bool HALF, bool UNITS>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs R, int N, int heads, int tokens,
+__global__ void __launch_bounds__(kRopeThreads, rope_blocks(sizeof(IO))) rope_kernel(const __grid_constant__ RopeArgs R, int N, int heads, int tokens,
                                                             const int32_t *__restrict__ pos, const IO *x,
                                                             int64_t x_stride, IO *out, int64_t out_stride, float sign) {
-    __shared__ float2 cs[kRopeTokens][kRopeMaxPairs];
+    extern __shared__ __align__(16) float2 cs[];   // [tokens][pairs], see turn_place
     const int n0 = blockIdx.x * tokens, tid = threadIdx.x;
     const int live = min(tokens, N - n0);
     grid_dep_wait();
     for (int j = tid; j < live * R.pairs; j += kRopeThreads) {
         const int t = j / R.pairs, i = j - t * R.pairs;
-        cs[t][i] = rope_turn(R, pos[n0 + t], i);
+        cs[t * R.pairs + turn_place<UNITS>(i, R.pairs)] = rope_turn(R, pos[n0 + t], i);
     }
     __syncthreads();
     if (UNITS) {
@@ -168,7 +177,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             Run8<IO> r0, r1;
             r0.load(xp + o0);
             r1.load(xp + o1);
-            if (u < turning) turn_unit<IO, HALF>(r0, r1, &cs[t][u * 8], sign);
+            if (u < turning) turn_unit<IO, HALF>(r0, r1, cs + t * R.pairs, u, R.pairs, sign);
             r0.store(op + o0);
             r1.store(op + o1);
         }
@@ -176,7 +185,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         const int per_head = R.D - R.pairs, per_token = heads * per_head;
         for (int j = tid; j < live * per_token; j += kRopeThreads) {
             const int t = j / per_token, r = j - t * per_token, h = r / per_head, e = r - h * per_head;
-            turn_scalar<IO, HALF>(x + (n0 + t) * x_stride + h * R.D, out + (n0 + t) * out_stride + h * R.D, cs[t],
+            turn_scalar<IO, HALF>(x + (n0 + t) * x_stride + h * R.D, out + (n0 + t) * out_stride + h * R.D, cs + t * R.pairs,
                                   R.rot, R.D, sign, e);
         }
     }
@@ -187,12 +196,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 // key goes, or that it is dead) is decided by one thread per token beside the
 // cos and sin.
 template <typename IO, bool HALF, bool UNITS>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(
+__global__ void __launch_bounds__(kRopeThreads, rope_blocks(sizeof(IO))) rope_append_kernel(
     const __grid_constant__ RopeArgs R, const __grid_constant__ KvArgs C, int layer, int B, int T, int tokens, int HQ,
     const int32_t *__restrict__ slot_idx, const int32_t *__restrict__ n_tokens, const int32_t *__restrict__ pos,
     const IO *__restrict__ q, int64_t q_stride, const IO *__restrict__ k, int64_t k_stride, const IO *__restrict__ v,
     int64_t v_stride, IO *__restrict__ q_out) {
-    __shared__ float2 cs[kRopeTokens][kRopeMaxPairs];
+    extern __shared__ __align__(16) float2 cs[];   // [tokens][pairs], see turn_place
     __shared__ int64_t row_s[kRopeTokens];   // the token's row in the pool, -1: its q is zero and nothing is written
     __shared__ int pos_s[kRopeTokens];
     const int tid = threadIdx.x;
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(
     __syncthreads();
     for (int j = tid; j < live * R.pairs; j += kRopeThreads) {
         const int t = j / R.pairs, i = j - t * R.pairs;
-        cs[t][i] = rope_turn(R, pos_s[t], i);
+        cs[t * R.pairs + turn_place<UNITS>(i, R.pairs)] = rope_turn(R, pos_s[t], i);
     }
     __syncthreads();
     const int heads = HQ + 2 * C.HKV;
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(
             } else {
                 r0.load(src + o0);
                 r1.load(src + o1);
-                if (u < turning && !is_v) turn_unit<IO, HALF>(r0, r1, &cs[t][u * 8], 1.0f);
+                if (u < turning && !is_v) turn_unit<IO, HALF>(r0, r1, cs + t * R.pairs, u, R.pairs, 1.0f);
             }
             r0.store(dst + o0);
             r1.store(dst + o1);
@@ -263,13 +272,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(
                 dst[i1] = row < 0 ? from_f32<IO>(0.0f) : src[i1];
             }
         } else {
-            turn_scalar<IO, HALF>(src, dst, cs[t], R.rot, R.D, 1.0f, u);
+            turn_scalar<IO, HALF>(src, dst, cs + t * R.pairs, R.rot, R.D, 1.0f, u);
         }
     }
 }
 
-// Four tokens a block once that still gives every SM several blocks.
-static int tokens_per_block(int64_t n) { return n >= 4096 ? kRopeTokens : 1; }
+// Four tokens a block once that still gives every SM several blocks, and more while they do not fill the block's threads
+// twice (n tokens of `units` units each).  82 x 725 tokens, 6 + 2 x 2 heads of 128 bf16, 80 units: 71 us with four, 63
+// with eight; 54 x 1141 tokens, 3 + 2 heads of 64, 20 units: 37 us with four, 27 with sixteen.
+static int tokens_per_block(int64_t n, int units) {
+    int t = n >= 4096 ? 4 : 1;
+    while (t >= 4 && t < kRopeTokens && t * units < 2 * kRopeThreads && n >= 4096 * t) t *= 2;
+    return t;
+}
 
 RopeArgs rope_args(const gdn_spec_rope_plan *p) {
     RopeArgs R;
@@ -284,8 +299,8 @@ RopeArgs rope_args(const gdn_spec_rope_plan *p) {
 template <typename IO, bool HALF, bool UNITS>
 static cudaError_t run_rope(const RopeArgs &R, int N, int heads, const int32_t *pos, const void *x, int64_t x_stride,
                             void *out, int64_t out_stride, bool transpose, cudaStream_t st) {
-    const int tokens = tokens_per_block(N);
-    return launch_dependent(rope_kernel<IO, HALF, UNITS>, dim3((N + tokens - 1) / tokens), dim3(kRopeThreads), 0, st, R, N,
+    const int tokens = tokens_per_block(N, heads * R.D / 16);
+    return launch_dependent(rope_kernel<IO, HALF, UNITS>, dim3((N + tokens - 1) / tokens), dim3(kRopeThreads), tokens * R.pairs * sizeof(float2), st, R, N,
                             heads, tokens, pos, static_cast<const IO *>(x), x_stride, static_cast<IO *>(out), out_stride,
                             transpose ? -1.0f : 1.0f);
 }
@@ -309,9 +324,9 @@ static cudaError_t run_append(const RopeArgs &R, const KvArgs &C, int layer, con
                               const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *q_out,
                               cudaStream_t st) {
     const int64_t all = (int64_t)B * T;
-    const int tokens = tokens_per_block(all);
+    const int tokens = tokens_per_block(all, (HQ + 2 * C.HKV) * C.D / 16);
     return launch_dependent(rope_append_kernel<IO, HALF, UNITS>, dim3((unsigned)((all + tokens - 1) / tokens)),
-                            dim3(kRopeThreads), 0, st, R, C, layer, B, T, tokens, HQ, slot_idx, n_tokens, pos,
+                            dim3(kRopeThreads), tokens * R.pairs * sizeof(float2), st, R, C, layer, B, T, tokens, HQ, slot_idx, n_tokens, pos,
                             static_cast<const IO *>(q), q_stride, static_cast<const IO *>(k), k_stride,
                             static_cast<const IO *>(v), v_stride, static_cast<IO *>(q_out));
 }
