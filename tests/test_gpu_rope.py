@@ -182,3 +182,24 @@ def test_append_refusals():
                 lambda: binding.rope_append(plan, cache, 0, slots, q.transpose(1, 2), k, v)):
         with pytest.raises(binding.GdnSpecError):
             bad()
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n,heads,D,rot", [(33001, 1, 64, 64), (17003, 2, 128, 48), (33005, 1, 40, 24), (16387, 3, 256, 256)])
+def test_many_tokens_of_few_heads(io, layout, n, heads, D, rot):
+    """Blocks of eight and sixteen tokens, the last one short."""
+    rng = np.random.default_rng(6)
+    x = ref.draw(rng, (n, heads, D), io)
+    pos = rng.integers(0, 200000, n).astype(np.int32)
+    got = binding.rope(binding.RopePlan(D, rot, layout=layout), torch.from_numpy(pos).cuda(), x.cuda())
+    f, m = ref.frequencies(rot)
+    x64 = x.double().numpy()
+    close(got.double().cpu().numpy(), ref.rotate(x64, pos, f, m, rot, layout), x64, io, m, rot, layout)
+
+
+@pytest.mark.parametrize("io,T,HQ,HKV,D,rot,P,layout", [
+    ("bf16", 6700, 1, 1, 32, 16, 128, "half"), ("fp32", 4100, 2, 1, 64, 64, 64, "interleaved"),
+    ("bf16", 6601, 1, 1, 24, 20, 32, "interleaved")])
+def test_append_many_tokens_of_few_heads(io, T, HQ, HKV, D, rot, P, layout):
+    test_append(io, T, HQ, HKV, D, rot, P, layout, False)
