@@ -346,9 +346,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         const int x = x0 + lane, d4 = x / live, r = x - d4 * live;
         JoinSum sum;
         if (x < work)
-            for (int c = first + pl; c <= last; c += kJoinLanes) {
-                const int64_t part = part_of(c);
-                sum.add(A.part_ml[part * A.MT + r], A.part_o[(part * D4 + d4) * A.MT + r]);
+            for (int c = first + pl; c <= last; c += 4 * kJoinLanes) {   // four pieces' loads in flight
+                float2 ml[4];
+                float4 o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t part = part_of(min(c + k * kJoinLanes, last));
+                    ml[k] = A.part_ml[part * A.MT + r];
+                    o[k] = A.part_o[(part * D4 + d4) * A.MT + r];
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + k * kJoinLanes <= last) sum.add(ml[k], o[k]);
             }
         o_s[pl][lane] = sum.o;
         ml_s[pl][lane] = make_float2(sum.m, sum.l);
