@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     grid_dep_launch();
     const int tid = threadIdx.x;
     const int words = (C.num_pages + 31) >> 5;
+    const uint32_t first = tid < words ? C.free_bits[tid] : 0u;   // on its way while the rows' chain of loads runs
+    bool mine_ok = false;                                         // of row tid
     int total = 0;
     for (int b0 = 0; b0 < B; b0 += kAllocThreads) {
         const int b = b0 + tid;
@@ -121,6 +123,7 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
         if (b < B) {
             ends[b + 1] = total + before + d.need;
             done[b] = d.ok ? 1 : 0;
+            if (b0 == 0) mine_ok = d.ok;
         }
         total += chunk;
     }
@@ -128,8 +131,8 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     // free pages, counted only when something is asked for
     int avail = 0;
     if (total > 0) {
-        int mine = 0;
-        for (int w = tid; w < words; w += kAllocThreads) mine += __popc(C.free_bits[w]);
+        int mine = __popc(first);
+        for (int w = tid + kAllocThreads; w < words; w += kAllocThreads) mine += __popc(C.free_bits[w]);
         block_scan(mine, warp_sums, &avail);
     }
     __syncthreads();
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     int base = 0;
     for (int w0 = 0; w0 < words && base < give; w0 += kAllocThreads) {
         const int w = w0 + tid;
-        const uint32_t bits = w < words ? C.free_bits[w] : 0u;
+        const uint32_t bits = w0 == 0 ? first : w < words ? C.free_bits[w] : 0u;
         int chunk;
         const int before = block_scan(__popc(bits), warp_sums, &chunk);   // of the slice's words below
         word_s[tid] = bits;
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     }
     __syncthreads();   // the counts were read above
     for (int b = tid; b < B; b += kAllocThreads) {
-        if (!done[b]) continue;
+        if (b == tid ? !mine_ok : !done[b]) continue;
         const int need = ends[b + 1] - ends[b];
         if (need > 0 && ends[b + 1] > give) {
             done[b] = 0;
