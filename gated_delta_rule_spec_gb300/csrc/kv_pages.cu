@@ -12,7 +12,7 @@
 // million pages) to count what is free, then walks it in slices of 1024 words
 // until the rows' demand is met.  Within a slice every page that is handed out has a
 // thread of its own, which finds its bit and its row by bisection (a thread per
-// word took 16 us for 512 pages, this takes 7 us).
+// word took 16 us for 512 pages, this takes 6 us).
 // Everything that moves key/value rows is a launch of its own over the whole
 // machine, bound by HBM.
 #include "kv_common.cuh"
