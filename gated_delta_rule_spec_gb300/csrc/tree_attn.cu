@@ -16,9 +16,9 @@
 // g, g + 4, ... with key k; the maximum is a shuffle over eight lanes, and the sums
 // run over output columns, VEC consecutive ones per lane.  Rows of keys and queries
 // are padded by 16 bytes, so that the pieces read together fall in different banks.
-// 16 sequences of 5000 tokens, 4 heads of 128 fp32, 8 drafts: 69 us, 3.6 TB/s, half of
+// 16 sequences of 5000 tokens, 4 heads of 128 fp32, 8 drafts: 73 us, 3.4 TB/s, half of
 // HBM's rate, with the issue slots 58% and the shared-memory pipe 53% busy; 8 of them
-// with 32 rows a head: 86 us, where a warp's 16 multiply-adds for 5 wide reads take
+// with 32 rows a head: 87 us, where a warp's 16 multiply-adds for 5 wide reads take
 // 8.7 wavefronts and the pipe is busy 72% of a tile.
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
@@ -79,9 +79,11 @@ template <> __device__ __forceinline__ float2 load2<__nv_bfloat16>(const __nv_bf
     return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
 }
 
+__device__ __forceinline__ uint32_t smem_of(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
 // Sixteen bytes from global to shared memory; zeros where !live.
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(live ? 16 : 0)
                  : "memory");
 }
@@ -131,7 +133,8 @@ __global__ void __launch_bounds__(32 * kSplit * WR, attn_blocks(WR, RW, NG)) tre
     constexpr int kThreads = 32 * kSplit * WR, MT = WR * RW, R = RW / 4;
     constexpr int kPiece = 16 / sizeof(IO);                                     // elements of 16 bytes
     constexpr int kCopied = kAttnTile * 32 / kThreads;                          // tokens that a warp copies
-    constexpr int kLanes = NG * 32 * VEC / kPiece < 32 ? NG * 32 * VEC / kPiece : 32;   // lanes that copy a token
+    constexpr int kRun = NG * 32 * VEC / kPiece, kLanes = kRun < 32 ? kRun : 32;   // pieces of a token, lanes that copy it
+    constexpr int kSteps = kRun / kLanes;
     constexpr int kChains = R == 1 ? 4 : R == 2 ? 2 : 1;   // sums of a score, so that their additions overlap
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int scratch[kAttnScratch];
@@ -148,6 +151,9 @@ __global__ void __launch_bounds__(32 * kSplit * WR, attn_blocks(WR, RW, NG)) tre
     const int group = blockIdx.x / A.NQT, qt = blockIdx.x - group * A.NQT;
     float *const my_p = Ps + warp * RW * kWarpKeys;
     const IO *const my_q = Qs + (r0 + rg) * KLD;
+    const int at = lane % kLanes * kPiece;                   // the lane's element of the tokens that it copies
+    const uint32_t k_dst = smem_of(Ks + (warp * kCopied + lane / kLanes) * KLD + at);
+    const uint32_t v_dst = smem_of(Vs + (warp * kCopied + lane / kLanes) * D + at);
     grid_dep_wait();
 
     attn_dead_rows<IO>(A, blockIdx.x, gridDim.x, tid, kThreads);
@@ -161,6 +167,7 @@ __global__ void __launch_bounds__(32 * kSplit * WR, attn_blocks(WR, RW, NG)) tre
         if (live <= 0) continue;
         const int kv = pc.len + pc.cnt, pieces = D / kPiece;
         const int fr = warp * kCopied + lane % kCopied;   // this lane looks up that token of a tile
+        const bool together = A.C.P >= kAttnTile;
         const auto page_of = [&](int t) {   // of this thread's token of tile t
             const int tok = t * kAttnTile + fr;
             return t < pc.t1 && tok < kv ? A.C.page_table[(int64_t)pc.slot * A.C.max_pages + (tok >> A.C.logP)] : 0;
@@ -170,17 +177,25 @@ __global__ void __launch_bounds__(32 * kSplit * WR, attn_blocks(WR, RW, NG)) tre
             const bool ok = page >= 0 && page < A.C.num_pages, there = tok < kv && ok;
             if (tok < kv && !ok) atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
             const int64_t mine = there ? kv_elem(A.C, A.layer, pc.h, ((int64_t)page << A.C.logP) + (tok & (A.C.P - 1))) : -1;
+            // Rows past the end are zeros, whatever the page holds there.  Where a page holds a tile its rows follow the
+            // warp's first one.
+            const int64_t start = together ? __shfl_sync(0xffffffffu, mine, 0) : 0;
+            const int left = kv - t * kAttnTile - warp * kCopied;
+            const uint32_t kd = k_dst + buf * kAttnTile * KLD * (uint32_t)sizeof(IO);
+            const uint32_t vd = v_dst + buf * kAttnTile * D * (uint32_t)sizeof(IO);
 #pragma unroll
             for (int i = 0; i < kCopied; i += 32 / kLanes) {
                 const int r = i + lane / kLanes;
-                int64_t e = __shfl_sync(0xffffffffu, mine, r);
-                const bool live_row = e >= 0;   // rows past the end are zeros, whatever the page holds there
-                if (!live_row) e = 0;
-                const IO *k = static_cast<const IO *>(A.C.k) + e, *v = static_cast<const IO *>(A.C.v) + e;
-                IO *kd = Ks + (buf * kAttnTile + warp * kCopied + r) * KLD, *vd = Vs + (buf * kAttnTile + warp * kCopied + r) * D;
-                for (int c = lane % kLanes; c < pieces; c += kLanes) {
-                    copy16(kd + c * kPiece, k + c * kPiece, live_row);
-                    copy16(vd + c * kPiece, v + c * kPiece, live_row);
+                int64_t e = together ? (r < left ? start : -1) : __shfl_sync(0xffffffffu, mine, r);
+                const bool live_row = e >= 0;
+                if (together) e = max(start, (int64_t)0) + r * D;
+                else if (!live_row) e = 0;
+                const IO *k = static_cast<const IO *>(A.C.k) + e + at, *v = static_cast<const IO *>(A.C.v) + e + at;
+#pragma unroll
+                for (int c = 0; c < kSteps; ++c) {
+                    if (at + c * kLanes * kPiece >= D) break;
+                    copy16(kd + (i * KLD + c * kLanes * kPiece) * (uint32_t)sizeof(IO), k + c * kLanes * kPiece, live_row);
+                    copy16(vd + (i * D + c * kLanes * kPiece) * (uint32_t)sizeof(IO), v + c * kLanes * kPiece, live_row);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -189,7 +204,7 @@ __global__ void __launch_bounds__(32 * kSplit * WR, attn_blocks(WR, RW, NG)) tre
         __syncthreads();   // the piece before is done with shared memory
         for (int r = warp * (32 / kLanes) + lane / kLanes; r < MT; r += kThreads / kLanes) {
             const IO *q = static_cast<const IO *>(A.q) + (r < live ? attn_out_row(A, pc.b, pc.h, qt * MT + r) * D : 0);
-            for (int c = lane % kLanes; c < pieces; c += kLanes) copy16(Qs + r * KLD + c * kPiece, q + c * kPiece, r < live);
+            for (int c = lane % kLanes; c < pieces; c += kLanes) copy16(smem_of(Qs + r * KLD + c * kPiece), q + c * kPiece, r < live);
         }
         fetch(pc.t0, 0, page);
         page = page_of(pc.t0 + 1);   // always a tile ahead of its copy
