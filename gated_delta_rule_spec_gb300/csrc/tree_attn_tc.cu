@@ -28,7 +28,7 @@
 // The G query heads of a kv head are rows of the same tile, so every key and value is
 // copied once for all of them, and with fewer rows the copies are the bound: 4 rows of
 // 131072 tokens, 32 heads on 8 of 128: 252 us, 0.99 of the copy bandwidth; 128 rows of 8
-// drafts over up to 4096 tokens, 16 heads on 2 of 256: 130 us, 0.82.
+// drafts over up to 4096 tokens, 16 heads on 2 of 256: 128 us, 0.83.
 //
 // The running maximum is only moved when a row's maximum has grown by more than 2^8
 // over it: until then the probabilities are taken against the old one, which is exact
