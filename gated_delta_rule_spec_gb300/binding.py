@@ -177,6 +177,17 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _scratch(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory for one call on ``stream``, from that stream's pool: when it is dropped with the kernels
+    still queued, the allocator hands it out again to work behind them on the same stream only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> None:
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise GdnSpecError(f"{name}: want contiguous CUDA {dtype} {tuple(shape)}, got "
@@ -679,7 +690,7 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
     ``layer`` of the cache.  tree_mask int64 [B, T]: bit n of a node's word lets it
     attend to node n (None: a chain); tree_len int32 [B]: the rows' nodes (None: T);
     scale: D^-0.5 by default; lse fp32 [B, T, HQ]: written when given; workspace: uint8,
-    at least ``tree_attn_workspace`` bytes (None: allocated)."""
+    at least ``tree_attn_workspace`` bytes (None: allocated for the call on its stream)."""
     B = _rows(slot_idx, "slot_idx")
     if q.dim() != 4:
         raise GdnSpecError(f"q: want [B, T, HQ, D], got {tuple(q.shape)}")
@@ -696,8 +707,7 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, T, HQ))
     if workspace is None:
-        workspace = torch.empty(max(16, tree_attn_workspace(cache, B, T, HQ)), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(max(16, tree_attn_workspace(cache, B, T, HQ)), torch.uint8, q.device, stream)
     else:
         _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
     rc = load().gdn_spec_tree_attn(cache._ref, layer, _ptr(slot_idx), B, T, HQ, _ptr(q),
