@@ -180,12 +180,22 @@ def _stream(stream) -> int:
 def _scratch(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     """Memory for one call on ``stream``, from that stream's pool: when it is dropped with the kernels
     still queued, the allocator hands it out again to work behind them on the same stream only."""
-    if stream is None:
+    if stream is None or stream.cuda_stream == _stream(None):
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """A result that a call on ``stream`` writes and the caller gets: from that stream's pool, so that
+    nothing queued before on the current stream still uses the memory, and noted as used on the
+    current stream too, where the caller may read it (after a wait) and drop it."""
+    out = _scratch(shape, dtype, device, stream)
+    if stream is not None and stream.cuda_stream != _stream(None):
+        out.record_stream(torch.cuda.current_stream())
+    return out
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> None:
@@ -275,7 +285,7 @@ def verify(layer: SpecLayer, cursors: SpecCursors, slot_idx: torch.Tensor, q, k,
     _need(A_log, "A_log", torch.float32, shp["A_log"])
     _need(dt_bias, "dt_bias", torch.float32, shp["dt_bias"])
     if out is None:
-        out = torch.empty(shp["out"], dtype=io, device=q.device)
+        out = _result(shp["out"], io, q.device, stream)
     _need(out, "out", io, shp["out"])
     rc = load().gdn_spec_verify(ctypes.byref(layer.desc()), ctypes.byref(cursors.desc()),
                                 _ptr(slot_idx), B, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b),
@@ -301,7 +311,7 @@ def verify_d(layer: SpecLayer, dring: torch.Tensor, cursors: SpecCursors, slot_i
     _need(dt_bias, "dt_bias", torch.float32, shp["dt_bias"])
     _need(dring, "dring", torch.float32, (layer.num_slots, layer.HV, layer.L, layer.V))
     if out is None:
-        out = torch.empty(shp["out"], dtype=io, device=q.device)
+        out = _result(shp["out"], io, q.device, stream)
     _need(out, "out", io, shp["out"])
     rc = load().gdn_spec_verify_d(ctypes.byref(layer.desc()), _ptr(dring), ctypes.byref(cursors.desc()),
                                   _ptr(slot_idx), B, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b),
@@ -348,7 +358,7 @@ def prefill(layer: SpecLayer, cursors: SpecCursors, slot_idx: torch.Tensor, q, k
     _need(A_log, "A_log", torch.float32, (HV,))
     _need(dt_bias, "dt_bias", torch.float32, (HV, K) if layer.per_key_gate else (HV,))
     if out is None:
-        out = torch.empty((B, N, HV, V), dtype=io, device=q.device)
+        out = _result((B, N, HV, V), io, q.device, stream)
     _need(out, "out", io, (B, N, HV, V))
     rc = load().gdn_spec_prefill(ctypes.byref(layer.desc()), ctypes.byref(cursors.desc()),
                                  _ptr(slot_idx), B, N, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b),
@@ -372,11 +382,11 @@ def snapshot_verify(layer: SpecLayer, cursors: SpecCursors, slot_idx: torch.Tens
     _need(A_log, "A_log", torch.float32, shp["A_log"])
     _need(dt_bias, "dt_bias", torch.float32, shp["dt_bias"])
     if out is None:
-        out = torch.empty(shp["out"], dtype=io, device=q.device)
+        out = _result(shp["out"], io, q.device, stream)
     _need(out, "out", io, shp["out"])
     sshape = (B, layer.T, layer.HV, layer.V, layer.K)
     if snap is None:
-        snap = torch.empty(sshape, dtype=torch.float32, device=q.device)
+        snap = _result(sshape, torch.float32, q.device, stream)
     _need(snap, "snap", torch.float32, sshape)
     rc = load().gdn_spec_snapshot_verify(ctypes.byref(layer.desc()), ctypes.byref(cursors.desc()),
                                          _ptr(slot_idx), B, _ptr(q), _ptr(k), _ptr(v), _ptr(a),
@@ -482,9 +492,9 @@ def kv_init(cache: KvCache, stream=None) -> None:
     _check(load().gdn_spec_kv_init(cache._ref, _stream(stream)), "gdn_spec_kv_init")
 
 
-def _done(done: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
+def _done(done: torch.Tensor | None, like: torch.Tensor, stream) -> torch.Tensor:
     if done is None:
-        return torch.empty_like(like)
+        return _result(like.shape, torch.int32, like.device, stream)
     _need(done, "done", torch.int32, like.shape)
     return done
 
@@ -502,7 +512,7 @@ def kv_reserve(cache: KvCache, slot_idx: torch.Tensor, T: int, n_tokens: torch.T
     """gdn_spec_kv_reserve: pages for T (or n_tokens[b] <= T) more tokens of every row's
     slot.  Returns int32 [B]: 1 where the row is served."""
     B = _rows(slot_idx, "slot_idx")
-    done = _done(done, slot_idx)
+    done = _done(done, slot_idx, stream)
     if n_tokens is not None:
         _need(n_tokens, "n_tokens", torch.int32, (B,))
     rc = load().gdn_spec_kv_reserve(cache._ref, _ptr(slot_idx), B, T, _ptr(n_tokens), _ptr(done),
@@ -517,7 +527,7 @@ def kv_fork(cache: KvCache, src_idx: torch.Tensor, dst_idx: torch.Tensor,
     shared.  Returns int32 [B]: 1 where the row is served."""
     B = _rows(src_idx, "src_idx")
     _need(dst_idx, "dst_idx", torch.int32, (B,))
-    done = _done(done, src_idx)
+    done = _done(done, src_idx, stream)
     rc = load().gdn_spec_kv_fork(cache._ref, _ptr(src_idx), _ptr(dst_idx), B, _ptr(done),
                                  _stream(stream))
     _check(rc, "gdn_spec_kv_fork")
@@ -627,7 +637,7 @@ def rope(plan: RopePlan, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor |
     _need(pos, "pos", torch.int32, (N,))
     xs = _token_stride(x, "x", x.dtype, (N, heads, D))
     if out is None:
-        out, os_ = torch.empty((N, heads, D), dtype=x.dtype, device=x.device), heads * D
+        out, os_ = _result((N, heads, D), x.dtype, x.device, stream), heads * D
     else:
         os_ = _token_stride(out, "out", x.dtype, (N, heads, D))
     code = DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_FP32
@@ -656,7 +666,7 @@ def rope_append(plan: RopePlan, cache: KvCache, layer: int, slot_idx: torch.Tens
     if n_tokens is not None:
         _need(n_tokens, "n_tokens", torch.int32, (B,))
     if q_out is None:
-        q_out = torch.empty((B, T, HQ, cache.D), dtype=io, device=q.device)
+        q_out = _result((B, T, HQ, cache.D), io, q.device, stream)
     else:
         _need(q_out, "q_out", io, (B, T, HQ, cache.D))
     rc = load().gdn_spec_rope_append(plan._ref, cache._ref, layer, _ptr(slot_idx), B, T,
@@ -701,7 +711,7 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
     if tree_len is not None:
         _need(tree_len, "tree_len", torch.int32, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(q.shape, q.dtype, q.device, stream)
     else:
         _need(out, "out", cache.io_torch, (B, T, HQ, cache.D))
     if lse is not None:

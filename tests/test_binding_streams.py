@@ -25,10 +25,11 @@ class FakeLibrary:
 
 
 class Watch:
-    """The binding over stand-ins: `made` lists (shape, dtype, the stream that was current)."""
+    """The binding over stand-ins: `made` lists (shape, dtype, the stream that was current), `noted` the
+    other streams that a tensor is said to be used on."""
 
     def __init__(self, monkeypatch):
-        self.made, self.now = [], None
+        self.made, self.noted, self.now = [], [], None
         empty = torch.empty
 
         @contextlib.contextmanager
@@ -45,6 +46,9 @@ class Watch:
         monkeypatch.setattr(binding, "load", lambda lib=FakeLibrary(): lib)
         monkeypatch.setattr(binding, "_need", lambda *a: None)
         monkeypatch.setattr(binding, "_token_stride", lambda t, *a: 8)
+        monkeypatch.setattr(binding, "_stream", lambda s: 5 if s is None else s.cuda_stream)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda: "current")
+        monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: self.noted.append((tuple(t.shape), s)))
         monkeypatch.setattr(torch.cuda, "stream", under)
         monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
         self.cache = binding.KvCache(1, 4, 2, 16, 64, 2, 4, device="cpu")
@@ -57,6 +61,49 @@ def test_the_workspace_is_taken_where_the_call_runs(monkeypatch):
     w, s = Watch(monkeypatch), FakeStream()
     binding.tree_attn(w.cache, 0, w.slots, w.q, out=w.q, stream=s)
     assert w.made == [((4096,), torch.uint8, s)]
+
+
+def results(w):
+    """Calls that make what they return, as functions of the stream: (call, shapes)."""
+    plan, layer = binding.RopePlan(64), binding.SpecLayer(2, 4, 32, 32, 3, 16, 2, device="cpu")
+    cur = binding.SpecCursors(2, device="cpu")
+    args = [w.q] * 7
+    ring = layer.new_dring()
+    out, snap = (2, 3, 4, 32), (2, 3, 4, 32, 32)
+    return [
+        (lambda s: binding.tree_attn(w.cache, 0, w.slots, w.q, workspace=w.slots, stream=s), [(2, 3, 4, 64)]),
+        (lambda s: binding.rope_append(plan, w.cache, 0, w.slots, w.q, w.q, w.q, stream=s), [(2, 3, 4, 64)]),
+        (lambda s: binding.rope(plan, w.slots, w.q[0], stream=s), [(3, 4, 64)]),
+        (lambda s: binding.kv_reserve(w.cache, w.slots, 4, stream=s), [(2,)]),
+        (lambda s: binding.kv_fork(w.cache, w.slots, w.slots, stream=s), [(2,)]),
+        (lambda s: binding.verify(layer, cur, w.slots, *args, stream=s), [out]),
+        (lambda s: binding.verify_d(layer, ring, cur, w.slots, *args, stream=s), [out]),
+        (lambda s: binding.prefill(layer, cur, w.slots, *args, stream=s), [out]),
+        (lambda s: binding.snapshot_verify(layer, cur, w.slots, *args, stream=s), [out, snap])]
+
+
+@pytest.mark.parametrize("which", range(9))
+def test_results_are_taken_where_the_call_runs(monkeypatch, which):
+    plan = binding.RopePlan(64)
+    w, s = Watch(monkeypatch), FakeStream()
+    monkeypatch.setattr(binding, "RopePlan", lambda D: plan)
+    call, shapes = results(w)[which]
+    call(s)
+    assert [(x[0], x[2]) for x in w.made] == [(shape, s) for shape in shapes]
+    assert w.noted == [(shape, "current") for shape in shapes]
+
+
+@pytest.mark.parametrize("which", range(9))
+def test_no_stream_and_the_current_one_need_no_note(monkeypatch, which):
+    plan = binding.RopePlan(64)
+    w, s = Watch(monkeypatch), FakeStream()
+    monkeypatch.setattr(binding, "RopePlan", lambda D: plan)
+    s.cuda_stream = 5                                  # the current stream's handle
+    call, shapes = results(w)[which]
+    for stream in (None, s):
+        w.made.clear()
+        call(stream)
+        assert [(x[0], x[2]) for x in w.made] == [(shape, None) for shape in shapes] and w.noted == []
 
 
 def attention_case():
@@ -90,4 +137,37 @@ def test_the_attention_on_a_stream_that_is_behind():
         s.synchronize()
         assert torch.equal(out, want)
         assert all(bool(x.isnan().all()) for x in taken)
+    assert binding.kv_read_status(cache) == 0
+
+
+@pytest.mark.gpu
+def test_results_on_a_stream_that_is_behind():
+    """The current stream is held up with a write to a block that is then dropped: a result may not be
+    taken from it.  And a result that the current stream still has to read is not handed out again by its own
+    stream, however soon it is dropped."""
+    cache, slots, q = attention_case()
+    plan, pos = binding.RopePlan(128), torch.arange(32, dtype=torch.int32, device="cuda")
+    x = q.view(32, 16, 128)
+    want = binding.rope(plan, pos, x)
+    want_attn = binding.tree_attn(cache, 0, slots, q)
+    work = torch.empty(binding.tree_attn_workspace(cache, 4, 8, 16), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(20_000_000)
+        late = [torch.full_like(q, float("nan")) for _ in range(4)]
+        del late                                       # free for the current stream, written in 10 ms
+        got = binding.rope(plan, pos, x, stream=s)
+        got_attn = binding.tree_attn(cache, 0, slots, q, workspace=work, stream=s)
+        s.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(got_attn, want_attn)
+        torch.cuda._sleep(20_000_000)
+        copy = torch.empty_like(got)
+        copy.copy_(got)                                # reads `got` in 10 ms
+        del got, got_attn
+        for _ in range(4):
+            binding.rope(plan, pos, -x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want)
     assert binding.kv_read_status(cache) == 0
