@@ -440,7 +440,11 @@ class KvCache:
     """The paged key/value cache of all softmax-attention layers: ``k`` and ``v``
     [n_layers, num_pages, HKV, P, D], the slots' page tables and lengths, the pages'
     holders.  A new cache is empty (keys and values uninitialised); ``tensors`` gives
-    some or all of its tensors instead (as they are, nothing is reset)."""
+    some or all of its tensors instead (as they are, nothing is reset).  A tensor may be
+    replaced by another of its shape (``cache.length = x``: the calls from then on use x); the
+    dimensions are fixed."""
+
+    _DIMS = ("n_layers", "num_pages", "HKV", "P", "D", "num_slots", "max_pages", "io_code", "io_torch")
 
     def __init__(self, n_layers: int, num_pages: int, HKV: int, P: int, D: int, num_slots: int,
                  max_pages: int, io_dtype: str = "bf16", device="cuda", tensors: dict | None = None):
@@ -450,7 +454,6 @@ class KvCache:
         self.io_torch = _IO_TORCH[self.io_code]
         t = dict(tensors or {})
         shape, i32 = (n_layers, num_pages, HKV, P, D), torch.int32
-        words = (num_pages + 31) // 32
         new = {"k": lambda: torch.empty(shape, dtype=self.io_torch, device=device),
                "v": lambda: torch.empty(shape, dtype=self.io_torch, device=device),
                "page_table": lambda: torch.full((num_slots, max_pages), -1, dtype=i32, device=device),
@@ -459,22 +462,38 @@ class KvCache:
                "ref": lambda: torch.zeros(num_pages, dtype=i32, device=device),
                "free_bits": lambda: self._all_free(num_pages, device),
                "status": lambda: torch.zeros(4, dtype=i32, device=device)}
-        want = {"k": shape, "v": shape, "page_table": (num_slots, max_pages), "n_pages": (num_slots,),
-                "length": (num_slots,), "ref": (num_pages,), "free_bits": (words,), "status": None}
         for name, make in new.items():
             x = t.pop(name, None)
             if x is None:
                 x = make()
-            elif name == "status":
-                _need(x, name, i32, x.shape)
             else:
-                _need(x, name, self.io_torch if name in "kv" else i32, want[name])
+                self._need_tensor(name, x)
             setattr(self, name, x)
         if t:
             raise GdnSpecError(f"unknown cache tensors: {sorted(t)}")
+        self._tensors = tuple(new)
         self._desc = KvCacheDesc(n_layers, num_pages, HKV, P, D, self.io_code, num_slots, max_pages,
                                  *(getattr(self, n).data_ptr() for n in new))
         self._ref = ctypes.byref(self._desc)
+
+    def _need_tensor(self, name: str, x: torch.Tensor) -> None:
+        pool = (self.n_layers, self.num_pages, self.HKV, self.P, self.D)
+        want = {"k": pool, "v": pool, "page_table": (self.num_slots, self.max_pages),
+                "n_pages": (self.num_slots,), "length": (self.num_slots,), "ref": (self.num_pages,),
+                "free_bits": ((self.num_pages + 31) // 32,), "status": x.shape}
+        if name == "status" and x.numel() < 1:
+            raise GdnSpecError("status: want one word at least")
+        _need(x, name, self.io_torch if name in ("k", "v") else torch.int32, want[name])
+
+    def __setattr__(self, name: str, value) -> None:
+        # The calls pass the descriptor's addresses, so they follow a tensor that is replaced.
+        if "_desc" in self.__dict__:
+            if name in self._DIMS:
+                raise GdnSpecError(f"{name}: a cache's dimensions are fixed")
+            if name in self._tensors:
+                self._need_tensor(name, value)
+                setattr(self._desc, name, value.data_ptr())
+        object.__setattr__(self, name, value)
 
     @staticmethod
     def _all_free(num_pages: int, device) -> torch.Tensor:
