@@ -44,14 +44,17 @@ inline cudaError_t kernel_setup(KernelSetup &ks, const void *kern, size_t smem, 
     return cudaSuccess;
 }
 
-// Programmatic dependent launch, for the short kernels that follow one
-// another in a step (commit, fold, cursor move): such a kernel may start while
-// the kernel before it in the stream is finishing, and calls grid_dep_wait()
-// before its first global memory access (it returns once every grid the
-// kernel depends on has completed and its memory is visible; at once for a
-// kernel launched without the attribute).  grid_dep_launch() lets the next
-// kernel start its own launch early; only the commit and the cursor move call
-// it, right after their wait, so at most two neighbouring kernels overlap.
+// Programmatic dependent launch, for the kernels that follow one another in a
+// step (commit, fold, cursor move; the cache's pages, rotary positions, tree
+// attention and its join): such a kernel may start while the kernel before it in
+// the stream is finishing.  grid_dep_wait() returns once every grid the kernel
+// depends on has completed and its memory is visible (at once for a kernel
+// launched without the attribute); grid_dep_launch() lets the next kernel start
+// its own launch early, which the exit of a block does too.  The rule that keeps
+// the order: every block calls grid_dep_wait() before it touches global memory,
+// calls grid_dep_launch() or leaves, by whatever way.  Then a kernel that starts
+// early waits for the one before it, which had itself waited for the one before
+// that, and no kernel's memory accesses overlap another's.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

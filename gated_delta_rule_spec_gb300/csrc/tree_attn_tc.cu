@@ -756,7 +756,11 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     uint32_t have;
     asm("mov.u32 %0, %dynamic_smem_size;" : "=r"(have));
     if (pad + L::kOffMisc + sizeof(Misc) > have) {   // the segment does not start where it always has
-        if (tid == 0) atomicOr(A.C.status, GDN_SPEC_ST_TIMEOUT);
+        grid_dep_wait();
+        if (tid == 0) {
+            atomicOr(A.C.status, GDN_SPEC_ST_TIMEOUT);
+            if (qt == 0) attn_note(A, group, false, AttnPiece(), 1);   // the join finds an empty chunk
+        }
         return;
     }
     if (tid == 0) {
