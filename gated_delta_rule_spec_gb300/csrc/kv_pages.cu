@@ -24,6 +24,10 @@ constexpr int kAllocThreads = 1024;
 constexpr int kAllocRows = 8192;      // rows of one reserve or fork: their running demand is kept in shared memory
 constexpr int kCopyThreads = 256;
 constexpr int kMoveMaxT = 1024;       // window of a commit with a path
+// Table entries (rows times columns) of a fork that the allocating block looks at itself; beyond them a launch of its
+// own does.  What looking at them adds to a fork, in the block and as a launch: 32 rows of 126 columns 0.9 and 2.3 us,
+// 128 of 65 1.8 and 1.4, 256 of 126 4.2 and 1.9, 64 of 8189 25 and 3.
+constexpr int64_t kForkInline = 6 << 10;
 
 // Exclusive prefix sum over the block's threads; *total is the block's sum.
 __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
@@ -96,12 +100,40 @@ __device__ __forceinline__ Demand row_demand(const KvArgs &C, const int32_t *src
     return d;
 }
 
+// Whether one of the first n entries of a slot's table, as far as they fall to this
+// lane, is no page.
+__device__ __forceinline__ bool bad_pages(const KvArgs &C, int slot, int n, int lane, int lanes) {
+    const int32_t *t = C.page_table + (int64_t)slot * C.max_pages;
+    bool bad = false;
+#pragma unroll 4
+    for (int i = lane; i < n; i += lanes) bad |= (uint32_t)t[i] >= (uint32_t)C.num_pages;
+    return bad;
+}
+
+// done[b]: the pages of row b's source are pages, as far as its committed tokens
+// reach (other reasons to refuse a row are the allocation's).  A block a row.
+__global__ void __launch_bounds__(kCopyThreads) kv_fork_check_kernel(KvArgs C, const int32_t *__restrict__ src_idx,
+                                                                     int32_t *__restrict__ done) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int src = src_idx[blockIdx.x];
+    int np;
+    uint32_t bits;
+    const int len = kv_slot_length(C, src, &np, &bits);
+    const bool bad = len > 0 && bad_pages(C, src, (int)(((int64_t)len + C.P - 1) >> C.logP), threadIdx.x, kCopyThreads);
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) done[blockIdx.x] = !any;
+}
+
 // Hand out pages for every row (FORK: the page of a partly filled tail, and the
-// destination's counts).  Demand sums are held below 2^31 by the host.
+// destination's counts).  Demand sums are held below 2^31 by the host.  A fork's row
+// whose source holds an entry that is no page is refused like the others, before it
+// asks for any: `checked` says that done[] has the answer, else a warp a row looks
+// at the entries here.
 template <bool FORK>
 __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const int32_t *__restrict__ src_idx,
                                                                  const int32_t *__restrict__ dst_idx, int B, int T,
-                                                                 const int32_t *__restrict__ n_tokens,
+                                                                 const int32_t *__restrict__ n_tokens, bool checked,
                                                                  int32_t *__restrict__ done) {
     __shared__ int warp_sums[33];
     __shared__ int ends[kAllocRows + 1];   // running demand before row b
@@ -118,6 +150,26 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
         const int b = b0 + tid;
         Demand d = {-1, 0, 0, false};
         if (b < B) d = row_demand<FORK>(C, src_idx, dst_idx, n_tokens, T, b);
+        if (FORK) {
+            bool bad = false;
+            if (checked) {
+                bad = d.ok && !done[b];
+            } else {
+                word_s[tid] = d.ok ? d.have + d.need : 0;   // entries in use
+                rank_s[tid] = d.ok ? src_idx[b] : 0;
+                __syncthreads();
+                for (int r = tid >> 5; r < min(kAllocThreads, B - b0); r += kAllocThreads >> 5) {
+                    const bool lane_bad = bad_pages(C, rank_s[r], word_s[r], tid & 31, 32);
+                    if (__any_sync(0xffffffffu, lane_bad) && (tid & 31) == 0) rank_s[r] = -1;
+                }
+                __syncthreads();
+                bad = rank_s[tid] < 0;
+            }
+            if (bad) {
+                atomicOr(C.status, GDN_SPEC_ST_PAGE_OOR);
+                d = {-1, 0, 0, false};
+            }
+        }
         int chunk;
         const int before = block_scan(d.need, warp_sums, &chunk);
         if (b < B) {
@@ -215,7 +267,9 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     }
 }
 
-// The rest of a fork: shared pages, and the copied rows of the last page.
+// The rest of a fork: shared pages, and the copied rows of the last page.  The entries
+// are pages, unless a destination is also a source, which the call forbids: the
+// tests here keep that inside the pool too.
 // Grid (rows, parts): a block copies the rows of one head of one layer's keys or
 // values at a time (one contiguous run), four 16-byte loads in flight per thread.
 __global__ void __launch_bounds__(kCopyThreads) kv_fork_copy_kernel(KvArgs C, const int32_t *__restrict__ src_idx,
@@ -426,7 +480,7 @@ int kv_move_max_window() { return kMoveMaxT; }
 cudaError_t launch_kv_reserve(const KvArgs &C, const int32_t *slot_idx, int B, int T, const int32_t *n_tokens,
                               int32_t *done, cudaStream_t stream) {
     return launch_dependent(kv_alloc_kernel<false>, dim3(1), dim3(kAllocThreads), 0, stream, C, slot_idx, slot_idx, B,
-                            T, n_tokens, done);
+                            T, n_tokens, false, done);
 }
 
 // Blocks along a row's layers, heads, keys and values: as many as there are
@@ -438,8 +492,12 @@ static int copy_parts(int B, int most, int blocks) {
 
 cudaError_t launch_kv_fork(const KvArgs &C, const int32_t *src_idx, const int32_t *dst_idx, int B, int32_t *done,
                            int es, cudaStream_t stream) {
-    cudaError_t e = launch_dependent(kv_alloc_kernel<true>, dim3(1), dim3(kAllocThreads), 0, stream, C, src_idx, dst_idx,
-                                     B, 0, (const int32_t *)nullptr, done);
+    cudaError_t e = cudaSuccess;
+    const bool check = (int64_t)B * C.max_pages > kForkInline;
+    if (check) e = launch_dependent(kv_fork_check_kernel, dim3(B), dim3(kCopyThreads), 0, stream, C, src_idx, done);
+    if (e == cudaSuccess)
+        e = launch_dependent(kv_alloc_kernel<true>, dim3(1), dim3(kAllocThreads), 0, stream, C, src_idx, dst_idx, B, 0,
+                             (const int32_t *)nullptr, check, done);
     if (e != cudaSuccess) return e;
     const int parts = copy_parts(B, C.n_layers * C.HKV * 2, 8192);
     return launch_dependent(kv_fork_copy_kernel, dim3(B, parts), dim3(kCopyThreads), 0, stream, C, src_idx, dst_idx,

@@ -398,6 +398,9 @@ int gdn_spec_kv_reserve(const gdn_spec_kv_cache *cache, const int32_t *slot_idx,
  * by gdn_spec_kv_reserve.  A negative index on either side is a padding row.
  * B <= 8192.
  *   done      int32 [B], device (written)
+ * Device status: SLOT_OOR, CURSOR_CORRUPT, SLOT_BUSY, NO_PAGES, PAGE_OOR (a page of the
+ * source's committed tokens is not one of the pool); such a row gives done = 0, and its
+ * destination stays empty.
  */
 int gdn_spec_kv_fork(const gdn_spec_kv_cache *cache, const int32_t *src_idx, const int32_t *dst_idx,
                      int32_t B, int32_t *done, void *stream);
@@ -418,7 +421,9 @@ int gdn_spec_kv_fork(const gdn_spec_kv_cache *cache, const int32_t *src_idx, con
 int gdn_spec_kv_commit(const gdn_spec_kv_cache *cache, const int32_t *slot_idx, int32_t B, int32_t T,
                        const int32_t *path, const int32_t *accept_len, void *stream);
 
-/* gdn_spec_kv_free -- each row's slot becomes empty; a page that no slot holds any more is free. */
+/* gdn_spec_kv_free -- each row's slot becomes empty; a page that no slot holds any more is free.
+ * Device status: SLOT_OOR, CURSOR_CORRUPT (counts out of range: the row is left as it is; a page that
+ * nobody holds: it stays as it is), PAGE_OOR (an entry that is no page is dropped). */
 int gdn_spec_kv_free(const gdn_spec_kv_cache *cache, const int32_t *slot_idx, int32_t B, void *stream);
 
 /* gdn_spec_kv_read_status -- as gdn_spec_read_status, for a cache's status word. */
