@@ -498,7 +498,9 @@ int gdn_spec_rope(const gdn_spec_rope_plan *plan, int32_t N, int32_t heads, int3
  *   pos    int32 [B, T], device; NULL: length + t (a chain)
  *   q_out  io_dtype [B, T, HQ, D], dense (written; zeros for padding rows and t >= n_tokens)
  * T >= 1, any length.  Device status: SLOT_OOR, ACCEPT_RANGE (n_tokens),
- * CURSOR_CORRUPT, NO_PAGES, PAGE_OOR; such a row writes zeros to q_out only.
+ * CURSOR_CORRUPT, NO_PAGES: such a row writes zeros to q_out only.  PAGE_OOR: the tokens
+ * whose place in the page table is no page write zeros to q_out only; the row's other
+ * tokens are served (with the entry mended, the same call serves the whole row).
  */
 int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache *cache, int32_t layer,
                          const int32_t *slot_idx, int32_t B, int32_t T, const int32_t *n_tokens,
