@@ -100,6 +100,15 @@ __device__ __forceinline__ Demand row_demand(const KvArgs &C, const int32_t *src
     return d;
 }
 
+// Word w of the free pages, without bits past the last page (which a caller's
+// bitmap may hold: pages of those numbers have no counts to write).
+__device__ __forceinline__ uint32_t free_word(const KvArgs &C, int w) {
+    const int left = C.num_pages - w * 32;   // w is below 2^26
+    if (left <= 0) return 0u;
+    const uint32_t bits = C.free_bits[w];
+    return left < 32 ? bits & ((1u << left) - 1) : bits;
+}
+
 // Whether one of the first n entries of a slot's table, as far as they fall to this
 // lane, is no page.
 __device__ __forceinline__ bool bad_pages(const KvArgs &C, int slot, int n, int lane, int lanes) {
@@ -143,7 +152,7 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     grid_dep_launch();
     const int tid = threadIdx.x;
     const int words = (C.num_pages + 31) >> 5;
-    const uint32_t first = tid < words ? C.free_bits[tid] : 0u;   // on its way while the rows' chain of loads runs
+    const uint32_t first = free_word(C, tid);   // on its way while the rows' chain of loads runs
     bool mine_ok = false;                                         // of row tid
     int total = 0;
     for (int b0 = 0; b0 < B; b0 += kAllocThreads) {
@@ -184,7 +193,7 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     int avail = 0;
     if (total > 0) {
         int mine = __popc(first);
-        for (int w = tid + kAllocThreads; w < words; w += kAllocThreads) mine += __popc(C.free_bits[w]);
+        for (int w = tid + kAllocThreads; w < words; w += kAllocThreads) mine += __popc(free_word(C, w));
         block_scan(mine, warp_sums, &avail);
     }
     __syncthreads();
@@ -202,7 +211,7 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(KvArgs C, const
     int base = 0;
     for (int w0 = 0; w0 < words && base < give; w0 += kAllocThreads) {
         const int w = w0 + tid;
-        const uint32_t bits = w0 == 0 ? first : w < words ? C.free_bits[w] : 0u;
+        const uint32_t bits = w0 == 0 ? first : free_word(C, w);
         int chunk;
         const int before = block_scan(__popc(bits), warp_sums, &chunk);   // of the slice's words below
         word_s[tid] = bits;
