@@ -350,7 +350,9 @@ const char *gdn_spec_prefill_path(const gdn_spec_layer *layer);
  * length[s] + node) in the same pages.  A page may be held by several slots
  * (ref counts them); only full pages are ever shared, so no shared page is
  * written.  Page p is free exactly when ref[p] == 0 and bit p % 32 of
- * free_bits[p / 32] is set.  num_pages * P and max_pages * P are below 2^31.
+ * free_bits[p / 32] is set.  num_pages * P and max_pages * P are below 2^31, and
+ * n_layers * HKV is at most 2^20 (GDN_SPEC_EUNSUPPORTED otherwise, as for the
+ * limits that the calls name).
  */
 typedef struct {
     int32_t n_layers;     /* softmax-attention layers                                   */
@@ -380,7 +382,8 @@ int gdn_spec_kv_init(const gdn_spec_kv_cache *cache, void *stream);
  * pages of lowest number are handed out in row order, so the tables depend only
  * on the calls made.  Row b is served when it lacks none or when the pages that
  * rows 0..b lack together are free (rows that are refused for another reason
- * lack none); otherwise it keeps what it has and NO_PAGES is set.  B <= 8192.
+ * lack none); otherwise it keeps what it has and NO_PAGES is set.  B <= 8192, and
+ * B * max_pages is below 2^31.
  *   n_tokens  int32 [B], device, 0 <= n_tokens <= T, or NULL
  *   done      int32 [B], device (written): 1 where the row is served, else 0
  * Device status: SLOT_OOR, ACCEPT_RANGE (n_tokens), CURSOR_CORRUPT, NO_PAGES.
@@ -480,7 +483,7 @@ int gdn_spec_rope_init_freqs(gdn_spec_rope_plan *plan, int32_t D, int32_t rot, i
  *   pos   int32 [N], device
  *   x     io_dtype [N, heads, D]: token n at x + n * x_stride elements, its heads dense
  *   out   io_dtype [N, heads, D]: token stride out_stride; may be x itself with the same stride
- * Strides are multiples of 8 elements, at least heads * D.
+ * Strides are multiples of 8 elements, at least heads * D, which is at most 2^22.
  */
 int gdn_spec_rope(const gdn_spec_rope_plan *plan, int32_t N, int32_t heads, int32_t io_dtype,
                   const int32_t *pos, const void *x, int64_t x_stride, void *out, int64_t out_stride,
@@ -497,10 +500,11 @@ int gdn_spec_rope(const gdn_spec_rope_plan *plan, int32_t N, int32_t heads, int3
  *          slices of one projection's output.  Strides are multiples of 8 elements.
  *   pos    int32 [B, T], device; NULL: length + t (a chain)
  *   q_out  io_dtype [B, T, HQ, D], dense (written; zeros for padding rows and t >= n_tokens)
- * T >= 1, any length.  Device status: SLOT_OOR, ACCEPT_RANGE (n_tokens),
- * CURSOR_CORRUPT, NO_PAGES: such a row writes zeros to q_out only.  PAGE_OOR: the tokens
- * whose place in the page table is no page write zeros to q_out only; the row's other
- * tokens are served (with the entry mended, the same call serves the whole row).
+ * T >= 1, any length; B * T is below 2^31 and (HQ + 2 HKV) * D at most 2^22.
+ * Device status: SLOT_OOR, ACCEPT_RANGE (n_tokens), CURSOR_CORRUPT, NO_PAGES: such a
+ * row writes zeros to q_out only.  PAGE_OOR: the tokens whose place in the page table is
+ * no page write zeros to q_out only; the row's other tokens are served (with the entry
+ * mended, the same call serves the whole row).
  */
 int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache *cache, int32_t layer,
                          const int32_t *slot_idx, int32_t B, int32_t T, const int32_t *n_tokens,
@@ -525,9 +529,10 @@ int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache
  *              aligned; its contents need not be kept or cleared, and calls that may run at
  *              the same time need one each
  * Two kernels (gdn_spec_tree_attn_path): "tc" -- bf16, at most 128 query heads a kv
- * head: TMA and tcgen05, the probabilities rounded to bf16 for the second
- * product; "generic" -- otherwise: fp32 throughout on the CUDA cores.  1 <= T <= 64; B * T is
- * below 2^31, and B * HKV times (8 + the tiles of 32 tokens that a slot can hold) at most 2e9.
+ * head, n_layers * num_pages * HKV * P below 2^31: TMA and tcgen05, the probabilities
+ * rounded to bf16 for the second product; "generic" -- otherwise: fp32 throughout on
+ * the CUDA cores.  1 <= T <= 64; HQ / HKV is at most 4096, B * T below 2^31, and B * HKV
+ * times (8 + the tiles of 32 tokens that a slot can hold) at most 2e9.
  * Device status: SLOT_OOR, ACCEPT_RANGE (tree_len), CURSOR_CORRUPT, NO_PAGES (the row
  * gives zeros), PAGE_OOR, TIMEOUT.
  */
