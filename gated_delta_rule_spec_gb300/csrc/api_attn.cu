@@ -328,7 +328,9 @@ int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int3
                        void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
     int rc = check_attn(cache, B, T, HQ);
     if (rc) return rc;
-    if (layer < 0 || layer >= cache->n_layers || !(scale > 0.0f) || !std::isfinite(scale)) return GDN_SPEC_EINVAL;
+    // scores are scaled in powers of two, by a factor that has to be finite too
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    if (layer < 0 || layer >= cache->n_layers || !(scale > 0.0f) || !std::isfinite(scale_log2)) return GDN_SPEC_EINVAL;
     if (B == 0) return GDN_SPEC_OK;
     if (!slot_idx || !q || !out || !workspace) return GDN_SPEC_EINVAL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return GDN_SPEC_EALIGN;
@@ -340,7 +342,7 @@ int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int3
     A.slot_idx = slot_idx;
     A.tree_mask = tree_mask;
     A.tree_len = tree_len;
-    A.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    A.scale_log2 = scale_log2;
     A.q = q;
     A.out = out;
     A.lse = lse;

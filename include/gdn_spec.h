@@ -522,7 +522,7 @@ int gdn_spec_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_kv_cache
  *   q          io_dtype [B, T, HQ, D]; HKV divides HQ, head h reads kv head h / (HQ / HKV)
  *   tree_mask  uint64 [B, T], device; NULL: a chain (node t attends to nodes 0..t)
  *   tree_len   int32 [B], device, 0 <= tree_len <= T; NULL: T
- *   scale      > 0
+ *   scale      > 0, and scale * log2(e) a finite fp32 number
  *   out        io_dtype [B, T, HQ, D] (written)
  *   lse        fp32 [B, T, HQ] (written), natural log of the softmax denominator; or NULL
  *   workspace  device memory of workspace_bytes >= gdn_spec_tree_attn_workspace, 16-byte

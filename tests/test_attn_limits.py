@@ -4,7 +4,7 @@ import ctypes
 import os
 import re
 
-from tests.test_attn_validation import EUNSUP, FAKE, OK, attn, cache, lib, plan  # noqa: F401
+from tests.test_attn_validation import EINVAL, EUNSUP, FAKE, OK, attn, cache, lib, plan  # noqa: F401
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "gdn_spec.h")
 
@@ -55,3 +55,11 @@ def test_elements_of_a_token(lib):
     assert rope(1 << 15) == OK and rope((1 << 15) + 1) == EUNSUP
     assert append((1 << 15) - 4) == OK and append((1 << 15) - 3) == EUNSUP
     assert append(8, 1 << 25, 64) == EUNSUP
+
+
+def test_scale(lib):
+    """Scores are taken in powers of two: a scale whose product with log2(e) is no fp32 number gave NaN."""
+    top = 3.4028234663852886e38 / 1.4426950408889634
+    assert "scale > 0, and scale * log2(e) a finite fp32 number" in entry("gdn_spec_tree_attn -- softmax", "int gdn_spec_tree_attn(")
+    for scale, want in ((0.999 * top, OK), (1.001 * top, EINVAL), (3.4e38, EINVAL), (1e-45, OK)):
+        assert attn(lib, cache(), scale=scale) == want, scale
