@@ -224,7 +224,7 @@ int gdn_spec_rope_init_freqs(gdn_spec_rope_plan *plan, int32_t D, int32_t rot, i
     p.mscale = (float)mscale;
     const int rc = check_plan(&p);
     if (rc) return rc;
-    if (!std::isfinite(mscale)) return GDN_SPEC_EINVAL;
+    if (!std::isfinite(p.mscale)) return GDN_SPEC_EINVAL;   // as the fp32 number that is kept
     for (int i = 0; i < rot / 2; ++i) {
         if (!std::isfinite(freqs[i])) return GDN_SPEC_EINVAL;
         p.freq[i] = turn_bits(freqs[i]);

@@ -4,6 +4,9 @@ import ctypes
 import os
 import re
 
+import pytest
+
+from gated_delta_rule_spec_gb300 import binding
 from tests.test_attn_validation import EINVAL, EUNSUP, FAKE, OK, attn, cache, lib, plan  # noqa: F401
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "gdn_spec.h")
@@ -63,3 +66,11 @@ def test_scale(lib):
     assert "scale > 0, and scale * log2(e) a finite fp32 number" in entry("gdn_spec_tree_attn -- softmax", "int gdn_spec_tree_attn(")
     for scale, want in ((0.999 * top, OK), (1.001 * top, EINVAL), (3.4e38, EINVAL), (1e-45, OK)):
         assert attn(lib, cache(), scale=scale) == want, scale
+
+
+def test_factor_on_cos_and_sin(lib):
+    """The plan keeps the factor in fp32, where it has to be finite."""
+    assert plan(8, 2, freqs=[1.0], mscale=3e38).mscale > 0
+    for mscale in (1e39, -1e39, 1e300):
+        with pytest.raises(binding.GdnSpecError):
+            plan(8, 2, freqs=[1.0], mscale=mscale)
