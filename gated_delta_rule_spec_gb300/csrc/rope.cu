@@ -303,9 +303,10 @@ template <typename IO, bool HALF, bool UNITS>
 static cudaError_t run_rope(const RopeArgs &R, int N, int heads, const int32_t *pos, const void *x, int64_t x_stride,
                             void *out, int64_t out_stride, bool transpose, cudaStream_t st) {
     const int tokens = tokens_per_block(N, heads * R.D / 16);
-    return launch_dependent(rope_kernel<IO, HALF, UNITS>, dim3((N + tokens - 1) / tokens), dim3(kRopeThreads), tokens * R.pairs * sizeof(float2), st, R, N,
-                            heads, tokens, pos, static_cast<const IO *>(x), x_stride, static_cast<IO *>(out), out_stride,
-                            transpose ? -1.0f : 1.0f);
+    const int64_t blocks = ((int64_t)N + tokens - 1) / tokens;
+    return launch_dependent(rope_kernel<IO, HALF, UNITS>, dim3((unsigned)blocks), dim3(kRopeThreads),
+                            tokens * R.pairs * sizeof(float2), st, R, N, heads, tokens, pos, static_cast<const IO *>(x), x_stride,
+                            static_cast<IO *>(out), out_stride, transpose ? -1.0f : 1.0f);
 }
 
 cudaError_t launch_rope(const gdn_spec_rope_plan *plan, int N, int heads, bool bf16, const int32_t *pos, const void *x,
