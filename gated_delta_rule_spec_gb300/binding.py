@@ -596,25 +596,29 @@ class RopePlan:
                  scaling: str = "none", factor: float = 1.0, original: float = 0.0,
                  fast: float = 32.0, slow: float = 1.0, low: float = 1.0, high: float = 4.0,
                  freqs=None, mscale: float = 1.0):
-        self.D, self.rot = D, D if rot is None else rot
+        rot = D if rot is None else rot
         if layout not in _ROPE_LAYOUT or scaling not in _ROPE_KIND:
             raise GdnSpecError(f"rotary layout {layout!r} or scaling {scaling!r} is not known")
         self._desc = RopePlanDesc()
         self._ref = ctypes.byref(self._desc)
         if freqs is not None:
             f = [float(x) for x in freqs]
-            if len(f) != self.rot // 2:
-                raise GdnSpecError(f"freqs: want {self.rot // 2} values, got {len(f)}")
+            if len(f) != rot // 2:
+                raise GdnSpecError(f"freqs: want {rot // 2} values, got {len(f)}")
             arr = (ctypes.c_double * max(len(f), 1))(*f)
-            rc = load().gdn_spec_rope_init_freqs(self._ref, D, self.rot, _ROPE_LAYOUT[layout], arr, mscale)
+            rc = load().gdn_spec_rope_init_freqs(self._ref, D, rot, _ROPE_LAYOUT[layout], arr, mscale)
             _check(rc, "gdn_spec_rope_init_freqs")
             return
         yarn = scaling == "yarn"
         sc = RopeScalingDesc(_ROPE_KIND[scaling], 0, factor, original, fast if yarn else low,
                              slow if yarn else high)
-        rc = load().gdn_spec_rope_init(self._ref, D, self.rot, _ROPE_LAYOUT[layout], base,
+        rc = load().gdn_spec_rope_init(self._ref, D, rot, _ROPE_LAYOUT[layout], base,
                                        ctypes.byref(sc))
         _check(rc, "gdn_spec_rope_init")
+
+    # What the calls are checked against is what the kernels get.
+    D = property(lambda self: self._desc.D)
+    rot = property(lambda self: self._desc.rot)
 
     def desc(self) -> RopePlanDesc:
         return self._desc

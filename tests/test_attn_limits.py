@@ -74,3 +74,14 @@ def test_factor_on_cos_and_sin(lib):
     for mscale in (1e39, -1e39, 1e300):
         with pytest.raises(binding.GdnSpecError):
             plan(8, 2, freqs=[1.0], mscale=mscale)
+
+
+def test_a_plans_dims_are_the_descriptors(lib):
+    """rope() checks x against the plan's head dim, the kernel reads the descriptor's: one number."""
+    p = binding.RopePlan(128, 64)
+    assert (p.D, p.rot) == (p.desc().D, p.desc().rot) == (128, 64)
+    with pytest.raises(AttributeError):
+        p.D = 64
+    with pytest.raises(AttributeError):
+        p.rot = 32
+    assert binding.RopePlan(64).rot == 64
