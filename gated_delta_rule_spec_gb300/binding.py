@@ -192,8 +192,10 @@ def _result(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     """A result that a call on ``stream`` writes and the caller gets: from that stream's pool, so that
     nothing queued before on the current stream still uses the memory, and noted as used on the
     current stream too, where the caller may read it (after a wait) and drop it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     out = _scratch(shape, dtype, device, stream)
-    if stream is not None and stream.cuda_stream != _stream(None):
+    if stream.cuda_stream != _stream(None):
         out.record_stream(torch.cuda.current_stream())
     return out
 
