@@ -1,11 +1,13 @@
-"""A speculative step of a hybrid model's layers through the library: two softmax-attention
-layers over the paged cache around one gated-delta-rule layer's ring.
+"""The speculative step of a hybrid model's two kinds of layers through the library.
 
-Three prompts go into the cache in windows, each is forked, and then the same tokens are
-run twice: as one drafted tree for the softmax-attention layers (rotary positions and
-append, tree attention, commit of the accepted path), and one after another on the
-forks (windows of one token).  The drafted chain also goes through the
-gated-delta-rule layer's verify, commit and fold.  Printed: how far the tree's outputs
+Two softmax-attention layers over the paged cache, one feeding the other: three prompts go
+into the cache in windows, each is forked, and then the same tokens are run twice, as one
+drafted tree (rotary positions and append, tree attention, commit of the accepted path),
+and one after another on the forks (windows of one token).
+
+Beside them, one gated-delta-rule layer: it takes chains only, so no tree can go through it, and
+it is shown by itself, with a chain of its own inputs, as long as the accepted path, through
+verify, commit and fold.  Printed: how far the tree's outputs
 on the accepted path are from the sequential ones, and the pages in use.
 
     python examples/hybrid_tree_step.py        (needs a GPU)
@@ -49,7 +51,8 @@ def tree(parent):
 
 
 def delta_layer_step(chain, B, gen):
-    """The drafted chain through one gated-delta-rule layer: verify, commit, fold."""
+    """A window of random inputs through one gated-delta-rule layer, `chain` tokens of it accepted: verify,
+    commit, fold."""
     H, HV, K, V, T = 4, 8, 128, 128, 4
     layer, cur = binding.SpecLayer(H, HV, K, V, T, 64, B), binding.SpecCursors(B)
     slots = torch.arange(B, dtype=torch.int32, device="cuda")

@@ -17,9 +17,10 @@
 // run over output columns, VEC consecutive ones per lane.  Rows of keys and queries
 // are padded by 16 bytes, so that the pieces read together fall in different banks.
 // 16 sequences of 5000 tokens, 4 heads of 128 fp32, 8 drafts: 73 us, 3.4 TB/s, half of
-// HBM's rate, with the issue slots 58% and the shared-memory pipe 53% busy; 8 of them
-// with 32 rows a head: 87 us, where a warp's 16 multiply-adds for 5 wide reads take
-// 8.7 wavefronts and the pipe is busy 72% of a tile.
+// HBM's rate, with the issue slots 58% and the shared-memory pipe 53% busy: no pipe
+// bounds it, the latency of tiles between two block barriers each does.  8 of them with
+// 32 rows a head: 87 us, where a warp's 16 multiply-adds for 5 wide reads take 8.7
+// wavefronts; the pipe is busy 58% of the kernel and the issue slots 57%.
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
 
@@ -88,7 +89,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live)
                  : "memory");
 }
 
-// Blocks of an SM that the registers leave room for.
+// Blocks of an SM that the registers leave room for.  (At the 128 registers of two blocks
+// the kernels of 24 and 32 rows keep 4 to 92 bytes a thread in local memory, most of
+// them with 32 rows of 128 fp32.)
 __host__ __device__ constexpr int attn_blocks(int WR, int RW, int NG) {
     return WR == 2 ? (NG == 2 ? 1 : 2) : NG == 2 ? 2 : 4;
 }

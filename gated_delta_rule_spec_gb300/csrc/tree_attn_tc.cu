@@ -22,19 +22,22 @@
 // blocks while the tensor core is busy, so one warp that issued both products of a
 // tile took longer than its softmax (32 rows of 64 drafts over up to 8192 tokens, 64
 // heads on 8 of 128: 466 us; with tiles of 128 keys and one buffer of S, where scores,
-// softmax and sums wait for one another, 492 us; as it is 333 us, 0.53 of the bf16 rate).
+// softmax and sums wait for one another, 492 us; as it is 333 us when the same call is
+// replayed, 0.53 of the bf16 rate, and 349 to 352 us in calls on changing inputs).
 // There the first product bounds it: an MMA of 128 x 64 takes as long as one of
 // 128 x 128, because the query rows come from shared memory.
 // The G query heads of a kv head are rows of the same tile, so every key and value is
 // copied once for all of them, and with fewer rows the copies are the bound: 4 rows of
-// 131072 tokens, 32 heads on 8 of 128: 252 us, 0.99 of the copy bandwidth; 128 rows of 8
-// drafts over up to 4096 tokens, 16 heads on 2 of 256: 128 us, 0.83.
+// 131072 tokens, 32 heads on 8 of 128: 251 to 255 us, 0.97 to 0.99 of the copy bandwidth;
+// 128 rows of 8 drafts over up to 4096 tokens, 16 heads on 2 of 256: 128 to 130 us, 0.82.
 //
 // The running maximum is only moved when a row's maximum has grown by more than 2^8
-// over it: until then the probabilities are taken against the old one, which is exact
+// over it, an idea published for attention kernels of this generation: until then the probabilities are taken against the old one, which is exact
 // (they and their sum stay below 2^8 times as large, far inside fp32 and bf16's
 // range), and O is not read and rescaled.  P is rounded to bf16 because it is an
-// operand of the second product; m, l and O are fp32.
+// operand of the second product; m, l and O are fp32, and l is the sum of the values
+// before that rounding, so that lse keeps fp32's accuracy (out is off by 0.0023 of
+// itself against 64 bits, where its own rounding alone is 0.0017).
 //
 // Rows of a tile past the last token, which hold whatever the page or the buffer held,
 // and drafted tokens with a value that is not finite are zeroed in the V tile before
