@@ -49,26 +49,21 @@
 // Every wait is bounded.  One that runs out raises the block's abort flag, on which all
 // roles leave their loops; the producer then waits for the copies it has in flight and
 // the MMA warp for its MMAs, TMEM is freed, and the status word gets TIMEOUT.
-#include <mutex>
 #include <type_traits>
 
-#include <cuda.h>
-
 #include "attn_common.cuh"
+#include "attn_tc.cuh"
 #include "launch_setup.cuh"
-#include "ptx_attn.cuh"
 
 namespace gdnspec {
 namespace tat {
 
 constexpr int kRows = 128;               // query rows of an MMA
 constexpr uint32_t kTmemCols = 512;
-constexpr float kGrow = 8.0f;            // log2 of what the maximum may grow by before it is moved
 constexpr int kSmemMax = 232448;
 
 constexpr int kTile = 64;                // keys of a tile
 constexpr int kMaxStages = 12;
-constexpr uint32_t kPolls = 1u << 18;    // of a wait, before it gives up (half a second)
 
 template <int D, int NQ>
 struct Lay {
@@ -109,80 +104,6 @@ struct Misc {
     uint32_t tmem;
     int abort;
 };
-
-// Bounded wait of a whole warp, which also ends when another role has given up; one
-// answer for all lanes.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit = kPolls) {
-    bool ok = false;
-    for (uint32_t it = 0; !ok && it < limit; ++it) {
-        ok = ptx::mbar_try_wait(bar, parity);
-        if (!ok && (it & 15u) == 15u && *abort) break;
-    }
-    if (!ok) *abort = 1;
-    return __all_sync(0xffffffffu, ok);
-}
-
-// A value that all lanes hold, from one of them: the tensor core's operands are uniform
-// registers, and values that come from memory or from a loop are only seen to be
-// uniform behind a shuffle (without it each MMA costs some 300 cycles to issue).
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-// Place in a ring of `size` stages.
-struct Place {
-    uint32_t at = 0, ph = 0;
-    __device__ __forceinline__ void step(uint32_t size) {
-        if (++at == size) {
-            at = 0;
-            ph ^= 1u;
-        }
-    }
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// What a tcgen05.ld brought is only valid behind its wait: uses depend on this.
-template <int N>
-__device__ __forceinline__ void landed(uint32_t (&r)[N]) {
-    ptx::tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 // Barrier of the softmax warpgroups; whether any thread came with `bad`.
 __device__ __forceinline__ bool any_at_barrier(int threads, bool bad) {
@@ -342,11 +263,6 @@ __device__ __forceinline__ void produce(const AttnArgs &A, const CUtensorMap *mq
 }
 
 // ------------------------------------------------------------------ MMA warps
-
-__device__ __forceinline__ void commit(uint32_t bar) {
-    if (ptx::elect_one()) ptx::mma_commit(bar);
-    __syncwarp();
-}
 
 // When a warp gives up, none of its MMAs is running when TMEM is freed.
 __device__ __forceinline__ void drain(Misc *ms, int who) {
@@ -819,36 +735,6 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 }
 
 // ------------------------------------------------------------------ host
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// bf16 tensor of `rank` dims, the innermost `dims[0]` dense; strides in elements.
-bool bf16_map(CUtensorMap *map, const void *p, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-              const cuuint32_t *box) {
-    const EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t bytes[3];
-    cuuint32_t one[3] = {1, 1, 1};
-    for (int i = 0; i + 1 < rank; ++i) bytes[i] = strides[i] * 2;
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), dims, bytes, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int D, int NQ>
 cudaError_t run(const AttnArgs &A, cudaStream_t st) {
