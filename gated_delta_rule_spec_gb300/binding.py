@@ -12,7 +12,9 @@ cursors with torch and produce the C descriptors.
 
 The softmax-attention layers of a hybrid model: ``KvCache`` is the paged cache of
 all of them, ``kv_*`` its pages, ``RopePlan`` / ``rope`` / ``rope_append`` the
-rotary positions and ``tree_attn`` the attention of a drafted window.
+rotary positions and ``tree_attn`` the attention of a drafted window.  Prompts of any
+length go through them packed: ``HeadNorm`` / ``norm_rope_append`` (also ``norm_rope`` and
+its gradient ``norm_rope_grad``) and ``prompt_attn``.
 """
 from __future__ import annotations
 
@@ -77,6 +79,10 @@ class RopePlanDesc(ctypes.Structure):
                 ("mscale", ctypes.c_float), ("freq", ctypes.c_uint64 * 128)]
 
 
+class HeadNormDesc(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
 _lib = None
 EXPORTS = ("gdn_spec_verify", "gdn_spec_verify_d", "gdn_spec_commit", "gdn_spec_fold",
            "gdn_spec_reset", "gdn_spec_prefill",
@@ -86,7 +92,10 @@ EXPORTS = ("gdn_spec_verify", "gdn_spec_verify_d", "gdn_spec_commit", "gdn_spec_
            "gdn_spec_kv_init", "gdn_spec_kv_reserve", "gdn_spec_kv_fork", "gdn_spec_kv_commit",
            "gdn_spec_kv_free", "gdn_spec_kv_read_status", "gdn_spec_rope_init",
            "gdn_spec_rope_init_freqs", "gdn_spec_rope", "gdn_spec_rope_append",
-           "gdn_spec_tree_attn", "gdn_spec_tree_attn_workspace", "gdn_spec_tree_attn_path")
+           "gdn_spec_tree_attn", "gdn_spec_tree_attn_workspace", "gdn_spec_tree_attn_path",
+           "gdn_spec_norm_rope", "gdn_spec_norm_rope_grad", "gdn_spec_norm_rope_grad_workspace",
+           "gdn_spec_norm_rope_append", "gdn_spec_prompt_attn", "gdn_spec_prompt_attn_workspace",
+           "gdn_spec_prompt_attn_path")
 
 
 def library_path() -> str:
@@ -147,10 +156,23 @@ def load() -> ctypes.CDLL:
     lib.gdn_spec_tree_attn_workspace.restype = I64
     lib.gdn_spec_tree_attn_path.argtypes = [KP, I32, I32]
     lib.gdn_spec_tree_attn_path.restype = ctypes.c_char_p
+    NP = ctypes.POINTER(HeadNormDesc)
+    lib.gdn_spec_norm_rope.argtypes = [RP, NP, I32, I32, I32, P, P, I64, P, I64, P]
+    lib.gdn_spec_norm_rope_grad.argtypes = [RP, NP, I32, I32, I32, P, P, I64, P, I64, P, I64, P, P, I64, P]
+    lib.gdn_spec_norm_rope_grad_workspace.argtypes = [I32, I32, I32]
+    lib.gdn_spec_norm_rope_grad_workspace.restype = I64
+    lib.gdn_spec_norm_rope_append.argtypes = [RP, NP, NP, KP, I32, P, P, I32, I32, P, I32, P, I64, P, I64, P,
+                                              I64, P, P]
+    lib.gdn_spec_prompt_attn.argtypes = [KP, I32, P, P, I32, I32, I32, P, ctypes.c_float, P, P, P, I64, P]
+    lib.gdn_spec_prompt_attn_workspace.argtypes = [KP, I32, I32, I32]
+    lib.gdn_spec_prompt_attn_workspace.restype = I64
+    lib.gdn_spec_prompt_attn_path.argtypes = [KP, I32]
+    lib.gdn_spec_prompt_attn_path.restype = ctypes.c_char_p
     for name in ("gdn_spec_kv_init", "gdn_spec_kv_reserve", "gdn_spec_kv_fork", "gdn_spec_kv_commit",
                  "gdn_spec_kv_free", "gdn_spec_kv_read_status", "gdn_spec_rope_init",
                  "gdn_spec_rope_init_freqs", "gdn_spec_rope", "gdn_spec_rope_append",
-                 "gdn_spec_tree_attn"):
+                 "gdn_spec_tree_attn", "gdn_spec_norm_rope", "gdn_spec_norm_rope_grad",
+                 "gdn_spec_norm_rope_append", "gdn_spec_prompt_attn"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -750,4 +772,185 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
                                    cache.D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
                                    _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "gdn_spec_tree_attn")
+    return out
+
+
+# ------------------------------------------------ prompts, packed
+
+def _here(t: torch.Tensor, name: str) -> None:
+    """The calls launch on the current device: a tensor of another one is refused."""
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise GdnSpecError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+class HeadNorm:
+    """The norm of every head, x / sqrt(mean(x^2) + eps) * (weight + offset): ``weight`` is fp32 [D]
+    on the GPU and is read by the calls as it is then; ``offset`` is 1 where a model keeps its
+    weights around zero."""
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6, offset: float = 0.0):
+        if weight.dim() != 1:
+            raise GdnSpecError(f"weight: want one dimension, got {tuple(weight.shape)}")
+        _need(weight, "weight", torch.float32, (weight.shape[0],))
+        self._weight, self._desc = weight, HeadNormDesc(weight.data_ptr(), eps, offset)
+        self._ref = ctypes.byref(self._desc)
+
+    # What the calls pass is what was checked.
+    weight = property(lambda self: self._weight)
+    eps = property(lambda self: self._desc.eps)
+    offset = property(lambda self: self._desc.offset)
+    D = property(lambda self: self._weight.shape[0])
+
+    def desc(self) -> HeadNormDesc:
+        return self._desc
+
+
+def _norm_of(norm: HeadNorm | None, plan: RopePlan, name: str):
+    if norm is None:
+        return None
+    if norm.D != plan.D:
+        raise GdnSpecError(f"{name}: weights of {norm.D} dims for heads of {plan.D}")
+    _here(norm.weight, name)
+    return norm._ref
+
+
+def norm_rope(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.Tensor,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gdn_spec_norm_rope: every head of x [N, heads, D] (tokens may be strided) normed and turned
+    to positions pos [N].  out may be x."""
+    N, heads, D = x.shape if x.dim() == 3 else (0, 0, 0)
+    if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float32) or D != plan.D:
+        raise GdnSpecError(f"x: want bf16 or fp32 [N, heads, {plan.D}], got {x.dtype} {tuple(x.shape)}")
+    _need(pos, "pos", torch.int32, (N,))
+    xs = _token_stride(x, "x", x.dtype, (N, heads, D))
+    _here(x, "x")
+    if out is None:
+        out, os_ = _result((N, heads, D), x.dtype, x.device, stream), heads * D
+    else:
+        os_ = _token_stride(out, "out", x.dtype, (N, heads, D))
+    code = DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_FP32
+    rc = load().gdn_spec_norm_rope(plan._ref, _norm_of(norm, plan, "norm"), N, heads, code, _ptr(pos), _ptr(x),
+                                   xs, _ptr(out), os_, _stream(stream))
+    _check(rc, "gdn_spec_norm_rope")
+    return out
+
+
+def norm_rope_grad_workspace(N: int, heads: int, D: int) -> int:
+    """gdn_spec_norm_rope_grad_workspace: bytes that a call of this size needs on the current device."""
+    n = load().gdn_spec_norm_rope_grad_workspace(N, heads, D)
+    if n < 0:
+        _check(n, "gdn_spec_norm_rope_grad_workspace")
+    return n
+
+
+def norm_rope_grad(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.Tensor, dy: torch.Tensor,
+                   dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """gdn_spec_norm_rope_grad: (dx, dw), the gradients of norm_rope's x [N, heads, D] and of the
+    norm's weight (fp32 [D]) from dy, that of its result.  Tokens of x, dy and dx may be strided;
+    dx may be x or dy; workspace: uint8, at least ``norm_rope_grad_workspace`` bytes (None:
+    allocated for the call on its stream)."""
+    N, heads, D = x.shape if x.dim() == 3 else (0, 0, 0)
+    if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float32) or D != plan.D:
+        raise GdnSpecError(f"x: want bf16 or fp32 [N, heads, {plan.D}], got {x.dtype} {tuple(x.shape)}")
+    _need(pos, "pos", torch.int32, (N,))
+    xs = _token_stride(x, "x", x.dtype, (N, heads, D))
+    ys = _token_stride(dy, "dy", x.dtype, (N, heads, D))
+    _here(x, "x")
+    if dx is None:
+        dx, ds = _result((N, heads, D), x.dtype, x.device, stream), heads * D
+    else:
+        ds = _token_stride(dx, "dx", x.dtype, (N, heads, D))
+    if dw is None:
+        dw = _result((D,), torch.float32, x.device, stream)
+    else:
+        _need(dw, "dw", torch.float32, (D,))
+    if workspace is None:
+        workspace = _scratch(max(16, norm_rope_grad_workspace(N, heads, D)), torch.uint8, x.device, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    code = DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_FP32
+    rc = load().gdn_spec_norm_rope_grad(plan._ref, _norm_of(norm, plan, "norm"), N, heads, code, _ptr(pos), _ptr(x),
+                                        xs, _ptr(dy), ys, _ptr(dx), ds, _ptr(dw), _ptr(workspace),
+                                        workspace.numel(), _stream(stream))
+    _check(rc, "gdn_spec_norm_rope_grad")
+    return dx, dw
+
+
+def norm_rope_append(plan: RopePlan, cache: KvCache, layer: int, slot_idx: torch.Tensor, starts: torch.Tensor,
+                     q, k, v, q_norm: HeadNorm | None = None, k_norm: HeadNorm | None = None,
+                     pos: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """gdn_spec_norm_rope_append: packed prompts, row b's tokens starts[b] .. starts[b + 1] of
+    q [N, HQ, D], k and v [N, HKV, D] (slices of one projection's output, say).  Normed and rotated
+    q [N, HQ, D]; normed and rotated k, and v, go behind the slots' committed tokens in ``layer`` of
+    the cache.  A norm of None leaves that side as it is; pos int32 [N]: length + t where None."""
+    B = _rows(slot_idx, "slot_idx")
+    _need(starts, "starts", torch.int32, (B + 1,))
+    if q.dim() != 3:
+        raise GdnSpecError(f"q: want [N, heads, D], got {tuple(q.shape)}")
+    N, HQ, _ = q.shape
+    io, kv_shape = cache.io_torch, (N, cache.HKV, cache.D)
+    qs = _token_stride(q, "q", io, (N, HQ, cache.D))
+    ks = _token_stride(k, "k", io, kv_shape)
+    vs = _token_stride(v, "v", io, kv_shape)
+    _here(q, "q")
+    _here(cache.k, "cache")
+    if pos is not None:
+        _need(pos, "pos", torch.int32, (N,))
+    if q_out is None:
+        q_out = _result((N, HQ, cache.D), io, q.device, stream)
+    else:
+        _need(q_out, "q_out", io, (N, HQ, cache.D))
+    rc = load().gdn_spec_norm_rope_append(plan._ref, _norm_of(q_norm, plan, "q_norm"), _norm_of(k_norm, plan, "k_norm"),
+                                          cache._ref, layer, _ptr(slot_idx), _ptr(starts), B, N, _ptr(pos), HQ,
+                                          _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_out), _stream(stream))
+    _check(rc, "gdn_spec_norm_rope_append")
+    return q_out
+
+
+def prompt_attn_path(cache: KvCache, HQ: int) -> str:
+    r = load().gdn_spec_prompt_attn_path(cache._ref, HQ)
+    if r is None:
+        raise GdnSpecError("invalid cache descriptor or head count")
+    return r.decode()
+
+
+def prompt_attn_workspace(cache: KvCache, B: int, N: int, HQ: int) -> int:
+    """gdn_spec_prompt_attn_workspace: bytes that a call of this size needs on the current device."""
+    n = load().gdn_spec_prompt_attn_workspace(cache._ref, B, N, HQ)
+    if n < 0:
+        _check(n, "gdn_spec_prompt_attn_workspace")
+    return n
+
+
+def prompt_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, starts: torch.Tensor, q: torch.Tensor,
+                scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gdn_spec_prompt_attn: causal attention [N, HQ, D] of packed prompts, row b's tokens
+    starts[b] .. starts[b + 1] of q [N, HQ, D], over ``layer`` of the cache.  scale: D^-0.5 by
+    default; lse fp32 [N, HQ]: written when given; workspace: uint8, at least
+    ``prompt_attn_workspace`` bytes (None: allocated for the call on its stream)."""
+    B = _rows(slot_idx, "slot_idx")
+    _need(starts, "starts", torch.int32, (B + 1,))
+    if q.dim() != 3:
+        raise GdnSpecError(f"q: want [N, HQ, D], got {tuple(q.shape)}")
+    N, HQ, _ = q.shape
+    _need(q, "q", cache.io_torch, (N, HQ, cache.D))
+    _here(q, "q")
+    _here(cache.k, "cache")
+    if out is None:
+        out = _result(q.shape, q.dtype, q.device, stream)
+    else:
+        _need(out, "out", cache.io_torch, (N, HQ, cache.D))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (N, HQ))
+    if workspace is None:
+        workspace = _scratch(max(16, prompt_attn_workspace(cache, B, N, HQ)), torch.uint8, q.device, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    rc = load().gdn_spec_prompt_attn(cache._ref, layer, _ptr(slot_idx), _ptr(starts), B, N, HQ, _ptr(q),
+                                     cache.D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
+                                     _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "gdn_spec_prompt_attn")
     return out

@@ -7,6 +7,7 @@
 
 #include "attn_common.cuh"
 #include "launch_setup.cuh"
+#include "prompt_common.cuh"
 
 namespace gdnspec {
 
@@ -28,11 +29,25 @@ cudaError_t launch_rope_append(const gdn_spec_rope_plan *plan, const KvArgs &C, 
                                const int32_t *slot_idx, int B, int T, const int32_t *n_tokens, const int32_t *pos, int HQ,
                                const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                                int64_t v_stride, void *q_out, cudaStream_t st);
+cudaError_t launch_norm_rope(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *norm, int N, int heads, bool bf16,
+                             const int32_t *pos, const void *x, int64_t x_stride, void *out, int64_t out_stride, cudaStream_t st);
+cudaError_t launch_norm_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *q_norm, const gdn_spec_head_norm *k_norm,
+                                    const PromptArgs &A, bool bf16, const int32_t *pos, const void *q, int64_t q_stride,
+                                    const void *k, int64_t k_stride, const void *v, int64_t v_stride, cudaStream_t st);
+int norm_grad_blocks(int N, int heads, int sms);
+cudaError_t launch_norm_rope_grad(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *norm, int N, int heads, bool bf16,
+                                  int sms, const int32_t *pos, const void *x, int64_t x_stride, const void *dy, int64_t dy_stride,
+                                  void *dx, int64_t dx_stride, float *dw, float *part, cudaStream_t st);
 void tree_attn_cut(AttnArgs *A, int sms, int es);
 cudaError_t launch_tree_attn(const AttnArgs &A, bool bf16, cudaStream_t st);
 bool tree_attn_tc_supported(const KvArgs &C, int G, bool bf16);
 void tree_attn_tc_cut(AttnArgs *A, int sms);
 cudaError_t launch_tree_attn_tc(const AttnArgs &A, cudaStream_t st);
+void prompt_attn_cut(PromptArgs *A, int sms);
+cudaError_t launch_prompt_attn(const PromptArgs &A, cudaStream_t st);
+bool prompt_attn_tc_supported(const KvArgs &C);
+void prompt_attn_tc_cut(PromptArgs *A, int sms);
+cudaError_t launch_prompt_attn_tc(const PromptArgs &A, cudaStream_t st);
 
 }  // namespace gdnspec
 
@@ -96,6 +111,11 @@ int check_plan(const gdn_spec_rope_plan *p) {
     return GDN_SPEC_OK;
 }
 
+int check_norm(const gdn_spec_head_norm *n) {
+    if (!n || !n->weight || !(n->eps > 0.0f) || !std::isfinite(n->eps) || !std::isfinite(n->offset)) return GDN_SPEC_EINVAL;
+    return (reinterpret_cast<uintptr_t>(n->weight) & 3u) ? GDN_SPEC_EALIGN : GDN_SPEC_OK;
+}
+
 // Radians per position as a fraction of 2^64 of a turn (whole turns fall away).
 uint64_t turn_bits(double f) {
     double t = f / kTwoPi;
@@ -147,6 +167,38 @@ int attn_args(const gdn_spec_kv_cache *c, int32_t B, int32_t T, int32_t HQ, Attn
 int64_t part_rows(const AttnArgs &A) { return A.groups < 2 ? 0 : (int64_t)A.groups * A.NQT * 2 * A.MT; }
 int64_t workspace_bytes_of(const AttnArgs &A) {
     return part_rows(A) * ((int64_t)A.C.D * 4 + 8) + (int64_t)A.groups * sizeof(AttnCut);
+}
+
+// Checks of a call over packed prompts that do not need a device.
+int check_prompt(const gdn_spec_kv_cache *c, int32_t B, int32_t N, int32_t HQ) {
+    const int rc = check_cache(c);
+    if (rc) return rc;
+    if (B < 0 || N < 0 || HQ <= 0 || HQ % c->HKV != 0) return GDN_SPEC_EINVAL;
+    if (HQ / c->HKV > 4096) return GDN_SPEC_EUNSUPPORTED;
+    if (c->io_dtype == GDN_SPEC_DTYPE_BF16 && !prompt_attn_tc_supported(kv_args(c))) return GDN_SPEC_EUNSUPPORTED;
+    // the line of items' keys is counted in 63 bits: an item a token and part of a group of heads at most
+    const double items = ((double)N + B) * c->HKV * (HQ / c->HKV / 64 + 1);
+    if (items * ((double)c->max_pages * c->P + 1024) > 4.0e18) return GDN_SPEC_EUNSUPPORTED;
+    return GDN_SPEC_OK;
+}
+
+int prompt_args(const gdn_spec_kv_cache *c, int32_t B, int32_t N, int32_t HQ, PromptArgs *A) {
+    A->C = kv_args(c);
+    A->layer = 0;
+    A->B = B;
+    A->N = N;
+    A->HQ = HQ;
+    A->G = HQ / c->HKV;
+    int sms;
+    const int rc = device_sms(&sms);
+    if (rc) return rc;
+    if (c->io_dtype == GDN_SPEC_DTYPE_BF16) prompt_attn_tc_cut(A, sms); else prompt_attn_cut(A, sms);
+    return GDN_SPEC_OK;
+}
+
+int64_t part_rows(const PromptArgs &A) { return (int64_t)A.groups * 2 * A.MT; }
+int64_t workspace_bytes_of(const PromptArgs &A) {
+    return part_rows(A) * ((int64_t)A.C.D * 4 + 8) + (int64_t)A.groups * sizeof(PromptCut);
 }
 
 }  // namespace
@@ -352,6 +404,137 @@ int gdn_spec_tree_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int3
     A.wait_limit = data_wait_limit();
     if (attn_on_tc(cache, HQ)) return cuda_rc(launch_tree_attn_tc(A, as_stream(stream)));
     return cuda_rc(launch_tree_attn(A, cache->io_dtype == GDN_SPEC_DTYPE_BF16, as_stream(stream)));
+}
+
+const char *gdn_spec_prompt_attn_path(const gdn_spec_kv_cache *cache, int32_t HQ) {
+    if (check_prompt(cache, 0, 0, HQ) != GDN_SPEC_OK) return nullptr;
+    return cache->io_dtype == GDN_SPEC_DTYPE_BF16 ? "tc" : "generic";
+}
+
+int64_t gdn_spec_prompt_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, int32_t N, int32_t HQ) {
+    int rc = check_prompt(cache, B, N, HQ);
+    if (rc) return rc;
+    PromptArgs A = {};
+    if ((rc = prompt_args(cache, B, N, HQ, &A))) return rc;
+    return workspace_bytes_of(A);
+}
+
+int gdn_spec_prompt_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int32_t *slot_idx, const int32_t *starts,
+                         int32_t B, int32_t N, int32_t HQ, const void *q, float scale, void *out, float *lse,
+                         void *workspace, int64_t workspace_bytes, void *stream) {
+    int rc = check_prompt(cache, B, N, HQ);
+    if (rc) return rc;
+    // scores are scaled in powers of two, by a factor that has to be finite too
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    if (layer < 0 || layer >= cache->n_layers || !(scale > 0.0f) || !std::isfinite(scale_log2)) return GDN_SPEC_EINVAL;
+    if (B == 0 || N == 0) return GDN_SPEC_OK;
+    if (!slot_idx || !starts || !q || !out || !workspace) return GDN_SPEC_EINVAL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return GDN_SPEC_EALIGN;
+    PromptArgs A = {};
+    if ((rc = prompt_args(cache, B, N, HQ, &A))) return rc;
+    const int64_t rows = part_rows(A);
+    if (workspace_bytes < workspace_bytes_of(A)) return GDN_SPEC_EINVAL;
+    A.layer = layer;
+    A.slot_idx = slot_idx;
+    A.starts = starts;
+    A.scale_log2 = scale_log2;
+    A.q = q;
+    A.out = out;
+    A.lse = lse;
+    A.part_o = static_cast<float4 *>(workspace);
+    A.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + rows * cache->D * 4);
+    A.cuts = reinterpret_cast<PromptCut *>(static_cast<char *>(workspace) + rows * ((int64_t)cache->D * 4 + 8));
+    A.wait_limit = data_wait_limit();
+    if (cache->io_dtype == GDN_SPEC_DTYPE_BF16) return cuda_rc(launch_prompt_attn_tc(A, as_stream(stream)));
+    return cuda_rc(launch_prompt_attn(A, as_stream(stream)));
+}
+
+int gdn_spec_norm_rope(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *norm, int32_t N, int32_t heads,
+                       int32_t io_dtype, const int32_t *pos, const void *x, int64_t x_stride, void *out, int64_t out_stride,
+                       void *stream) {
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if ((rc = check_norm(norm))) return rc;
+    if (io_dtype != GDN_SPEC_DTYPE_BF16 && io_dtype != GDN_SPEC_DTYPE_FP32) return GDN_SPEC_EDTYPE;
+    if (N < 0 || heads <= 0) return GDN_SPEC_EINVAL;
+    const int64_t row = (int64_t)heads * plan->D;
+    if (x_stride < row || out_stride < row || (x && x == out && x_stride != out_stride)) return GDN_SPEC_EINVAL;
+    if (x_stride % 8 != 0 || out_stride % 8 != 0) return GDN_SPEC_EALIGN;
+    if (row > (1 << 22)) return GDN_SPEC_EUNSUPPORTED;
+    if (N == 0) return GDN_SPEC_OK;
+    if (!pos || !x || !out) return GDN_SPEC_EINVAL;
+    if (!aligned16(x) || !aligned16(out)) return GDN_SPEC_EALIGN;
+    return cuda_rc(launch_norm_rope(plan, norm, N, heads, io_dtype == GDN_SPEC_DTYPE_BF16, pos, x, x_stride, out, out_stride,
+                                    as_stream(stream)));
+}
+
+int64_t gdn_spec_norm_rope_grad_workspace(int32_t N, int32_t heads, int32_t D) {
+    if (N < 0 || heads <= 0 || D <= 0) return GDN_SPEC_EINVAL;
+    if (D % 8 != 0) return GDN_SPEC_EALIGN;
+    if (D > 256 || (int64_t)heads * D > (1 << 22)) return GDN_SPEC_EUNSUPPORTED;
+    int sms;
+    const int rc = device_sms(&sms);
+    if (rc) return rc;
+    const int blocks = norm_grad_blocks(N, heads, sms);
+    return blocks < 2 ? 0 : (int64_t)blocks * D * (int64_t)sizeof(float);
+}
+
+int gdn_spec_norm_rope_grad(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *norm, int32_t N, int32_t heads,
+                            int32_t io_dtype, const int32_t *pos, const void *x, int64_t x_stride, const void *dy,
+                            int64_t dy_stride, void *dx, int64_t dx_stride, float *dw, void *workspace,
+                            int64_t workspace_bytes, void *stream) {
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if ((rc = check_norm(norm))) return rc;
+    if (io_dtype != GDN_SPEC_DTYPE_BF16 && io_dtype != GDN_SPEC_DTYPE_FP32) return GDN_SPEC_EDTYPE;
+    if (N < 0 || heads <= 0) return GDN_SPEC_EINVAL;
+    const int64_t row = (int64_t)heads * plan->D;
+    if (x_stride < row || dy_stride < row || dx_stride < row) return GDN_SPEC_EINVAL;
+    if ((dx && dx == x && dx_stride != x_stride) || (dx && dx == dy && dx_stride != dy_stride)) return GDN_SPEC_EINVAL;
+    if (x_stride % 8 != 0 || dy_stride % 8 != 0 || dx_stride % 8 != 0) return GDN_SPEC_EALIGN;
+    if (row > (1 << 22)) return GDN_SPEC_EUNSUPPORTED;
+    if (!dw) return GDN_SPEC_EINVAL;
+    if (!aligned16(dw)) return GDN_SPEC_EALIGN;
+    if (N == 0) return cuda_rc(cudaMemsetAsync(dw, 0, plan->D * sizeof(float), as_stream(stream)));
+    if (!pos || !x || !dy || !dx) return GDN_SPEC_EINVAL;
+    if (!aligned16(x) || !aligned16(dy) || !aligned16(dx) || !aligned16(workspace)) return GDN_SPEC_EALIGN;
+    int sms;
+    if ((rc = device_sms(&sms))) return rc;
+    const int blocks = norm_grad_blocks(N, heads, sms);
+    if (blocks > 1 && (!workspace || workspace_bytes < (int64_t)blocks * plan->D * (int64_t)sizeof(float))) return GDN_SPEC_EINVAL;
+    return cuda_rc(launch_norm_rope_grad(plan, norm, N, heads, io_dtype == GDN_SPEC_DTYPE_BF16, sms, pos, x, x_stride, dy,
+                                         dy_stride, dx, dx_stride, dw, static_cast<float *>(workspace), as_stream(stream)));
+}
+
+int gdn_spec_norm_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *q_norm,
+                              const gdn_spec_head_norm *k_norm, const gdn_spec_kv_cache *cache, int32_t layer,
+                              const int32_t *slot_idx, const int32_t *starts, int32_t B, int32_t N, const int32_t *pos,
+                              int32_t HQ, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, void *q_out, void *stream) {
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if ((rc = check_cache(cache))) return rc;
+    if ((q_norm && (rc = check_norm(q_norm))) || (k_norm && (rc = check_norm(k_norm)))) return rc;
+    if (plan->D != cache->D) return GDN_SPEC_EINVAL;
+    if (layer < 0 || layer >= cache->n_layers || B < 0 || N < 0 || HQ <= 0) return GDN_SPEC_EINVAL;
+    const int64_t kv_row = (int64_t)cache->HKV * cache->D, q_row = (int64_t)HQ * cache->D;
+    if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row) return GDN_SPEC_EINVAL;
+    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0) return GDN_SPEC_EALIGN;
+    if (q_row + 2 * kv_row > (1 << 22)) return GDN_SPEC_EUNSUPPORTED;
+    if (B == 0 || N == 0) return GDN_SPEC_OK;
+    if (!slot_idx || !starts || !q || !k || !v || !q_out) return GDN_SPEC_EINVAL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return GDN_SPEC_EALIGN;
+    PromptArgs A = {};
+    A.C = kv_args(cache);
+    A.layer = layer;
+    A.B = B;
+    A.N = N;
+    A.HQ = HQ;
+    A.slot_idx = slot_idx;
+    A.starts = starts;
+    A.out = q_out;
+    return cuda_rc(launch_norm_rope_append(plan, q_norm, k_norm, A, cache->io_dtype == GDN_SPEC_DTYPE_BF16, pos, q, q_stride, k,
+                                           k_stride, v, v_stride, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,273 @@
+// prompt_attn.cu -- attention of packed prompts over the paged cache on the CUDA cores
+// (fp32), and the join of split items for both kernels.
+//
+// Per query row, one pass over the keys with a running maximum m and sum l in powers of
+// two: for a tile's scores s (times scale log2 e),
+//   m' = max(m, max s),  l' = l 2^(m-m') + sum 2^(s-m'),  o' = o 2^(m-m') + sum 2^(s-m') v,
+// and the row's output is o / l.  A row that has seen nothing yet has m = -inf, l = 0.
+//
+// A block of 256 threads holds 64 query rows and walks tiles of 64 keys.  A thread forms
+// the scores of four rows with four keys, then, with the probabilities in shared memory
+// where the keys were, the sums of the same rows over DP / 16 columns.
+#include "launch_setup.cuh"
+#include "prompt_common.cuh"
+
+namespace gdnspec {
+
+constexpr int kPromptThreads = 256;
+constexpr int kPromptRows = 64, kPromptTile = 64;
+
+// Q and K rows and V rows of a block, in floats; the probabilities lie where the keys were.
+constexpr int prompt_q_ld(int DP) { return DP + 4; }
+constexpr size_t prompt_smem(int DP) { return sizeof(float) * (size_t)(kPromptRows * prompt_q_ld(DP) + kPromptTile * (prompt_q_ld(DP) + DP)); }
+
+__device__ __forceinline__ void prompt_copy16(void *dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kPromptThreads) prompt_attn_kernel(const __grid_constant__ PromptArgs A) {
+    constexpr int LD = DP + 4, PLD = kPromptTile + 4, NG = DP / 64;   // groups of 64 columns, four of each a thread's
+    extern __shared__ __align__(16) float sm[];
+    __shared__ PromptScratch scratch;
+    __shared__ int64_t elem_s[kPromptTile];   // where a tile's keys and values lie in the pool
+    float *const Qs = sm, *const Ks = Qs + kPromptRows * LD, *const Vs = Ks + kPromptTile * LD, *const Ps = Ks;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, r0 = ty * 4, D = A.C.D, D4 = D >> 2;
+    const float *const qg = static_cast<const float *>(A.q);
+    grid_dep_wait();
+
+    prompt_dead_tokens<float>(A, tid, kPromptThreads);
+    const PromptPlan plan = prompt_plan<kPromptThreads>(A, &scratch);
+    PromptWalk walk(A, plan);
+    if (tid == 0) prompt_note(A, walk, plan.chunk);
+    PromptPiece pc;
+    while (walk.next(A, &pc)) {
+        const PromptItem &it = pc.it;
+        __syncthreads();   // the piece before is done with shared memory
+        for (int x = tid; x < kPromptRows * (DP / 4); x += kPromptThreads) {
+            const int r = x / (DP / 4), d = x % (DP / 4) * 4;
+            bool on;
+            const int64_t row = prompt_out_row(A, it, r, &on);
+            on = on && d < D;
+            prompt_copy16(Qs + r * LD + d, qg + (on ? row * D + d : 0), on);
+        }
+        int see[4];   // keys that the thread's rows attend to
+        float m[4], l[4], acc[4][NG * 4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bool on;
+            prompt_out_row(A, it, r0 + i, &on);
+            see[i] = on ? it.len + it.q0 + (r0 + i) / A.GS + 1 : 0;
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+        }
+        const int all = it.len + it.q0 + 1;   // keys that every row attends to
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            const int k0 = t * kPromptTile;
+            const bool edge = k0 + kPromptTile > all;
+            __syncthreads();   // the tile before is done with
+            if (tid < kPromptTile) {
+                int64_t e = -1;
+                if (k0 + tid < it.keys) {
+                    const int64_t row = kv_token_row(A.C, it.slot, k0 + tid);
+                    if (row < 0) atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+                    else e = kv_elem(A.C, A.layer, it.h, row);
+                }
+                elem_s[tid] = e;
+            }
+            __syncthreads();
+            for (int x = tid; x < kPromptTile * (DP / 4); x += kPromptThreads) {   // rows past the end are zeros
+                const int r = x / (DP / 4), d = x % (DP / 4) * 4;
+                const int64_t e = elem_s[r];
+                const bool on = e >= 0 && d < D;
+                const int64_t at = on ? e + d : 0;
+                prompt_copy16(Ks + r * LD + d, static_cast<const float *>(A.C.k) + at, on);
+                prompt_copy16(Vs + r * DP + d, static_cast<const float *>(A.C.v) + at, on);
+            }
+            asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+            float s[4][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < DP; d += 4) {
+                float4 q[4], k[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    q[i] = *reinterpret_cast<const float4 *>(Qs + (r0 + i) * LD + d);
+                    k[i] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * i) * LD + d);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i][j] = fmaf(q[i].x, k[j].x, s[i][j]);
+                        s[i][j] = fmaf(q[i].y, k[j].y, s[i][j]);
+                        s[i][j] = fmaf(q[i].z, k[j].z, s[i][j]);
+                        s[i][j] = fmaf(q[i].w, k[j].w, s[i][j]);
+                    }
+            }
+            __syncthreads();   // the keys are done with: the probabilities take their place
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = edge && k0 + tx + 16 * j >= see[i] ? -INFINITY : s[i][j] * A.scale_log2;
+                    top = fmaxf(top, s[i][j]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float mn = fmaxf(m[i], top), base = mn == -INFINITY ? 0.0f : mn, al = exp2f(m[i] - base);
+                m[i] = mn;
+                l[i] *= al;
+#pragma unroll
+                for (int j = 0; j < NG * 4; ++j) acc[i][j] *= al;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = exp2f(s[i][j] - base);
+                    l[i] += p;   // this thread's keys only, until the end
+                    Ps[(r0 + i) * PLD + tx + 16 * j] = p;
+                }
+            }
+            __syncwarp();   // a row's probabilities are read by the half warp that wrote them
+            // In a tile that some row does not see all of, masked keys are left out by a test, so that an infinity or
+            // NaN there stays without effect.
+            const auto add = [&](auto test) {
+#pragma unroll 2
+                for (int k = 0; k < kPromptTile; k += 4) {
+                    float4 p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(Ps + (r0 + i) * PLD + k);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const float4 v = *reinterpret_cast<const float4 *>(Vs + (k + e) * DP + g * 64 + tx * 4);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float x = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+                                if (decltype(test)::value && x == 0.0f) continue;
+                                acc[i][g * 4] = fmaf(x, v.x, acc[i][g * 4]);
+                                acc[i][g * 4 + 1] = fmaf(x, v.y, acc[i][g * 4 + 1]);
+                                acc[i][g * 4 + 2] = fmaf(x, v.z, acc[i][g * 4 + 2]);
+                                acc[i][g * 4 + 3] = fmaf(x, v.w, acc[i][g * 4 + 3]);
+                            }
+                        }
+                }
+            };
+            if (edge) add(std::true_type());
+            else add(std::false_type());
+        }
+        const int64_t part = (int64_t)blockIdx.x * 2 + pc.side();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+            bool on;
+            const int64_t row = prompt_out_row(A, it, r0 + i, &on);
+            if (!on) continue;
+            const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int d = g * 64 + tx * 4;
+                if (d >= D) continue;
+                const float *a = acc[i] + g * 4;
+                if (pc.whole())
+                    *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + row * D + d) =
+                        make_float4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+                else
+                    A.part_o[(part * D4 + d / 4) * A.MT + r0 + i] = make_float4(a[0], a[1], a[2], a[3]);
+            }
+            if (tx == 0) {
+                if (!pc.whole()) A.part_ml[part * A.MT + r0 + i] = make_float2(m[i], l[i]);
+                else if (A.lse) A.lse[row] = attn_lse(m[i], l[i]);
+            }
+        }
+    }
+    grid_dep_launch();
+}
+
+// ------------------------------------------------------------------ join
+
+constexpr int kPromptJoinThreads = 256;
+
+// Block (g, part), for the item that chunk g starts inside of; the blocks of all chunks that do share the item's
+// elements.  A thread takes the same four dims of one row from every piece, in order.
+template <typename IO>
+__global__ void __launch_bounds__(kPromptJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs A) {
+    grid_dep_wait();
+    const int g = blockIdx.x + 1;
+    const PromptCut cut = A.cuts[g];
+    const PromptItem &it = cut.item;
+    if (it.b < 0) return;
+    if (it.tile_at(A, (int64_t)g * cut.chunk) == 0) return;   // a cut between items
+    // the cuts inside the item: from the first that leaves a tile before it on
+    const int64_t begin = it.pos + A.gap;
+    const int first = (int)((begin + A.TN + cut.chunk - 1) / cut.chunk) - 1, last = (int)((begin + it.keys - 1) / cut.chunk);
+    const int D4 = A.C.D >> 2, rows = min(A.tokens, it.cnt - it.q0) * A.GS, work = rows * D4;
+    const int block = (g - 1 - first) * gridDim.y + blockIdx.y, blocks = (last - first) * gridDim.y;   // of the item
+    for (int x = block * kPromptJoinThreads + threadIdx.x; x < work; x += blocks * kPromptJoinThreads) {
+        const int d4 = x / rows, r = x - d4 * rows;
+        bool on;
+        const int64_t row = prompt_out_row(A, it, r, &on);
+        if (!on) continue;
+        float m = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = first; c <= last; ++c) {
+            const int64_t part = (int64_t)c * 2 + (c == first ? 1 : 0);
+            const float2 ml = A.part_ml[part * A.MT + r];
+            const float4 po = A.part_o[(part * D4 + d4) * A.MT + r];
+            if (ml.y == 0.0f) continue;   // that piece saw nothing, its sums may be anything
+            const float mn = fmaxf(m, ml.x), wa = exp2f(m - mn), wb = exp2f(ml.x - mn);
+            l = l * wa + ml.y * wb;
+            o.x = o.x * wa + po.x * wb;
+            o.y = o.y * wa + po.y * wb;
+            o.z = o.z * wa + po.z * wb;
+            o.w = o.w * wa + po.w * wb;
+            m = mn;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        IO out[4] = {from_f32<IO>(o.x * inv), from_f32<IO>(o.y * inv), from_f32<IO>(o.z * inv), from_f32<IO>(o.w * inv)};
+        IO *op = static_cast<IO *>(A.out) + row * A.C.D + 4 * d4;
+        if (sizeof(IO) == 2) *reinterpret_cast<uint2 *>(op) = *reinterpret_cast<const uint2 *>(out);
+        else *reinterpret_cast<uint4 *>(op) = *reinterpret_cast<const uint4 *>(out);
+        if (A.lse && d4 == 0) A.lse[row] = attn_lse(m, l);
+    }
+}
+
+cudaError_t launch_prompt_join(const PromptArgs &A, bool bf16, cudaStream_t stream) {
+    if (A.groups < 2) return cudaSuccess;
+    const dim3 grid(A.groups - 1, 8);
+    return bf16 ? launch_dependent(prompt_join_kernel<__nv_bfloat16>, grid, dim3(kPromptJoinThreads), 0, stream, A)
+                : launch_dependent(prompt_join_kernel<float>, grid, dim3(kPromptJoinThreads), 0, stream, A);
+}
+
+// ------------------------------------------------------------------ launch
+
+template <int DP>
+static cudaError_t run_prompt_attn(const PromptArgs &A, cudaStream_t st) {
+    static KernelSetup setup;
+    int sms;
+    const cudaError_t e = kernel_setup(setup, (const void *)prompt_attn_kernel<DP>, prompt_smem(DP), &sms);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(prompt_attn_kernel<DP>, dim3(A.groups), dim3(kPromptThreads), prompt_smem(DP), st, A);
+}
+
+// The cut of the work on a machine of `sms` SMs.
+void prompt_attn_cut(PromptArgs *A, int sms) {
+    A->TN = kPromptTile;
+    A->MT = kPromptRows;
+    A->HS = (A->G + A->MT - 1) / A->MT;
+    A->GS = (A->G + A->HS - 1) / A->HS;
+    A->tokens = A->MT / A->GS;
+    A->groups = sms * (A->C.D > 128 ? 1 : 2);   // as many blocks as the registers and the shared memory leave room for
+    A->gap = kPromptTile;
+}
+
+cudaError_t launch_prompt_attn(const PromptArgs &A, cudaStream_t st) {
+    const cudaError_t e = A.C.D <= 64 ? run_prompt_attn<64>(A, st) : A.C.D <= 128 ? run_prompt_attn<128>(A, st) : run_prompt_attn<256>(A, st);
+    return e != cudaSuccess ? e : launch_prompt_join(A, false, st);
+}
+
+}  // namespace gdnspec

@@ -1,0 +1,861 @@
+// prompt_attn_tc.cu -- attention of packed prompts over the paged cache on the tensor
+// cores (bf16; heads of other than 64, 128 or 256 dims are filled up with zeros to the
+// next of them in shared memory).
+//
+// A block works through the pieces of its chunk (prompt_common.cuh) in tiles of 128 keys:
+//   S = Q K^T     tcgen05.mma kind::f16, 128 query rows x 128 keys, fp32 in TMEM
+//   P = 2^(S scale log2 e - m), rounded to bf16, back into TMEM over S
+//   O += P V      tcgen05.mma kind::f16, P from TMEM, V as it lies in its pages
+//                 (token rows of 64-element runs: the MN-major operand), fp32 in TMEM
+// D <= 128: two streams of 128 query rows, a warpgroup for the softmax of each, share every
+// key and value tile; while one's scores are softened, the other's products run.
+// D = 256: one stream, whose O takes half of TMEM, with its scores in two buffers, so that
+// the next tile's scores are formed while a softmax runs.
+//
+// One warp copies the pages' rows by TMA into one ring of 32 KB stages, one issues all
+// products, and two look through the values (below).  Products that one thread issues run in
+// order, so a stream's next scores may be issued right behind the sums that read the
+// probabilities in the same columns, without a wait between them.
+//
+// The running maximum is only moved when a row's maximum has grown by more than 2^8 over
+// it, an idea published for attention kernels of this generation: until then the
+// probabilities are taken against the old one, which is exact (they and their sum stay below 2^8
+// times as large, far inside fp32 and bf16's range), and O is not read and rescaled.  P is
+// rounded to bf16 because it is an operand of the second product; m, l and O are fp32, and
+// l is the sum of the values before that rounding, so that lse keeps fp32's accuracy.
+//
+// Rows of a tile past the last token hold whatever the page or the buffer held, and a token
+// behind the one that asks may hold anything; 0 times NaN is not 0.  So in the tiles
+// that not every row of the block sees whole, two warps look for value rows that are
+// not finite, before the products get the tile, and zero them; the terms of those that
+// some rows see are added to these rows at the end.
+//
+// Every wait is bounded.  One that runs out raises the block's abort flag, on which all
+// roles leave their loops; the producer then waits for the copies it has in flight and
+// the MMA warp for its MMAs, TMEM is freed, and the status word gets TIMEOUT.
+#include <type_traits>
+
+#include "attn_tc.cuh"
+#include "launch_setup.cuh"
+#include "prompt_common.cuh"
+
+namespace gdnspec {
+namespace pat {
+
+using tat::ex2;
+using tat::landed;
+using tat::max3;
+using tat::pack_bf16;
+using tat::pair;
+using tat::uniform;
+using tat::unpair;
+using tat::wait;
+
+constexpr int kRows = 128;               // query rows of an MMA
+constexpr int kTile = 128;               // keys of a tile
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmemMax = 232448;
+constexpr int kMaxStages = 10;
+constexpr int kCleaners = 2;             // warps that look through values
+constexpr int kNotes = 4;                // pieces whose rows that are not finite are kept
+
+template <int D>
+struct Lay {
+    static constexpr int NS = D == 256 ? 1 : 2;                // streams
+    static constexpr int kThreads = NS * 128 + 128;            // softmax warpgroups; producer, MMA, two cleaners
+    static constexpr int kParts = D == 256 ? 2 : 1;            // stages of a tile: keys in halves of the dims, values of the tokens
+    static constexpr uint32_t kKBlocks = D / 64 / kParts;      // 64-dim blocks of a stage of keys
+    static constexpr uint32_t kVBlocks = D / 64;               // of values
+    static constexpr int kVRows = kTile / kParts;              // tokens of a stage of values
+    static constexpr uint32_t kKBlock = kTile * 128, kVBlock = kVRows * 128;
+    static constexpr uint32_t kStage = kTile * D * 2 / kParts;
+    static constexpr uint32_t kQTile = kRows * D * 2;
+    // Stages stand in two rings, of keys and of values, so that a stage's barriers are met by the same warps in every phase.
+    static constexpr int NK = D == 64 ? 5 : 2, NV = D == 64 ? 5 : 3, NST = NK + NV;
+    static constexpr uint32_t kOffKV = NS * kQTile;
+    static constexpr uint32_t kOffMisc = kOffKV + NST * kStage;
+    // TMEM columns: two buffers of S (one for each of two streams), then O
+    __host__ __device__ static constexpr uint32_t col_s(int x) { return x * kTile; }
+    __host__ __device__ static constexpr uint32_t col_o(int s) { return 256 + s * 128; }
+};
+
+// Value rows of a piece that one of the cleaners found not finite, from its first key that not all rows see on.
+struct Note {
+    int piece;                            // the piece's number; another one's: there are none
+    unsigned long long rows[4];
+};
+
+// Shared memory behind the tiles.
+struct Misc {
+    uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], pv_done, drain;
+    Note notes[kCleaners][kNotes];
+    int done[8];                          // pieces that a warp of the softmax is done with
+    PromptScratch scratch;
+    uint32_t tmem;
+    int abort;
+};
+
+// What a piece asks of the streams.
+template <int D>
+struct Span {
+    int n[2];                             // tiles of each stream
+    int units;                            // tiles of the piece that any stream takes
+    int all;                              // keys that every row of the block sees
+    __device__ __forceinline__ Span(const PromptArgs &A, const PromptPiece &pc) {
+        using L = Lay<D>;
+        const int tq = A.tokens / L::NS;
+        units = 0;
+#pragma unroll
+        for (int s = 0; s < L::NS; ++s) {
+            const int first = pc.it.q0 + s * tq;   // the stream's first token
+            const int keys = first < pc.it.cnt ? pc.keys_to(first + tq) : 0;
+            n[s] = max(0, min(pc.t1, (keys + kTile - 1) / kTile) - pc.t0);
+            units = max(units, n[s]);
+        }
+        all = pc.it.len + pc.it.q0 + 1;
+    }
+};
+
+// Place in the ring of keys or of values: the stage and its phase.
+template <int D, bool KEYS>
+struct Ring {
+    uint32_t at = KEYS ? 0 : Lay<D>::NK, ph = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == (KEYS ? Lay<D>::NK : Lay<D>::NST)) {
+            at = KEYS ? 0 : Lay<D>::NK;
+            ph ^= 1u;
+        }
+    }
+};
+
+// ------------------------------------------------------------------ producer warp
+
+// One lane issues: a copy's operands are uniform registers.  The lanes look up the pages of a tile's boxes side by side.
+// In the order of use: with two streams keys and values of each tile in turn; with one, whose
+// scores run a tile ahead, K0 K1 V0 K2 V1 ...
+template <int D>
+__device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *mq, const CUtensorMap *mk,
+                                        const CUtensorMap *mv, Misc *ms, uint32_t base, const PromptPlan &plan) {
+    using L = Lay<D>;
+    const int lane = threadIdx.x & 31;
+    const int log_br = min(A.C.logP, 7), BR = 1 << log_br;     // tokens of a box: within a page and within a tile
+    const int tq = A.tokens / L::NS;
+    const uint32_t q_bytes = 128u * A.GS * min(tq, A.N);       // one 64-dim block of one query tile
+    Ring<D, true> k_ring;
+    Ring<D, false> v_ring;
+    uint32_t issued[2] = {0, 0}, q_issued[2] = {0, 0};         // of values, of keys
+    bool ok = true;
+    PromptWalk walk(A, plan);
+    PromptPiece pc;
+    // one stage of keys or values of the tile at `tok`, whose boxes' pool rows are `row`
+    const auto stage = [&](auto &ring, auto keys_c, int part, int row, int boxes) {
+        constexpr bool keys = decltype(keys_c)::value;
+        if (!wait(ptx::smem_addr(&ms->empty[ring.at]), ring.ph ^ 1u, &ms->abort)) return false;
+        const uint32_t bar = uniform(ptx::smem_addr(&ms->full[ring.at])), dst = uniform(base + L::kOffKV + ring.at * L::kStage);
+        const CUtensorMap *map = keys ? mk : mv;
+        const int rows_here = keys ? kTile : L::kVRows;        // tokens of the stage
+        const int box = min(BR, rows_here);                    // of a copy
+        const int first = keys ? 0 : part * L::kVRows;         // token of the tile where the stage starts
+        const int blocks = keys ? L::kKBlocks : L::kVBlocks, blk0 = keys ? part * L::kKBlocks : 0;
+        const uint32_t block = keys ? L::kKBlock : L::kVBlock;
+        // boxes of `box` tokens that lie before the end
+        const int n = max(0, min((boxes * BR - first) >> (31 - __clz(box)), rows_here >> (31 - __clz(box))));
+        const bool whole = keys ? A.k_whole : A.v_whole;
+        int mine = 0;   // pool row of copy `lane` of this stage
+        {
+            const int tok = first + lane * box;                // of the tile
+            mine = __shfl_sync(0xffffffffu, row, min(31, tok >> log_br)) + (tok & (BR - 1));
+        }
+        if (whole) {
+            const int r = __shfl_sync(0xffffffffu, mine, 0);
+            if (ptx::elect_one()) {
+                ptx::mbar_expect_tx(bar, n ? L::kStage : 0);
+                if (n) ptx::tma_load_3d(dst, map, bar, 0, r, blk0);
+            }
+        } else {
+            int rows[kTile / 16];
+#pragma unroll
+            for (int c = 0; c < kTile / 16; ++c) rows[c] = __shfl_sync(0xffffffffu, mine, c);
+            if (ptx::elect_one()) {
+                ptx::mbar_expect_tx(bar, (uint32_t)box * 128u * blocks * n);
+#pragma unroll
+                for (int c = 0; c < kTile / 16; ++c) {
+                    if (c >= n) break;
+                    for (int b = 0; b < blocks; ++b)
+                        ptx::tma_load_3d(dst + b * block + c * box * 128u, map, bar, (blk0 + b) * 64, rows[c], 0);
+                }
+            }
+        }
+        __syncwarp();
+        ++issued[keys];
+        ring.step();
+        return true;
+    };
+    while (ok && walk.next(A, &pc)) {
+        const PromptItem &it = pc.it;
+        const Span<D> sp(A, pc);
+        const int kv = min(it.keys, (pc.t0 + sp.units) * kTile);
+        const int32_t *table = A.C.page_table + (int64_t)it.slot * A.C.max_pages;
+        // the page of box `lane` of tile u: looked up a tile before it is used
+        const auto page_of = [&](int u) {
+            const int tok = (pc.t0 + u) * kTile + lane * BR;
+            return u < sp.units && lane * BR < kTile && tok < kv ? table[tok >> A.C.logP] : 0;
+        };
+        const auto row_of = [&](int u, int page) {
+            const int tok = (pc.t0 + u) * kTile + lane * BR;
+            if (u < sp.units && lane * BR < kTile && tok < kv && (page < 0 || page >= A.C.num_pages)) {
+                atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+                page = 0;
+            }
+            return ((A.layer * A.C.num_pages + page) * A.C.HKV + it.h) * A.C.P + (tok & (A.C.P - 1));
+        };
+        const auto boxes_of = [&](int u) { return (min(kTile, kv - (pc.t0 + u) * kTile) + BR - 1) >> log_br; };
+        const auto copy_k = [&](int u, int row) {
+            bool good = true;
+#pragma unroll
+            for (int p = 0; p < L::kParts; ++p) good = good && stage(k_ring, std::true_type(), p, row, boxes_of(u));
+            return good;
+        };
+        const auto copy_v = [&](int u, int row) {
+            bool good = true;
+#pragma unroll
+            for (int p = 0; p < L::kParts; ++p) good = good && stage(v_ring, std::false_type(), p, row, boxes_of(u));
+            return good;
+        };
+        int row = row_of(0, page_of(0)), page = page_of(1);
+        ok = copy_k(0, row);
+#pragma unroll
+        for (int s = 0; s < L::NS; ++s) {   // the query tiles, behind the first keys
+            if (!ok || sp.n[s] == 0) continue;
+            ok = wait(ptx::smem_addr(&ms->q_empty[s]), (q_issued[s] & 1u) ^ 1u, &ms->abort);
+            if (!ok) break;
+            const uint32_t bar = uniform(ptx::smem_addr(&ms->q_full[s])), dst = uniform(base + s * L::kQTile);
+            if (ptx::elect_one()) {
+                ptx::mbar_expect_tx(bar, q_bytes * L::kVBlocks);
+#pragma unroll
+                for (int blk = 0; blk < (int)L::kVBlocks; ++blk)
+                    ptx::tma_load_3d(dst + blk * (kRows * 128u), mq, bar, blk * 64, it.h * A.G + it.part * A.GS,
+                                     it.first + it.q0 + s * tq);
+            }
+            __syncwarp();
+            ++q_issued[s];
+        }
+        for (int u = 0; ok && u < sp.units; ++u) {
+            const int next = row_of(u + 1, page);
+            page = page_of(u + 2);
+            if (L::NS == 1 && u + 1 < sp.units) ok = copy_k(u + 1, next);
+            ok = ok && copy_v(u, row);
+            if (L::NS == 2 && ok && u + 1 < sp.units) ok = copy_k(u + 1, next);
+            row = next;
+        }
+    }
+    if (!ok) {   // copies in flight land before the block's shared memory goes away
+        for (uint32_t p = issued[1] > L::NK ? issued[1] - L::NK : 0; p < issued[1]; ++p)
+            ptx::mbar_wait(ptx::smem_addr(&ms->full[p % L::NK]), (p / L::NK) & 1u);
+        for (uint32_t p = issued[0] > L::NV ? issued[0] - L::NV : 0; p < issued[0]; ++p)
+            ptx::mbar_wait(ptx::smem_addr(&ms->full[L::NK + p % L::NV]), (p / L::NV) & 1u);
+#pragma unroll
+        for (int s = 0; s < L::NS; ++s)
+            if (q_issued[s]) ptx::mbar_wait(ptx::smem_addr(&ms->q_full[s]), (q_issued[s] - 1) & 1u);
+    }
+}
+
+// ------------------------------------------------------------------ MMA warp
+
+// A place in the sequence of tiles, piece after piece.
+template <int D>
+struct Cursor {
+    PromptWalk walk;
+    PromptPiece pc;
+    int u, units, n[2];
+    bool live;
+    __device__ __forceinline__ void open(const PromptArgs &A) {
+        do {
+            live = walk.next(A, &pc);
+            if (!live) return;
+            const Span<D> sp(A, pc);
+            units = sp.units;
+            n[0] = sp.n[0];
+            n[1] = Lay<D>::NS == 2 ? sp.n[1] : 0;
+        } while (units == 0);
+        u = 0;
+    }
+    __device__ __forceinline__ Cursor(const PromptArgs &A, const PromptPlan &plan) : walk(A, plan) { open(A); }
+    __device__ __forceinline__ void step(const PromptArgs &A) {
+        if (++u == units) open(A);
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void multiply(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const PromptPlan &plan) {
+    using L = Lay<D>;
+    constexpr uint32_t idesc_s = ptx::idesc_bf16(kRows, kTile), idesc_o = ptx::idesc_bf16(kRows, D) | ptx::kIdescBMn;
+    const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
+    Ring<D, true> k_ring;
+    Ring<D, false> v_ring;
+    uint32_t q_ph = 0, p_ph = 0, o_ph = 0;   // bit of a stream or buffer: parity of its next wait
+    uint32_t s_seq = 0, p_seq = 0;           // tiles whose scores were issued, whose sums were (one stream)
+    bool ok = true;
+
+    // S of buffer x from query tile s: the keys' stages have landed
+    const auto scores_part = [&](int s, int x, int part, uint32_t st, bool first) {
+        const uint64_t a = ptx::smem_desc_sw128(uniform(base + s * L::kQTile + part * (L::kKBlocks * kRows * 128u)));
+        const uint64_t b = ptx::smem_desc_sw128(uniform(base + L::kOffKV + st * L::kStage));
+        const uint32_t d = uniform(tmem + L::col_s(x));
+        if (ptx::elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < (int)L::kKBlocks * 4; ++ks)   // descriptors count in 16 bytes
+                ptx::mma_bf16(d, a + ((ks >> 2) * (kRows * 128u) + (ks & 3) * 32u) / 16,
+                              b + ((ks >> 2) * L::kKBlock + (ks & 3) * 32u) / 16, idesc_s, !first || ks != 0);
+        }
+        __syncwarp();
+    };
+    const auto sums_part = [&](int s, int x, int part, uint32_t st, bool first) {
+        const uint64_t b = ptx::smem_desc_sw128_mn(uniform(base + L::kOffKV + st * L::kStage), L::kVBlock);
+        const uint32_t d = uniform(tmem + L::col_o(s)), p = uniform(tmem + L::col_s(x) + part * (L::kVRows / 2));
+        const uint32_t keep = uniform(!first);
+        if (ptx::elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < L::kVRows / 16; ++ks)
+                ptx::mma_bf16_tmem_a(d, p + ks * 8, b + ks * 2048u / 16, idesc_o, ks != 0 ? 1u : keep);
+        }
+        __syncwarp();
+    };
+    const auto issue = [&](uint64_t &b) { tat::commit(bar(b)); };
+
+    Cursor<D> q(A, plan), p = q;   // scores run ahead of sums
+    if (L::NS == 2) {
+        // scores of unit q for stream s; `first`: of the unit
+        const auto scores = [&](int s, bool first) {
+            if (q.u == 0) {
+                ok = wait(bar(ms->q_full[s]), (q_ph >> s) & 1u, &ms->abort, A.wait_limit);
+                q_ph ^= 1u << s;
+            }
+            if (first) ok = ok && wait(bar(ms->full[k_ring.at]), k_ring.ph, &ms->abort, A.wait_limit);
+            if (!ok) return;
+            ptx::tc_fence_after_sync();
+            scores_part(s, s, 0, k_ring.at, true);
+            issue(ms->s_full[s]);
+            if (q.u == q.n[s] - 1) issue(ms->q_empty[s]);
+            if (s == 1 || q.u >= q.n[1]) {
+                issue(ms->empty[k_ring.at]);
+                k_ring.step();
+            }
+        };
+        if (q.live) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (ok && q.u < q.n[s]) scores(s, s == 0 || q.u >= q.n[0]);
+        }
+        while (ok && p.live) {
+            q.step(A);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (p.u < p.n[s]) {
+                    if (s == 0 || p.u >= p.n[0]) ok = wait(bar(ms->clean[v_ring.at]), v_ring.ph, &ms->abort, A.wait_limit);
+                    if (ok && p.u == 0) {
+                        ok = wait(bar(ms->o_empty[s]), ((o_ph >> s) & 1u) ^ 1u, &ms->abort);
+                        o_ph ^= 1u << s;
+                    }
+                    ok = ok && wait(bar(ms->p_full[s]), (p_ph >> s) & 1u, &ms->abort);
+                    p_ph ^= 1u << s;
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    sums_part(s, s, 0, v_ring.at, p.u == 0);
+                    if (p.u == p.n[s] - 1) issue(ms->o_full[s]);
+                    if (s == 1 || p.u >= p.n[1]) {
+                        issue(ms->empty[v_ring.at]);
+                        v_ring.step();
+                    }
+                }
+                if (q.live && q.u < q.n[s]) scores(s, s == 0 || q.u >= q.n[0]);
+                if (!ok) break;
+            }
+            p.step(A);
+        }
+    } else {
+        const auto scores = [&] {   // of unit q, into the next buffer
+            const int x = s_seq & 1;
+            if (q.u == 0) {
+                ok = wait(bar(ms->q_full[0]), q_ph, &ms->abort, A.wait_limit);
+                q_ph ^= 1u;
+            }
+#pragma unroll
+            for (int part = 0; part < L::kParts; ++part) {
+                ok = ok && wait(bar(ms->full[k_ring.at]), k_ring.ph, &ms->abort, A.wait_limit);
+                if (!ok) return;
+                ptx::tc_fence_after_sync();
+                scores_part(0, x, part, k_ring.at, part == 0);
+                issue(ms->empty[k_ring.at]);
+                k_ring.step();
+            }
+            issue(ms->s_full[x]);
+            if (q.u == q.n[0] - 1) issue(ms->q_empty[0]);
+            ++s_seq;
+        };
+        // Scores run a tile ahead.  The buffer that they take was read by the sums of the tile before the last, which were
+        // issued before them.
+        if (q.live) scores();
+        while (ok && p.live) {
+            q.step(A);
+            const bool same = q.live && q.u != 0;   // (the keys of another piece come behind this one's values)
+            if (same) scores();
+            const int x = p_seq & 1;
+            if (ok && p.u == 0) {
+                ok = wait(bar(ms->o_empty[0]), o_ph ^ 1u, &ms->abort);
+                o_ph ^= 1u;
+            }
+            ok = ok && wait(bar(ms->p_full[x]), (p_ph >> x) & 1u, &ms->abort);
+            p_ph ^= 1u << x;
+#pragma unroll
+            for (int part = 0; part < L::kParts; ++part) {
+                ok = ok && wait(bar(ms->clean[v_ring.at]), v_ring.ph, &ms->abort, A.wait_limit);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                sums_part(0, x, part, v_ring.at, p.u == 0 && part == 0);
+                issue(ms->empty[v_ring.at]);
+                v_ring.step();
+            }
+            if (!ok) break;
+            issue(ms->pv_done);
+            if (p.u == p.n[0] - 1) issue(ms->o_full[0]);
+            ++p_seq;
+            if (q.live && !same) scores();
+            p.step(A);
+        }
+    }
+    if (!ok) {   // none of this warp's MMAs is running when TMEM is freed
+        tat::commit(bar(ms->drain));
+        ptx::mbar_wait(bar(ms->drain), 0);
+    }
+}
+
+// ------------------------------------------------------------------ cleaners
+
+// Eight rows of a stage of values, the first `row` of it and `key` of the piece, of which those in `any` (four bits each) are
+// not finite: the ones that not every row sees (keys from `all` on) become zeros, and the piece's own are noted.
+template <int D>
+__device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, int all, int keys, unsigned any, int piece,
+                                    int who) {
+    using L = Lay<D>;
+    const int lane = threadIdx.x & 31;
+    Note *const note = &ms->notes[who][piece % kNotes];
+    if (note->piece != piece) {   // the place held an earlier piece's: all are done with it
+        const volatile int *done = ms->done;
+        for (int w = 0; w < L::NS * 4; ++w)
+            for (uint32_t it = 0; done[w] < piece - kNotes + 1; ++it) {
+                if (it == tat::kPolls || *(volatile int *)&ms->abort) {
+                    ms->abort = 1;
+                    return false;
+                }
+                __nanosleep(100);
+            }
+        __syncwarp();
+        if (lane < 4) note->rows[lane] = 0;
+        if (lane == 0) note->piece = piece;
+        __syncwarp();
+    }
+    for (int y = 0; y < 8; ++y) {
+        if (key + y < all || !((any >> (4 * y)) & 15u)) continue;
+        for (int c = lane; c < (int)L::kVBlocks * 8; c += 32)
+            *reinterpret_cast<uint4 *>(tile + (c >> 3) * L::kVBlock + (row + y) * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        if (key + y < keys && lane == 0) note->rows[(key + y - all) >> 6] |= 1ull << ((key + y - all) & 63);
+    }
+    __syncwarp();
+    return true;
+}
+
+// Warp `who` of two looks at half of the tokens of every stage of values: where the tile holds keys that some row does not
+// see, rows that are not finite become zeros, and those of the piece's own keys are noted.
+template <int D>
+__device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm, const PromptPlan &plan, int who) {
+    using L = Lay<D>;
+    constexpr int kRowsHere = L::kVRows / kCleaners;
+    const int lane = threadIdx.x & 31;
+    const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
+    Ring<D, false> ring;
+    bool ok = true;
+    int piece = 0;
+    PromptWalk walk(A, plan);
+    PromptPiece pc;
+    for (; ok && walk.next(A, &pc); ++piece) {
+        const Span<D> sp(A, pc);
+        for (int u = 0; ok && u < sp.units; ++u) {
+            const int k0 = (pc.t0 + u) * kTile;
+            for (int part = 0; ok && part < L::kParts; ++part) {
+                ok = wait(bar(ms->full[ring.at]), ring.ph, &ms->abort, A.wait_limit);
+                if (ok && k0 + kTile > sp.all) {
+                    uint8_t *tile = sm + L::kOffKV + ring.at * L::kStage;
+                    const int row0 = who * kRowsHere;                       // of the stage
+                    const int key0 = k0 + part * L::kVRows + row0;          // its key
+                    for (int r = 0; ok && r < kRowsHere; r += 8) {
+                        if (key0 + r + 8 <= sp.all) continue;
+                        // four lanes a row, each 16 of its bytes at a time; odd rows begin with their second half, so that
+                        // two rows' pieces fall in different banks
+                        __nv_bfloat162 acc = __float2bfloat162_rn(0.0f);
+                        const __nv_bfloat162 zero = acc;
+                        const uint8_t *row = tile + (row0 + r + (lane >> 2)) * 128;
+#pragma unroll
+                        for (int b = 0; b < (int)L::kVBlocks; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int c = (lane & 3) + 4 * (h ^ ((lane >> 2) & 1));
+                                const uint4 x = *reinterpret_cast<const uint4 *>(row + b * L::kVBlock + c * 16);
+                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)   // an infinity times zero is NaN too
+                                    acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), zero, acc);
+                            }
+                        const unsigned any = __ballot_sync(0xffffffffu, __hisnan(acc.x) || __hisnan(acc.y));
+                        if (any) ok = remove<D>(ms, tile, row0 + r, key0 + r, sp.all, pc.it.keys, any, piece, who);
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(ms->clean[ring.at]));
+                ring.step();
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ softmax
+
+// The terms of value rows that are not finite, for a row that sees `own` keys from `all` on: weight and value from memory.
+// o: dims from d0 on of the row's unnormalised sums over m.
+__device__ __noinline__ void add_removed(const PromptArgs &A, const Misc *ms, int piece, const PromptItem &it, int all, int own,
+                                         int64_t qrow, float m, int d0, int dims, float *o) {
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(A.q) + qrow * A.C.D;
+    for (int i = 0; i < own; ++i) {
+        bool there = false;
+        for (int w = 0; w < kCleaners; ++w) {
+            const Note &note = ms->notes[w][piece % kNotes];
+            there |= note.piece == piece && ((note.rows[i >> 6] >> (i & 63)) & 1);
+        }
+        if (!there) continue;
+        const int64_t row = kv_token_row(A.C, it.slot, all + i);
+        if (row < 0) continue;
+        const int64_t e = kv_elem(A.C, A.layer, it.h, row);
+        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(A.C.k) + e, *v = static_cast<const __nv_bfloat16 *>(A.C.v) + e;
+        float s = 0.0f;
+        for (int d = 0; d < A.C.D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
+        const float p = __bfloat162float(__float2bfloat16_rn(ex2(s * A.scale_log2 - m)));
+        for (int d = 0; d < dims; ++d) o[d] = fmaf(p, __bfloat162float(v[d0 + d]), o[d]);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t tmem, const PromptPlan &plan, int tid_all) {
+    using L = Lay<D>;
+    const int s = L::NS == 2 ? tid_all >> 7 : 0, tid = tid_all & 127, warp = tid >> 5;
+    const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+    const int tq = A.tokens / L::NS, RT = tq * A.GS;
+    const int my_row = s * RT + tid;                           // row of the block's MT
+    const float c = A.scale_log2;
+    const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
+    uint32_t seq = 0, outs = 0;                                // tiles taken, pieces put out
+    int piece = 0;
+    bool ok = true;
+    PromptWalk walk(A, plan);
+    PromptPiece pc;
+    for (; ok && walk.next(A, &pc); ++piece) {
+        const PromptItem &it = pc.it;
+        const Span<D> sp(A, pc);
+        const int n = sp.n[s];
+        bool on;
+        const int64_t row = prompt_out_row(A, it, my_row, &on);
+        on = on && tid < RT;
+        const bool whole = pc.whole();
+        const int64_t part = (int64_t)blockIdx.x * 2 + pc.side();
+        const int own = s * tq + tid / A.GS;                   // keys of the block's tokens that the row sees, less one
+        const int see = on ? sp.all + own : 0;                 // keys that the row sees
+        const int see_all = sp.all + s * tq;                   // that every row of the stream sees
+        const bool warp_on = __any_sync(0xffffffffu, on);
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; ok && j < n; ++j, ++seq) {
+            const int x = L::NS == 2 ? s : seq & 1, k0 = (pc.t0 + j) * kTile;
+            const uint32_t s_addr = lane_addr + L::col_s(x);
+            ok = wait(bar(ms->s_full[x]), (L::NS == 2 ? seq : seq >> 1) & 1u, &ms->abort);
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+            if (warp_on) {
+                uint32_t sc[kTile];
+#pragma unroll
+                for (int y = 0; y < kTile; y += 32) ptx::tmem_ld32_bits(s_addr + y, sc + y);
+                landed(sc);
+                if (k0 + kTile > see_all) {
+                    const int lim = see - k0;
+#pragma unroll
+                    for (int y = 0; y < kTile; ++y)
+                        if (y >= lim) sc[y] = 0xff800000u;
+                }
+                // eight chains of three-input maxima: one chain's latency would be the whole row's
+                float tops[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const auto f = [&](int z) { return __uint_as_float(sc[y + 8 * z]); };
+                    float t = max3(f(0), f(1), f(2));
+#pragma unroll
+                    for (int z = 3; z + 1 < 16; z += 2) t = max3(t, f(z), f(z + 1));
+                    tops[y] = fmaxf(t, f(15));
+                }
+                const float top = c * max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]),
+                                           fmaxf(tops[6], tops[7]));
+                const bool move = top > m + tat::kGrow;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float to = move ? top : m;
+                    const float al = m == -INFINITY ? 0.0f : ex2(m - to);
+                    l *= al;
+                    m = to;
+                    if (j > 0) {   // O holds the sums up to the tile before this one
+                        // (with two streams they were issued before these scores, so they are done)
+                        if (L::NS == 1) ok = wait(bar(ms->pv_done), (seq - 1) & 1u, &ms->abort);
+                        if (!ok) break;
+                        ptx::tc_fence_after_sync();
+#pragma unroll 1
+                        for (int y = 0; y < D; y += 32) {
+                            uint32_t u[32];
+                            ptx::tmem_ld32_bits(lane_addr + L::col_o(s) + y, u);
+                            landed(u);
+#pragma unroll
+                            for (int z = 0; z < 32; ++z) u[z] = __float_as_uint(__uint_as_float(u[z]) * al);
+                            ptx::tmem_st16_bits(lane_addr + L::col_o(s) + y, u);
+                            ptx::tmem_st16_bits(lane_addr + L::col_o(s) + y + 16, u + 16);
+                        }
+                    }
+                }
+                const float off = m == -INFINITY ? 0.0f : -m;
+                const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
+#pragma unroll
+                for (int y = 0; y < kTile; y += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) {
+                        float a, b;
+                        unpair(tat::fma2(pair(__uint_as_float(sc[y + 2 * z]), __uint_as_float(sc[y + 2 * z + 1])), c2, off2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[z & 3] = tat::add2(sum[z & 3], pair(a, b));
+                        p[z] = pack_bf16(a, b);
+                    }
+                    ptx::tmem_st16_bits(s_addr + y / 2, p);
+                }
+                float s0, s1;
+                unpair(tat::add2(tat::add2(sum[0], sum[1]), tat::add2(sum[2], sum[3])), s0, s1);
+                l += s0 + s1;
+                ptx::tmem_st_wait();
+            }
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->p_full[x]));
+        }
+        if (!ok) break;
+        if (n > 0) {
+            ok = wait(bar(ms->o_full[s]), outs & 1u, &ms->abort);
+            if (!ok) break;
+            ++outs;
+            ptx::tc_fence_after_sync();
+            if (warp_on) {
+                bool removed = false;
+                for (int w = 0; w < kCleaners; ++w)
+                    removed |= *(volatile int *)&ms->notes[w][piece % kNotes].piece == piece;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+                for (int d0 = 0; d0 < A.C.D; d0 += 32) {
+                    const int dims = min(32, A.C.D - d0);
+                    uint32_t u[32];
+                    ptx::tmem_ld32_bits(lane_addr + L::col_o(s) + d0, u);
+                    landed(u);
+                    float f[32];
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) f[y] = __uint_as_float(u[y]);
+                    if (!on) continue;
+                    if (removed) {   // rare: a copy of its own, so that f stays in registers
+                        float g[32];
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) g[y] = f[y];
+                        add_removed(A, ms, piece, it, sp.all, own, row, m, d0, dims, g);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) f[y] = g[y];
+                    }
+                    if (whole) {
+                        uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) + row * A.C.D + d0);
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+                            if (y < dims)
+                                out[y / 8] = make_uint4(pack_bf16(f[y] * inv, f[y + 1] * inv), pack_bf16(f[y + 2] * inv, f[y + 3] * inv),
+                                                        pack_bf16(f[y + 4] * inv, f[y + 5] * inv),
+                                                        pack_bf16(f[y + 6] * inv, f[y + 7] * inv));
+                    } else {
+                        float4 *po = A.part_o + (part * (A.C.D / 4) + d0 / 4) * A.MT + my_row;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4)
+                            if (y < dims) po[(int64_t)(y / 4) * A.MT] = make_float4(f[y], f[y + 1], f[y + 2], f[y + 3]);
+                    }
+                }
+            }
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->o_empty[s]));
+        }
+        if (on) {
+            if (!whole) A.part_ml[part * A.MT + my_row] = make_float2(m, l);
+            else if (A.lse) A.lse[row] = attn_lse(m, l);
+        }
+        __syncwarp();
+        if ((tid & 31) == 0) *(volatile int *)&ms->done[tid_all >> 5] = piece + 1;
+    }
+}
+
+// The registers of the launch are shared out anew: the softmax holds a row of scores.
+template <int REGS> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+template <int D>
+__global__ void __launch_bounds__(Lay<D>::kThreads, 1)
+prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptArgs A) {
+    using L = Lay<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *sm = smem_raw + pad;
+    Misc *ms = reinterpret_cast<Misc *>(sm + L::kOffMisc);
+    const uint32_t base = raw + pad;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    uint32_t have;
+    asm("mov.u32 %0, %dynamic_smem_size;" : "=r"(have));
+    if (pad + L::kOffMisc + sizeof(Misc) > have) {   // the segment does not start where it always has
+        grid_dep_wait();
+        if (tid == 0) {
+            atomicOr(A.C.status, GDN_SPEC_ST_TIMEOUT);
+            PromptCut none;
+            none.item.b = -1;
+            A.cuts[blockIdx.x] = none;   // the join finds an empty chunk
+        }
+        return;
+    }
+    if (tid == 0) {
+        const auto init = [](uint64_t &b, uint32_t n) { ptx::mbar_init(ptx::smem_addr(&b), n); };
+        for (int i = 0; i < L::NST; ++i) {
+            init(ms->full[i], 1);
+            init(ms->empty[i], 1);
+            init(ms->clean[i], kCleaners);
+        }
+        for (int i = 0; i < 2; ++i) {
+            init(ms->q_full[i], 1);
+            init(ms->q_empty[i], 1);
+            init(ms->s_full[i], 1);
+            init(ms->p_full[i], 4);
+            init(ms->o_full[i], 1);
+            init(ms->o_empty[i], 4);
+        }
+        init(ms->pv_done, 1);
+        init(ms->drain, 1);
+        for (int w = 0; w < kCleaners; ++w)
+            for (int i = 0; i < kNotes; ++i) ms->notes[w][i].piece = -1;
+        for (int i = 0; i < 8; ++i) ms->done[i] = 0;
+        ms->abort = 0;
+        ptx::mbar_init_fence();
+        ptx::prefetch_tmap(&mq);
+        ptx::prefetch_tmap(&mk);
+        ptx::prefetch_tmap(&mv);
+    }
+    if (warp == 0) ptx::tmem_alloc(ptx::smem_addr(&ms->tmem), kTmemCols);
+    grid_dep_wait();   // nothing in global memory was touched so far
+    const PromptPlan plan = prompt_plan<L::kThreads>(A, &ms->scratch);
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = ms->tmem;
+
+    // Registers of a thread with 384 of them: 168 at launch; 2 x 128 x 200 + 128 x 104 = 384 x 168.
+    if (warp < L::NS * 4) {
+        if (L::NS == 2) more_registers<200>();
+        // while the first tile is on its way
+        prompt_dead_tokens<__nv_bfloat16>(A, tid, L::NS * 128);
+        soften<D>(A, ms, tmem, plan, tid);
+    } else {
+        if (L::NS == 2) fewer_registers<104>();
+        const int role = warp - L::NS * 4;
+        if (role == 0) {
+            if (ptx::elect_one()) prompt_note(A, PromptWalk(A, plan), plan.chunk);
+            __syncwarp();
+            produce<D>(A, &mq, &mk, &mv, ms, base, plan);
+        } else if (role == 1) {
+            multiply<D>(A, ms, base, tmem, plan);
+        } else {
+            clean<D>(A, ms, sm, plan, role - 2);
+        }
+        __syncwarp();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    if (warp == 0) ptx::tmem_dealloc(tmem, kTmemCols);
+    if (tid == 0 && ms->abort) atomicOr(A.C.status, GDN_SPEC_ST_TIMEOUT);
+    grid_dep_launch();
+}
+
+// ------------------------------------------------------------------ host
+
+template <int D>
+cudaError_t run(const PromptArgs &A, cudaStream_t st) {
+    using L = Lay<D>;
+    static_assert(L::kOffMisc + sizeof(Misc) <= kSmemMax && L::NST <= kMaxStages, "shared memory");
+    // room to reach a 1024-byte boundary (the dynamic segment starts on one: there is no static one)
+    constexpr size_t need = L::kOffMisc + sizeof(Misc) + 1024;
+    constexpr size_t smem = need < (size_t)kSmemMax ? need : (size_t)kSmemMax;
+    static KernelSetup setup;
+    int sms;
+    cudaError_t e = kernel_setup(setup, (const void *)prompt_attn_tc_kernel<D>, smem, &sms);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t rows = (cuuint64_t)A.C.n_layers * A.C.num_pages * A.C.HKV * A.C.P, dims = A.C.D;
+    // Keys and values as (64 dims, token rows, blocks of 64 dims) where a box can hold all of a stage's blocks (they land
+    // one after another), else as (dims, token rows, 1) with a box for each block; dims past the head's are filled with
+    // zeros.
+    const auto map_kv = [&](CUtensorMap *map, const void *p, bool whole, int tokens, uint32_t blocks) {
+        const cuuint64_t size[3] = {whole ? 64 : dims, rows, whole ? dims / 64 : 1}, stride[2] = {dims, 64};
+        const cuuint32_t box[3] = {64, (cuuint32_t)(A.C.P < tokens ? A.C.P : tokens), whole ? blocks : 1u};
+        return tat::bf16_map(map, p, 3, size, stride, box);
+    };
+    const int tq = A.tokens / L::NS;
+    const cuuint64_t q_dims[3] = {dims, (cuuint64_t)A.HQ, (cuuint64_t)A.N}, q_stride[2] = {dims, (cuuint64_t)A.HQ * dims};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)A.GS, (cuuint32_t)(tq < A.N ? tq : A.N)};
+    CUtensorMap mq, mk, mv;
+    if (!map_kv(&mk, A.C.k, A.k_whole, kTile, L::kKBlocks) || !map_kv(&mv, A.C.v, A.v_whole, L::kVRows, L::kVBlocks) ||
+        !tat::bf16_map(&mq, A.q, 3, q_dims, q_stride, q_box))
+        return cudaErrorInvalidValue;
+    return launch_dependent(prompt_attn_tc_kernel<D>, dim3(A.groups), dim3(L::kThreads), smem, st, mq, mk, mv, A);
+}
+
+}  // namespace pat
+
+// Rows of the pool are coordinates of a copy.
+bool prompt_attn_tc_supported(const KvArgs &C) { return (int64_t)C.n_layers * C.num_pages * C.HKV * C.P <= INT32_MAX; }
+
+// The cut of the work: a stream's query tile holds whole tokens, as many as fit in 128 rows.
+void prompt_attn_tc_cut(PromptArgs *A, int sms) {
+    const int streams = A->C.D > 128 ? 1 : 2;
+    A->HS = (A->G + pat::kRows - 1) / pat::kRows;
+    A->GS = (A->G + A->HS - 1) / A->HS;
+    A->tokens = streams * (pat::kRows / A->GS);
+    A->MT = A->tokens * A->GS;
+    A->TN = pat::kTile;
+    A->k_whole = A->C.P >= pat::kTile && A->C.D % 64 == 0 && A->C.D != 192;
+    A->v_whole = A->C.P >= pat::kTile / (A->C.D > 128 ? 2 : 1) && A->C.D % 64 == 0 && A->C.D != 192;
+    A->groups = sms;
+    A->gap = 4 * pat::kTile;
+}
+
+cudaError_t launch_prompt_attn_tc(const PromptArgs &A, cudaStream_t st) {
+    const cudaError_t e = A.C.D <= 64 ? pat::run<64>(A, st) : A.C.D <= 128 ? pat::run<128>(A, st) : pat::run<256>(A, st);
+    return e != cudaSuccess ? e : launch_prompt_join(A, true, st);
+}
+
+}  // namespace gdnspec

@@ -1,0 +1,333 @@
+// prompt_common.cuh -- how the work of the attention of packed prompts is cut and put
+// together again; shared by its kernels and by the kernel that joins split items.
+//
+// Row b of a call owns tokens starts[b] .. starts[b + 1] of the packed tensors.  Its item
+// (h, i) is one kv head h and one block i of `tokens` consecutive tokens: the block's
+// tokens times the GS query heads of the group are the rows of the products (row r is
+// token r / GS, head r % GS), and its keys are the committed ones and those of the
+// tokens up to the block's last.  A group of more heads than a block has rows goes in HS
+// parts, each like a kv head of its own.
+//
+// Items stand in one line, rows first, then heads, then blocks; an item's length is its keys
+// plus `gap`, what it costs besides them, so a row's part of the line is an arithmetic
+// series and both directions (the place where item i starts, the item at a place) are
+// closed forms.  The line is cut into equal chunks, one for each block of the grid, which
+// finds its own from the counts on the device.  So one long prompt, many short ones and
+// single tokens behind long contexts all spread evenly over the machine, and nothing
+// about the lengths is known on the host.  A cut inside an item falls on a key tile and
+// leaves unnormalised pieces in the workspace (at most two a chunk), which the join
+// kernel merges in order: the result does not depend on timing.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace gdnspec {
+
+struct PromptArgs {
+    KvArgs C;
+    int layer, B, N, HQ, G;
+    int GS, HS;                // heads of a part of a group, parts of a group
+    const int32_t *slot_idx, *starts;
+    float scale_log2;          // scale * log2(e): probabilities are powers of two
+    const void *q;
+    void *out;
+    float *lse;
+    float4 *part_o;            // [groups][2][D / 4][MT] unnormalised sums of a piece
+    float2 *part_ml;           // [groups][2][MT] (maximum in log2 units, sum)
+    struct PromptCut *cuts;    // [groups] where each chunk starts, for the join
+    int TN, MT, tokens;        // keys of a tile; rows and tokens of a block
+    int groups, gap;
+    bool k_whole, v_whole;     // tensor-core kernel: one copy holds all dims of a stage
+    uint32_t wait_limit;
+};
+
+struct PromptRow {
+    int slot, len, cnt;        // cnt = 0: nothing to compute
+    int first, owned;          // its tokens in the packed tensors
+};
+
+__device__ __forceinline__ PromptRow prompt_row(const PromptArgs &A, int b, uint32_t *bits) {
+    PromptRow r;
+    r.slot = A.slot_idx[b];
+    r.first = A.starts[b];
+    const int end = A.starts[b + 1];
+    *bits = 0;
+    if (r.first < 0 || end < r.first || end > A.N) {   // no range of tokens: there is nothing that could be written
+        *bits = GDN_SPEC_ST_ACCEPT_RANGE;
+        r.first = r.owned = r.len = r.cnt = 0;
+        return r;
+    }
+    r.cnt = r.owned = end - r.first;
+    r.len = kv_row(A.C, r.slot, r.cnt, r.cnt, bits);
+    if (r.len < 0) r.len = r.cnt = 0;
+    return r;
+}
+
+// The line of one row: `blocks` items for each of its heads, block i starting `before(i)` behind the head's start.
+struct PromptLine {
+    int blocks;
+    int64_t step, head;        // an item's length without its own tokens; a head's
+    int tokens;
+    __device__ __forceinline__ PromptLine(const PromptArgs &A, const PromptRow &r) : tokens(A.tokens) {
+        blocks = (r.cnt + A.tokens - 1) / A.tokens;
+        step = (int64_t)r.len + A.gap;
+        head = blocks ? before(blocks - 1) + step + r.cnt : 0;
+    }
+    __device__ __forceinline__ int64_t before(int64_t i) const { return i * step + tokens * (i * (i + 1) / 2); }
+    // the item at place `off` of the head
+    __device__ __forceinline__ int at(int64_t off) const {
+        // tokens / 2 i^2 + b i = off, in the form without a difference; the loops take what fp32 is off by
+        const float b = (float)step + 0.5f * tokens;
+        int i = (int)fminf(2.0f * (float)off / (b + sqrtf(b * b + 2.0f * tokens * (float)off)), 2.0e9f);
+        i = max(0, min(i, blocks - 1));
+        while (i > 0 && before(i) > off) --i;
+        while (i + 1 < blocks && before(i + 1) <= off) ++i;
+        return i;
+    }
+};
+
+__device__ __forceinline__ int64_t prompt_span(const PromptArgs &A, const PromptRow &r) {
+    return PromptLine(A, r).head * A.C.HKV * A.HS;
+}
+
+// One item: what it covers and where it stands in the line.
+struct PromptItem {
+    int b, slot, len, cnt, first;
+    int h, part, q0;           // kv head, part of its group, the block's first token of the row
+    int keys, tiles;
+    int64_t pos;               // its place in the line
+    // The tile on which a cut at this place of the line falls.
+    __device__ __forceinline__ int tile_at(const PromptArgs &A, int64_t place) const {
+        const int64_t off = place - pos - A.gap;
+        return off <= 0 ? 0 : off >= keys ? tiles : (int)(off / A.TN);
+    }
+};
+
+// Where a chunk starts, noted by its block for the join; item.b = -1: past the end.
+struct __align__(16) PromptCut {
+    PromptItem item;
+    int64_t chunk;
+};
+
+struct PromptPlan {
+    int64_t total, chunk;      // length of the line and of a chunk
+    int b;                     // the row at the chunk's start (-1: past the end)
+    int64_t off;               // and the place in the row's part
+};
+
+struct PromptScratch {
+    int64_t sums[32], off;
+    int b;
+};
+
+// Sum over the block of x; *before: of the threads below.
+template <int THREADS>
+__device__ __forceinline__ int64_t prompt_scan(int64_t x, PromptScratch *sc, int64_t *before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sc->sums[warp] = inc;
+    __syncthreads();
+    int64_t sum = 0, base = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const int64_t s = sc->sums[w];
+        if (w < warp) base += s;
+        sum += s;
+    }
+    *before = base + inc - x;
+    __syncthreads();
+    return sum;
+}
+
+// By all threads of a block: the line's length and the row at place blockIdx.x * chunk.
+// The grid's first block records the rows' status bits.
+template <int THREADS>
+__device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScratch *sc) {
+    PromptPlan p;
+    const int tid = threadIdx.x;
+    p.total = 0;
+    int64_t mine = 0, before = 0;   // of the first THREADS rows
+    for (int b0 = 0; b0 < A.B; b0 += THREADS) {
+        int64_t x = 0, ex;
+        if (b0 + tid < A.B) {
+            uint32_t bits;
+            const PromptRow r = prompt_row(A, b0 + tid, &bits);
+            if (bits && blockIdx.x == 0) atomicOr(A.C.status, bits);
+            x = prompt_span(A, r);
+        }
+        const int64_t sum = prompt_scan<THREADS>(x, sc, &ex);
+        if (b0 == 0) { mine = x; before = ex; }
+        p.total += sum;
+    }
+    // a chunk is a tile at least, so that cuts inside an item fall on different tiles
+    p.chunk = max((int64_t)A.TN, (p.total + A.groups - 1) / A.groups);
+    const int64_t at = (int64_t)blockIdx.x * p.chunk;
+    if (tid == 0) sc->b = -1;
+    __syncthreads();
+    if (at < p.total) {
+        int64_t base = 0;
+        for (int b0 = 0; b0 < A.B; b0 += THREADS) {
+            int64_t x = mine, ex = before;
+            if (b0 > 0) {
+                x = 0;
+                if (b0 + tid < A.B) {
+                    uint32_t bits;
+                    x = prompt_span(A, prompt_row(A, b0 + tid, &bits));
+                }
+            }
+            int64_t sum = 0;
+            if (A.B > THREADS) {
+                int64_t e2;
+                sum = prompt_scan<THREADS>(x, sc, &e2);
+                ex = e2;
+            }
+            if (x > 0 && base + ex <= at && at < base + ex + x) {
+                sc->b = b0 + tid;
+                sc->off = at - base - ex;
+            }
+            base += sum;
+        }
+    }
+    __syncthreads();
+    p.b = sc->b;
+    p.off = sc->off;
+    return p;
+}
+
+// The pieces of a block's chunk, one after another.  Every thread that walks does so alone.
+struct PromptPiece {
+    PromptItem it;
+    int t0, t1;                // key tiles [t0, t1) of the item's
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == it.tiles; }
+    // which of the block's two pieces it would be kept as: 1 if it starts its item
+    __device__ __forceinline__ int side() const { return t0 == 0; }
+    // keys that the tokens before `token` of the row attend to at most
+    __device__ __forceinline__ int keys_to(int token) const { return it.len + min(it.cnt, token); }
+};
+
+struct PromptWalk {
+    PromptItem it;
+    int hp, i, blocks;         // head times parts of it, block, the row's blocks
+    int64_t start, end;        // the chunk
+    bool live;
+
+    __device__ __forceinline__ void load(const PromptArgs &A) {
+        uint32_t bits;
+        const PromptRow r = prompt_row(A, it.b, &bits);
+        it.slot = r.slot, it.len = r.len, it.cnt = r.cnt, it.first = r.first;
+        blocks = (r.cnt + A.tokens - 1) / A.tokens;
+    }
+    __device__ __forceinline__ void set(const PromptArgs &A) {
+        it.h = A.HS == 1 ? hp : hp / A.HS;
+        it.part = A.HS == 1 ? 0 : hp - it.h * A.HS;
+        it.q0 = i * A.tokens;
+        it.keys = it.len + min(it.cnt, it.q0 + A.tokens);
+        it.tiles = (it.keys + A.TN - 1) / A.TN;
+    }
+    __device__ __forceinline__ PromptWalk(const PromptArgs &A, const PromptPlan &p) {
+        live = p.b >= 0;
+        if (!live) return;
+        start = (int64_t)blockIdx.x * p.chunk;
+        end = min(p.total, start + p.chunk);
+        it.b = p.b;
+        uint32_t bits;
+        const PromptRow r = prompt_row(A, p.b, &bits);
+        it.slot = r.slot, it.len = r.len, it.cnt = r.cnt, it.first = r.first;
+        const PromptLine line(A, r);
+        blocks = line.blocks;
+        hp = (int)(p.off / line.head);
+        const int64_t in = p.off - hp * line.head;
+        i = line.at(in);
+        it.pos = start - (in - line.before(i));
+        set(A);
+    }
+    __device__ __forceinline__ bool next(const PromptArgs &A, PromptPiece *pc) {
+        while (live) {
+            pc->it = it;
+            pc->t0 = it.tile_at(A, start);
+            pc->t1 = it.tile_at(A, end);
+            it.pos += it.keys + A.gap;
+            if (it.pos >= end) {
+                live = false;
+            } else {
+                if (++i == blocks) {
+                    i = 0;
+                    if (++hp == A.C.HKV * A.HS) {
+                        hp = 0;
+                        do {
+                            if (++it.b >= A.B) {   // not reached while the line is as planned
+                                live = false;
+                                break;
+                            }
+                            load(A);
+                        } while (it.cnt == 0);
+                    }
+                }
+                if (live) set(A);
+            }
+            if (pc->t0 < pc->t1) return true;
+        }
+        return false;
+    }
+};
+
+// The chunk's note; by one thread, before the walk begins.
+__device__ __forceinline__ void prompt_note(const PromptArgs &A, const PromptWalk &w, int64_t chunk) {
+    PromptCut c;
+    if (w.live) c.item = w.it;
+    else c.item.b = -1;
+    c.chunk = chunk;
+    A.cuts[blockIdx.x] = c;
+}
+
+// Row of the output for row r of an item's block, and whether the row is one.
+__device__ __forceinline__ int64_t prompt_out_row(const PromptArgs &A, const PromptItem &it, int r, bool *on) {
+    const int t = r / A.GS, g = it.part * A.GS + r - t * A.GS;
+    *on = t < A.tokens && it.q0 + t < it.cnt && g < A.G;
+    return ((int64_t)it.first + it.q0 + t) * A.HQ + it.h * A.G + g;
+}
+
+// The row that owns `token` where starts ascends: the last one that starts at or before it; by a whole warp, 32 rows looked
+// at in one step.  In [0, B) always.
+__device__ __forceinline__ int prompt_owner(const int32_t *starts, int B, int token) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = B;   // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && starts[at] <= token);
+        const int k = max(0, 31 - __clz(below));   // the last lane that starts at or before it (rows ascend)
+        const int end = lo + n;
+        lo += k * step;
+        n = min(step, end - lo);
+    }
+    return lo;
+}
+
+// Tokens of rows that nothing computes (padding rows, rows that were refused): zeros, and an lse of -inf.  By `threads`
+// threads (whole warps) of each block; every block takes an equal share of the packed tokens.
+template <typename IO>
+__device__ __forceinline__ void prompt_dead_tokens(const PromptArgs &A, int thread, int threads) {
+    const int n0 = (int)((int64_t)A.N * blockIdx.x / gridDim.x), n1 = (int)((int64_t)A.N * (blockIdx.x + 1) / gridDim.x);
+    if (n0 >= n1) return;
+    for (int b = prompt_owner(A.starts, A.B, n0); b < A.B && A.starts[b] < n1; ++b) {
+        uint32_t bits;
+        const PromptRow r = prompt_row(A, b, &bits);
+        if (r.cnt || !r.owned) continue;
+        const int64_t t0 = max(n0, r.first), t1 = min(n1, r.first + r.owned);
+        float4 *o = reinterpret_cast<float4 *>(static_cast<IO *>(A.out) + t0 * A.HQ * A.C.D);
+        const int64_t n = (t1 - t0) * A.HQ * A.C.D * (int64_t)sizeof(IO) / 16;
+        for (int64_t i = thread; i < n; i += threads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (A.lse)
+            for (int64_t i = thread; i < (t1 - t0) * A.HQ; i += threads) A.lse[t0 * A.HQ + i] = -INFINITY;
+    }
+}
+
+cudaError_t launch_prompt_join(const PromptArgs &A, bool bf16, cudaStream_t stream);
+
+}  // namespace gdnspec

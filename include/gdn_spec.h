@@ -66,7 +66,7 @@
 extern "C" {
 #endif
 
-#define GDN_SPEC_ABI_VERSION 5   /* 2: adds gdn_spec_prefill and the snapshot comparison calls;
+#define GDN_SPEC_ABI_VERSION 6   /* 2: adds gdn_spec_prefill and the snapshot comparison calls;
                                     3: adds gdn_spec_verify_d, gdn_spec_set_wait_limit, commit's
                                        cursor check and the poisoning of rows a fold or prefill
                                        could not finish;
@@ -74,7 +74,10 @@ extern "C" {
                                        the tensor-core KDA verify ("tc_kda");
                                     5: adds the softmax-attention layers' step: gdn_spec_tree_attn,
                                        gdn_spec_rope and gdn_spec_rope_append, and the paged cache
-                                       gdn_spec_kv_* */
+                                       gdn_spec_kv_*;
+                                    6: adds prompts through the softmax-attention layers:
+                                       gdn_spec_prompt_attn, gdn_spec_norm_rope, its gradient and
+                                       gdn_spec_norm_rope_append */
 
 /* host-side error codes (return values) */
 #define GDN_SPEC_OK            0
@@ -547,6 +550,110 @@ int64_t gdn_spec_tree_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, 
 /* Name of the kernel gdn_spec_tree_attn would launch ("tc", "generic"), or NULL if the descriptor is
  * invalid.  Host only. */
 const char *gdn_spec_tree_attn_path(const gdn_spec_kv_cache *cache, int32_t T, int32_t HQ);
+
+/* ----------------------------------------------------------------------
+ * Prompts of any length, packed: row b of a call owns tokens starts[b] ..
+ * starts[b + 1] of tensors that hold N tokens, one row behind another.  Per layer:
+ * gdn_spec_norm_rope_append, then gdn_spec_prompt_attn; before them
+ * gdn_spec_kv_reserve and after all layers gdn_spec_kv_commit with path = NULL,
+ * both with the rows' counts.  Rows of one token (decode) go beside prompts in the
+ * same call.
+ *   starts  int32 [B + 1], device: ascending, 0 <= starts[b] <= starts[b + 1] <= N.
+ *           A row whose two entries are not so owns nothing (ACCEPT_RANGE).  Tokens
+ *           that no row owns are neither read nor written.
+ * Rows with slot_idx < 0, and rows refused with a status bit, get zeros.
+ * ---------------------------------------------------------------------- */
+
+/* The norm of a head x of D dims: x / sqrt(mean(x^2) + eps) * (weight + offset). */
+typedef struct {
+    const float *weight;  /* fp32 [D], device                                          */
+    float eps;            /* > 0                                                       */
+    float offset;         /* 0; 1 where a model keeps weights around zero              */
+} gdn_spec_head_norm;
+
+/*
+ * gdn_spec_norm_rope -- out = R norm(x): every head of token n normed, then turned
+ * to position pos[n] as by gdn_spec_rope.  fp32 throughout, rounded once; the sum
+ * of squares has to be finite in fp32.
+ *   arguments and limits as gdn_spec_rope; out may be x itself with the same stride
+ */
+int gdn_spec_norm_rope(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *norm, int32_t N,
+                       int32_t heads, int32_t io_dtype, const int32_t *pos, const void *x,
+                       int64_t x_stride, void *out, int64_t out_stride, void *stream);
+
+/*
+ * gdn_spec_norm_rope_grad -- the gradients of gdn_spec_norm_rope's x and weight from
+ * that of its result: with g = R^T dy, r = 1 / sqrt(mean(x^2) + eps), w = weight + offset,
+ *   dx = r (w g - r^2 x mean(w g x)),   dw = sum over tokens and heads of r x g
+ * The same call gives the same bits.
+ *   x, dy, dx  io_dtype [N, heads, D], strides as gdn_spec_rope's; dx (written) may be x or
+ *              dy itself with the same stride
+ *   dw         fp32 [D], 16-byte aligned (written; zeros where N = 0)
+ *   workspace  device memory of workspace_bytes >= gdn_spec_norm_rope_grad_workspace, 16-byte
+ *              aligned, as gdn_spec_tree_attn's; may be NULL where that is 0
+ */
+int gdn_spec_norm_rope_grad(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *norm, int32_t N,
+                            int32_t heads, int32_t io_dtype, const int32_t *pos, const void *x,
+                            int64_t x_stride, const void *dy, int64_t dy_stride, void *dx,
+                            int64_t dx_stride, float *dw, void *workspace, int64_t workspace_bytes,
+                            void *stream);
+
+/* Bytes of workspace for such a call on the current device, or a negative GDN_SPEC_E* code. */
+int64_t gdn_spec_norm_rope_grad_workspace(int32_t N, int32_t heads, int32_t D);
+
+/*
+ * gdn_spec_norm_rope_append -- q_out = R norm(q) of packed prompts; R norm(k) and v are
+ * written behind the committed tokens of their rows' slots, token t of row b at length + t.
+ * length is not changed, and the pages must have been reserved, as for
+ * gdn_spec_rope_append.
+ *   q_norm, k_norm  NULL: no norm on that side
+ *   starts          int32 [B + 1], above
+ *   pos             int32 [N], device; NULL: length + t
+ *   q               io_dtype [N, HQ, D], k, v io_dtype [N, HKV, D]: token n at n * {q,k,v}_stride
+ *                   elements, its heads dense.  Strides are multiples of 8 elements.
+ *   q_out           io_dtype [N, HQ, D], dense (written)
+ * (HQ + 2 HKV) * D is at most 2^22.  q_out overlaps none of q, k, v.
+ * Device status: SLOT_OOR, ACCEPT_RANGE (starts), CURSOR_CORRUPT, NO_PAGES: such a row
+ * writes zeros to q_out only.  PAGE_OOR: as gdn_spec_rope_append.
+ */
+int gdn_spec_norm_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_head_norm *q_norm,
+                              const gdn_spec_head_norm *k_norm, const gdn_spec_kv_cache *cache,
+                              int32_t layer, const int32_t *slot_idx, const int32_t *starts, int32_t B,
+                              int32_t N, const int32_t *pos, int32_t HQ, const void *q, int64_t q_stride,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              void *q_out, void *stream);
+
+/*
+ * gdn_spec_prompt_attn -- causal softmax attention of packed prompts over one layer of the
+ * cache.  Token t of row b attends to the length committed tokens of its slot and to the
+ * row's tokens 0..t (cache positions length ..  length + t, written before):
+ *   out = sum_j p_j v_j,  p = softmax_j(scale <q, k_j>)
+ * What a token does not attend to has no effect on it, whatever its bits.
+ *   q          io_dtype [N, HQ, D], dense; HKV divides HQ, head h reads kv head h / (HQ / HKV)
+ *   starts     int32 [B + 1], above
+ *   scale      > 0, and scale * log2(e) a finite fp32 number
+ *   out        io_dtype [N, HQ, D], dense (written)
+ *   lse        fp32 [N, HQ] (written), natural log of the softmax denominator; -inf for rows
+ *              that get zeros; or NULL
+ *   workspace  as gdn_spec_tree_attn's, workspace_bytes >= gdn_spec_prompt_attn_workspace
+ * Two kernels (gdn_spec_prompt_attn_path): "tc" -- bf16: TMA and tcgen05, the probabilities
+ * rounded to bf16 for the second product; n_layers * num_pages * HKV * P is below 2^31 --
+ * and "generic" -- fp32 throughout on the CUDA cores.  HQ / HKV is at most 4096, and
+ * (N + B) * HKV * (1 + HQ / HKV / 64) * (max_pages * P + 1024) at most 4e18.
+ * Device status: SLOT_OOR, ACCEPT_RANGE (starts), CURSOR_CORRUPT, NO_PAGES (the row gets
+ * zeros), PAGE_OOR (the row's outputs are not valid), TIMEOUT.
+ */
+int gdn_spec_prompt_attn(const gdn_spec_kv_cache *cache, int32_t layer, const int32_t *slot_idx,
+                         const int32_t *starts, int32_t B, int32_t N, int32_t HQ, const void *q,
+                         float scale, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+                         void *stream);
+
+/* Bytes of workspace for such a call on the current device, or a negative GDN_SPEC_E* code. */
+int64_t gdn_spec_prompt_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, int32_t N, int32_t HQ);
+
+/* Name of the kernel gdn_spec_prompt_attn would launch ("tc", "generic"), or NULL if the
+ * descriptor or the head count is invalid.  Host only. */
+const char *gdn_spec_prompt_attn_path(const gdn_spec_kv_cache *cache, int32_t HQ);
 
 #ifdef __cplusplus
 }
