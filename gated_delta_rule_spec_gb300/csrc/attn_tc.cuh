@@ -14,11 +14,15 @@ namespace tat {
 
 constexpr float kGrow = 8.0f;            // log2 of what the maximum may grow by before it is moved
 constexpr uint32_t kPolls = 1u << 18;    // of a wait, before it gives up (half a second)
+constexpr uint32_t kLooks = 1;          // at a barrier, before the polls
 
 // Bounded wait of a whole warp, which also ends when another role has given up; one
-// answer for all lanes.
+// answer for all lanes.  It looks first: a phase that has passed costs some 50 cycles so,
+// and 260 by a poll.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit = kPolls) {
     bool ok = false;
+    if (limit) ok = ptx::mbar_test_wait(bar, parity);
+#pragma unroll 1
     for (uint32_t it = 0; !ok && it < limit; ++it) {
         ok = ptx::mbar_try_wait(bar, parity);
         if (!ok && (it & 15u) == 15u && *abort) break;

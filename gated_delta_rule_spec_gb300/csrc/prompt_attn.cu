@@ -15,7 +15,7 @@
 namespace gdnspec {
 
 constexpr int kPromptThreads = 256;
-constexpr int kPromptRows = 64, kPromptTile = 64;
+constexpr int kPromptRows = 64, kPromptLogTile = 6, kPromptTile = 1 << kPromptLogTile;
 
 // Q and K rows and V rows of a block, in floats; the probabilities lie where the keys were.
 constexpr int prompt_q_ld(int DP) { return DP + 4; }
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kPromptJoinThreads) prompt_join_kernel(const _
     if (it.tile_at(A, (int64_t)g * cut.chunk) == 0) return;   // a cut between items
     // the cuts inside the item: from the first that leaves a tile before it on
     const int64_t begin = it.pos + A.gap;
-    const int first = (int)((begin + A.TN + cut.chunk - 1) / cut.chunk) - 1, last = (int)((begin + it.keys - 1) / cut.chunk);
+    const int first = (int)((begin + (1 << A.log_tn) + cut.chunk - 1) / cut.chunk) - 1, last = (int)((begin + it.keys - 1) / cut.chunk);
     const int D4 = A.C.D >> 2, rows = min(A.tokens, it.cnt - it.q0) * A.GS, work = rows * D4;
     const int block = (g - 1 - first) * gridDim.y + blockIdx.y, blocks = (last - first) * gridDim.y;   // of the item
     for (int x = block * kPromptJoinThreads + threadIdx.x; x < work; x += blocks * kPromptJoinThreads) {
@@ -256,7 +256,7 @@ static cudaError_t run_prompt_attn(const PromptArgs &A, cudaStream_t st) {
 
 // The cut of the work on a machine of `sms` SMs.
 void prompt_attn_cut(PromptArgs *A, int sms) {
-    A->TN = kPromptTile;
+    A->log_tn = kPromptLogTile;
     A->MT = kPromptRows;
     A->HS = (A->G + A->MT - 1) / A->MT;
     A->GS = (A->G + A->HS - 1) / A->HS;

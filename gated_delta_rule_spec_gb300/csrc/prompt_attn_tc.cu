@@ -33,6 +33,7 @@
 // Every wait is bounded.  One that runs out raises the block's abort flag, on which all
 // roles leave their loops; the producer then waits for the copies it has in flight and
 // the MMA warp for its MMAs, TMEM is freed, and the status word gets TIMEOUT.
+#include <cstddef>
 #include <type_traits>
 
 #include "attn_tc.cuh"
@@ -52,11 +53,11 @@ using tat::unpair;
 using tat::wait;
 
 constexpr int kRows = 128;               // query rows of an MMA
-constexpr int kTile = 128;               // keys of a tile
+constexpr int kLogTile = 7, kTile = 1 << kLogTile;   // keys of a tile
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemMax = 232448;
 constexpr int kMaxStages = 10;
-constexpr int kCleaners = 2;             // warps that look through values
+constexpr int kCleaners = 1;             // warps that look through values
 constexpr int kNotes = 4;                // pieces whose rows that are not finite are kept
 
 template <int D>
@@ -88,12 +89,30 @@ struct Note {
 // Shared memory behind the tiles.
 struct Misc {
     uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], pv_done, drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], pv_done[2], turn[2], drain[2];
     Note notes[kCleaners][kNotes];
     int done[8];                          // pieces that a warp of the softmax is done with
     PromptScratch scratch;
     uint32_t tmem;
     int abort;
+};
+
+// The barriers' addresses.
+struct Bars {
+    uint32_t misc;
+    __device__ __forceinline__ uint32_t at(size_t offset, uint32_t i) const { return misc + (uint32_t)offset + 8u * i; }
+    __device__ __forceinline__ uint32_t full(uint32_t i) const { return at(offsetof(Misc, full), i); }
+    __device__ __forceinline__ uint32_t empty(uint32_t i) const { return at(offsetof(Misc, empty), i); }
+    __device__ __forceinline__ uint32_t clean(uint32_t i) const { return at(offsetof(Misc, clean), i); }
+    __device__ __forceinline__ uint32_t q_full(uint32_t i) const { return at(offsetof(Misc, q_full), i); }
+    __device__ __forceinline__ uint32_t q_empty(uint32_t i) const { return at(offsetof(Misc, q_empty), i); }
+    __device__ __forceinline__ uint32_t s_full(uint32_t i) const { return at(offsetof(Misc, s_full), i); }
+    __device__ __forceinline__ uint32_t p_full(uint32_t i) const { return at(offsetof(Misc, p_full), i); }
+    __device__ __forceinline__ uint32_t o_full(uint32_t i) const { return at(offsetof(Misc, o_full), i); }
+    __device__ __forceinline__ uint32_t o_empty(uint32_t i) const { return at(offsetof(Misc, o_empty), i); }
+    __device__ __forceinline__ uint32_t pv_done(uint32_t i) const { return at(offsetof(Misc, pv_done), i); }
+    __device__ __forceinline__ uint32_t turn(uint32_t i) const { return at(offsetof(Misc, turn), i); }
+    __device__ __forceinline__ uint32_t drain(uint32_t i) const { return at(offsetof(Misc, drain), i); }
 };
 
 // What a piece asks of the streams.
@@ -136,7 +155,7 @@ struct Ring {
 // scores run a tile ahead, K0 K1 V0 K2 V1 ...
 template <int D>
 __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *mq, const CUtensorMap *mk,
-                                        const CUtensorMap *mv, Misc *ms, uint32_t base, const PromptPlan &plan) {
+                                        const CUtensorMap *mv, Misc *ms, uint32_t base, const PromptWalk &begin) {
     using L = Lay<D>;
     const int lane = threadIdx.x & 31;
     const int log_br = min(A.C.logP, 7), BR = 1 << log_br;     // tokens of a box: within a page and within a tile
@@ -144,9 +163,10 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
     const uint32_t q_bytes = 128u * A.GS * min(tq, A.N);       // one 64-dim block of one query tile
     Ring<D, true> k_ring;
     Ring<D, false> v_ring;
-    uint32_t issued[2] = {0, 0}, q_issued[2] = {0, 0};         // of values, of keys
+    uint32_t issued[2] = {0, 0};                               // stages of values, of keys
+    uint32_t q_issued = 0, q_any = 0;                          // bit of a stream: parity of its query tiles, whether there was one
     bool ok = true;
-    PromptWalk walk(A, plan);
+    PromptWalk walk = begin;
     PromptPiece pc;
     // one stage of keys or values of the tile at `tok`, whose boxes' pool rows are `row`
     const auto stage = [&](auto &ring, auto keys_c, int part, int row, int boxes) {
@@ -157,7 +177,8 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
         const int rows_here = keys ? kTile : L::kVRows;        // tokens of the stage
         const int box = min(BR, rows_here);                    // of a copy
         const int first = keys ? 0 : part * L::kVRows;         // token of the tile where the stage starts
-        const int blocks = keys ? L::kKBlocks : L::kVBlocks, blk0 = keys ? part * L::kKBlocks : 0;
+        constexpr int blocks = keys ? L::kKBlocks : L::kVBlocks;
+        const int blk0 = keys ? part * L::kKBlocks : 0;
         const uint32_t block = keys ? L::kKBlock : L::kVBlock;
         // boxes of `box` tokens that lie before the end
         const int n = max(0, min((boxes * BR - first) >> (31 - __clz(box)), rows_here >> (31 - __clz(box))));
@@ -182,6 +203,7 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
 #pragma unroll
                 for (int c = 0; c < kTile / 16; ++c) {
                     if (c >= n) break;
+#pragma unroll
                     for (int b = 0; b < blocks; ++b)
                         ptx::tma_load_3d(dst + b * block + c * box * 128u, map, bar, (blk0 + b) * 64, rows[c], 0);
                 }
@@ -213,41 +235,46 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
         const auto boxes_of = [&](int u) { return (min(kTile, kv - (pc.t0 + u) * kTile) + BR - 1) >> log_br; };
         const auto copy_k = [&](int u, int row) {
             bool good = true;
-#pragma unroll
+#pragma unroll 1
             for (int p = 0; p < L::kParts; ++p) good = good && stage(k_ring, std::true_type(), p, row, boxes_of(u));
             return good;
         };
         const auto copy_v = [&](int u, int row) {
             bool good = true;
-#pragma unroll
+#pragma unroll 1
             for (int p = 0; p < L::kParts; ++p) good = good && stage(v_ring, std::false_type(), p, row, boxes_of(u));
             return good;
         };
-        int row = row_of(0, page_of(0)), page = page_of(1);
-        ok = copy_k(0, row);
+        // (one place for the keys' copies and one for the values': they are long)
+        constexpr int kLag = L::NS == 1 ? 1 : 0;
+        int page = page_of(0), next = page_of(1), row = 0;
+#pragma unroll 1
+        for (int u = 0; ok && u < sp.units + kLag; ++u) {
+            const int before = row;
+            row = row_of(u, page);
+            page = next;
+            next = page_of(u + 2);
+            if (u < sp.units) ok = copy_k(u, row);
+            if (u == 0) {   // the query tiles, behind the first keys
+#pragma unroll 1
+                for (int s = 0; s < L::NS; ++s) {
+                    if (!ok || sp.n[s] == 0) continue;
+                    ok = wait(ptx::smem_addr(&ms->q_empty[s]), ((q_issued >> s) & 1u) ^ 1u, &ms->abort);
+                    if (!ok) break;
+                    const uint32_t bar = uniform(ptx::smem_addr(&ms->q_full[s])), dst = uniform(base + s * L::kQTile);
+                    if (ptx::elect_one()) {
+                        ptx::mbar_expect_tx(bar, q_bytes * L::kVBlocks);
 #pragma unroll
-        for (int s = 0; s < L::NS; ++s) {   // the query tiles, behind the first keys
-            if (!ok || sp.n[s] == 0) continue;
-            ok = wait(ptx::smem_addr(&ms->q_empty[s]), (q_issued[s] & 1u) ^ 1u, &ms->abort);
-            if (!ok) break;
-            const uint32_t bar = uniform(ptx::smem_addr(&ms->q_full[s])), dst = uniform(base + s * L::kQTile);
-            if (ptx::elect_one()) {
-                ptx::mbar_expect_tx(bar, q_bytes * L::kVBlocks);
-#pragma unroll
-                for (int blk = 0; blk < (int)L::kVBlocks; ++blk)
-                    ptx::tma_load_3d(dst + blk * (kRows * 128u), mq, bar, blk * 64, it.h * A.G + it.part * A.GS,
-                                     it.first + it.q0 + s * tq);
+                        for (int blk = 0; blk < (int)L::kVBlocks; ++blk)
+                            ptx::tma_load_3d(dst + blk * (kRows * 128u), mq, bar, blk * 64, it.h * A.G + it.part * A.GS,
+                                             it.first + it.q0 + s * tq);
+                    }
+                    __syncwarp();
+                    q_issued ^= 1u << s;
+                    q_any |= 1u << s;
+                }
             }
-            __syncwarp();
-            ++q_issued[s];
-        }
-        for (int u = 0; ok && u < sp.units; ++u) {
-            const int next = row_of(u + 1, page);
-            page = page_of(u + 2);
-            if (L::NS == 1 && u + 1 < sp.units) ok = copy_k(u + 1, next);
-            ok = ok && copy_v(u, row);
-            if (L::NS == 2 && ok && u + 1 < sp.units) ok = copy_k(u + 1, next);
-            row = next;
+            if (ok && u >= kLag) ok = copy_v(u - kLag, kLag ? before : row);
         }
     }
     if (!ok) {   // copies in flight land before the block's shared memory goes away
@@ -257,7 +284,7 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
             ptx::mbar_wait(ptx::smem_addr(&ms->full[L::NK + p % L::NV]), (p / L::NV) & 1u);
 #pragma unroll
         for (int s = 0; s < L::NS; ++s)
-            if (q_issued[s]) ptx::mbar_wait(ptx::smem_addr(&ms->q_full[s]), (q_issued[s] - 1) & 1u);
+            if ((q_any >> s) & 1u) ptx::mbar_wait(ptx::smem_addr(&ms->q_full[s]), ((q_issued >> s) & 1u) ^ 1u);
     }
 }
 
@@ -281,154 +308,221 @@ struct Cursor {
         } while (units == 0);
         u = 0;
     }
-    __device__ __forceinline__ Cursor(const PromptArgs &A, const PromptPlan &plan) : walk(A, plan) { open(A); }
+    __device__ __forceinline__ Cursor(const PromptArgs &A, const PromptWalk &begin) : walk(begin) { open(A); }
     __device__ __forceinline__ void step(const PromptArgs &A) {
         if (++u == units) open(A);
     }
 };
 
+// What an MMA needs is made uniform before the waits that it hangs on, so that only the issue is behind them; one
+// lane issues, and commits to the barriers that follow.  In the elected lane only:
+
+// Scores of one stage of keys (b) with the query tile's dims that go with them (a) into d; add: onto what d holds.
 template <int D>
-__device__ __forceinline__ void multiply(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const PromptPlan &plan) {
+__device__ __forceinline__ void scores_mma(uint32_t d, uint64_t a, uint64_t b, bool add) {
     using L = Lay<D>;
-    constexpr uint32_t idesc_s = ptx::idesc_bf16(kRows, kTile), idesc_o = ptx::idesc_bf16(kRows, D) | ptx::kIdescBMn;
-    const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
+    constexpr uint32_t idesc = ptx::idesc_bf16(kRows, kTile);
+#pragma unroll
+    for (int ks = 0; ks < (int)L::kKBlocks * 4; ++ks)   // descriptors count in 16 bytes
+        ptx::mma_bf16(d, a + ((ks >> 2) * (kRows * 128u) + (ks & 3) * 32u) / 16,
+                      b + ((ks >> 2) * L::kKBlock + (ks & 3) * 32u) / 16, idesc, add || ks != 0);
+}
+
+// Sums over one stage of values (b) with its probabilities (p) into d.
+template <int D>
+__device__ __forceinline__ void sums_mma(uint32_t d, uint32_t p, uint64_t b, uint32_t add) {
+    using L = Lay<D>;
+    constexpr uint32_t idesc = ptx::idesc_bf16(kRows, D) | ptx::kIdescBMn;
+#pragma unroll
+    for (int ks = 0; ks < L::kVRows / 16; ++ks)
+        ptx::mma_bf16_tmem_a(d, p + ks * 8, b + ks * 2048u / 16, idesc, ks != 0 ? 1u : add);
+}
+
+template <int D> __device__ __forceinline__ uint64_t keys_desc(uint32_t base, uint32_t stage) {
+    return ptx::smem_desc_sw128(uniform(base + Lay<D>::kOffKV + stage * Lay<D>::kStage));
+}
+template <int D> __device__ __forceinline__ uint64_t values_desc(uint32_t base, uint32_t stage) {
+    return ptx::smem_desc_sw128_mn(uniform(base + Lay<D>::kOffKV + stage * Lay<D>::kStage), Lay<D>::kVBlock);
+}
+
+// When a warp gives up, none of its MMAs is running when TMEM is freed.
+__device__ __forceinline__ void drain(const Bars &bars, int who) {
+    tat::commit(bars.drain(who));
+    ptx::mbar_wait(bars.drain(who), 0);
+}
+
+// Two streams: all products of stream s by one warp, the other's by another, so that what one does between its issues (its
+// waits and its bookkeeping take some hundred cycles) is covered by the other's MMAs.  They issue in turns, a tile's
+// sums and the next tile's scores at a time: issued side by side both streams' products would end at the same time,
+// then both softmaxes would run at the same time, and the tensor core would be idle meanwhile.  A tile that the
+// stream takes no part in is released when it has landed.
+template <int D>
+__device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem,
+                                                const PromptWalk &begin, int s) {
+    using L = Lay<D>;
+    const Bars bars{ptx::smem_addr(ms)};
     Ring<D, true> k_ring;
     Ring<D, false> v_ring;
-    uint32_t q_ph = 0, p_ph = 0, o_ph = 0;   // bit of a stream or buffer: parity of its next wait
-    uint32_t s_seq = 0, p_seq = 0;           // tiles whose scores were issued, whose sums were (one stream)
+    uint32_t q_ph = 0, p_ph = 0, o_ph = 1, turn_ph = s ^ 1u;   // the first stream has the first turn
+    const uint32_t s_col = uniform(tmem + L::col_s(s)), o_col = uniform(tmem + L::col_o(s));
+    const uint64_t a = ptx::smem_desc_sw128(uniform(base + s * L::kQTile));
+    const uint32_t s_full = uniform(bars.s_full(s)), q_empty = uniform(bars.q_empty(s)), o_full = uniform(bars.o_full(s)),
+                   other = uniform(bars.turn(s ^ 1));
     bool ok = true;
-
-    // S of buffer x from query tile s: the keys' stages have landed
-    const auto scores_part = [&](int s, int x, int part, uint32_t st, bool first) {
-        const uint64_t a = ptx::smem_desc_sw128(uniform(base + s * L::kQTile + part * (L::kKBlocks * kRows * 128u)));
-        const uint64_t b = ptx::smem_desc_sw128(uniform(base + L::kOffKV + st * L::kStage));
-        const uint32_t d = uniform(tmem + L::col_s(x));
+    Cursor<D> q(A, begin), p = q;   // scores run a tile ahead of sums
+    const auto wait_keys = [&] {
+        ok = ok && wait(bars.full(k_ring.at), k_ring.ph, &ms->abort, A.wait_limit);
+        if (q.u == 0 && q.n[s] > 0) {
+            ok = ok && wait(bars.q_full(s), q_ph, &ms->abort, A.wait_limit);
+            q_ph ^= 1u;
+        }
+    };
+    // a piece's first scores, out of turn: its queries come when the scores of the piece before are done
+    const auto first_scores = [&] {
+        const uint64_t b = keys_desc<D>(base, k_ring.at);
+        const uint32_t empty = uniform(bars.empty(k_ring.at));
+        const bool mine = q.n[s] > 0, last = q.n[s] == 1;
+        wait_keys();
+        if (!ok) return;
+        ptx::tc_fence_after_sync();
         if (ptx::elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < (int)L::kKBlocks * 4; ++ks)   // descriptors count in 16 bytes
-                ptx::mma_bf16(d, a + ((ks >> 2) * (kRows * 128u) + (ks & 3) * 32u) / 16,
-                              b + ((ks >> 2) * L::kKBlock + (ks & 3) * 32u) / 16, idesc_s, !first || ks != 0);
+            if (mine) {
+                scores_mma<D>(s_col, a, b, false);
+                ptx::mma_commit(s_full);
+                ptx::mma_commit(empty);
+                if (last) ptx::mma_commit(q_empty);
+            } else {
+                ptx::mbar_arrive(empty);
+            }
         }
         __syncwarp();
+        k_ring.step();
     };
-    const auto sums_part = [&](int s, int x, int part, uint32_t st, bool first) {
-        const uint64_t b = ptx::smem_desc_sw128_mn(uniform(base + L::kOffKV + st * L::kStage), L::kVBlock);
-        const uint32_t d = uniform(tmem + L::col_o(s)), p = uniform(tmem + L::col_s(x) + part * (L::kVRows / 2));
-        const uint32_t keep = uniform(!first);
-        if (ptx::elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < L::kVRows / 16; ++ks)
-                ptx::mma_bf16_tmem_a(d, p + ks * 8, b + ks * 2048u / 16, idesc_o, ks != 0 ? 1u : keep);
-        }
-        __syncwarp();
-    };
-    const auto issue = [&](uint64_t &b) { tat::commit(bar(b)); };
-
-    Cursor<D> q(A, plan), p = q;   // scores run ahead of sums
-    if (L::NS == 2) {
-        // scores of unit q for stream s; `first`: of the unit
-        const auto scores = [&](int s, bool first) {
-            if (q.u == 0) {
-                ok = wait(bar(ms->q_full[s]), (q_ph >> s) & 1u, &ms->abort, A.wait_limit);
-                q_ph ^= 1u << s;
-            }
-            if (first) ok = ok && wait(bar(ms->full[k_ring.at]), k_ring.ph, &ms->abort, A.wait_limit);
-            if (!ok) return;
-            ptx::tc_fence_after_sync();
-            scores_part(s, s, 0, k_ring.at, true);
-            issue(ms->s_full[s]);
-            if (q.u == q.n[s] - 1) issue(ms->q_empty[s]);
-            if (s == 1 || q.u >= q.n[1]) {
-                issue(ms->empty[k_ring.at]);
-                k_ring.step();
-            }
-        };
-        if (q.live) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (ok && q.u < q.n[s]) scores(s, s == 0 || q.u >= q.n[0]);
-        }
-        while (ok && p.live) {
-            q.step(A);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (p.u < p.n[s]) {
-                    if (s == 0 || p.u >= p.n[0]) ok = wait(bar(ms->clean[v_ring.at]), v_ring.ph, &ms->abort, A.wait_limit);
-                    if (ok && p.u == 0) {
-                        ok = wait(bar(ms->o_empty[s]), ((o_ph >> s) & 1u) ^ 1u, &ms->abort);
-                        o_ph ^= 1u << s;
-                    }
-                    ok = ok && wait(bar(ms->p_full[s]), (p_ph >> s) & 1u, &ms->abort);
-                    p_ph ^= 1u << s;
-                    if (!ok) break;
-                    ptx::tc_fence_after_sync();
-                    sums_part(s, s, 0, v_ring.at, p.u == 0);
-                    if (p.u == p.n[s] - 1) issue(ms->o_full[s]);
-                    if (s == 1 || p.u >= p.n[1]) {
-                        issue(ms->empty[v_ring.at]);
-                        v_ring.step();
-                    }
-                }
-                if (q.live && q.u < q.n[s]) scores(s, s == 0 || q.u >= q.n[0]);
-                if (!ok) break;
-            }
-            p.step(A);
-        }
-    } else {
-        const auto scores = [&] {   // of unit q, into the next buffer
-            const int x = s_seq & 1;
-            if (q.u == 0) {
-                ok = wait(bar(ms->q_full[0]), q_ph, &ms->abort, A.wait_limit);
-                q_ph ^= 1u;
-            }
-#pragma unroll
-            for (int part = 0; part < L::kParts; ++part) {
-                ok = ok && wait(bar(ms->full[k_ring.at]), k_ring.ph, &ms->abort, A.wait_limit);
-                if (!ok) return;
-                ptx::tc_fence_after_sync();
-                scores_part(0, x, part, k_ring.at, part == 0);
-                issue(ms->empty[k_ring.at]);
-                k_ring.step();
-            }
-            issue(ms->s_full[x]);
-            if (q.u == q.n[0] - 1) issue(ms->q_empty[0]);
-            ++s_seq;
-        };
-        // Scores run a tile ahead.  The buffer that they take was read by the sums of the tile before the last, which were
-        // issued before them.
-        if (q.live) scores();
-        while (ok && p.live) {
-            q.step(A);
-            const bool same = q.live && q.u != 0;   // (the keys of another piece come behind this one's values)
-            if (same) scores();
-            const int x = p_seq & 1;
-            if (ok && p.u == 0) {
-                ok = wait(bar(ms->o_empty[0]), o_ph ^ 1u, &ms->abort);
+    if (q.live) first_scores();
+    while (ok && p.live) {
+        const bool sums = p.u < p.n[s], ends = p.u == p.n[s] - 1;
+        const uint32_t add = uniform(p.u != 0);
+        q.step(A);
+        const bool same = q.live && q.u != 0, scores = same && q.u < q.n[s], q_ends = q.u == q.n[s] - 1;
+        const uint64_t bk = keys_desc<D>(base, k_ring.at), bv = values_desc<D>(base, v_ring.at);
+        const uint32_t k_empty = uniform(bars.empty(k_ring.at)), v_empty = uniform(bars.empty(v_ring.at));
+        ok = wait(bars.clean(v_ring.at), v_ring.ph, &ms->abort, A.wait_limit);
+        if (same) wait_keys();
+        if (sums) {
+            if (p.u == 0) {
+                ok = ok && wait(bars.o_empty(s), o_ph, &ms->abort);
                 o_ph ^= 1u;
             }
-            ok = ok && wait(bar(ms->p_full[x]), (p_ph >> x) & 1u, &ms->abort);
-            p_ph ^= 1u << x;
-#pragma unroll
-            for (int part = 0; part < L::kParts; ++part) {
-                ok = ok && wait(bar(ms->clean[v_ring.at]), v_ring.ph, &ms->abort, A.wait_limit);
-                if (!ok) break;
-                ptx::tc_fence_after_sync();
-                sums_part(0, x, part, v_ring.at, p.u == 0 && part == 0);
-                issue(ms->empty[v_ring.at]);
-                v_ring.step();
+            ok = ok && wait(bars.p_full(s), p_ph, &ms->abort);
+            p_ph ^= 1u;
+        }
+        ok = ok && wait(bars.turn(s), turn_ph, &ms->abort);
+        turn_ph ^= 1u;
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        if (ptx::elect_one()) {
+            if (sums) {
+                sums_mma<D>(o_col, s_col, bv, add);
+                ptx::mma_commit(v_empty);
+                if (ends) ptx::mma_commit(o_full);
+            } else {
+                ptx::mbar_arrive(v_empty);
             }
+            if (scores) {
+                scores_mma<D>(s_col, a, bk, false);
+                ptx::mma_commit(s_full);
+                ptx::mma_commit(k_empty);
+                if (q_ends) ptx::mma_commit(q_empty);
+            } else if (same) {
+                ptx::mbar_arrive(k_empty);
+            }
+            ptx::mbar_arrive(other);
+        }
+        __syncwarp();
+        v_ring.step();
+        if (same) k_ring.step();
+        else if (q.live) first_scores();
+        p.step(A);
+    }
+    if (!ok) drain(bars, s);
+}
+
+// One stream: its scores by one warp, a tile ahead, its sums by another.
+template <int D>
+__device__ __forceinline__ void multiply_scores(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const PromptWalk &begin) {
+    using L = Lay<D>;
+    const Bars bars{ptx::smem_addr(ms)};
+    Ring<D, true> ring;
+    uint32_t seq = 0, q_ph = 0;
+    const uint32_t q_empty = uniform(bars.q_empty(0));
+    bool ok = true;
+    for (Cursor<D> q(A, begin); ok && q.live; q.step(A), ++seq) {
+        const int x = seq & 1;
+        const uint32_t d = uniform(tmem + L::col_s(x)), s_full = uniform(bars.s_full(x));
+        const bool ends = q.u == q.n[0] - 1;
+        if (q.u == 0) {
+            ok = wait(bars.q_full(0), q_ph, &ms->abort, A.wait_limit);
+            q_ph ^= 1u;
+        }
+        // the buffer is free once the sums of the tile before the last, which read its probabilities, are done
+        if (seq > 1) ok = ok && wait(bars.pv_done(x), ((seq >> 1) & 1u) ^ 1u, &ms->abort);
+#pragma unroll
+        for (int part = 0; part < L::kParts; ++part) {
+            const uint64_t a = ptx::smem_desc_sw128(uniform(base + part * (L::kKBlocks * kRows * 128u)));
+            const uint64_t b = keys_desc<D>(base, ring.at);
+            const uint32_t empty = uniform(bars.empty(ring.at));
+            ok = ok && wait(bars.full(ring.at), ring.ph, &ms->abort, A.wait_limit);
             if (!ok) break;
-            issue(ms->pv_done);
-            if (p.u == p.n[0] - 1) issue(ms->o_full[0]);
-            ++p_seq;
-            if (q.live && !same) scores();
-            p.step(A);
+            ptx::tc_fence_after_sync();
+            if (ptx::elect_one()) {
+                scores_mma<D>(d, a, b, part != 0);
+                if (part == L::kParts - 1) ptx::mma_commit(s_full);
+                ptx::mma_commit(empty);
+                if (part == L::kParts - 1 && ends) ptx::mma_commit(q_empty);
+            }
+            __syncwarp();
+            ring.step();
         }
     }
-    if (!ok) {   // none of this warp's MMAs is running when TMEM is freed
-        tat::commit(bar(ms->drain));
-        ptx::mbar_wait(bar(ms->drain), 0);
+    if (!ok) drain(bars, 0);
+}
+
+template <int D>
+__device__ __forceinline__ void multiply_sums(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const PromptWalk &begin) {
+    using L = Lay<D>;
+    const Bars bars{ptx::smem_addr(ms)};
+    Ring<D, false> ring;
+    uint32_t seq = 0, p_ph = 0, o_ph = 1;   // p_ph: bit of a buffer
+    const uint32_t o_col = uniform(tmem + L::col_o(0)), o_full = uniform(bars.o_full(0));
+    bool ok = true;
+    for (Cursor<D> p(A, begin); ok && p.live; p.step(A), ++seq) {
+        const int x = seq & 1;
+        const uint32_t s_col = uniform(tmem + L::col_s(x)), pv_done = uniform(bars.pv_done(x)), add = uniform(p.u != 0);
+        const bool ends = p.u == p.n[0] - 1;
+        if (p.u == 0) {
+            ok = wait(bars.o_empty(0), o_ph, &ms->abort);
+            o_ph ^= 1u;
+        }
+#pragma unroll
+        for (int part = 0; part < L::kParts; ++part) {
+            const uint64_t b = values_desc<D>(base, ring.at);
+            const uint32_t empty = uniform(bars.empty(ring.at));
+            ok = ok && wait(bars.clean(ring.at), ring.ph, &ms->abort, A.wait_limit);
+            if (part == 0) ok = ok && wait(bars.p_full(x), (p_ph >> x) & 1u, &ms->abort);
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+            if (ptx::elect_one()) {
+                sums_mma<D>(o_col, s_col + part * (L::kVRows / 2), b, part != 0 ? 1u : add);
+                ptx::mma_commit(empty);
+                if (part == L::kParts - 1) ptx::mma_commit(pv_done);
+                if (part == L::kParts - 1 && ends) ptx::mma_commit(o_full);
+            }
+            __syncwarp();
+            ring.step();
+        }
+        p_ph ^= 1u << x;
     }
+    if (!ok) drain(bars, 1);
 }
 
 // ------------------------------------------------------------------ cleaners
@@ -456,6 +550,7 @@ __device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, i
         if (lane == 0) note->piece = piece;
         __syncwarp();
     }
+#pragma unroll 1
     for (int y = 0; y < 8; ++y) {
         if (key + y < all || !((any >> (4 * y)) & 15u)) continue;
         for (int c = lane; c < (int)L::kVBlocks * 8; c += 32)
@@ -469,26 +564,27 @@ __device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, i
 // Warp `who` of two looks at half of the tokens of every stage of values: where the tile holds keys that some row does not
 // see, rows that are not finite become zeros, and those of the piece's own keys are noted.
 template <int D>
-__device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm, const PromptPlan &plan, int who) {
+__device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm, const PromptWalk &begin, int who) {
     using L = Lay<D>;
     constexpr int kRowsHere = L::kVRows / kCleaners;
     const int lane = threadIdx.x & 31;
-    const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
+    const Bars bars{ptx::smem_addr(ms)};
     Ring<D, false> ring;
     bool ok = true;
     int piece = 0;
-    PromptWalk walk(A, plan);
+    PromptWalk walk = begin;
     PromptPiece pc;
     for (; ok && walk.next(A, &pc); ++piece) {
         const Span<D> sp(A, pc);
         for (int u = 0; ok && u < sp.units; ++u) {
             const int k0 = (pc.t0 + u) * kTile;
             for (int part = 0; ok && part < L::kParts; ++part) {
-                ok = wait(bar(ms->full[ring.at]), ring.ph, &ms->abort, A.wait_limit);
+                ok = wait(bars.full(ring.at), ring.ph, &ms->abort, A.wait_limit);
                 if (ok && k0 + kTile > sp.all) {
                     uint8_t *tile = sm + L::kOffKV + ring.at * L::kStage;
                     const int row0 = who * kRowsHere;                       // of the stage
                     const int key0 = k0 + part * L::kVRows + row0;          // its key
+#pragma unroll 1
                     for (int r = 0; ok && r < kRowsHere; r += 8) {
                         if (key0 + r + 8 <= sp.all) continue;
                         // four lanes a row, each 16 of its bytes at a time; odd rows begin with their second half, so that
@@ -513,7 +609,7 @@ __device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm
                     ptx::fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(ms->clean[ring.at]));
+                if (lane == 0) ptx::mbar_arrive(bars.clean(ring.at));
                 ring.step();
             }
         }
@@ -539,25 +635,51 @@ __device__ __noinline__ void add_removed(const PromptArgs &A, const Misc *ms, in
         const int64_t e = kv_elem(A.C, A.layer, it.h, row);
         const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(A.C.k) + e, *v = static_cast<const __nv_bfloat16 *>(A.C.v) + e;
         float s = 0.0f;
+#pragma unroll 1
         for (int d = 0; d < A.C.D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
         const float p = __bfloat162float(__float2bfloat16_rn(ex2(s * A.scale_log2 - m)));
+#pragma unroll 1
         for (int d = 0; d < dims; ++d) o[d] = fmaf(p, __bfloat162float(v[d0 + d]), o[d]);
     }
 }
 
+// Scores of a tile that the row does not see, all but the first `lim`, are set to -inf where they lie.
+__device__ __noinline__ void cut_scores(uint32_t s_addr, int lim) {
+#pragma unroll 1
+    for (int y = 0; y < kTile; y += 16) {
+        uint32_t sc[16];
+        ptx::tmem_ld16_bits(s_addr + y, sc);
+        landed(sc);
+#pragma unroll
+        for (int z = 0; z < 16; ++z)
+            if (y + z >= lim) sc[z] = 0xff800000u;
+        ptx::tmem_st16_bits(s_addr + y, sc);
+    }
+    ptx::tmem_st_wait();
+}
+
+// Maxima of a quarter of a tile's scores, in eight chains of three-input ones (one chain's latency would be the whole row's).
+__device__ __forceinline__ void row_maxima(const uint32_t (&sc)[32], float (&tops)[8]) {
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+        const auto f = [&](int z) { return __uint_as_float(sc[y + 8 * z]); };
+        tops[y] = max3(max3(tops[y], f(0), f(1)), f(2), f(3));
+    }
+}
+
 template <int D>
-__device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t tmem, const PromptPlan &plan, int tid_all) {
+__device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t tmem, const PromptWalk &begin, int tid_all) {
     using L = Lay<D>;
     const int s = L::NS == 2 ? tid_all >> 7 : 0, tid = tid_all & 127, warp = tid >> 5;
     const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
     const int tq = A.tokens / L::NS, RT = tq * A.GS;
     const int my_row = s * RT + tid;                           // row of the block's MT
     const float c = A.scale_log2;
-    const auto bar = [](uint64_t &b) { return ptx::smem_addr(&b); };
+    const Bars bars{ptx::smem_addr(ms)};
     uint32_t seq = 0, outs = 0;                                // tiles taken, pieces put out
     int piece = 0;
     bool ok = true;
-    PromptWalk walk(A, plan);
+    PromptWalk walk = begin;
     PromptPiece pc;
     for (; ok && walk.next(A, &pc); ++piece) {
         const PromptItem &it = pc.it;
@@ -576,29 +698,31 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
         for (int j = 0; ok && j < n; ++j, ++seq) {
             const int x = L::NS == 2 ? s : seq & 1, k0 = (pc.t0 + j) * kTile;
             const uint32_t s_addr = lane_addr + L::col_s(x);
-            ok = wait(bar(ms->s_full[x]), (L::NS == 2 ? seq : seq >> 1) & 1u, &ms->abort);
+            ok = wait(bars.s_full(x), (L::NS == 2 ? seq : seq >> 1) & 1u, &ms->abort);
             if (!ok) break;
             ptx::tc_fence_after_sync();
+            const auto hand_on = [&] {
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if ((tid & 31) == 0) ptx::mbar_arrive(bars.p_full(x));
+            };
             if (warp_on) {
-                uint32_t sc[kTile];
-#pragma unroll
-                for (int y = 0; y < kTile; y += 32) ptx::tmem_ld32_bits(s_addr + y, sc + y);
-                landed(sc);
-                if (k0 + kTile > see_all) {
-                    const int lim = see - k0;
-#pragma unroll
-                    for (int y = 0; y < kTile; ++y)
-                        if (y >= lim) sc[y] = 0xff800000u;
-                }
-                // eight chains of three-input maxima: one chain's latency would be the whole row's
+                // Two passes over the scores, 32 at a time, each half's next load under way while the other is worked on:
+                // the maximum, then the probabilities.
+                uint32_t sa[32], sb[32];
                 float tops[8];
+                if (k0 + kTile > see_all) cut_scores(s_addr, see - k0);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    const auto f = [&](int z) { return __uint_as_float(sc[y + 8 * z]); };
-                    float t = max3(f(0), f(1), f(2));
+                for (int y = 0; y < 8; ++y) tops[y] = -INFINITY;
+                ptx::tmem_ld32_bits(s_addr, sa);
 #pragma unroll
-                    for (int z = 3; z + 1 < 16; z += 2) t = max3(t, f(z), f(z + 1));
-                    tops[y] = fmaxf(t, f(15));
+                for (int y = 0; y < kTile; y += 64) {
+                    landed(sa);
+                    ptx::tmem_ld32_bits(s_addr + y + 32, sb);
+                    row_maxima(sa, tops);
+                    landed(sb);
+                    ptx::tmem_ld32_bits(s_addr + ((y + 64) & (kTile - 1)), sa);   // in the end the first again
+                    row_maxima(sb, tops);
                 }
                 const float top = c * max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]),
                                            fmaxf(tops[6], tops[7]));
@@ -610,8 +734,9 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                     m = to;
                     if (j > 0) {   // O holds the sums up to the tile before this one
                         // (with two streams they were issued before these scores, so they are done)
-                        if (L::NS == 1) ok = wait(bar(ms->pv_done), (seq - 1) & 1u, &ms->abort);
+                        if (L::NS == 1) ok = wait(bars.pv_done(x ^ 1), ((seq - 1) >> 1) & 1u, &ms->abort);
                         if (!ok) break;
+                        landed(sa);   // (on its way since above; a wait in the loop would otherwise be behind its use)
                         ptx::tc_fence_after_sync();
 #pragma unroll 1
                         for (int y = 0; y < D; y += 32) {
@@ -628,32 +753,40 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                 const float off = m == -INFINITY ? 0.0f : -m;
                 const uint64_t c2 = pair(c, c), off2 = pair(off, off);
                 uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
-#pragma unroll
-                for (int y = 0; y < kTile; y += 32) {
+                const auto probabilities = [&](const uint32_t (&sc)[32], uint32_t to) {
                     uint32_t p[16];
 #pragma unroll
                     for (int z = 0; z < 16; ++z) {
                         float a, b;
-                        unpair(tat::fma2(pair(__uint_as_float(sc[y + 2 * z]), __uint_as_float(sc[y + 2 * z + 1])), c2, off2), a, b);
+                        unpair(tat::fma2(pair(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, off2), a, b);
                         a = ex2(a);
                         b = ex2(b);
                         sum[z & 3] = tat::add2(sum[z & 3], pair(a, b));
                         p[z] = pack_bf16(a, b);
                     }
-                    ptx::tmem_st16_bits(s_addr + y / 2, p);
+                    ptx::tmem_st16_bits(to, p);   // over scores that have been read
+                };
+#pragma unroll
+                for (int y = 0; y < kTile; y += 64) {
+                    landed(sa);
+                    ptx::tmem_ld32_bits(s_addr + y + 32, sb);
+                    probabilities(sa, s_addr + y / 2);
+                    landed(sb);
+                    if (y == 0) ptx::tmem_ld32_bits(s_addr + 64, sa);
+                    probabilities(sb, s_addr + y / 2 + 16);
                 }
+                ptx::tmem_st_wait();
+                hand_on();
                 float s0, s1;
                 unpair(tat::add2(tat::add2(sum[0], sum[1]), tat::add2(sum[2], sum[3])), s0, s1);
                 l += s0 + s1;
-                ptx::tmem_st_wait();
+            } else {
+                hand_on();
             }
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->p_full[x]));
         }
         if (!ok) break;
         if (n > 0) {
-            ok = wait(bar(ms->o_full[s]), outs & 1u, &ms->abort);
+            ok = wait(bars.o_full(s), outs & 1u, &ms->abort);
             if (!ok) break;
             ++outs;
             ptx::tc_fence_after_sync();
@@ -698,7 +831,7 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
             }
             ptx::tc_fence_before_sync();
             __syncwarp();
-            if ((tid & 31) == 0) ptx::mbar_arrive(bar(ms->o_empty[s]));
+            if ((tid & 31) == 0) ptx::mbar_arrive(bars.o_empty(s));
         }
         if (on) {
             if (!whole) A.part_ml[part * A.MT + my_row] = make_float2(m, l);
@@ -707,14 +840,6 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
         __syncwarp();
         if ((tid & 31) == 0) *(volatile int *)&ms->done[tid_all >> 5] = piece + 1;
     }
-}
-
-// The registers of the launch are shared out anew: the softmax holds a row of scores.
-template <int REGS> __device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS> __device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
 template <int D>
@@ -744,7 +869,7 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         const auto init = [](uint64_t &b, uint32_t n) { ptx::mbar_init(ptx::smem_addr(&b), n); };
         for (int i = 0; i < L::NST; ++i) {
             init(ms->full[i], 1);
-            init(ms->empty[i], 1);
+            init(ms->empty[i], L::NS);   // warps that use the stage
             init(ms->clean[i], kCleaners);
         }
         for (int i = 0; i < 2; ++i) {
@@ -754,9 +879,10 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             init(ms->p_full[i], 4);
             init(ms->o_full[i], 1);
             init(ms->o_empty[i], 4);
+            init(ms->pv_done[i], 1);
+            init(ms->turn[i], 1);
+            init(ms->drain[i], 1);
         }
-        init(ms->pv_done, 1);
-        init(ms->drain, 1);
         for (int w = 0; w < kCleaners; ++w)
             for (int i = 0; i < kNotes; ++i) ms->notes[w][i].piece = -1;
         for (int i = 0; i < 8; ++i) ms->done[i] = 0;
@@ -769,28 +895,30 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (warp == 0) ptx::tmem_alloc(ptx::smem_addr(&ms->tmem), kTmemCols);
     grid_dep_wait();   // nothing in global memory was touched so far
     const PromptPlan plan = prompt_plan<L::kThreads>(A, &ms->scratch);
+    const PromptWalk begin(A, plan);
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = ms->tmem;
 
-    // Registers of a thread with 384 of them: 168 at launch; 2 x 128 x 200 + 128 x 104 = 384 x 168.
     if (warp < L::NS * 4) {
-        if (L::NS == 2) more_registers<200>();
         // while the first tile is on its way
         prompt_dead_tokens<__nv_bfloat16>(A, tid, L::NS * 128);
-        soften<D>(A, ms, tmem, plan, tid);
+        soften<D>(A, ms, tmem, begin, tid);
     } else {
-        if (L::NS == 2) fewer_registers<104>();
         const int role = warp - L::NS * 4;
         if (role == 0) {
-            if (ptx::elect_one()) prompt_note(A, PromptWalk(A, plan), plan.chunk);
+            if (ptx::elect_one()) prompt_note(A, begin, plan.chunk);
             __syncwarp();
-            produce<D>(A, &mq, &mk, &mv, ms, base, plan);
+            produce<D>(A, &mq, &mk, &mv, ms, base, begin);
+        } else if (role == 3) {
+            clean<D>(A, ms, sm, begin, 0);
+        } else if (L::NS == 2) {
+            multiply_stream<D>(A, ms, base, tmem, begin, role - 1);
         } else if (role == 1) {
-            multiply<D>(A, ms, base, tmem, plan);
+            multiply_scores<D>(A, ms, base, tmem, begin);
         } else {
-            clean<D>(A, ms, sm, plan, role - 2);
+            multiply_sums<D>(A, ms, base, tmem, begin);
         }
         __syncwarp();
     }
@@ -846,7 +974,7 @@ void prompt_attn_tc_cut(PromptArgs *A, int sms) {
     A->GS = (A->G + A->HS - 1) / A->HS;
     A->tokens = streams * (pat::kRows / A->GS);
     A->MT = A->tokens * A->GS;
-    A->TN = pat::kTile;
+    A->log_tn = pat::kLogTile;
     A->k_whole = A->C.P >= pat::kTile && A->C.D % 64 == 0 && A->C.D != 192;
     A->v_whole = A->C.P >= pat::kTile / (A->C.D > 128 ? 2 : 1) && A->C.D % 64 == 0 && A->C.D != 192;
     A->groups = sms;

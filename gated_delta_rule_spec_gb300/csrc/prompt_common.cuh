@@ -35,7 +35,7 @@ struct PromptArgs {
     float4 *part_o;            // [groups][2][D / 4][MT] unnormalised sums of a piece
     float2 *part_ml;           // [groups][2][MT] (maximum in log2 units, sum)
     struct PromptCut *cuts;    // [groups] where each chunk starts, for the join
-    int TN, MT, tokens;        // keys of a tile; rows and tokens of a block
+    int log_tn, MT, tokens;    // keys of a tile (2^log_tn); rows and tokens of a block
     int groups, gap;
     bool k_whole, v_whole;     // tensor-core kernel: one copy holds all dims of a stage
     uint32_t wait_limit;
@@ -99,7 +99,7 @@ struct PromptItem {
     // The tile on which a cut at this place of the line falls.
     __device__ __forceinline__ int tile_at(const PromptArgs &A, int64_t place) const {
         const int64_t off = place - pos - A.gap;
-        return off <= 0 ? 0 : off >= keys ? tiles : (int)(off / A.TN);
+        return off <= 0 ? 0 : off >= keys ? tiles : (int)(off >> A.log_tn);
     }
 };
 
@@ -152,6 +152,7 @@ __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScr
     const int tid = threadIdx.x;
     p.total = 0;
     int64_t mine = 0, before = 0;   // of the first THREADS rows
+#pragma unroll 1
     for (int b0 = 0; b0 < A.B; b0 += THREADS) {
         int64_t x = 0, ex;
         if (b0 + tid < A.B) {
@@ -165,12 +166,13 @@ __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScr
         p.total += sum;
     }
     // a chunk is a tile at least, so that cuts inside an item fall on different tiles
-    p.chunk = max((int64_t)A.TN, (p.total + A.groups - 1) / A.groups);
+    p.chunk = max((int64_t)1 << A.log_tn, (p.total + A.groups - 1) / A.groups);
     const int64_t at = (int64_t)blockIdx.x * p.chunk;
     if (tid == 0) sc->b = -1;
     __syncthreads();
     if (at < p.total) {
         int64_t base = 0;
+#pragma unroll 1
         for (int b0 = 0; b0 < A.B; b0 += THREADS) {
             int64_t x = mine, ex = before;
             if (b0 > 0) {
@@ -227,7 +229,7 @@ struct PromptWalk {
         it.part = A.HS == 1 ? 0 : hp - it.h * A.HS;
         it.q0 = i * A.tokens;
         it.keys = it.len + min(it.cnt, it.q0 + A.tokens);
-        it.tiles = (it.keys + A.TN - 1) / A.TN;
+        it.tiles = (it.keys + (1 << A.log_tn) - 1) >> A.log_tn;
     }
     __device__ __forceinline__ PromptWalk(const PromptArgs &A, const PromptPlan &p) {
         live = p.b >= 0;
@@ -246,35 +248,40 @@ struct PromptWalk {
         it.pos = start - (in - line.before(i));
         set(A);
     }
-    __device__ __forceinline__ bool next(const PromptArgs &A, PromptPiece *pc) {
-        while (live) {
-            pc->it = it;
-            pc->t0 = it.tile_at(A, start);
-            pc->t1 = it.tile_at(A, end);
-            it.pos += it.keys + A.gap;
-            if (it.pos >= end) {
-                live = false;
-            } else {
-                if (++i == blocks) {
-                    i = 0;
-                    if (++hp == A.C.HKV * A.HS) {
-                        hp = 0;
-                        do {
-                            if (++it.b >= A.B) {   // not reached while the line is as planned
-                                live = false;
-                                break;
-                            }
-                            load(A);
-                        } while (it.cnt == 0);
-                    }
-                }
-                if (live) set(A);
-            }
-            if (pc->t0 < pc->t1) return true;
-        }
-        return false;
-    }
+    __device__ __forceinline__ bool next(const PromptArgs &A, PromptPiece *pc);
 };
+
+// Not inlined: a kernel has many walkers, and its loops have to stay near in the instruction cache.
+static __device__ __noinline__ bool prompt_next(const PromptArgs &A, PromptWalk &w, PromptPiece *pc) {
+    while (w.live) {
+        PromptItem &it = w.it;
+        pc->it = it;
+        pc->t0 = it.tile_at(A, w.start);
+        pc->t1 = it.tile_at(A, w.end);
+        it.pos += it.keys + A.gap;
+        if (it.pos >= w.end) {
+            w.live = false;
+        } else {
+            if (++w.i == w.blocks) {
+                w.i = 0;
+                if (++w.hp == A.C.HKV * A.HS) {
+                    w.hp = 0;
+                    do {
+                        if (++it.b >= A.B) {   // not reached while the line is as planned
+                            w.live = false;
+                            break;
+                        }
+                        w.load(A);
+                    } while (it.cnt == 0);
+                }
+            }
+            if (w.live) w.set(A);
+        }
+        if (pc->t0 < pc->t1) return true;
+    }
+    return false;
+}
+__device__ __forceinline__ bool PromptWalk::next(const PromptArgs &A, PromptPiece *pc) { return prompt_next(A, *this, pc); }
 
 // The chunk's note; by one thread, before the walk begins.
 __device__ __forceinline__ void prompt_note(const PromptArgs &A, const PromptWalk &w, int64_t chunk) {
@@ -312,7 +319,7 @@ __device__ __forceinline__ int prompt_owner(const int32_t *starts, int B, int to
 // Tokens of rows that nothing computes (padding rows, rows that were refused): zeros, and an lse of -inf.  By `threads`
 // threads (whole warps) of each block; every block takes an equal share of the packed tokens.
 template <typename IO>
-__device__ __forceinline__ void prompt_dead_tokens(const PromptArgs &A, int thread, int threads) {
+__device__ __noinline__ void prompt_dead_tokens(const PromptArgs &A, int thread, int threads) {
     const int n0 = (int)((int64_t)A.N * blockIdx.x / gridDim.x), n1 = (int)((int64_t)A.N * (blockIdx.x + 1) / gridDim.x);
     if (n0 >= n1) return;
     for (int b = prompt_owner(A.starts, A.B, n0); b < A.B && A.starts[b] < n1; ++b) {
