@@ -59,6 +59,7 @@ constexpr int kSmemMax = 232448;
 constexpr int kMaxStages = 10;
 constexpr int kCleaners = 1;             // warps that look through values
 constexpr int kNotes = 4;                // pieces whose rows that are not finite are kept
+constexpr int kPieces = 4;               // pieces that are described at a time
 
 template <int D>
 struct Lay {
@@ -80,6 +81,15 @@ struct Lay {
     __host__ __device__ static constexpr uint32_t col_o(int s) { return 256 + s * 128; }
 };
 
+// A piece as its readers need it.  The producer walks and describes the pieces in shared memory, a few ahead: walkers of
+// all warps' own would cost each of them some thousand cycles a piece.
+struct __align__(16) PieceInfo {
+    int slot, len, cnt, first;            // the row: its slot, committed tokens, tokens, and the first of them
+    int h, part, q0, keys;                // as in PromptItem
+    int tiles, t0, n[2];                  // tiles of the item, the piece's first, tiles that each stream takes
+    int units, all, whole, pad;           // tiles of the piece (0: there is none), keys that all its rows see, whether it is the item
+};
+
 // Value rows of a piece that one of the cleaners found not finite, from its first key that not all rows see on.
 struct Note {
     int piece;                            // the piece's number; another one's: there are none
@@ -89,7 +99,9 @@ struct Note {
 // Shared memory behind the tiles.
 struct Misc {
     uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], pv_done[2], turn[2], drain[2];
+    PieceInfo pieces[kPieces];
     Note notes[kCleaners][kNotes];
     int done[8];                          // pieces that a warp of the softmax is done with
     PromptScratch scratch;
@@ -104,6 +116,8 @@ struct Bars {
     __device__ __forceinline__ uint32_t full(uint32_t i) const { return at(offsetof(Misc, full), i); }
     __device__ __forceinline__ uint32_t empty(uint32_t i) const { return at(offsetof(Misc, empty), i); }
     __device__ __forceinline__ uint32_t clean(uint32_t i) const { return at(offsetof(Misc, clean), i); }
+    __device__ __forceinline__ uint32_t piece_full(uint32_t i) const { return at(offsetof(Misc, piece_full), i); }
+    __device__ __forceinline__ uint32_t piece_empty(uint32_t i) const { return at(offsetof(Misc, piece_empty), i); }
     __device__ __forceinline__ uint32_t q_full(uint32_t i) const { return at(offsetof(Misc, q_full), i); }
     __device__ __forceinline__ uint32_t q_empty(uint32_t i) const { return at(offsetof(Misc, q_empty), i); }
     __device__ __forceinline__ uint32_t s_full(uint32_t i) const { return at(offsetof(Misc, s_full), i); }
@@ -115,24 +129,21 @@ struct Bars {
     __device__ __forceinline__ uint32_t drain(uint32_t i) const { return at(offsetof(Misc, drain), i); }
 };
 
-// What a piece asks of the streams.
-template <int D>
-struct Span {
-    int n[2];                             // tiles of each stream
-    int units;                            // tiles of the piece that any stream takes
-    int all;                              // keys that every row of the block sees
-    __device__ __forceinline__ Span(const PromptArgs &A, const PromptPiece &pc) {
-        using L = Lay<D>;
-        const int tq = A.tokens / L::NS;
-        units = 0;
-#pragma unroll
-        for (int s = 0; s < L::NS; ++s) {
-            const int first = pc.it.q0 + s * tq;   // the stream's first token
-            const int keys = first < pc.it.cnt ? pc.keys_to(first + tq) : 0;
-            n[s] = max(0, min(pc.t1, (keys + kTile - 1) / kTile) - pc.t0);
-            units = max(units, n[s]);
+// The next piece's description from the ring, for a warp that goes through the pieces; false: there is none, or the
+// wait ran out (*ok).
+struct PieceReader {
+    uint32_t at = 0, ph = 0;
+    __device__ __forceinline__ bool next(Misc *ms, const Bars &bars, PieceInfo *info, bool *ok) {
+        *ok = wait(bars.piece_full(at), ph, &ms->abort);
+        if (!*ok) return false;
+        *info = ms->pieces[at];
+        __syncwarp();
+        if (ptx::elect_one()) ptx::mbar_arrive(bars.piece_empty(at));
+        if (++at == kPieces) {
+            at = 0;
+            ph ^= 1u;
         }
-        all = pc.it.len + pc.it.q0 + 1;
+        return info->units > 0;
     }
 };
 
@@ -168,6 +179,37 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
     bool ok = true;
     PromptWalk walk = begin;
     PromptPiece pc;
+    uint32_t at = 0, ph = 1;                                   // place in the ring of pieces
+    // the piece pc's description; at the end (!any) that there is none
+    const auto describe = [&](bool any, PieceInfo *info) {
+        info->units = 0;
+        if (any) {
+            const PromptItem &it = pc.it;
+            info->slot = it.slot, info->len = it.len, info->cnt = it.cnt, info->first = it.first;
+            info->h = it.h, info->part = it.part, info->q0 = it.q0, info->keys = it.keys;
+            info->tiles = it.tiles, info->t0 = pc.t0, info->n[1] = 0;
+#pragma unroll
+            for (int s = 0; s < L::NS; ++s) {
+                const int first = it.q0 + s * tq;              // the stream's first token
+                const int keys = first < it.cnt ? it.len + min(it.cnt, first + tq) : 0;
+                info->n[s] = max(0, min(pc.t1, (keys + kTile - 1) >> kLogTile) - pc.t0);
+                info->units = max(info->units, info->n[s]);
+            }
+            info->all = it.len + it.q0 + 1;
+            info->whole = pc.whole();
+        }
+        if (!wait(ptx::smem_addr(&ms->piece_empty[at]), ph, &ms->abort)) return false;
+        if (ptx::elect_one()) {
+            ms->pieces[at] = *info;
+            ptx::mbar_arrive(ptx::smem_addr(&ms->piece_full[at]));
+        }
+        __syncwarp();
+        if (++at == kPieces) {
+            at = 0;
+            ph ^= 1u;
+        }
+        return true;
+    };
     // one stage of keys or values of the tile at `tok`, whose boxes' pool rows are `row`
     const auto stage = [&](auto &ring, auto keys_c, int part, int row, int boxes) {
         constexpr bool keys = decltype(keys_c)::value;
@@ -214,9 +256,12 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
         ring.step();
         return true;
     };
-    while (ok && walk.next(A, &pc)) {
+    while (ok) {
+        const bool any = walk.next(A, &pc);
+        PieceInfo sp;
+        ok = describe(any, &sp);
+        if (!ok || !any) break;
         const PromptItem &it = pc.it;
-        const Span<D> sp(A, pc);
         const int kv = min(it.keys, (pc.t0 + sp.units) * kTile);
         const int32_t *table = A.C.page_table + (int64_t)it.slot * A.C.max_pages;
         // the page of box `lane` of tile u: looked up a tile before it is used
@@ -290,27 +335,17 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
 
 // ------------------------------------------------------------------ MMA warp
 
-// A place in the sequence of tiles, piece after piece.
-template <int D>
+// A place in the sequence of tiles, piece after piece: tile u of a piece's `units`, of which stream s takes n.
 struct Cursor {
-    PromptWalk walk;
-    PromptPiece pc;
-    int u, units, n[2];
-    bool live;
-    __device__ __forceinline__ void open(const PromptArgs &A) {
-        do {
-            live = walk.next(A, &pc);
-            if (!live) return;
-            const Span<D> sp(A, pc);
-            units = sp.units;
-            n[0] = sp.n[0];
-            n[1] = Lay<D>::NS == 2 ? sp.n[1] : 0;
-        } while (units == 0);
+    int u = 0, units = 0, n = 0;
+    bool live = false;
+    // Opens the next piece.
+    __device__ __forceinline__ void open(Misc *ms, const Bars &bars, PieceReader &reader, int s, bool *ok) {
+        PieceInfo info;
+        live = reader.next(ms, bars, &info, ok);
         u = 0;
-    }
-    __device__ __forceinline__ Cursor(const PromptArgs &A, const PromptWalk &begin) : walk(begin) { open(A); }
-    __device__ __forceinline__ void step(const PromptArgs &A) {
-        if (++u == units) open(A);
+        units = info.units;
+        n = s ? info.n[1] : info.n[0];
     }
 };
 
@@ -358,7 +393,7 @@ __device__ __forceinline__ void drain(const Bars &bars, int who) {
 // stream takes no part in is released when it has landed.
 template <int D>
 __device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem,
-                                                const PromptWalk &begin, int s) {
+                                                int s) {
     using L = Lay<D>;
     const Bars bars{ptx::smem_addr(ms)};
     Ring<D, true> k_ring;
@@ -369,10 +404,11 @@ __device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, u
     const uint32_t s_full = uniform(bars.s_full(s)), q_empty = uniform(bars.q_empty(s)), o_full = uniform(bars.o_full(s)),
                    other = uniform(bars.turn(s ^ 1));
     bool ok = true;
-    Cursor<D> q(A, begin), p = q;   // scores run a tile ahead of sums
+    PieceReader reader;
+    Cursor q, p;                   // scores run a tile ahead of sums
     const auto wait_keys = [&] {
         ok = ok && wait(bars.full(k_ring.at), k_ring.ph, &ms->abort, A.wait_limit);
-        if (q.u == 0 && q.n[s] > 0) {
+        if (q.u == 0 && q.n > 0) {
             ok = ok && wait(bars.q_full(s), q_ph, &ms->abort, A.wait_limit);
             q_ph ^= 1u;
         }
@@ -381,7 +417,7 @@ __device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, u
     const auto first_scores = [&] {
         const uint64_t b = keys_desc<D>(base, k_ring.at);
         const uint32_t empty = uniform(bars.empty(k_ring.at));
-        const bool mine = q.n[s] > 0, last = q.n[s] == 1;
+        const bool mine = q.n > 0, last = q.n == 1;
         wait_keys();
         if (!ok) return;
         ptx::tc_fence_after_sync();
@@ -398,12 +434,13 @@ __device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, u
         __syncwarp();
         k_ring.step();
     };
+    q.open(ms, bars, reader, s, &ok);
     if (q.live) first_scores();
+    p = q;
     while (ok && p.live) {
-        const bool sums = p.u < p.n[s], ends = p.u == p.n[s] - 1;
+        const bool sums = p.u < p.n, ends = p.u == p.n - 1;
         const uint32_t add = uniform(p.u != 0);
-        q.step(A);
-        const bool same = q.live && q.u != 0, scores = same && q.u < q.n[s], q_ends = q.u == q.n[s] - 1;
+        const bool same = ++q.u < q.units, scores = same && q.u < q.n, q_ends = q.u == q.n - 1;
         const uint64_t bk = keys_desc<D>(base, k_ring.at), bv = values_desc<D>(base, v_ring.at);
         const uint32_t k_empty = uniform(bars.empty(k_ring.at)), v_empty = uniform(bars.empty(v_ring.at));
         ok = wait(bars.clean(v_ring.at), v_ring.ph, &ms->abort, A.wait_limit);
@@ -440,26 +477,37 @@ __device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, u
         }
         __syncwarp();
         v_ring.step();
-        if (same) k_ring.step();
-        else if (q.live) first_scores();
-        p.step(A);
+        if (same) {
+            k_ring.step();
+            ++p.u;
+        } else {   // both go on to the next piece
+            q.open(ms, bars, reader, s, &ok);
+            if (q.live) first_scores();
+            p = q;
+        }
     }
     if (!ok) drain(bars, s);
 }
 
 // One stream: its scores by one warp, a tile ahead, its sums by another.
 template <int D>
-__device__ __forceinline__ void multiply_scores(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const PromptWalk &begin) {
+__device__ __forceinline__ void multiply_scores(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem) {
     using L = Lay<D>;
     const Bars bars{ptx::smem_addr(ms)};
     Ring<D, true> ring;
     uint32_t seq = 0, q_ph = 0;
     const uint32_t q_empty = uniform(bars.q_empty(0));
     bool ok = true;
-    for (Cursor<D> q(A, begin); ok && q.live; q.step(A), ++seq) {
+    PieceReader reader;
+    Cursor q;
+    for (;; ++seq) {
+        if (++q.u >= q.units) {
+            q.open(ms, bars, reader, 0, &ok);
+            if (!q.live) break;
+        }
         const int x = seq & 1;
         const uint32_t d = uniform(tmem + L::col_s(x)), s_full = uniform(bars.s_full(x));
-        const bool ends = q.u == q.n[0] - 1;
+        const bool ends = q.u == q.n - 1;
         if (q.u == 0) {
             ok = wait(bars.q_full(0), q_ph, &ms->abort, A.wait_limit);
             q_ph ^= 1u;
@@ -483,22 +531,29 @@ __device__ __forceinline__ void multiply_scores(const PromptArgs &A, Misc *ms, u
             __syncwarp();
             ring.step();
         }
+        if (!ok) break;
     }
     if (!ok) drain(bars, 0);
 }
 
 template <int D>
-__device__ __forceinline__ void multiply_sums(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem, const PromptWalk &begin) {
+__device__ __forceinline__ void multiply_sums(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem) {
     using L = Lay<D>;
     const Bars bars{ptx::smem_addr(ms)};
     Ring<D, false> ring;
     uint32_t seq = 0, p_ph = 0, o_ph = 1;   // p_ph: bit of a buffer
     const uint32_t o_col = uniform(tmem + L::col_o(0)), o_full = uniform(bars.o_full(0));
     bool ok = true;
-    for (Cursor<D> p(A, begin); ok && p.live; p.step(A), ++seq) {
+    PieceReader reader;
+    Cursor p;
+    for (;; ++seq) {
+        if (++p.u >= p.units) {
+            p.open(ms, bars, reader, 0, &ok);
+            if (!p.live) break;
+        }
         const int x = seq & 1;
         const uint32_t s_col = uniform(tmem + L::col_s(x)), pv_done = uniform(bars.pv_done(x)), add = uniform(p.u != 0);
-        const bool ends = p.u == p.n[0] - 1;
+        const bool ends = p.u == p.n - 1;
         if (p.u == 0) {
             ok = wait(bars.o_empty(0), o_ph, &ms->abort);
             o_ph ^= 1u;
@@ -521,6 +576,7 @@ __device__ __forceinline__ void multiply_sums(const PromptArgs &A, Misc *ms, uin
             ring.step();
         }
         p_ph ^= 1u << x;
+        if (!ok) break;
     }
     if (!ok) drain(bars, 1);
 }
@@ -564,7 +620,7 @@ __device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, i
 // Warp `who` of two looks at half of the tokens of every stage of values: where the tile holds keys that some row does not
 // see, rows that are not finite become zeros, and those of the piece's own keys are noted.
 template <int D>
-__device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm, const PromptWalk &begin, int who) {
+__device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm, int who) {
     using L = Lay<D>;
     constexpr int kRowsHere = L::kVRows / kCleaners;
     const int lane = threadIdx.x & 31;
@@ -572,12 +628,11 @@ __device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm
     Ring<D, false> ring;
     bool ok = true;
     int piece = 0;
-    PromptWalk walk = begin;
-    PromptPiece pc;
-    for (; ok && walk.next(A, &pc); ++piece) {
-        const Span<D> sp(A, pc);
+    PieceReader reader;
+    PieceInfo sp;
+    for (; ok && reader.next(ms, bars, &sp, &ok); ++piece) {
         for (int u = 0; ok && u < sp.units; ++u) {
-            const int k0 = (pc.t0 + u) * kTile;
+            const int k0 = (sp.t0 + u) * kTile;
             for (int part = 0; ok && part < L::kParts; ++part) {
                 ok = wait(bars.full(ring.at), ring.ph, &ms->abort, A.wait_limit);
                 if (ok && k0 + kTile > sp.all) {
@@ -604,7 +659,7 @@ __device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm
                                     acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), zero, acc);
                             }
                         const unsigned any = __ballot_sync(0xffffffffu, __hisnan(acc.x) || __hisnan(acc.y));
-                        if (any) ok = remove<D>(ms, tile, row0 + r, key0 + r, sp.all, pc.it.keys, any, piece, who);
+                        if (any) ok = remove<D>(ms, tile, row0 + r, key0 + r, sp.all, sp.keys, any, piece, who);
                     }
                     ptx::fence_proxy_async_smem();
                 }
@@ -620,7 +675,7 @@ __device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm
 
 // The terms of value rows that are not finite, for a row that sees `own` keys from `all` on: weight and value from memory.
 // o: dims from d0 on of the row's unnormalised sums over m.
-__device__ __noinline__ void add_removed(const PromptArgs &A, const Misc *ms, int piece, const PromptItem &it, int all, int own,
+__device__ __noinline__ void add_removed(const PromptArgs &A, const Misc *ms, int piece, const PieceInfo &it, int all, int own,
                                          int64_t qrow, float m, int d0, int dims, float *o) {
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(A.q) + qrow * A.C.D;
     for (int i = 0; i < own; ++i) {
@@ -658,6 +713,13 @@ __device__ __noinline__ void cut_scores(uint32_t s_addr, int lim) {
     ptx::tmem_st_wait();
 }
 
+// 32 bytes, on a boundary of as many.
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // Maxima of a quarter of a tile's scores, in eight chains of three-input ones (one chain's latency would be the whole row's).
 __device__ __forceinline__ void row_maxima(const uint32_t (&sc)[32], float (&tops)[8]) {
 #pragma unroll
@@ -668,7 +730,7 @@ __device__ __forceinline__ void row_maxima(const uint32_t (&sc)[32], float (&top
 }
 
 template <int D>
-__device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t tmem, const PromptWalk &begin, int tid_all) {
+__device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t tmem, int tid_all) {
     using L = Lay<D>;
     const int s = L::NS == 2 ? tid_all >> 7 : 0, tid = tid_all & 127, warp = tid >> 5;
     const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
@@ -676,27 +738,29 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
     const int my_row = s * RT + tid;                           // row of the block's MT
     const float c = A.scale_log2;
     const Bars bars{ptx::smem_addr(ms)};
+    // whole sectors at a time, where rows begin on them
+    const bool wide = (reinterpret_cast<uintptr_t>(A.out) & 31) == 0 && A.C.D % 16 == 0;
     uint32_t seq = 0, outs = 0;                                // tiles taken, pieces put out
     int piece = 0;
     bool ok = true;
-    PromptWalk walk = begin;
-    PromptPiece pc;
-    for (; ok && walk.next(A, &pc); ++piece) {
-        const PromptItem &it = pc.it;
-        const Span<D> sp(A, pc);
-        const int n = sp.n[s];
-        bool on;
-        const int64_t row = prompt_out_row(A, it, my_row, &on);
-        on = on && tid < RT;
-        const bool whole = pc.whole();
-        const int64_t part = (int64_t)blockIdx.x * 2 + pc.side();
-        const int own = s * tq + tid / A.GS;                   // keys of the block's tokens that the row sees, less one
+    const int own = s * tq + tid / A.GS;                       // the row's token of the block
+    const int head = tid - (own - s * tq) * A.GS;              // and head of the group's part
+    PieceReader reader;
+    PieceInfo it;
+    for (; ok && reader.next(ms, bars, &it, &ok); ++piece) {
+        const PieceInfo &sp = it;
+        const int n = s ? it.n[1] : it.n[0];
+        const int g = it.part * A.GS + head;
+        const bool on = tid < RT && it.q0 + own < it.cnt && g < A.G;
+        const int64_t row = ((int64_t)it.first + it.q0 + own) * A.HQ + it.h * A.G + g;
+        const bool whole = it.whole != 0;
+        const int64_t part = (int64_t)blockIdx.x * 2 + (it.t0 == 0);
         const int see = on ? sp.all + own : 0;                 // keys that the row sees
         const int see_all = sp.all + s * tq;                   // that every row of the stream sees
         const bool warp_on = __any_sync(0xffffffffu, on);
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; ok && j < n; ++j, ++seq) {
-            const int x = L::NS == 2 ? s : seq & 1, k0 = (pc.t0 + j) * kTile;
+            const int x = L::NS == 2 ? s : seq & 1, k0 = (it.t0 + j) * kTile;
             const uint32_t s_addr = lane_addr + L::col_s(x);
             ok = wait(bars.s_full(x), (L::NS == 2 ? seq : seq >> 1) & 1u, &ms->abort);
             if (!ok) break;
@@ -814,13 +878,19 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                         for (int y = 0; y < 32; ++y) f[y] = g[y];
                     }
                     if (whole) {
-                        uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) + row * A.C.D + d0);
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(A.out) + row * A.C.D + d0;
+                        uint32_t w[16];
 #pragma unroll
-                        for (int y = 0; y < 32; y += 8)
-                            if (y < dims)
-                                out[y / 8] = make_uint4(pack_bf16(f[y] * inv, f[y + 1] * inv), pack_bf16(f[y + 2] * inv, f[y + 3] * inv),
-                                                        pack_bf16(f[y + 4] * inv, f[y + 5] * inv),
-                                                        pack_bf16(f[y + 6] * inv, f[y + 7] * inv));
+                        for (int y = 0; y < 16; ++y) w[y] = pack_bf16(f[2 * y] * inv, f[2 * y + 1] * inv);
+                        if (wide && dims == 32) {
+                            store32(out, w);
+                            store32(out + 16, w + 8);
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                if (8 * y < dims)
+                                    reinterpret_cast<uint4 *>(out)[y] = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+                        }
                     } else {
                         float4 *po = A.part_o + (part * (A.C.D / 4) + d0 / 4) * A.MT + my_row;
 #pragma unroll
@@ -872,6 +942,10 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             init(ms->empty[i], L::NS);   // warps that use the stage
             init(ms->clean[i], kCleaners);
         }
+        for (int i = 0; i < kPieces; ++i) {
+            init(ms->piece_full[i], 1);
+            init(ms->piece_empty[i], L::NS * 4 + 2 + kCleaners);   // warps that read it
+        }
         for (int i = 0; i < 2; ++i) {
             init(ms->q_full[i], 1);
             init(ms->q_empty[i], 1);
@@ -895,7 +969,6 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (warp == 0) ptx::tmem_alloc(ptx::smem_addr(&ms->tmem), kTmemCols);
     grid_dep_wait();   // nothing in global memory was touched so far
     const PromptPlan plan = prompt_plan<L::kThreads>(A, &ms->scratch);
-    const PromptWalk begin(A, plan);
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
@@ -904,21 +977,22 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (warp < L::NS * 4) {
         // while the first tile is on its way
         prompt_dead_tokens<__nv_bfloat16>(A, tid, L::NS * 128);
-        soften<D>(A, ms, tmem, begin, tid);
+        soften<D>(A, ms, tmem, tid);
     } else {
         const int role = warp - L::NS * 4;
         if (role == 0) {
+            const PromptWalk begin(A, plan);
             if (ptx::elect_one()) prompt_note(A, begin, plan.chunk);
             __syncwarp();
             produce<D>(A, &mq, &mk, &mv, ms, base, begin);
         } else if (role == 3) {
-            clean<D>(A, ms, sm, begin, 0);
+            clean<D>(A, ms, sm, 0);
         } else if (L::NS == 2) {
-            multiply_stream<D>(A, ms, base, tmem, begin, role - 1);
+            multiply_stream<D>(A, ms, base, tmem, role - 1);
         } else if (role == 1) {
-            multiply_scores<D>(A, ms, base, tmem, begin);
+            multiply_scores<D>(A, ms, base, tmem);
         } else {
-            multiply_sums<D>(A, ms, base, tmem, begin);
+            multiply_sums<D>(A, ms, base, tmem);
         }
         __syncwarp();
     }

@@ -201,7 +201,7 @@ __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScr
     return p;
 }
 
-// The pieces of a block's chunk, one after another.  Every thread that walks does so alone.
+// The pieces of a block's chunk, one after another, for whoever walks.
 struct PromptPiece {
     PromptItem it;
     int t0, t1;                // key tiles [t0, t1) of the item's
@@ -248,40 +248,35 @@ struct PromptWalk {
         it.pos = start - (in - line.before(i));
         set(A);
     }
-    __device__ __forceinline__ bool next(const PromptArgs &A, PromptPiece *pc);
-};
-
-// Not inlined: a kernel has many walkers, and its loops have to stay near in the instruction cache.
-static __device__ __noinline__ bool prompt_next(const PromptArgs &A, PromptWalk &w, PromptPiece *pc) {
-    while (w.live) {
-        PromptItem &it = w.it;
-        pc->it = it;
-        pc->t0 = it.tile_at(A, w.start);
-        pc->t1 = it.tile_at(A, w.end);
-        it.pos += it.keys + A.gap;
-        if (it.pos >= w.end) {
-            w.live = false;
-        } else {
-            if (++w.i == w.blocks) {
-                w.i = 0;
-                if (++w.hp == A.C.HKV * A.HS) {
-                    w.hp = 0;
-                    do {
-                        if (++it.b >= A.B) {   // not reached while the line is as planned
-                            w.live = false;
-                            break;
-                        }
-                        w.load(A);
-                    } while (it.cnt == 0);
+    __device__ __forceinline__ bool next(const PromptArgs &A, PromptPiece *pc) {
+        while (live) {
+            pc->it = it;
+            pc->t0 = it.tile_at(A, start);
+            pc->t1 = it.tile_at(A, end);
+            it.pos += it.keys + A.gap;
+            if (it.pos >= end) {
+                live = false;
+            } else {
+                if (++i == blocks) {
+                    i = 0;
+                    if (++hp == A.C.HKV * A.HS) {
+                        hp = 0;
+                        do {
+                            if (++it.b >= A.B) {   // not reached while the line is as planned
+                                live = false;
+                                break;
+                            }
+                            load(A);
+                        } while (it.cnt == 0);
+                    }
                 }
+                if (live) set(A);
             }
-            if (w.live) w.set(A);
+            if (pc->t0 < pc->t1) return true;
         }
-        if (pc->t0 < pc->t1) return true;
+        return false;
     }
-    return false;
-}
-__device__ __forceinline__ bool PromptWalk::next(const PromptArgs &A, PromptPiece *pc) { return prompt_next(A, *this, pc); }
+};
 
 // The chunk's note; by one thread, before the walk begins.
 __device__ __forceinline__ void prompt_note(const PromptArgs &A, const PromptWalk &w, int64_t chunk) {
