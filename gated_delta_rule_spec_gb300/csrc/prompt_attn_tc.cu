@@ -729,6 +729,23 @@ __device__ __forceinline__ void row_maxima(const uint32_t (&sc)[32], float (&top
     }
 }
 
+__device__ __forceinline__ float row_maximum(const float (&tops)[8]) {
+    return max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7]));
+}
+
+// 2^(c score + off) of a quarter of a tile's scores, rounded to bf16 in p; their sum, before the rounding, to `sum`.
+__device__ __forceinline__ void probabilities(const uint32_t (&sc)[32], uint32_t *p, uint64_t c2, uint64_t off2, uint64_t (&sum)[2]) {
+#pragma unroll
+    for (int z = 0; z < 16; ++z) {
+        float a, b;
+        unpair(tat::fma2(pair(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, off2), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        sum[z & 1] = tat::add2(sum[z & 1], pair(a, b));
+        p[z] = pack_bf16(a, b);
+    }
+}
+
 template <int D>
 __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t tmem, int tid_all) {
     using L = Lay<D>;
@@ -771,28 +788,55 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                 if ((tid & 31) == 0) ptx::mbar_arrive(bars.p_full(x));
             };
             if (warp_on) {
-                // Two passes over the scores, 32 at a time, each half's next load under way while the other is worked on:
-                // the maximum, then the probabilities.
-                uint32_t sa[32], sb[32];
-                float tops[8];
                 if (k0 + kTile > see_all) cut_scores(s_addr, see - k0);
+                // One pass, 32 scores at a time, the next ones' load under way: the probabilities against the maximum so far and,
+                // beside them, the tile's maximum.  They are kept until it is known that it has not grown too far.
+                float tops[8];
 #pragma unroll
                 for (int y = 0; y < 8; ++y) tops[y] = -INFINITY;
-                ptx::tmem_ld32_bits(s_addr, sa);
-#pragma unroll
-                for (int y = 0; y < kTile; y += 64) {
+                const uint64_t c2 = pair(c, c);
+                float s0 = 0.0f;
+                bool move = j == 0;
+                if (!move) {
+                    uint32_t sa[32], sb[32], p[64];
+                    uint64_t sum[2] = {0, 0};   // pairs of zeros
+                    const float off = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t off2 = pair(off, off);
+                    ptx::tmem_ld32_bits(s_addr, sa);
                     landed(sa);
-                    ptx::tmem_ld32_bits(s_addr + y + 32, sb);
+                    ptx::tmem_ld32_bits(s_addr + 32, sb);
                     row_maxima(sa, tops);
+                    probabilities(sa, p, c2, off2, sum);
                     landed(sb);
-                    ptx::tmem_ld32_bits(s_addr + ((y + 64) & (kTile - 1)), sa);   // in the end the first again
+                    ptx::tmem_ld32_bits(s_addr + 64, sa);
                     row_maxima(sb, tops);
+                    probabilities(sb, p + 16, c2, off2, sum);
+                    landed(sa);
+                    ptx::tmem_ld32_bits(s_addr + 96, sb);
+                    row_maxima(sa, tops);
+                    probabilities(sa, p + 32, c2, off2, sum);
+                    landed(sb);
+                    row_maxima(sb, tops);
+                    probabilities(sb, p + 48, c2, off2, sum);
+                    const float top = c * row_maximum(tops);
+                    move = __any_sync(0xffffffffu, top > m + tat::kGrow);
+                    if (!move) {
+#pragma unroll
+                        for (int y = 0; y < 64; y += 16) ptx::tmem_st16_bits(s_addr + y, p + y);
+                        float s1;
+                        unpair(tat::add2(sum[0], sum[1]), s0, s1);
+                        s0 += s1;
+                    }
                 }
-                const float top = c * max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]),
-                                           fmaxf(tops[6], tops[7]));
-                const bool move = top > m + tat::kGrow;
-                if (__any_sync(0xffffffffu, move)) {
-                    const float to = move ? top : m;
+                if (move) {   // a piece's first tile, or one whose maximum is to be moved: in two passes
+                    uint32_t sc[32];
+#pragma unroll 1
+                    for (int y = 0; y < kTile; y += 32) {
+                        ptx::tmem_ld32_bits(s_addr + y, sc);
+                        landed(sc);
+                        row_maxima(sc, tops);
+                    }
+                    const float top = c * row_maximum(tops), to = top > m + tat::kGrow ? top : m;
                     const float al = m == -INFINITY ? 0.0f : ex2(m - to);
                     l *= al;
                     m = to;
@@ -800,50 +844,35 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                         // (with two streams they were issued before these scores, so they are done)
                         if (L::NS == 1) ok = wait(bars.pv_done(x ^ 1), ((seq - 1) >> 1) & 1u, &ms->abort);
                         if (!ok) break;
-                        landed(sa);   // (on its way since above; a wait in the loop would otherwise be behind its use)
                         ptx::tc_fence_after_sync();
 #pragma unroll 1
                         for (int y = 0; y < D; y += 32) {
-                            uint32_t u[32];
-                            ptx::tmem_ld32_bits(lane_addr + L::col_o(s) + y, u);
-                            landed(u);
+                            ptx::tmem_ld32_bits(lane_addr + L::col_o(s) + y, sc);
+                            landed(sc);
 #pragma unroll
-                            for (int z = 0; z < 32; ++z) u[z] = __float_as_uint(__uint_as_float(u[z]) * al);
-                            ptx::tmem_st16_bits(lane_addr + L::col_o(s) + y, u);
-                            ptx::tmem_st16_bits(lane_addr + L::col_o(s) + y + 16, u + 16);
+                            for (int z = 0; z < 32; ++z) sc[z] = __float_as_uint(__uint_as_float(sc[z]) * al);
+                            ptx::tmem_st16_bits(lane_addr + L::col_o(s) + y, sc);
+                            ptx::tmem_st16_bits(lane_addr + L::col_o(s) + y + 16, sc + 16);
                         }
                     }
-                }
-                const float off = m == -INFINITY ? 0.0f : -m;
-                const uint64_t c2 = pair(c, c), off2 = pair(off, off);
-                uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
-                const auto probabilities = [&](const uint32_t (&sc)[32], uint32_t to) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int z = 0; z < 16; ++z) {
-                        float a, b;
-                        unpair(tat::fma2(pair(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, off2), a, b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        sum[z & 3] = tat::add2(sum[z & 3], pair(a, b));
-                        p[z] = pack_bf16(a, b);
+                    const float off = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t off2 = pair(off, off);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+                    for (int y = 0; y < kTile; y += 32) {
+                        uint32_t p[16];
+                        ptx::tmem_ld32_bits(s_addr + y, sc);
+                        landed(sc);
+                        probabilities(sc, p, c2, off2, sum);
+                        ptx::tmem_st16_bits(s_addr + y / 2, p);   // over scores that have been read
                     }
-                    ptx::tmem_st16_bits(to, p);   // over scores that have been read
-                };
-#pragma unroll
-                for (int y = 0; y < kTile; y += 64) {
-                    landed(sa);
-                    ptx::tmem_ld32_bits(s_addr + y + 32, sb);
-                    probabilities(sa, s_addr + y / 2);
-                    landed(sb);
-                    if (y == 0) ptx::tmem_ld32_bits(s_addr + 64, sa);
-                    probabilities(sb, s_addr + y / 2 + 16);
+                    float s1;
+                    unpair(tat::add2(sum[0], sum[1]), s0, s1);
+                    s0 += s1;
                 }
                 ptx::tmem_st_wait();
                 hand_on();
-                float s0, s1;
-                unpair(tat::add2(tat::add2(sum[0], sum[1]), tat::add2(sum[2], sum[3])), s0, s1);
-                l += s0 + s1;
+                l += s0;
             } else {
                 hand_on();
             }
@@ -1052,7 +1081,7 @@ void prompt_attn_tc_cut(PromptArgs *A, int sms) {
     A->k_whole = A->C.P >= pat::kTile && A->C.D % 64 == 0 && A->C.D != 192;
     A->v_whole = A->C.P >= pat::kTile / (A->C.D > 128 ? 2 : 1) && A->C.D % 64 == 0 && A->C.D != 192;
     A->groups = sms;
-    A->gap = 4 * pat::kTile;
+    A->gap = (streams == 2 ? 3 : 4) * pat::kTile;
 }
 
 cudaError_t launch_prompt_attn_tc(const PromptArgs &A, cudaStream_t st) {
