@@ -21,7 +21,7 @@ namespace gdnspec {
 
 constexpr int kNormThreads = kRopeThreads;
 constexpr int kNormEntries = 8;   // elements or pairs of a head that a lane of its warp takes at most
-constexpr int norm_blocks(size_t es) { return es == 2 ? 6 : 5; }   // of an SM
+constexpr int kNormBlocks = 4;    // of an SM: with six the append spills (45000 tokens of 32 + 2 x 8 heads: 226 us, 168 with four)
 
 // Threads that share a head of `units` units of 16 elements: the next power of two.
 __host__ __device__ inline int head_lanes(int units) {
@@ -63,6 +63,19 @@ __device__ __forceinline__ void load_weights(float (&a)[8], float (&b)[8], const
         z[0] = w.x, z[1] = w.y, z[2] = w.z, z[3] = w.w;
     }
 }
+
+// Head `h` of token `t` of the block's, of the heads that a thread comes to in steps.
+struct HeadWalk {
+    int t, h, dt, dh, heads;
+    __device__ __forceinline__ HeadWalk(int first, int step, int heads_) : heads(heads_) {
+        t = first / heads, h = first - t * heads;
+        dt = step / heads, dh = step - dt * heads;
+    }
+    __device__ __forceinline__ void step() {
+        t += dt, h += dh;
+        if (h >= heads) h -= heads, ++t;
+    }
+};
 
 // Sum over the `lanes` threads (a power of two, neighbours) of a head; the same in all of them.
 __device__ __forceinline__ float head_sum(float x, int lanes) {
@@ -127,7 +140,7 @@ __device__ __forceinline__ void norm_turn_scalar(const IO *src, IO *dst, const f
 // x and out may be the same memory (a head is read before it is written, by the threads that write it), so neither is
 // __restrict__.
 template <typename IO, bool HALF, bool UNITS>
-__global__ void __launch_bounds__(kNormThreads, norm_blocks(sizeof(IO)))
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks)
 norm_rope_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ NormArgs W, int N, int heads, int tokens,
                  const int32_t *__restrict__ pos, const IO *x, int64_t x_stride, IO *out, int64_t out_stride) {
     extern __shared__ __align__(16) float2 cs[];   // [tokens][pairs], see turn_place; then the weights
@@ -135,7 +148,26 @@ norm_rope_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ Nor
     const int tid = threadIdx.x;
     const int64_t n0 = (int64_t)blockIdx.x * tokens;
     const int live = (int)min((int64_t)tokens, N - n0);
+    const int units = R.D >> 4, lanes = head_lanes(units), u = tid & (lanes - 1), turning = R.rot >> 4;
+    const float inv_d = 1.0f / R.D;
+    int o0 = 0, o1 = 0;
+    if (UNITS) unit_runs<HALF>(u, R.rot, &o0, &o1);
+    HeadWalk at(tid / lanes, kNormThreads / lanes, heads), ahead = at;
+    // A head's elements are loaded while the one before it is worked on, the first ones while cos and sin are formed.  (x and
+    // out may be the same memory: those are other heads' places.)
+    Run8<IO> r0, r1;
+    const auto load = [&] {
+        r0.zero();
+        r1.zero();
+        if (UNITS && ahead.t < live && u < units) {
+            const IO *xp = x + (n0 + ahead.t) * x_stride + ahead.h * R.D;
+            r0.load(xp + o0);
+            r1.load(xp + o1);
+        }
+        ahead.step();
+    };
     grid_dep_wait();
+    load();
     stage_weights<HALF, UNITS>(ws, W, R);
     for (int j = tid; j < live * R.pairs; j += kNormThreads) {
         const int t = j / R.pairs, i = j - t * R.pairs;
@@ -143,25 +175,16 @@ norm_rope_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ Nor
     }
     __syncthreads();
     if (UNITS) {
-        const int units = R.D >> 4, lanes = head_lanes(units), u = tid & (lanes - 1), turning = R.rot >> 4;
-        const int all = live * heads, step = kNormThreads / lanes;
-        int o0, o1;
-        unit_runs<HALF>(u, R.rot, &o0, &o1);
         // (a warp's threads leave together: the shuffles need them all)
-        for (int j = tid / lanes; j - (tid & 31) / lanes < all; j += step) {
-            const int t = j / heads, h = j - t * heads;
-            const bool on = j < all && u < units;
-            const IO *xp = x + (n0 + t) * x_stride + h * R.D;
-            IO *op = out + (n0 + t) * out_stride + h * R.D;
-            float a[8] = {}, b[8] = {};
-            if (on) {
-                Run8<IO> r0, r1;
-                r0.load(xp + o0);
-                r1.load(xp + o1);
-                r0.get(a);
-                r1.get(b);
-            }
-            const float r = rsqrtf(head_sum(dot16(a, b, a, b), lanes) / R.D + W.eps);
+        const int all = live * heads;
+        for (int j = (tid & ~31) / lanes; j < all; j += kNormThreads / lanes, at.step()) {
+            const bool on = at.t < live && u < units;
+            IO *op = out + (n0 + at.t) * out_stride + at.h * R.D;
+            float a[8], b[8];
+            r0.get(a);
+            r1.get(b);
+            load();
+            const float r = rsqrtf(fmaf(head_sum(dot16(a, b, a, b), lanes), inv_d, W.eps));
             if (!on) continue;
             float wa[8], wb[8];
             load_weights(wa, wb, ws, u, units);
@@ -170,12 +193,12 @@ norm_rope_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ Nor
                 a[i] *= r * wa[i];
                 b[i] *= r * wb[i];
             }
-            if (u < turning) turn_unit<HALF>(a, b, cs + t * R.pairs, u, R.pairs, 1.0f);
-            Run8<IO> r0, r1;
-            r0.put(a);
-            r1.put(b);
-            r0.store(op + o0);
-            r1.store(op + o1);
+            if (u < turning) turn_unit<HALF>(a, b, cs + at.t * R.pairs, u, R.pairs, 1.0f);
+            Run8<IO> w0, w1;
+            w0.put(a);
+            w1.put(b);
+            w0.store(op + o0);
+            w1.store(op + o1);
         }
     } else {
         for (int j = tid >> 5; j < live * heads; j += kNormThreads / 32) {
@@ -189,7 +212,7 @@ norm_rope_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ Nor
 // Packed prompts: q normed and turned into q_out, k normed and turned and v copied into the pages.  What becomes of a
 // token (where its key goes, that it is dead, or that no row owns it) is found by a warp for each token of the block.
 template <typename IO, bool HALF, bool UNITS>
-__global__ void __launch_bounds__(kNormThreads, norm_blocks(sizeof(IO)))
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks)
 norm_append_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ NormArgs WQ, const __grid_constant__ NormArgs WK,
                    const __grid_constant__ PromptArgs A, int tokens, const int32_t *__restrict__ pos, const IO *__restrict__ q,
                    int64_t q_stride, const IO *__restrict__ k, int64_t k_stride, const IO *__restrict__ v, int64_t v_stride,
@@ -203,7 +226,30 @@ norm_append_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ N
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t n0 = (int64_t)blockIdx.x * tokens;
     const int live = (int)min((int64_t)tokens, A.N - n0);
+    const int HQ = A.HQ, heads = HQ + 2 * C.HKV, all = live * heads;
+    const int units = R.D >> 4, lanes = head_lanes(units), u = tid & (lanes - 1), turning = R.rot >> 4;
+    const float inv_d = 1.0f / R.D;
+    int o0 = 0, o1 = 0;
+    if (UNITS) unit_runs<HALF>(u, R.rot, &o0, &o1);
+    HeadWalk at(tid / lanes, kNormThreads / lanes, heads), ahead = at;
+    // A head's elements are loaded while the one before it is worked on, the first ones while the tokens' places and
+    // angles are formed (what no row owns is loaded for nothing).
+    Run8<IO> x0, x1;
+    const auto load = [&] {
+        x0.zero();
+        x1.zero();
+        if (UNITS && ahead.t < live && u < units) {
+            const int64_t token = n0 + ahead.t;
+            const int h = ahead.h;
+            const IO *src = h < HQ ? q + token * q_stride + h * R.D
+                          : h < HQ + C.HKV ? k + token * k_stride + (h - HQ) * R.D : v + token * v_stride + (h - HQ - C.HKV) * R.D;
+            x0.load(src + o0);
+            x1.load(src + o1);
+        }
+        ahead.step();
+    };
     grid_dep_wait();
+    load();
     stage_weights<HALF, UNITS>(wq, WQ, R);
     stage_weights<HALF, UNITS>(wk, WK, R);
     for (int64_t b = (int64_t)blockIdx.x * kNormThreads + tid; b < A.B; b += (int64_t)gridDim.x * kNormThreads) {
@@ -232,53 +278,30 @@ norm_append_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ N
         cs[t * R.pairs + turn_place<UNITS>(i, R.pairs)] = rope_turn(R, pos_s[t], i);
     }
     __syncthreads();
-    const int HQ = A.HQ, heads = HQ + 2 * C.HKV, all = live * heads;
     IO *kp = static_cast<IO *>(C.k), *vp = static_cast<IO *>(C.v);
-    // source and destination of head j of the block's; whether there is one
-    const auto place = [&](int j, int *t, int *h, const IO **src, IO **dst, int64_t *row) {
-        *t = j / heads;
-        *h = j - *t * heads;
-        if (j >= all) return false;
-        const int64_t token = n0 + *t;
-        *row = row_s[*t];
-        if (*row == kNobodys || (*row == kDead && *h >= HQ)) return false;
-        if (*h < HQ) {
-            *src = q + token * q_stride + *h * R.D;
-            *dst = q_out + (token * HQ + *h) * R.D;
-        } else if (*h < HQ + C.HKV) {
-            *src = k + token * k_stride + (*h - HQ) * R.D;
-            *dst = kp + kv_elem(C, A.layer, *h - HQ, *row);
-        } else {
-            *src = v + token * v_stride + (*h - HQ - C.HKV) * R.D;
-            *dst = vp + kv_elem(C, A.layer, *h - HQ - C.HKV, *row);
-        }
-        return true;
+    // where head h of the block's token t goes; null: nowhere
+    const auto place = [&](int t, int h) -> IO * {
+        const int64_t token = n0 + t, row = row_s[t];
+        if (h < HQ) return row == kNobodys ? nullptr : q_out + (token * HQ + h) * R.D;
+        if (row < 0) return nullptr;
+        return h < HQ + C.HKV ? kp + kv_elem(C, A.layer, h - HQ, row) : vp + kv_elem(C, A.layer, h - HQ - C.HKV, row);
     };
     if (UNITS) {
-        const int units = R.D >> 4, lanes = head_lanes(units), u = tid & (lanes - 1), turning = R.rot >> 4;
-        const int step = kNormThreads / lanes;
-        int o0, o1;
-        unit_runs<HALF>(u, R.rot, &o0, &o1);
-        for (int j = tid / lanes; j - lane / lanes < all; j += step) {
-            int t, h;
-            const IO *src;
-            IO *dst;
-            int64_t row = kNobodys;
-            const bool on = place(j, &t, &h, &src, &dst, &row) && u < units;
+        for (int j = (tid & ~31) / lanes; j < all; j += kNormThreads / lanes, at.step()) {
+            const int t = at.t, h = at.h;
+            IO *const dst = t < live && u < units ? place(t, h) : nullptr;
             const bool is_q = h < HQ, is_v = h >= HQ + C.HKV;
-            float a[8] = {}, b[8] = {};
-            Run8<IO> r0, r1;
-            r0.zero();
-            r1.zero();
-            if (on && row >= 0) {
-                r0.load(src + o0);
-                r1.load(src + o1);
-            }
+            float a[8], b[8];
+            Run8<IO> r0 = x0, r1 = x1;
+            load();
             r0.get(a);
             r1.get(b);
-            const float r = rsqrtf(head_sum(dot16(a, b, a, b), lanes) / R.D + (is_q ? WQ.eps : WK.eps));
-            if (!on) continue;
-            if (row >= 0 && !is_v) {
+            const float r = rsqrtf(fmaf(head_sum(dot16(a, b, a, b), lanes), inv_d, is_q ? WQ.eps : WK.eps));
+            if (!dst) continue;
+            if (row_s[t] < 0) {
+                r0.zero();
+                r1.zero();
+            } else if (!is_v) {
                 if (is_q ? WQ.weight != nullptr : WK.weight != nullptr) {
                     float wa[8], wb[8];
                     load_weights(wa, wb, is_q ? wq : wk, u, units);
@@ -297,13 +320,14 @@ norm_append_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ N
         }
     } else {
         for (int j = warp; j < all; j += kNormThreads / 32) {
-            int t, h;
-            const IO *src;
-            IO *dst;
-            int64_t row;
-            if (!place(j, &t, &h, &src, &dst, &row)) continue;
-            if (row < 0 || h >= HQ + C.HKV) {
-                for (int d = lane; d < R.D; d += 32) dst[d] = row < 0 ? from_f32<IO>(0.0f) : src[d];
+            const int t = j / heads, h = j - t * heads;
+            const int64_t token = n0 + t;
+            IO *const dst = place(t, h);
+            if (!dst) continue;
+            const IO *src = h < HQ ? q + token * q_stride + h * R.D
+                          : h < HQ + C.HKV ? k + token * k_stride + (h - HQ) * R.D : v + token * v_stride + (h - HQ - C.HKV) * R.D;
+            if (row_s[t] < 0 || h >= HQ + C.HKV) {
+                for (int d = lane; d < R.D; d += 32) dst[d] = row_s[t] < 0 ? from_f32<IO>(0.0f) : src[d];
                 continue;
             }
             const NormArgs &W = h < HQ ? WQ : WK;
@@ -318,7 +342,7 @@ norm_append_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ N
 // stays in registers; a block's is put together in shared memory and kept in `part` [blocks][D]
 // for the kernel that sums the blocks' (one block: it is dw).
 template <typename IO, bool HALF, bool UNITS>
-__global__ void __launch_bounds__(kNormThreads, 3)
+__global__ void __launch_bounds__(kNormThreads, 2)
 norm_grad_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ NormArgs W, int N, int heads, int tokens,
                  const int32_t *__restrict__ pos, const IO *x, int64_t x_stride, const IO *dy, int64_t dy_stride, IO *dx,
                  int64_t dx_stride, float *part) {
@@ -329,37 +353,52 @@ norm_grad_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ Nor
     int o0 = 0, o1 = 0;
     if (UNITS) unit_runs<HALF>(u, R.rot, &o0, &o1);
     float da[8] = {}, db[8] = {};   // of the unit's two runs, or of the lane's entries
+    const float inv_d = 1.0f / R.D;
+    const HeadWalk first(tid / lanes, kNormThreads / lanes, heads);
+    Run8<IO> x0, x1, y0, y1;        // the next head's elements, of x and of dy
+    const auto load = [&](int64_t n0, HeadWalk &ahead) {
+        x0.zero();
+        x1.zero();
+        y0.zero();
+        y1.zero();
+        if (ahead.t < tokens && n0 + ahead.t < N && u < units) {
+            const IO *xp = x + (n0 + ahead.t) * x_stride + ahead.h * R.D, *yp = dy + (n0 + ahead.t) * dy_stride + ahead.h * R.D;
+            x0.load(xp + o0);
+            x1.load(xp + o1);
+            y0.load(yp + o0);
+            y1.load(yp + o1);
+        }
+        ahead.step();
+    };
     grid_dep_wait();
     stage_weights<HALF, UNITS>(ws, W, R);
     for (int64_t n0 = (int64_t)blockIdx.x * tokens; n0 < N; n0 += (int64_t)gridDim.x * tokens) {
         const int live = (int)min((int64_t)tokens, N - n0), all = live * heads;
+        HeadWalk at = first, ahead = first;
+        if (UNITS) load(n0, ahead);
         __syncthreads();   // the tokens before are done with their cos and sin
         for (int j = tid; j < live * R.pairs; j += kNormThreads) {
             const int t = j / R.pairs, i = j - t * R.pairs;
             cs[t * R.pairs + turn_place<UNITS>(i, R.pairs)] = rope_turn(R, pos[n0 + t], i);
         }
         __syncthreads();
-        for (int j = tid / lanes; j - lane / lanes < all; j += kNormThreads / lanes) {
-            const int t = j / heads, h = j - t * heads;
+        for (int j = (tid & ~31) / lanes; j < all; j += kNormThreads / lanes, at.step()) {
+            const int t = at.t, h = at.h;
             const IO *xp = x + (n0 + t) * x_stride + h * R.D, *yp = dy + (n0 + t) * dy_stride + h * R.D;
             IO *op = dx + (n0 + t) * dx_stride + h * R.D;
             if (UNITS) {
-                const bool on = j < all && u < units;
-                float a[8] = {}, b[8] = {}, ga[8] = {}, gb[8] = {}, wa[8] = {}, wb[8] = {};
+                const bool on = t < live && u < units;
+                float a[8], b[8], ga[8], gb[8], wa[8] = {}, wb[8] = {};
+                x0.get(a);
+                x1.get(b);
+                y0.get(ga);
+                y1.get(gb);
+                load(n0, ahead);
                 if (on) {
-                    Run8<IO> r0, r1, g0, g1;
-                    r0.load(xp + o0);
-                    r1.load(xp + o1);
-                    g0.load(yp + o0);
-                    g1.load(yp + o1);
-                    r0.get(a);
-                    r1.get(b);
-                    g0.get(ga);
-                    g1.get(gb);
                     if (u < turning) turn_unit<HALF>(ga, gb, cs + t * R.pairs, u, R.pairs, -1.0f);
                     load_weights(wa, wb, ws, u, units);
                 }
-                const float r = rsqrtf(head_sum(dot16(a, b, a, b), lanes) / R.D + W.eps);
+                const float r = rsqrtf(fmaf(head_sum(dot16(a, b, a, b), lanes), inv_d, W.eps));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     da[i] = fmaf(r * a[i], ga[i], da[i]);
@@ -367,7 +406,7 @@ norm_grad_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ Nor
                     ga[i] *= wa[i];
                     gb[i] *= wb[i];
                 }
-                const float c = r * r * (head_sum(dot16(a, b, ga, gb), lanes) / R.D);
+                const float c = r * r * (head_sum(dot16(a, b, ga, gb), lanes) * inv_d);
                 if (!on) continue;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -476,9 +515,10 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float *__re
 
 // ------------------------------------------------------------------ launch
 
+// Tokens of a block: four once that still gives every SM several blocks, and more while they have few units of 16 elements.
 static int norm_tokens(int64_t n, int units) {
     int t = n >= 4096 ? 4 : 1;
-    while (t >= 4 && t < kRopeTokens && t * units < 2 * kNormThreads && n >= 4096 * t) t *= 2;
+    while (t >= 4 && t < kRopeTokens && t * units < 8 * kNormThreads && n >= 4096 * t) t *= 2;
     return t;
 }
 
@@ -541,7 +581,7 @@ static int grad_tokens(int N, int heads) {
 }
 int norm_grad_blocks(int N, int heads, int sms) {
     const int64_t need = ((int64_t)N + grad_tokens(N, heads) - 1) / grad_tokens(N, heads);
-    return (int)(need < 3 * sms ? need : 3 * sms);
+    return (int)(need < 2 * sms ? need : 2 * sms);
 }
 
 template <typename IO, bool HALF, bool UNITS>
