@@ -64,7 +64,8 @@ constexpr int kPieces = 4;               // pieces that are described at a time
 template <int D>
 struct Lay {
     static constexpr int NS = D == 256 ? 1 : 2;                // streams
-    static constexpr int kThreads = NS * 128 + 128;            // softmax warpgroups; producer, MMA, two cleaners
+    static constexpr int kProducers = NS == 1 ? 2 : 1;         // warps that copy
+    static constexpr int kThreads = NS * 128 + 96 + kProducers * 32;   // softmax warpgroups; producers, two for the MMAs, cleaner
     static constexpr int kParts = D == 256 ? 2 : 1;            // stages of a tile: keys in halves of the dims, values of the tokens
     static constexpr uint32_t kKBlocks = D / 64 / kParts;      // 64-dim blocks of a stage of keys
     static constexpr uint32_t kVBlocks = D / 64;               // of values
@@ -162,9 +163,11 @@ struct Ring {
 // ------------------------------------------------------------------ producer warp
 
 // One lane issues: a copy's operands are uniform registers.  The lanes look up the pages of a tile's boxes side by side.
-// In the order of use: with two streams keys and values of each tile in turn; with one, whose
-// scores run a tile ahead, K0 K1 V0 K2 V1 ...
-template <int D>
+// With two streams one warp copies keys and values of each tile in turn; with one, whose rings hold little more than a
+// tile, keys and values have a warp each, so that neither waits for the other's stage (4 x 1024 tokens behind 30000, 16
+// heads on 2 of 256: 1266 us with one warp, 1227 with two).  The keys' warp walks, describes the pieces and
+// copies the queries.
+template <int D, bool KEYS, bool VALUES>
 __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *mq, const CUtensorMap *mk,
                                         const CUtensorMap *mv, Misc *ms, uint32_t base, const PromptWalk &begin) {
     using L = Lay<D>;
@@ -179,6 +182,7 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
     bool ok = true;
     PromptWalk walk = begin;
     PromptPiece pc;
+    PieceReader reader;                                        // (of the values' warp)
     uint32_t at = 0, ph = 1;                                   // place in the ring of pieces
     // the piece pc's description; at the end (!any) that there is none
     const auto describe = [&](bool any, PieceInfo *info) {
@@ -257,53 +261,43 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
         return true;
     };
     while (ok) {
-        const bool any = walk.next(A, &pc);
         PieceInfo sp;
-        ok = describe(any, &sp);
+        bool any;
+        if (KEYS) {
+            any = walk.next(A, &pc);
+            ok = describe(any, &sp);
+        } else {
+            any = reader.next(ms, Bars{ptx::smem_addr(ms)}, &sp, &ok);
+        }
         if (!ok || !any) break;
-        const PromptItem &it = pc.it;
-        const int kv = min(it.keys, (pc.t0 + sp.units) * kTile);
-        const int32_t *table = A.C.page_table + (int64_t)it.slot * A.C.max_pages;
-        // the page of box `lane` of tile u: looked up a tile before it is used
+        const int kv = min(sp.keys, (sp.t0 + sp.units) * kTile);
+        const int32_t *table = A.C.page_table + (int64_t)sp.slot * A.C.max_pages;
+        // the page of box `lane` of tile u: looked up two tiles before it is used
         const auto page_of = [&](int u) {
-            const int tok = (pc.t0 + u) * kTile + lane * BR;
+            const int tok = (sp.t0 + u) * kTile + lane * BR;
             return u < sp.units && lane * BR < kTile && tok < kv ? table[tok >> A.C.logP] : 0;
         };
         const auto row_of = [&](int u, int page) {
-            const int tok = (pc.t0 + u) * kTile + lane * BR;
-            if (u < sp.units && lane * BR < kTile && tok < kv && (page < 0 || page >= A.C.num_pages)) {
+            const int tok = (sp.t0 + u) * kTile + lane * BR;
+            if (lane * BR < kTile && tok < kv && (page < 0 || page >= A.C.num_pages)) {
                 atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
                 page = 0;
             }
-            return ((A.layer * A.C.num_pages + page) * A.C.HKV + it.h) * A.C.P + (tok & (A.C.P - 1));
+            return ((A.layer * A.C.num_pages + page) * A.C.HKV + sp.h) * A.C.P + (tok & (A.C.P - 1));
         };
-        const auto boxes_of = [&](int u) { return (min(kTile, kv - (pc.t0 + u) * kTile) + BR - 1) >> log_br; };
-        const auto copy_k = [&](int u, int row) {
-            bool good = true;
+        int page = page_of(0), next = page_of(1);
 #pragma unroll 1
-            for (int p = 0; p < L::kParts; ++p) good = good && stage(k_ring, std::true_type(), p, row, boxes_of(u));
-            return good;
-        };
-        const auto copy_v = [&](int u, int row) {
-            bool good = true;
-#pragma unroll 1
-            for (int p = 0; p < L::kParts; ++p) good = good && stage(v_ring, std::false_type(), p, row, boxes_of(u));
-            return good;
-        };
-        // (one place for the keys' copies and one for the values': they are long)
-        constexpr int kLag = L::NS == 1 ? 1 : 0;
-        int page = page_of(0), next = page_of(1), row = 0;
-#pragma unroll 1
-        for (int u = 0; ok && u < sp.units + kLag; ++u) {
-            const int before = row;
-            row = row_of(u, page);
+        for (int u = 0; ok && u < sp.units; ++u) {
+            const int row = row_of(u, page), boxes = (min(kTile, kv - (sp.t0 + u) * kTile) + BR - 1) >> log_br;
             page = next;
             next = page_of(u + 2);
-            if (u < sp.units) ok = copy_k(u, row);
-            if (u == 0) {   // the query tiles, behind the first keys
+            if (KEYS)
+#pragma unroll 1
+                for (int p = 0; ok && p < L::kParts; ++p) ok = stage(k_ring, std::true_type(), p, row, boxes);
+            if (KEYS && u == 0) {   // the query tiles, behind the first keys
 #pragma unroll 1
                 for (int s = 0; s < L::NS; ++s) {
-                    if (!ok || sp.n[s] == 0) continue;
+                    if (!ok || (s ? sp.n[1] : sp.n[0]) == 0) continue;
                     ok = wait(ptx::smem_addr(&ms->q_empty[s]), ((q_issued >> s) & 1u) ^ 1u, &ms->abort);
                     if (!ok) break;
                     const uint32_t bar = uniform(ptx::smem_addr(&ms->q_full[s])), dst = uniform(base + s * L::kQTile);
@@ -311,15 +305,17 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
                         ptx::mbar_expect_tx(bar, q_bytes * L::kVBlocks);
 #pragma unroll
                         for (int blk = 0; blk < (int)L::kVBlocks; ++blk)
-                            ptx::tma_load_3d(dst + blk * (kRows * 128u), mq, bar, blk * 64, it.h * A.G + it.part * A.GS,
-                                             it.first + it.q0 + s * tq);
+                            ptx::tma_load_3d(dst + blk * (kRows * 128u), mq, bar, blk * 64, sp.h * A.G + sp.part * A.GS,
+                                             sp.first + sp.q0 + s * tq);
                     }
                     __syncwarp();
                     q_issued ^= 1u << s;
                     q_any |= 1u << s;
                 }
             }
-            if (ok && u >= kLag) ok = copy_v(u - kLag, kLag ? before : row);
+            if (VALUES)
+#pragma unroll 1
+                for (int p = 0; ok && p < L::kParts; ++p) ok = stage(v_ring, std::false_type(), p, row, boxes);
         }
     }
     if (!ok) {   // copies in flight land before the block's shared memory goes away
@@ -489,7 +485,8 @@ __device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, u
     if (!ok) drain(bars, s);
 }
 
-// One stream: its scores by one warp, a tile ahead, its sums by another.
+// One stream: its scores by one warp, a tile ahead, its sums by another.  (In turns, as above, they are no faster: 1234 us
+// against 1227 for 4 x 1024 tokens behind 30000, 16 heads on 2 of 256.)
 template <int D>
 __device__ __forceinline__ void multiply_scores(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem) {
     using L = Lay<D>;
@@ -973,7 +970,7 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         }
         for (int i = 0; i < kPieces; ++i) {
             init(ms->piece_full[i], 1);
-            init(ms->piece_empty[i], L::NS * 4 + 2 + kCleaners);   // warps that read it
+            init(ms->piece_empty[i], L::NS * 4 + 2 + kCleaners + L::kProducers - 1);   // warps that read it
         }
         for (int i = 0; i < 2; ++i) {
             init(ms->q_full[i], 1);
@@ -1013,7 +1010,9 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             const PromptWalk begin(A, plan);
             if (ptx::elect_one()) prompt_note(A, begin, plan.chunk);
             __syncwarp();
-            produce<D>(A, &mq, &mk, &mv, ms, base, begin);
+            produce<D, true, L::kProducers == 1>(A, &mq, &mk, &mv, ms, base, begin);
+        } else if (L::kProducers == 2 && role == 4) {
+            produce<D, false, true>(A, &mq, &mk, &mv, ms, base, PromptWalk());
         } else if (role == 3) {
             clean<D>(A, ms, sm, 0);
         } else if (L::NS == 2) {

@@ -231,6 +231,7 @@ struct PromptWalk {
         it.keys = it.len + min(it.cnt, it.q0 + A.tokens);
         it.tiles = (it.keys + (1 << A.log_tn) - 1) >> A.log_tn;
     }
+    __device__ __forceinline__ PromptWalk() : live(false) {}
     __device__ __forceinline__ PromptWalk(const PromptArgs &A, const PromptPlan &p) {
         live = p.b >= 0;
         if (!live) return;
