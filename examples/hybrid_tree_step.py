@@ -1,8 +1,9 @@
 """The speculative step of a hybrid model's two kinds of layers through the library.
 
 Two softmax-attention layers over the paged cache, one feeding the other: three prompts go
-into the cache in windows, each is forked, and then the same tokens are run twice, as one
-drafted tree (rotary positions and append, tree attention, commit of the accepted path),
+into the cache in one packed pass (the norms of q's and k's heads with the rotary positions and the
+append, causal attention), each is forked, and then the same tokens are run twice, as one
+drafted tree (norms, rotary positions and append, tree attention, commit of the accepted path),
 and one after another on the forks (windows of one token).
 
 Beside them, one gated-delta-rule layer: it takes chains only, so no tree can go through it, and
@@ -25,19 +26,32 @@ from gated_delta_rule_spec_gb300 import binding  # noqa: E402
 
 
 class AttentionLayer:
-    """One softmax-attention layer: projections, rotary positions, the cache, the output."""
+    """One softmax-attention layer: projections, the heads' norms, rotary positions, the cache, the output."""
 
     def __init__(self, index, dim, HQ, HKV, D, plan, gen):
         self.index, self.HQ, self.HKV, self.D, self.plan = index, HQ, HKV, D, plan
         w = lambda *s: (torch.randn(*s, generator=gen, device="cuda") * s[0] ** -0.5).to(torch.bfloat16)  # noqa: E731
         self.qkv, self.out = w(dim, (HQ + 2 * HKV) * D), w(HQ * D, dim)
+        around = lambda: binding.HeadNorm(0.1 * torch.randn(D, generator=gen, device="cuda"), offset=1.0)  # noqa: E731
+        self.q_norm, self.k_norm = around(), around()
 
-    def __call__(self, cache, slots, x, pos=None, mask=None, counts=None):
+    def append(self, cache, slots, starts, x, pos=None):
+        """Packed tokens x [N, dim]: their keys and values go into the cache; their queries, normed and turned."""
+        y = (x @ self.qkv).view(-1, self.HQ + 2 * self.HKV, self.D)
+        q, k, v = y.split([self.HQ, self.HKV, self.HKV], dim=1)
+        return binding.norm_rope_append(self.plan, cache, self.index, slots, starts, q, k, v, self.q_norm, self.k_norm, pos)
+
+    def prompt(self, cache, slots, starts, x):
+        """Prompts of any length, packed: row b's tokens are starts[b] .. starts[b + 1] of x [N, dim]."""
+        q = self.append(cache, slots, starts, x)
+        return x + binding.prompt_attn(cache, self.index, slots, starts, q).view(len(x), -1) @ self.out
+
+    def __call__(self, cache, slots, x, pos=None, mask=None):
+        """A window of T drafted tokens of every row, x [B, T, dim]."""
         B, T, _ = x.shape
-        y = (x @ self.qkv).view(B, T, self.HQ + 2 * self.HKV, self.D)
-        q, k, v = y.split([self.HQ, self.HKV, self.HKV], dim=2)
-        q = binding.rope_append(self.plan, cache, self.index, slots, q, k, v, pos=pos, n_tokens=counts)
-        o = binding.tree_attn(cache, self.index, slots, q, mask, counts)
+        starts = torch.arange(0, B * T + 1, T, dtype=torch.int32, device="cuda")
+        q = self.append(cache, slots, starts, x.flatten(0, 1), None if pos is None else pos.flatten())
+        o = binding.tree_attn(cache, self.index, slots, q.view(B, T, self.HQ, self.D), mask)
         return x + o.view(B, T, -1) @ self.out
 
 
@@ -82,12 +96,13 @@ def main(dim=256, HQ=8, HKV=2, D=64, P=16, prompts=(70, 5, 33), seed=0) -> float
             x = layer(cache, s, x, **kw)
         return x
 
-    # the prompts, in windows of at most 64 tokens of each
-    for at in range(0, max(prompts), 64):
-        counts = i32([max(0, min(64, n - at)) for n in prompts])
-        assert bool(binding.kv_reserve(cache, slots, 64, counts).all())
-        forward(slots, draw(64), counts=counts)
-        binding.kv_commit(cache, slots, counts, 64)
+    # the prompts, one behind another
+    counts, starts = i32(prompts), i32([sum(prompts[:b]) for b in range(B + 1)])
+    assert bool(binding.kv_reserve(cache, slots, max(prompts), counts).all())
+    h = torch.randn(sum(prompts), dim, generator=gen, device="cuda").to(torch.bfloat16)
+    for layer in layers:
+        h = layer.prompt(cache, slots, starts, h)
+    binding.kv_commit(cache, slots, counts, max(prompts))
     assert bool(binding.kv_fork(cache, slots, forks).all())
 
     # a tree of eight drafts; nodes 0, 2, 5, 7 are accepted

@@ -176,6 +176,7 @@ int check_prompt(const gdn_spec_kv_cache *c, int32_t B, int32_t N, int32_t HQ) {
     if (B < 0 || N < 0 || HQ <= 0 || HQ % c->HKV != 0) return GDN_SPEC_EINVAL;
     if (HQ / c->HKV > 4096) return GDN_SPEC_EUNSUPPORTED;
     if (c->io_dtype == GDN_SPEC_DTYPE_BF16 && !prompt_attn_tc_supported(kv_args(c))) return GDN_SPEC_EUNSUPPORTED;
+    if ((int64_t)c->max_pages * c->P > INT32_MAX - 1024) return GDN_SPEC_EUNSUPPORTED;   // a slot's tokens and some tiles, in 31 bits
     // the line of items' keys is counted in 63 bits: an item a token and part of a group of heads at most
     const double items = ((double)N + B) * c->HKV * (HQ / c->HKV / 64 + 1);
     if (items * ((double)c->max_pages * c->P + 1024) > 4.0e18) return GDN_SPEC_EUNSUPPORTED;

@@ -6,15 +6,18 @@
 //   m' = max(m, max s),  l' = l 2^(m-m') + sum 2^(s-m'),  o' = o 2^(m-m') + sum 2^(s-m') v,
 // and the row's output is o / l.  A row that has seen nothing yet has m = -inf, l = 0.
 //
-// A block of 256 threads holds 64 query rows and walks tiles of 64 keys.  A thread forms
-// the scores of four rows with four keys, then, with the probabilities in shared memory
-// where the keys were, the sums of the same rows over DP / 16 columns.
+// A block holds 64 query rows and walks tiles of 64 keys.  A thread forms the scores of eight rows
+// (four where D > 128) with four keys, then, with the probabilities in shared memory where the keys
+// were, the sums of the same rows over DP / 16 columns; sixteen threads share the rows.  The
+// values are copied while the scores are formed, two blocks an SM cover the rest.  2 prompts of
+// 1000 tokens behind 1000, 8 heads on 2 of 128: 300 us, 38 TFLOP/s, half of the fp32 rate (345 us
+// with four rows a thread); heads of 256, 600 tokens: 328 us, 36 TFLOP/s.  A wide read of shared memory feeds
+// 10 to 16 multiply-adds, which bounds it.
 #include "launch_setup.cuh"
 #include "prompt_common.cuh"
 
 namespace gdnspec {
 
-constexpr int kPromptThreads = 256;
 constexpr int kPromptRows = 64, kPromptLogTile = 6, kPromptTile = 1 << kPromptLogTile;
 
 // Q and K rows and V rows of a block, in floats; the probabilities lie where the keys were.
@@ -27,14 +30,20 @@ __device__ __forceinline__ void prompt_copy16(void *dst, const void *src, bool l
                  : "memory");
 }
 
+// Rows of a thread, threads of a block, and blocks of an SM, as many as the shared memory leaves room for.
+constexpr int prompt_rows(int DP) { return DP > 128 ? 4 : 8; }
+constexpr int prompt_threads(int DP) { return kPromptRows / prompt_rows(DP) * 16; }
+constexpr int prompt_blocks(int DP) { return DP > 128 ? 1 : 2; }
+
 template <int DP>
-__global__ void __launch_bounds__(kPromptThreads) prompt_attn_kernel(const __grid_constant__ PromptArgs A) {
+__global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_attn_kernel(const __grid_constant__ PromptArgs A) {
+    constexpr int RT = prompt_rows(DP), kPromptThreads = prompt_threads(DP);
     constexpr int LD = DP + 4, PLD = kPromptTile + 4, NG = DP / 64;   // groups of 64 columns, four of each a thread's
     extern __shared__ __align__(16) float sm[];
     __shared__ PromptScratch scratch;
-    __shared__ int64_t elem_s[kPromptTile];   // where a tile's keys and values lie in the pool
+    __shared__ int64_t elem_s[2][kPromptTile];   // where a tile's keys and values lie in the pool, this one's and the next's
     float *const Qs = sm, *const Ks = Qs + kPromptRows * LD, *const Vs = Ks + kPromptTile * LD, *const Ps = Ks;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, r0 = ty * 4, D = A.C.D, D4 = D >> 2;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, r0 = ty * RT, D = A.C.D, D4 = D >> 2;
     const float *const qg = static_cast<const float *>(A.q);
     grid_dep_wait();
 
@@ -53,10 +62,10 @@ __global__ void __launch_bounds__(kPromptThreads) prompt_attn_kernel(const __gri
             on = on && d < D;
             prompt_copy16(Qs + r * LD + d, qg + (on ? row * D + d : 0), on);
         }
-        int see[4];   // keys that the thread's rows attend to
-        float m[4], l[4], acc[4][NG * 4] = {};
+        int see[RT];   // keys that the thread's rows attend to
+        float m[RT], l[RT], acc[RT][NG * 4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RT; ++i) {
             bool on;
             prompt_out_row(A, it, r0 + i, &on);
             see[i] = on ? it.len + it.q0 + (r0 + i) / A.GS + 1 : 0;
@@ -64,52 +73,59 @@ __global__ void __launch_bounds__(kPromptThreads) prompt_attn_kernel(const __gri
             l[i] = 0.0f;
         }
         const int all = it.len + it.q0 + 1;   // keys that every row attends to
+        const auto look_up = [&](int t) {
+            if (tid < kPromptTile && t < pc.t1) {
+                int64_t e = -1;
+                if (t * kPromptTile + tid < it.keys) {
+                    const int64_t row = kv_token_row(A.C, it.slot, t * kPromptTile + tid);
+                    if (row < 0) atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
+                    else e = kv_elem(A.C, A.layer, it.h, row);
+                }
+                elem_s[t & 1][tid] = e;
+            }
+        };
+        look_up(pc.t0);
         for (int t = pc.t0; t < pc.t1; ++t) {
             const int k0 = t * kPromptTile;
             const bool edge = k0 + kPromptTile > all;
             __syncthreads();   // the tile before is done with
-            if (tid < kPromptTile) {
-                int64_t e = -1;
-                if (k0 + tid < it.keys) {
-                    const int64_t row = kv_token_row(A.C, it.slot, k0 + tid);
-                    if (row < 0) atomicOr(A.C.status, GDN_SPEC_ST_PAGE_OOR);
-                    else e = kv_elem(A.C, A.layer, it.h, row);
+            // rows past the end are zeros; the values are on their way while the scores are formed
+            const auto fetch = [&](float *to, int ld, const void *pool) {
+#pragma unroll 4
+                for (int x = tid; x < kPromptTile * (DP / 4); x += kPromptThreads) {
+                    const int r = x / (DP / 4), d = x % (DP / 4) * 4;
+                    const int64_t e = elem_s[t & 1][r];
+                    const bool on = e >= 0 && d < D;
+                    prompt_copy16(to + r * ld + d, static_cast<const float *>(pool) + (on ? e + d : 0), on);
                 }
-                elem_s[tid] = e;
-            }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            fetch(Ks, LD, A.C.k);
+            fetch(Vs, DP, A.C.v);
+            look_up(t + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
-            for (int x = tid; x < kPromptTile * (DP / 4); x += kPromptThreads) {   // rows past the end are zeros
-                const int r = x / (DP / 4), d = x % (DP / 4) * 4;
-                const int64_t e = elem_s[r];
-                const bool on = e >= 0 && d < D;
-                const int64_t at = on ? e + d : 0;
-                prompt_copy16(Ks + r * LD + d, static_cast<const float *>(A.C.k) + at, on);
-                prompt_copy16(Vs + r * DP + d, static_cast<const float *>(A.C.v) + at, on);
-            }
-            asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-            __syncthreads();
-            float s[4][4] = {};
+            float s[RT][4] = {};
 #pragma unroll 4
             for (int d = 0; d < DP; d += 4) {
-                float4 q[4], k[4];
+                float4 k[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    q[i] = *reinterpret_cast<const float4 *>(Qs + (r0 + i) * LD + d);
-                    k[i] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * i) * LD + d);
-                }
+                for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * LD + d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < RT; ++i) {
+                    const float4 q = *reinterpret_cast<const float4 *>(Qs + (r0 + i) * LD + d);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        s[i][j] = fmaf(q[i].x, k[j].x, s[i][j]);
-                        s[i][j] = fmaf(q[i].y, k[j].y, s[i][j]);
-                        s[i][j] = fmaf(q[i].z, k[j].z, s[i][j]);
-                        s[i][j] = fmaf(q[i].w, k[j].w, s[i][j]);
+                        s[i][j] = fmaf(q.x, k[j].x, s[i][j]);
+                        s[i][j] = fmaf(q.y, k[j].y, s[i][j]);
+                        s[i][j] = fmaf(q.z, k[j].z, s[i][j]);
+                        s[i][j] = fmaf(q.w, k[j].w, s[i][j]);
                     }
+                }
             }
             __syncthreads();   // the keys are done with: the probabilities take their place
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RT; ++i) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -130,22 +146,24 @@ __global__ void __launch_bounds__(kPromptThreads) prompt_attn_kernel(const __gri
                     Ps[(r0 + i) * PLD + tx + 16 * j] = p;
                 }
             }
-            __syncwarp();   // a row's probabilities are read by the half warp that wrote them
+            // a row's probabilities are read by the half warp that wrote them, the values by all
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
             // In a tile that some row does not see all of, masked keys are left out by a test, so that an infinity or
             // NaN there stays without effect.
             const auto add = [&](auto test) {
 #pragma unroll 2
                 for (int k = 0; k < kPromptTile; k += 4) {
-                    float4 p[4];
+                    float4 p[RT];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(Ps + (r0 + i) * PLD + k);
+                    for (int i = 0; i < RT; ++i) p[i] = *reinterpret_cast<const float4 *>(Ps + (r0 + i) * PLD + k);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             const float4 v = *reinterpret_cast<const float4 *>(Vs + (k + e) * DP + g * 64 + tx * 4);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < RT; ++i) {
                                 const float x = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
                                 if (decltype(test)::value && x == 0.0f) continue;
                                 acc[i][g * 4] = fmaf(x, v.x, acc[i][g * 4]);
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(kPromptThreads) prompt_attn_kernel(const __gri
         }
         const int64_t part = (int64_t)blockIdx.x * 2 + pc.side();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RT; ++i) {
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
             bool on;
@@ -251,7 +269,7 @@ static cudaError_t run_prompt_attn(const PromptArgs &A, cudaStream_t st) {
     int sms;
     const cudaError_t e = kernel_setup(setup, (const void *)prompt_attn_kernel<DP>, prompt_smem(DP), &sms);
     if (e != cudaSuccess) return e;
-    return launch_dependent(prompt_attn_kernel<DP>, dim3(A.groups), dim3(kPromptThreads), prompt_smem(DP), st, A);
+    return launch_dependent(prompt_attn_kernel<DP>, dim3(A.groups), dim3(prompt_threads(DP)), prompt_smem(DP), st, A);
 }
 
 // The cut of the work on a machine of `sms` SMs.
@@ -261,7 +279,7 @@ void prompt_attn_cut(PromptArgs *A, int sms) {
     A->HS = (A->G + A->MT - 1) / A->MT;
     A->GS = (A->G + A->HS - 1) / A->HS;
     A->tokens = A->MT / A->GS;
-    A->groups = sms * (A->C.D > 128 ? 1 : 2);   // as many blocks as the registers and the shared memory leave room for
+    A->groups = sms * prompt_blocks(A->C.D);
     A->gap = kPromptTile;
 }
 

@@ -559,8 +559,8 @@ const char *gdn_spec_tree_attn_path(const gdn_spec_kv_cache *cache, int32_t T, i
  * both with the rows' counts.  Rows of one token (decode) go beside prompts in the
  * same call.
  *   starts  int32 [B + 1], device: ascending, 0 <= starts[b] <= starts[b + 1] <= N.
- *           A row whose two entries are not so owns nothing (ACCEPT_RANGE).  Tokens
- *           that no row owns are neither read nor written.
+ *           A row whose two entries are not so owns nothing (ACCEPT_RANGE).  What
+ *           belongs to tokens that no row owns is left as it was.
  * Rows with slot_idx < 0, and rows refused with a status bit, get zeros.
  * ---------------------------------------------------------------------- */
 
@@ -629,7 +629,8 @@ int gdn_spec_norm_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_hea
  * row's tokens 0..t (cache positions length ..  length + t, written before):
  *   out = sum_j p_j v_j,  p = softmax_j(scale <q, k_j>)
  * What a token does not attend to has no effect on it, whatever its bits.
- *   q          io_dtype [N, HQ, D], dense; HKV divides HQ, head h reads kv head h / (HQ / HKV)
+ *   q          io_dtype [N, HQ, D], dense; HKV divides HQ, head h reads kv head h / (HQ / HKV);
+ *              out does not overlap it
  *   starts     int32 [B + 1], above
  *   scale      > 0, and scale * log2(e) a finite fp32 number
  *   out        io_dtype [N, HQ, D], dense (written)
@@ -638,8 +639,9 @@ int gdn_spec_norm_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_hea
  *   workspace  as gdn_spec_tree_attn's, workspace_bytes >= gdn_spec_prompt_attn_workspace
  * Two kernels (gdn_spec_prompt_attn_path): "tc" -- bf16: TMA and tcgen05, the probabilities
  * rounded to bf16 for the second product; n_layers * num_pages * HKV * P is below 2^31 --
- * and "generic" -- fp32 throughout on the CUDA cores.  HQ / HKV is at most 4096, and
- * (N + B) * HKV * (1 + HQ / HKV / 64) * (max_pages * P + 1024) at most 4e18.
+ * and "generic" -- fp32 throughout on the CUDA cores.  HQ / HKV is at most 4096,
+ * max_pages * P at most 2^31 - 1025, and (N + B) * HKV * (1 + HQ / HKV / 64) *
+ * (max_pages * P + 1024) at most 4e18.
  * Device status: SLOT_OOR, ACCEPT_RANGE (starts), CURSOR_CORRUPT, NO_PAGES (the row gets
  * zeros), PAGE_OOR (the row's outputs are not valid), TIMEOUT.
  */

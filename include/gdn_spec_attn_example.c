@@ -1,8 +1,9 @@
 /*
- * gdn_spec_attn_example.c -- one speculative step of a softmax-attention layer through
- * the C ABI of libgdnspec (include/gdn_spec.h): rotary positions and append, attention of
+ * gdn_spec_attn_example.c -- the softmax-attention layers through the C ABI of libgdnspec
+ * (include/gdn_spec.h).  One speculative step: rotary positions and append, attention of
  * the drafted tree, then, once for all layers, the commit of the accepted path and
- * the pages of the next window.
+ * the pages of the next window.  And one layer of packed prompts: the heads' norms with
+ * the rotary positions and the append, then causal attention.
  *
  * Every pointer in the cache and the arguments is caller-owned device memory of the
  * current CUDA device; no call allocates, and the calls are ordered on `stream`, so
@@ -47,5 +48,31 @@ int gdn_spec_attn_example_step(const gdn_spec_kv_cache *cache, const int32_t *sl
     uint32_t st = 0;
     rc = gdn_spec_kv_read_status(cache, &st, /*clear=*/1, stream);
     if (!rc && st) fprintf(stderr, "device status 0x%x\n", st);
+    return rc;
+}
+
+/* Row b's prompt is tokens starts[b] .. starts[b + 1] of qkv [N, HQ + 2 HKV, D] (bf16 here); its pages
+ * have been reserved.  After the last layer: gdn_spec_kv_commit with path = NULL and the rows' counts. */
+int gdn_spec_attn_example_prompt(const gdn_spec_kv_cache *cache, int32_t layer, const int32_t *slot_idx,
+                                 const int32_t *starts, int32_t B, int32_t N, const void *qkv,
+                                 const float *q_weight, const float *k_weight, void *q_rot, void *out,
+                                 void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const int32_t HQ = 16;
+    const gdn_spec_head_norm q_norm = {q_weight, 1.0e-6f, 1.0f}, k_norm = {k_weight, 1.0e-6f, 1.0f};
+    gdn_spec_rope_plan plan;
+    int rc = gdn_spec_rope_init(&plan, cache->D, 64, GDN_SPEC_ROPE_HALF, 1.0e6, NULL);
+    if (!rc && workspace_bytes < gdn_spec_prompt_attn_workspace(cache, B, N, HQ)) rc = GDN_SPEC_EINVAL;
+
+    const int64_t stride = (int64_t)(HQ + 2 * cache->HKV) * cache->D;
+    const char *q = (const char *)qkv;
+    const char *k = q + 2 * (int64_t)HQ * cache->D;
+    const char *v = k + 2 * (int64_t)cache->HKV * cache->D;
+    if (!rc)
+        rc = gdn_spec_norm_rope_append(&plan, &q_norm, &k_norm, cache, layer, slot_idx, starts, B, N, NULL,
+                                       HQ, q, stride, k, stride, v, stride, q_rot, stream);
+    if (!rc)
+        rc = gdn_spec_prompt_attn(cache, layer, slot_idx, starts, B, N, HQ, q_rot, 0.0625f, out, NULL,
+                                  workspace, workspace_bytes, stream);
     return rc;
 }

@@ -1,0 +1,47 @@
+"""What the packed prompts' calls allocate for themselves on a stream of their own comes from that stream's pool, and a
+tensor of another device than the current one is refused; the library, streams and checks are stand-ins."""
+import pytest
+import torch
+
+from gated_delta_rule_spec_gb300 import binding
+from tests.test_binding_streams import FakeStream, Watch
+
+
+def calls(w, plan):
+    norm, starts = binding.HeadNorm(torch.zeros(64)), torch.zeros(3, dtype=torch.int32)
+    x, pos = w.q[0], torch.zeros(3, dtype=torch.int32)
+    work = torch.zeros(64, dtype=torch.uint8)
+    u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
+    return [
+        (lambda s: binding.norm_rope(plan, norm, pos, x, stream=s), [((3, 4, 64), bf16)]),
+        (lambda s: binding.norm_rope_grad(plan, norm, pos, x, x, workspace=work, stream=s), [((3, 4, 64), bf16), ((64,), f32)]),
+        (lambda s: binding.norm_rope_grad(plan, norm, pos, x, x, dx=x, dw=norm.weight, stream=s), [((16,), u8)]),
+        (lambda s: binding.norm_rope_append(plan, w.cache, 0, w.slots, starts, x, x, x, stream=s), [((3, 4, 64), bf16)]),
+        (lambda s: binding.prompt_attn(w.cache, 0, w.slots, starts, x, workspace=work, stream=s), [((3, 4, 64), bf16)]),
+        (lambda s: binding.prompt_attn(w.cache, 0, w.slots, starts, x, out=x, stream=s), [((16,), u8)])]
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_results_and_workspaces_are_taken_where_the_call_runs(monkeypatch, which):
+    plan = binding.RopePlan(64)                                             # by the library itself
+    w, s = Watch(monkeypatch), FakeStream()
+    call, made = calls(w, plan)[which]
+    call(s)
+    assert [(shape, dtype, s) for shape, dtype in made] == w.made
+    results = [shape for shape, dtype in made if dtype != torch.uint8]
+    assert w.noted == [(shape, "current") for shape in results]            # read there by the caller, perhaps
+    w.made.clear(), w.noted.clear()
+    call(None)
+    assert [(shape, dtype, None) for shape, dtype in made] == w.made and not w.noted
+
+
+def test_another_device_is_refused(monkeypatch):
+    class Elsewhere:
+        is_cuda, device = True, "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(binding.GdnSpecError, match="cuda:1"):
+        binding._here(Elsewhere(), "x")
