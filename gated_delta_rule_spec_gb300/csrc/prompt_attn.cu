@@ -105,25 +105,35 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
             look_up(t + 1);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
+            // Sums of 64 terms, and of such sums: one chain over a long row would lose bits (below, too).
             float s[RT][4] = {};
+#pragma unroll 1
+            for (int d0 = 0; d0 < DP; d0 += 64) {
+                float u[RT][4] = {};
 #pragma unroll 4
-            for (int d = 0; d < DP; d += 4) {
-                float4 k[4];
+                for (int d = d0; d < d0 + 64; d += 4) {
+                    float4 k[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * LD + d);
+                    for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * LD + d);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const float4 q = *reinterpret_cast<const float4 *>(Qs + (r0 + i) * LD + d);
+                    for (int i = 0; i < RT; ++i) {
+                        const float4 q = *reinterpret_cast<const float4 *>(Qs + (r0 + i) * LD + d);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s[i][j] = fmaf(q.x, k[j].x, s[i][j]);
-                        s[i][j] = fmaf(q.y, k[j].y, s[i][j]);
-                        s[i][j] = fmaf(q.z, k[j].z, s[i][j]);
-                        s[i][j] = fmaf(q.w, k[j].w, s[i][j]);
+                        for (int j = 0; j < 4; ++j) {
+                            u[i][j] = fmaf(q.x, k[j].x, u[i][j]);
+                            u[i][j] = fmaf(q.y, k[j].y, u[i][j]);
+                            u[i][j] = fmaf(q.z, k[j].z, u[i][j]);
+                            u[i][j] = fmaf(q.w, k[j].w, u[i][j]);
+                        }
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[i][j] += u[i][j];
             }
             __syncthreads();   // the keys are done with: the probabilities take their place
+            float al[RT];
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
                 float top = -INFINITY;
@@ -134,11 +144,10 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
                 }
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float mn = fmaxf(m[i], top), base = mn == -INFINITY ? 0.0f : mn, al = exp2f(m[i] - base);
+                const float mn = fmaxf(m[i], top), base = mn == -INFINITY ? 0.0f : mn;
+                al[i] = exp2f(m[i] - base);
                 m[i] = mn;
-                l[i] *= al;
-#pragma unroll
-                for (int j = 0; j < NG * 4; ++j) acc[i][j] *= al;
+                l[i] *= al[i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float p = exp2f(s[i][j] - base);
@@ -151,6 +160,7 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
             __syncthreads();
             // In a tile that some row does not see all of, masked keys are left out by a test, so that an infinity or
             // NaN there stays without effect.
+            float sum[RT][NG * 4] = {};   // over the tile
             const auto add = [&](auto test) {
 #pragma unroll 2
                 for (int k = 0; k < kPromptTile; k += 4) {
@@ -166,16 +176,20 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
                             for (int i = 0; i < RT; ++i) {
                                 const float x = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
                                 if (decltype(test)::value && x == 0.0f) continue;
-                                acc[i][g * 4] = fmaf(x, v.x, acc[i][g * 4]);
-                                acc[i][g * 4 + 1] = fmaf(x, v.y, acc[i][g * 4 + 1]);
-                                acc[i][g * 4 + 2] = fmaf(x, v.z, acc[i][g * 4 + 2]);
-                                acc[i][g * 4 + 3] = fmaf(x, v.w, acc[i][g * 4 + 3]);
+                                sum[i][g * 4] = fmaf(x, v.x, sum[i][g * 4]);
+                                sum[i][g * 4 + 1] = fmaf(x, v.y, sum[i][g * 4 + 1]);
+                                sum[i][g * 4 + 2] = fmaf(x, v.z, sum[i][g * 4 + 2]);
+                                sum[i][g * 4 + 3] = fmaf(x, v.w, sum[i][g * 4 + 3]);
                             }
                         }
                 }
             };
             if (edge) add(std::true_type());
             else add(std::false_type());
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < NG * 4; ++j) acc[i][j] = fmaf(acc[i][j], al[i], sum[i][j]);
         }
         const int64_t part = (int64_t)blockIdx.x * 2 + pc.side();
 #pragma unroll
