@@ -197,9 +197,9 @@ int prompt_args(const gdn_spec_kv_cache *c, int32_t B, int32_t N, int32_t HQ, Pr
     return GDN_SPEC_OK;
 }
 
-int64_t part_rows(const PromptArgs &A) { return (int64_t)A.groups * 2 * A.MT; }
+int64_t part_rows(const PromptArgs &A) { return (int64_t)A.groups * A.waves * 2 * A.MT; }
 int64_t workspace_bytes_of(const PromptArgs &A) {
-    return part_rows(A) * ((int64_t)A.C.D * 4 + 8) + (int64_t)A.groups * sizeof(PromptCut);
+    return part_rows(A) * ((int64_t)A.C.D * 4 + 8) + (int64_t)A.groups * A.waves * sizeof(PromptCut);
 }
 
 }  // namespace

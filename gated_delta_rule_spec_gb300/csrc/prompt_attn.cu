@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
 
     prompt_dead_tokens<float>(A, tid, kPromptThreads);
     const PromptPlan plan = prompt_plan<kPromptThreads>(A, &scratch);
-    PromptWalk walk(A, plan);
-    if (tid == 0) prompt_note(A, walk, plan.chunk);
+    PromptWalk walk(A, plan, 0);   // (one wave: the keys and values are not what bounds it)
+    if (tid == 0) prompt_note(A, walk, plan.chunk, 0);
     PromptPiece pc;
     while (walk.next(A, &pc)) {
         const PromptItem &it = pc.it;
@@ -269,8 +269,9 @@ __global__ void __launch_bounds__(kPromptJoinThreads) prompt_join_kernel(const _
 }
 
 cudaError_t launch_prompt_join(const PromptArgs &A, bool bf16, cudaStream_t stream) {
-    if (A.groups < 2) return cudaSuccess;
-    const dim3 grid(A.groups - 1, 8);
+    const int chunks = A.groups * A.waves;
+    if (chunks < 2) return cudaSuccess;
+    const dim3 grid(chunks - 1, A.waves > 1 ? 4 : 8);   // (most cuts of many are one of a few pieces' item)
     return bf16 ? launch_dependent(prompt_join_kernel<__nv_bfloat16>, grid, dim3(kPromptJoinThreads), 0, stream, A)
                 : launch_dependent(prompt_join_kernel<float>, grid, dim3(kPromptJoinThreads), 0, stream, A);
 }
@@ -294,6 +295,7 @@ void prompt_attn_cut(PromptArgs *A, int sms) {
     A->GS = (A->G + A->HS - 1) / A->HS;
     A->tokens = A->MT / A->GS;
     A->groups = sms * prompt_blocks(A->C.D);
+    A->waves = 1;
     A->gap = kPromptTile;
 }
 

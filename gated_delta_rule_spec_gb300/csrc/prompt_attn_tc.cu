@@ -88,7 +88,7 @@ struct __align__(16) PieceInfo {
     int slot, len, cnt, first;            // the row: its slot, committed tokens, tokens, and the first of them
     int h, part, q0, keys;                // as in PromptItem
     int tiles, t0, n[2];                  // tiles of the item, the piece's first, tiles that each stream takes
-    int units, all, whole, pad;           // tiles of the piece (0: there is none), keys that all its rows see, whether it is the item
+    int units, all, whole, chunk;         // tiles of the piece (0: there is none), keys that all its rows see, whether it is the item, the chunk
 };
 
 // Value rows of a piece that one of the cleaners found not finite, from its first key that not all rows see on.
@@ -169,7 +169,7 @@ struct Ring {
 // copies the queries.
 template <int D, bool KEYS, bool VALUES>
 __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *mq, const CUtensorMap *mk,
-                                        const CUtensorMap *mv, Misc *ms, uint32_t base, const PromptWalk &begin) {
+                                        const CUtensorMap *mv, Misc *ms, uint32_t base, const PromptPlan &plan) {
     using L = Lay<D>;
     const int lane = threadIdx.x & 31;
     const int log_br = min(A.C.logP, 7), BR = 1 << log_br;     // tokens of a box: within a page and within a tile
@@ -180,7 +180,13 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
     uint32_t issued[2] = {0, 0};                               // stages of values, of keys
     uint32_t q_issued = 0, q_any = 0;                          // bit of a stream: parity of its query tiles, whether there was one
     bool ok = true;
-    PromptWalk walk = begin;
+    int wave = 0;
+    PromptWalk walk;
+    if (KEYS) {
+        walk = PromptWalk(A, plan, 0);
+        if (ptx::elect_one()) prompt_note(A, walk, plan.chunk, 0);
+        __syncwarp();
+    }
     PromptPiece pc;
     PieceReader reader;                                        // (of the values' warp)
     uint32_t at = 0, ph = 1;                                   // place in the ring of pieces
@@ -201,6 +207,7 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
             }
             info->all = it.len + it.q0 + 1;
             info->whole = pc.whole();
+            info->chunk = wave * A.groups + blockIdx.x;
         }
         if (!wait(ptx::smem_addr(&ms->piece_empty[at]), ph, &ms->abort)) return false;
         if (ptx::elect_one()) {
@@ -265,6 +272,12 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
         bool any;
         if (KEYS) {
             any = walk.next(A, &pc);
+            while (!any && wave + 1 < A.waves) {   // the block's next chunk
+                walk = PromptWalk(A, plan, ++wave);
+                if (ptx::elect_one()) prompt_note(A, walk, plan.chunk, wave);
+                __syncwarp();
+                any = walk.next(A, &pc);
+            }
             ok = describe(any, &sp);
         } else {
             any = reader.next(ms, Bars{ptx::smem_addr(ms)}, &sp, &ok);
@@ -318,6 +331,11 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
                 for (int p = 0; ok && p < L::kParts; ++p) ok = stage(v_ring, std::false_type(), p, row, boxes);
         }
     }
+    if (KEYS)   // (a walk that was broken off leaves its later chunks to be found empty)
+        for (++wave; wave < A.waves; ++wave) {
+            if (ptx::elect_one()) prompt_note(A, PromptWalk(), 1, wave);
+            __syncwarp();
+        }
     if (!ok) {   // copies in flight land before the block's shared memory goes away
         for (uint32_t p = issued[1] > L::NK ? issued[1] - L::NK : 0; p < issued[1]; ++p)
             ptx::mbar_wait(ptx::smem_addr(&ms->full[p % L::NK]), (p / L::NK) & 1u);
@@ -768,7 +786,7 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
         const bool on = tid < RT && it.q0 + own < it.cnt && g < A.G;
         const int64_t row = ((int64_t)it.first + it.q0 + own) * A.HQ + it.h * A.G + g;
         const bool whole = it.whole != 0;
-        const int64_t part = (int64_t)blockIdx.x * 2 + (it.t0 == 0);
+        const int64_t part = (int64_t)it.chunk * 2 + (it.t0 == 0);
         const int see = on ? sp.all + own : 0;                 // keys that the row sees
         const int see_all = sp.all + s * tq;                   // that every row of the stream sees
         const bool warp_on = __any_sync(0xffffffffu, on);
@@ -955,9 +973,7 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         grid_dep_wait();
         if (tid == 0) {
             atomicOr(A.C.status, GDN_SPEC_ST_TIMEOUT);
-            PromptCut none;
-            none.item.b = -1;
-            A.cuts[blockIdx.x] = none;   // the join finds an empty chunk
+            for (int w = 0; w < A.waves; ++w) prompt_note(A, PromptWalk(), 1, w);   // the join finds empty chunks
         }
         return;
     }
@@ -1007,12 +1023,9 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     } else {
         const int role = warp - L::NS * 4;
         if (role == 0) {
-            const PromptWalk begin(A, plan);
-            if (ptx::elect_one()) prompt_note(A, begin, plan.chunk);
-            __syncwarp();
-            produce<D, true, L::kProducers == 1>(A, &mq, &mk, &mv, ms, base, begin);
+            produce<D, true, L::kProducers == 1>(A, &mq, &mk, &mv, ms, base, plan);
         } else if (L::kProducers == 2 && role == 4) {
-            produce<D, false, true>(A, &mq, &mk, &mv, ms, base, PromptWalk());
+            produce<D, false, true>(A, &mq, &mk, &mv, ms, base, plan);
         } else if (role == 3) {
             clean<D>(A, ms, sm, 0);
         } else if (L::NS == 2) {
@@ -1080,6 +1093,10 @@ void prompt_attn_tc_cut(PromptArgs *A, int sms) {
     A->k_whole = A->C.P >= pat::kTile && A->C.D % 64 == 0 && A->C.D != 192;
     A->v_whole = A->C.P >= pat::kTile / (A->C.D > 128 ? 2 : 1) && A->C.D % 64 == 0 && A->C.D != 192;
     A->groups = sms;
+    // several waves where a layer of the pool is more than one wave's, and rows have blocks enough to read it again
+    const int64_t pool = (int64_t)A->C.num_pages * A->C.P * A->C.HKV * A->C.D * 4;
+    const int64_t waves = pool / kPromptWaveBytes + 1;
+    A->waves = A->N < 2 * (int64_t)A->tokens * A->B ? 1 : waves < kPromptWaves ? (int)waves : kPromptWaves;
     A->gap = (streams == 2 ? 3 : 4) * pat::kTile;
 }
 

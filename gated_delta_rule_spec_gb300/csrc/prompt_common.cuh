@@ -11,10 +11,13 @@
 // Items stand in one line, rows first, then heads, then blocks; an item's length is its keys
 // plus `gap`, what it costs besides them, so a row's part of the line is an arithmetic
 // series and both directions (the place where item i starts, the item at a place) are
-// closed forms.  The line is cut into equal chunks, one for each block of the grid, which
-// finds its own from the counts on the device.  So one long prompt, many short ones and
+// closed forms.  The line is cut into equal chunks, `waves` of them for each block of the grid,
+// which finds its own from the counts on the device.  So one long prompt, many short ones and
 // single tokens behind long contexts all spread evenly over the machine, and nothing
-// about the lengths is known on the host.  A cut inside an item falls on a key tile and
+// about the lengths is known on the host.  Chunk w * groups + g is block g's in wave w: where all
+// rows' keys and values are more than L2 holds, the blocks go through them together, a part that
+// L2 holds at a time (4 prompts of 1024 tokens behind 30000, 64 heads on 8 of 128, 400 MB: 10.0 GB
+// read from HBM in one wave, @@ in eight).  A cut inside an item falls on a key tile and
 // leaves unnormalised pieces in the workspace (at most two a chunk), which the join
 // kernel merges in order: the result does not depend on timing.
 #pragma once
@@ -32,11 +35,11 @@ struct PromptArgs {
     const void *q;
     void *out;
     float *lse;
-    float4 *part_o;            // [groups][2][D / 4][MT] unnormalised sums of a piece
-    float2 *part_ml;           // [groups][2][MT] (maximum in log2 units, sum)
-    struct PromptCut *cuts;    // [groups] where each chunk starts, for the join
+    float4 *part_o;            // [chunks][2][D / 4][MT] unnormalised sums of a piece
+    float2 *part_ml;           // [chunks][2][MT] (maximum in log2 units, sum)
+    struct PromptCut *cuts;    // [chunks] where each chunk starts, for the join
     int log_tn, MT, tokens;    // keys of a tile (2^log_tn); rows and tokens of a block
-    int groups, gap;
+    int groups, waves, gap;    // blocks; chunks of a block at most
     bool k_whole, v_whole;     // tensor-core kernel: one copy holds all dims of a stage
     uint32_t wait_limit;
 };
@@ -109,15 +112,19 @@ struct __align__(16) PromptCut {
     int64_t chunk;
 };
 
-struct PromptPlan {
-    int64_t total, chunk;      // length of the line and of a chunk
-    int b;                     // the row at the chunk's start (-1: past the end)
-    int64_t off;               // and the place in the row's part
-};
+constexpr int kPromptWaves = 4;                 // at most
+constexpr int64_t kPromptWaveBytes = 96 << 20;  // keys and values of a wave, of rows with several blocks
+constexpr int kPromptWaveKeys = 2048;           // of a chunk at least, where there are several of a block
 
 struct PromptScratch {
-    int64_t sums[32], off;
-    int b;
+    int64_t sums[32];
+    int64_t off[kPromptWaves];   // where the block's chunks start: the place in the row's part
+    int b[kPromptWaves];         // and the row (-1: past the end)
+};
+
+struct PromptPlan {
+    int64_t total, chunk;      // length of the line and of a chunk
+    const PromptScratch *at;   // the chunks' starts
 };
 
 // Sum over the block of x; *before: of the threads below.
@@ -144,14 +151,15 @@ __device__ __forceinline__ int64_t prompt_scan(int64_t x, PromptScratch *sc, int
     return sum;
 }
 
-// By all threads of a block: the line's length and the row at place blockIdx.x * chunk.
+// By all threads of a block: the line's length, and the rows at which its chunks start.
 // The grid's first block records the rows' status bits.
 template <int THREADS>
 __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScratch *sc) {
     PromptPlan p;
     const int tid = threadIdx.x;
     p.total = 0;
-    int64_t mine = 0, before = 0;   // of the first THREADS rows
+    p.at = sc;
+    int64_t mine = 0, before = 0, keys = 0;   // of the first THREADS rows; of this thread's rows
 #pragma unroll 1
     for (int b0 = 0; b0 < A.B; b0 += THREADS) {
         int64_t x = 0, ex;
@@ -160,44 +168,52 @@ __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScr
             const PromptRow r = prompt_row(A, b0 + tid, &bits);
             if (bits && blockIdx.x == 0) atomicOr(A.C.status, bits);
             x = prompt_span(A, r);
+            if (r.cnt > 2 * A.tokens) keys += r.len + r.cnt;
         }
         const int64_t sum = prompt_scan<THREADS>(x, sc, &ex);
         if (b0 == 0) { mine = x; before = ex; }
         p.total += sum;
     }
+    int64_t waves = 1;
+    if (A.waves > 1) {
+        int64_t ex;
+        keys = prompt_scan<THREADS>(keys, sc, &ex);
+        waves = min((int64_t)A.waves, keys * A.C.HKV * A.C.D * 4 / kPromptWaveBytes + 1);   // (16-bit keys and values)
+    }
     // a chunk is a tile at least, so that cuts inside an item fall on different tiles
-    p.chunk = max((int64_t)1 << A.log_tn, (p.total + A.groups - 1) / A.groups);
-    const int64_t at = (int64_t)blockIdx.x * p.chunk;
-    if (tid == 0) sc->b = -1;
+    p.chunk = (p.total + A.groups - 1) / A.groups;
+    if (waves > 1) p.chunk = max((p.total + A.groups * waves - 1) / (A.groups * waves), min(p.chunk, (int64_t)kPromptWaveKeys));
+    p.chunk = max((int64_t)1 << A.log_tn, p.chunk);
+    if (tid < kPromptWaves) sc->b[tid] = -1;
     __syncthreads();
-    if (at < p.total) {
-        int64_t base = 0;
+    int64_t base = 0;
 #pragma unroll 1
-        for (int b0 = 0; b0 < A.B; b0 += THREADS) {
-            int64_t x = mine, ex = before;
-            if (b0 > 0) {
-                x = 0;
-                if (b0 + tid < A.B) {
-                    uint32_t bits;
-                    x = prompt_span(A, prompt_row(A, b0 + tid, &bits));
-                }
+    for (int b0 = 0; b0 < A.B; b0 += THREADS) {
+        int64_t x = mine, ex = before;
+        if (b0 > 0) {
+            x = 0;
+            if (b0 + tid < A.B) {
+                uint32_t bits;
+                x = prompt_span(A, prompt_row(A, b0 + tid, &bits));
             }
-            int64_t sum = 0;
-            if (A.B > THREADS) {
-                int64_t e2;
-                sum = prompt_scan<THREADS>(x, sc, &e2);
-                ex = e2;
-            }
-            if (x > 0 && base + ex <= at && at < base + ex + x) {
-                sc->b = b0 + tid;
-                sc->off = at - base - ex;
-            }
-            base += sum;
         }
+        int64_t sum = 0;
+        if (A.B > THREADS) {
+            int64_t e2;
+            sum = prompt_scan<THREADS>(x, sc, &e2);
+            ex = e2;
+        }
+#pragma unroll 1
+        for (int w = 0; w < A.waves; ++w) {
+            const int64_t at = ((int64_t)w * A.groups + blockIdx.x) * p.chunk;
+            if (x > 0 && base + ex <= at && at < base + ex + x) {
+                sc->b[w] = b0 + tid;
+                sc->off[w] = at - base - ex;
+            }
+        }
+        base += sum;
     }
     __syncthreads();
-    p.b = sc->b;
-    p.off = sc->off;
     return p;
 }
 
@@ -232,19 +248,21 @@ struct PromptWalk {
         it.tiles = (it.keys + (1 << A.log_tn) - 1) >> A.log_tn;
     }
     __device__ __forceinline__ PromptWalk() : live(false) {}
-    __device__ __forceinline__ PromptWalk(const PromptArgs &A, const PromptPlan &p) {
-        live = p.b >= 0;
+    // Through the block's chunk of wave w.
+    __device__ __forceinline__ PromptWalk(const PromptArgs &A, const PromptPlan &p, int w) {
+        live = p.at->b[w] >= 0;
         if (!live) return;
-        start = (int64_t)blockIdx.x * p.chunk;
+        start = ((int64_t)w * A.groups + blockIdx.x) * p.chunk;
         end = min(p.total, start + p.chunk);
-        it.b = p.b;
+        it.b = p.at->b[w];
         uint32_t bits;
-        const PromptRow r = prompt_row(A, p.b, &bits);
+        const PromptRow r = prompt_row(A, it.b, &bits);
         it.slot = r.slot, it.len = r.len, it.cnt = r.cnt, it.first = r.first;
         const PromptLine line(A, r);
+        const int64_t off = p.at->off[w];
         blocks = line.blocks;
-        hp = (int)(p.off / line.head);
-        const int64_t in = p.off - hp * line.head;
+        hp = (int)(off / line.head);
+        const int64_t in = off - hp * line.head;
         i = line.at(in);
         it.pos = start - (in - line.before(i));
         set(A);
@@ -279,13 +297,13 @@ struct PromptWalk {
     }
 };
 
-// The chunk's note; by one thread, before the walk begins.
-__device__ __forceinline__ void prompt_note(const PromptArgs &A, const PromptWalk &w, int64_t chunk) {
+// The note of the block's chunk of wave w; by one thread, before the walk begins.
+__device__ __forceinline__ void prompt_note(const PromptArgs &A, const PromptWalk &walk, int64_t chunk, int w) {
     PromptCut c;
-    if (w.live) c.item = w.it;
+    if (walk.live) c.item = walk.it;
     else c.item.b = -1;
     c.chunk = chunk;
-    A.cuts[blockIdx.x] = c;
+    A.cuts[w * A.groups + blockIdx.x] = c;
 }
 
 // Row of the output for row r of an item's block, and whether the row is one.

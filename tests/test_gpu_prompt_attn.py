@@ -116,6 +116,14 @@ def test_one_long_prompt(io, HQ, HKV, D, n):
     Prompts(9, io, HQ, HKV, D, 64, counts=[n], lens=[77], poison=False).check()
 
 
+@pytest.mark.parametrize("HQ,HKV,D,counts,lens", [(8, 8, 256, [300, 1, 290], [13000, 5000, 12000]),
+                                                  (32, 16, 128, [290, 300], [26000, 13000])])
+def test_contexts_larger_than_a_wave(HQ, HKV, D, counts, lens):
+    """Rows of several blocks whose keys and values are more than are gone through at a time (96 MB)."""
+    assert (lens[0] + lens[-1]) * HKV * D * 4 > 96 << 20
+    Prompts(21, "bf16", HQ, HKV, D, 64, counts=counts, lens=lens, poison=False).check()
+
+
 def test_more_rows_than_a_block_scans_and_layers():
     """700 rows of 0 to 6 tokens, the last of three layers."""
     r = np.random.default_rng(10)
