@@ -658,6 +658,8 @@ def _token_stride(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) 
             return st[0]
         if st[0] == st[1] * shape[1]:
             return st[1]
+    if ok and nd == 3 and st[2] == 1 and st[1] == shape[2] and shape[0] > 1:
+        return st[0]
     ok = ok and (shape[-1] == 1 or st[-1] == 1) and (shape[-2] == 1 or st[-2] == shape[-1])
     step, span = None, 1
     for i in range(nd - 3, -1, -1):
@@ -777,10 +779,18 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
 
 # ------------------------------------------------ prompts, packed
 
-def _here(t: torch.Tensor, name: str) -> None:
-    """The calls launch on the current device: a tensor of another one is refused."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise GdnSpecError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _here(**tensors) -> None:
+    """The calls launch on the current device: tensors of another one are refused."""
+    now = None
+    for name, t in tensors.items():
+        if t.is_cuda:
+            now = _current_device() if now is None else now
+            if t.get_device() != now:
+                raise GdnSpecError(f"{name} is on {t.device}, the current device is cuda:{now}")
+
+
+# without the checks of torch.cuda.current_device: a CUDA tensor is there, so CUDA is up
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class HeadNorm:
@@ -793,13 +803,13 @@ class HeadNorm:
             raise GdnSpecError(f"weight: want one dimension, got {tuple(weight.shape)}")
         _need(weight, "weight", torch.float32, (weight.shape[0],))
         self._weight, self._desc = weight, HeadNormDesc(weight.data_ptr(), eps, offset)
-        self._ref = ctypes.byref(self._desc)
+        self._ref, self._D = ctypes.byref(self._desc), weight.shape[0]
 
     # What the calls pass is what was checked.
     weight = property(lambda self: self._weight)
     eps = property(lambda self: self._desc.eps)
     offset = property(lambda self: self._desc.offset)
-    D = property(lambda self: self._weight.shape[0])
+    D = property(lambda self: self._D)
 
     def desc(self) -> HeadNormDesc:
         return self._desc
@@ -808,9 +818,8 @@ class HeadNorm:
 def _norm_of(norm: HeadNorm | None, plan: RopePlan, name: str):
     if norm is None:
         return None
-    if norm.D != plan.D:
+    if norm._D != plan._desc.D:
         raise GdnSpecError(f"{name}: weights of {norm.D} dims for heads of {plan.D}")
-    _here(norm.weight, name)
     return norm._ref
 
 
@@ -823,7 +832,7 @@ def norm_rope(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.Tensor
         raise GdnSpecError(f"x: want bf16 or fp32 [N, heads, {plan.D}], got {x.dtype} {tuple(x.shape)}")
     _need(pos, "pos", torch.int32, (N,))
     xs = _token_stride(x, "x", x.dtype, (N, heads, D))
-    _here(x, "x")
+    _here(x=x, norm=norm._weight)
     if out is None:
         out, os_ = _result((N, heads, D), x.dtype, x.device, stream), heads * D
     else:
@@ -856,7 +865,7 @@ def norm_rope_grad(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.T
     _need(pos, "pos", torch.int32, (N,))
     xs = _token_stride(x, "x", x.dtype, (N, heads, D))
     ys = _token_stride(dy, "dy", x.dtype, (N, heads, D))
-    _here(x, "x")
+    _here(x=x, norm=norm._weight)
     if dx is None:
         dx, ds = _result((N, heads, D), x.dtype, x.device, stream), heads * D
     else:
@@ -894,8 +903,8 @@ def norm_rope_append(plan: RopePlan, cache: KvCache, layer: int, slot_idx: torch
     qs = _token_stride(q, "q", io, (N, HQ, cache.D))
     ks = _token_stride(k, "k", io, kv_shape)
     vs = _token_stride(v, "v", io, kv_shape)
-    _here(q, "q")
-    _here(cache.k, "cache")
+    _here(q=q, cache=cache.k, **{} if q_norm is None else {"q_norm": q_norm._weight},
+          **{} if k_norm is None else {"k_norm": k_norm._weight})
     if pos is not None:
         _need(pos, "pos", torch.int32, (N,))
     if q_out is None:
@@ -937,8 +946,7 @@ def prompt_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, starts: torc
         raise GdnSpecError(f"q: want [N, HQ, D], got {tuple(q.shape)}")
     N, HQ, _ = q.shape
     _need(q, "q", cache.io_torch, (N, HQ, cache.D))
-    _here(q, "q")
-    _here(cache.k, "cache")
+    _here(q=q, cache=cache.k)
     if out is None:
         out = _result(q.shape, q.dtype, q.device, stream)
     else:

@@ -11,8 +11,13 @@
 // take a head, 16 elements each (two runs of 8, a pair's halves in the half layout), so the
 // mean is a shuffle over them and a head is never read twice.  Heads of other than 1, 2, 4, 8
 // or 16 units leave some of the 2^k idle.  Dims that do not come in units of 16 go element by
-// element, a warp a head.
-// Sums are fp32: of 16 elements in a thread, then over the threads.
+// element, a warp a head.  A head's elements are loaded a step ahead, the first ones beside the
+// angles: what a block waits for is covered by its own loads and by the SM's other blocks.
+// 16384 x 16 heads of 128 bf16: 27 us (0.73 of the copy bandwidth), the gradient 46 us (0.64: two
+// sums a head, and 16 running sums of dw a thread leave two blocks an SM); the packed append of 36101
+// tokens of 32 + 2 x 8 heads: 169 us (0.77), with the search for a token's row and its page in each block.
+// Sums are fp32: of 16 elements in a thread, then over the threads; of dw, over a thread's heads, then
+// over threads, warps and blocks, always in the same order.
 #include "launch_setup.cuh"
 #include "prompt_common.cuh"
 #include "rope_common.cuh"
@@ -21,7 +26,7 @@ namespace gdnspec {
 
 constexpr int kNormThreads = kRopeThreads;
 constexpr int kNormEntries = 8;   // elements or pairs of a head that a lane of its warp takes at most
-constexpr int kNormBlocks = 4;    // of an SM: with six the append spills (45000 tokens of 32 + 2 x 8 heads: 226 us, 168 with four)
+constexpr int kNormBlocks = 4;    // of an SM: with six the append spills (36101 tokens of 32 + 2 x 8 heads: 226 us, 168 with four)
 
 // Threads that share a head of `units` units of 16 elements: the next power of two.
 __host__ __device__ inline int head_lanes(int units) {

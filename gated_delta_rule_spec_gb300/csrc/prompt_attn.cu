@@ -10,9 +10,10 @@
 // (four where D > 128) with four keys, then, with the probabilities in shared memory where the keys
 // were, the sums of the same rows over DP / 16 columns; sixteen threads share the rows.  The
 // values are copied while the scores are formed, two blocks an SM cover the rest.  2 prompts of
-// 1000 tokens behind 1000, 8 heads on 2 of 128: 300 us, 38 TFLOP/s, half of the fp32 rate (345 us
-// with four rows a thread); heads of 256, 600 tokens: 328 us, 36 TFLOP/s.  A wide read of shared memory feeds
-// 10 to 16 multiply-adds, which bounds it.
+// 1000 tokens behind 1000, 8 heads on 2 of 128: 313 us, 36 TFLOP/s, nearly half of the fp32 rate (345
+// us with four rows a thread); heads of 256, 600 tokens: 339 us, 34 TFLOP/s.  A wide read of shared
+// memory feeds 10 to 16 multiply-adds, which bounds it.  Sums are of 64 terms, and of such sums: with one
+// chain a row of 8267 keys was off by 1.1e-6 of itself, by 3.7e-7 so.
 #include "launch_setup.cuh"
 #include "prompt_common.cuh"
 
@@ -105,7 +106,6 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
             look_up(t + 1);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
-            // Sums of 64 terms, and of such sums: one chain over a long row would lose bits (below, too).
             float s[RT][4] = {};
 #pragma unroll 1
             for (int d0 = 0; d0 < DP; d0 += 64) {

@@ -12,27 +12,42 @@
 // D = 256: one stream, whose O takes half of TMEM, with its scores in two buffers, so that
 // the next tile's scores are formed while a softmax runs.
 //
-// One warp copies the pages' rows by TMA into one ring of 32 KB stages, one issues all
-// products, and two look through the values (below).  Products that one thread issues run in
-// order, so a stream's next scores may be issued right behind the sums that read the
-// probabilities in the same columns, without a wait between them.
+// Warps of their own copy the pages' rows by TMA into rings of stages (and walk and describe
+// the pieces to the others), issue the products, and look through the values
+// (below).  With two streams a warp issues all products of one: they run in order, so a
+// stream's next scores are issued right behind the sums that read the probabilities in the same
+// columns, without a wait between them.
+//
+// What bounds it is a stream's round: softmax, 950 cycles at best (MUFU: 512 for the
+// exponentials), sums and scores, 1024, and four hand-overs through barriers.  Two streams
+// fill the tensor core to 72% that way (4 x 1024 tokens behind 30000, 16 heads on 2 of 128: 525 us,
+// 1.6 PFLOP/s; 8192 tokens, 32 on 8 of 128: 374 us, 1.47; heads of 64, where a round
+// multiplies half as much: 456 us, 0.93 PFLOP/s).  What led there, first case: 770 us; scores in quarters
+// and walkers out of line, so that the loops stay in the instruction cache (a kernel of 170 KB
+// of code waited for instructions a third of the softmax's time): 600; pieces described once: 554;
+// probabilities in one pass against the maximum so far: 525.  Not faster: waiting by looking
+// at a barrier in a loop (13% slower: it takes the softmax's issue slots); one warp for both
+// streams' products (600 us as it stood then); both streams issuing at will (607); for D = 256 pairs of
+// blocks that share tiles by multicast.  D = 256: 16384 + 10308 tokens, 16 heads on 2: 1960 to
+// 2010 us, 1.55 PFLOP/s.
 //
 // The running maximum is only moved when a row's maximum has grown by more than 2^8 over
 // it, an idea published for attention kernels of this generation: until then the
 // probabilities are taken against the old one, which is exact (they and their sum stay below 2^8
 // times as large, far inside fp32 and bf16's range), and O is not read and rescaled.  P is
 // rounded to bf16 because it is an operand of the second product; m, l and O are fp32, and
-// l is the sum of the values before that rounding, so that lse keeps fp32's accuracy.
+// l is the sum of the values before that rounding, so that lse keeps fp32's accuracy (out is
+// off by 0.0020 to 0.0023 of itself against 64 bits, its own rounding alone is 0.0017).
 //
 // Rows of a tile past the last token hold whatever the page or the buffer held, and a token
 // behind the one that asks may hold anything; 0 times NaN is not 0.  So in the tiles
-// that not every row of the block sees whole, two warps look for value rows that are
-// not finite, before the products get the tile, and zero them; the terms of those that
+// that not every row of the block sees whole, a warp looks for value rows that are
+// not finite, before the products get the tile, and zeroes them; the terms of those that
 // some rows see are added to these rows at the end.
 //
 // Every wait is bounded.  One that runs out raises the block's abort flag, on which all
-// roles leave their loops; the producer then waits for the copies it has in flight and
-// the MMA warp for its MMAs, TMEM is freed, and the status word gets TIMEOUT.
+// roles leave their loops; the producers then wait for the copies they have in flight and
+// the MMA warps for their MMAs, TMEM is freed, and the status word gets TIMEOUT.
 #include <cstddef>
 #include <type_traits>
 
@@ -57,7 +72,6 @@ constexpr int kLogTile = 7, kTile = 1 << kLogTile;   // keys of a tile
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemMax = 232448;
 constexpr int kMaxStages = 10;
-constexpr int kCleaners = 1;             // warps that look through values
 constexpr int kNotes = 4;                // pieces whose rows that are not finite are kept
 constexpr int kPieces = 4;               // pieces that are described at a time
 
@@ -91,7 +105,7 @@ struct __align__(16) PieceInfo {
     int units, all, whole, chunk;         // tiles of the piece (0: there is none), keys that all its rows see, whether it is the item, the chunk
 };
 
-// Value rows of a piece that one of the cleaners found not finite, from its first key that not all rows see on.
+// Value rows of a piece that are not finite, from its first key that not all rows see on.
 struct Note {
     int piece;                            // the piece's number; another one's: there are none
     unsigned long long rows[4];
@@ -103,7 +117,7 @@ struct Misc {
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], pv_done[2], turn[2], drain[2];
     PieceInfo pieces[kPieces];
-    Note notes[kCleaners][kNotes];
+    Note notes[kNotes];
     int done[8];                          // pieces that a warp of the softmax is done with
     PromptScratch scratch;
     uint32_t tmem;
@@ -160,7 +174,7 @@ struct Ring {
     }
 };
 
-// ------------------------------------------------------------------ producer warp
+// ------------------------------------------------------------------ producer warps
 
 // One lane issues: a copy's operands are uniform registers.  The lanes look up the pages of a tile's boxes side by side.
 // With two streams one warp copies keys and values of each tile in turn; with one, whose rings hold little more than a
@@ -347,7 +361,7 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
     }
 }
 
-// ------------------------------------------------------------------ MMA warp
+// ------------------------------------------------------------------ MMA warps
 
 // A place in the sequence of tiles, piece after piece: tile u of a piece's `units`, of which stream s takes n.
 struct Cursor {
@@ -596,16 +610,15 @@ __device__ __forceinline__ void multiply_sums(const PromptArgs &A, Misc *ms, uin
     if (!ok) drain(bars, 1);
 }
 
-// ------------------------------------------------------------------ cleaners
+// ------------------------------------------------------------------ cleaner
 
 // Eight rows of a stage of values, the first `row` of it and `key` of the piece, of which those in `any` (four bits each) are
 // not finite: the ones that not every row sees (keys from `all` on) become zeros, and the piece's own are noted.
 template <int D>
-__device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, int all, int keys, unsigned any, int piece,
-                                    int who) {
+__device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, int all, int keys, unsigned any, int piece) {
     using L = Lay<D>;
     const int lane = threadIdx.x & 31;
-    Note *const note = &ms->notes[who][piece % kNotes];
+    Note *const note = &ms->notes[piece % kNotes];
     if (note->piece != piece) {   // the place held an earlier piece's: all are done with it
         const volatile int *done = ms->done;
         for (int w = 0; w < L::NS * 4; ++w)
@@ -632,12 +645,11 @@ __device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, i
     return true;
 }
 
-// Warp `who` of two looks at half of the tokens of every stage of values: where the tile holds keys that some row does not
-// see, rows that are not finite become zeros, and those of the piece's own keys are noted.
+// Looks at every stage of values: where the tile holds keys that some row does not see, rows that are not finite become
+// zeros, and those of the piece's own keys are noted.
 template <int D>
-__device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm, int who) {
+__device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm) {
     using L = Lay<D>;
-    constexpr int kRowsHere = L::kVRows / kCleaners;
     const int lane = threadIdx.x & 31;
     const Bars bars{ptx::smem_addr(ms)};
     Ring<D, false> ring;
@@ -652,16 +664,15 @@ __device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm
                 ok = wait(bars.full(ring.at), ring.ph, &ms->abort, A.wait_limit);
                 if (ok && k0 + kTile > sp.all) {
                     uint8_t *tile = sm + L::kOffKV + ring.at * L::kStage;
-                    const int row0 = who * kRowsHere;                       // of the stage
-                    const int key0 = k0 + part * L::kVRows + row0;          // its key
+                    const int key0 = k0 + part * L::kVRows;                 // the stage's first key
 #pragma unroll 1
-                    for (int r = 0; ok && r < kRowsHere; r += 8) {
+                    for (int r = 0; ok && r < L::kVRows; r += 8) {
                         if (key0 + r + 8 <= sp.all) continue;
                         // four lanes a row, each 16 of its bytes at a time; odd rows begin with their second half, so that
                         // two rows' pieces fall in different banks
                         __nv_bfloat162 acc = __float2bfloat162_rn(0.0f);
                         const __nv_bfloat162 zero = acc;
-                        const uint8_t *row = tile + (row0 + r + (lane >> 2)) * 128;
+                        const uint8_t *row = tile + (r + (lane >> 2)) * 128;
 #pragma unroll
                         for (int b = 0; b < (int)L::kVBlocks; ++b)
 #pragma unroll
@@ -674,7 +685,7 @@ __device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm
                                     acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), zero, acc);
                             }
                         const unsigned any = __ballot_sync(0xffffffffu, __hisnan(acc.x) || __hisnan(acc.y));
-                        if (any) ok = remove<D>(ms, tile, row0 + r, key0 + r, sp.all, sp.keys, any, piece, who);
+                        if (any) ok = remove<D>(ms, tile, r, key0 + r, sp.all, sp.keys, any, piece);
                     }
                     ptx::fence_proxy_async_smem();
                 }
@@ -694,11 +705,8 @@ __device__ __noinline__ void add_removed(const PromptArgs &A, const Misc *ms, in
                                          int64_t qrow, float m, int d0, int dims, float *o) {
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(A.q) + qrow * A.C.D;
     for (int i = 0; i < own; ++i) {
-        bool there = false;
-        for (int w = 0; w < kCleaners; ++w) {
-            const Note &note = ms->notes[w][piece % kNotes];
-            there |= note.piece == piece && ((note.rows[i >> 6] >> (i & 63)) & 1);
-        }
+        const Note &note = ms->notes[piece % kNotes];
+        const bool there = note.piece == piece && ((note.rows[i >> 6] >> (i & 63)) & 1);
         if (!there) continue;
         const int64_t row = kv_token_row(A.C, it.slot, all + i);
         if (row < 0) continue;
@@ -899,9 +907,7 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
             ++outs;
             ptx::tc_fence_after_sync();
             if (warp_on) {
-                bool removed = false;
-                for (int w = 0; w < kCleaners; ++w)
-                    removed |= *(volatile int *)&ms->notes[w][piece % kNotes].piece == piece;
+                const bool removed = *(volatile int *)&ms->notes[piece % kNotes].piece == piece;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
                 for (int d0 = 0; d0 < A.C.D; d0 += 32) {
@@ -982,11 +988,11 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         for (int i = 0; i < L::NST; ++i) {
             init(ms->full[i], 1);
             init(ms->empty[i], L::NS);   // warps that use the stage
-            init(ms->clean[i], kCleaners);
+            init(ms->clean[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             init(ms->piece_full[i], 1);
-            init(ms->piece_empty[i], L::NS * 4 + 2 + kCleaners + L::kProducers - 1);   // warps that read it
+            init(ms->piece_empty[i], L::NS * 4 + 2 + L::kProducers);   // warps that read it
         }
         for (int i = 0; i < 2; ++i) {
             init(ms->q_full[i], 1);
@@ -999,8 +1005,7 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             init(ms->turn[i], 1);
             init(ms->drain[i], 1);
         }
-        for (int w = 0; w < kCleaners; ++w)
-            for (int i = 0; i < kNotes; ++i) ms->notes[w][i].piece = -1;
+        for (int i = 0; i < kNotes; ++i) ms->notes[i].piece = -1;
         for (int i = 0; i < 8; ++i) ms->done[i] = 0;
         ms->abort = 0;
         ptx::mbar_init_fence();
@@ -1027,7 +1032,7 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         } else if (L::kProducers == 2 && role == 4) {
             produce<D, false, true>(A, &mq, &mk, &mv, ms, base, plan);
         } else if (role == 3) {
-            clean<D>(A, ms, sm, 0);
+            clean<D>(A, ms, sm);
         } else if (L::NS == 2) {
             multiply_stream<D>(A, ms, base, tmem, role - 1);
         } else if (role == 1) {

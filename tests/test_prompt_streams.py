@@ -42,6 +42,6 @@ def test_another_device_is_refused(monkeypatch):
         def get_device(self):
             return 1
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    with pytest.raises(binding.GdnSpecError, match="cuda:1"):
-        binding._here(Elsewhere(), "x")
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    with pytest.raises(binding.GdnSpecError, match="x is on cuda:1"):
+        binding._here(x=Elsewhere())
