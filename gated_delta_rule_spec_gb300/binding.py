@@ -820,6 +820,7 @@ def _norm_of(norm: HeadNorm | None, plan: RopePlan, name: str):
         return None
     if norm._D != plan._desc.D:
         raise GdnSpecError(f"{name}: weights of {norm.D} dims for heads of {plan.D}")
+    norm._desc.weight = norm._weight.data_ptr()          # a parameter's memory may have been replaced
     return norm._ref
 
 

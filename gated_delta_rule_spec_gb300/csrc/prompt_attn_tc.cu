@@ -721,10 +721,11 @@ __device__ __noinline__ void add_removed(const PromptArgs &A, const Misc *ms, in
     }
 }
 
-// Scores of a tile that the row does not see, all but the first `lim`, are set to -inf where they lie.
+// Scores of a tile that the row does not see, all but the first `lim`, are set to -inf where they lie.  By a whole warp, from
+// the first columns on that some row does not see.
 __device__ __noinline__ void cut_scores(uint32_t s_addr, int lim) {
 #pragma unroll 1
-    for (int y = 0; y < kTile; y += 16) {
+    for (int y = max(0, __reduce_min_sync(0xffffffffu, lim)) & ~15; y < kTile; y += 16) {
         uint32_t sc[16];
         ptx::tmem_ld16_bits(s_addr + y, sc);
         landed(sc);
@@ -786,8 +787,8 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
     const int own = s * tq + tid / A.GS;                       // the row's token of the block
     const int head = tid - (own - s * tq) * A.GS;              // and head of the group's part
     PieceReader reader;
-    PieceInfo it;
-    for (; ok && reader.next(ms, bars, &it, &ok); ++piece) {
+    PieceInfo it, next;
+    for (bool any = reader.next(ms, bars, &it, &ok); any; it = next, ++piece) {
         const PieceInfo &sp = it;
         const int n = s ? it.n[1] : it.n[0];
         const int g = it.part * A.GS + head;
@@ -795,7 +796,7 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
         const int64_t row = ((int64_t)it.first + it.q0 + own) * A.HQ + it.h * A.G + g;
         const bool whole = it.whole != 0;
         const int64_t part = (int64_t)it.chunk * 2 + (it.t0 == 0);
-        const int see = on ? sp.all + own : 0;                 // keys that the row sees
+        const int see = on ? sp.all + own : INT32_MAX;         // keys that the row sees (no row: whatever there is)
         const int see_all = sp.all + s * tq;                   // that every row of the stream sees
         const bool warp_on = __any_sync(0xffffffffu, on);
         float m = -INFINITY, l = 0.0f;
@@ -851,7 +852,7 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                         s0 += s1;
                     }
                 }
-                if (move) {   // a piece's first tile, or one whose maximum is to be moved: in two passes
+                if (move) {   // the maximum is to be moved: in two passes
                     uint32_t sc[32];
 #pragma unroll 1
                     for (int y = 0; y < kTile; y += 32) {
@@ -901,6 +902,8 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
             }
         }
         if (!ok) break;
+        any = reader.next(ms, bars, &next, &ok);   // (while the last sums run)
+        if (!ok) break;
         if (n > 0) {
             ok = wait(bars.o_full(s), outs & 1u, &ms->abort);
             if (!ok) break;
@@ -911,27 +914,25 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
                 for (int d0 = 0; d0 < A.C.D; d0 += 32) {
-                    const int dims = min(32, A.C.D - d0);
                     uint32_t u[32];
                     ptx::tmem_ld32_bits(lane_addr + L::col_o(s) + d0, u);
                     landed(u);
-                    float f[32];
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) f[y] = __uint_as_float(u[y]);
+                    const int dims = min(32, A.C.D - d0);
                     if (!on) continue;
-                    if (removed) {   // rare: a copy of its own, so that f stays in registers
+                    if (removed) {   // rare: a copy of its own, so that u stays in registers
                         float g[32];
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) g[y] = f[y];
+                        for (int y = 0; y < 32; ++y) g[y] = __uint_as_float(u[y]);
                         add_removed(A, ms, piece, it, sp.all, own, row, m, d0, dims, g);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) f[y] = g[y];
+                        for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(g[y]);
                     }
+                    const auto f = [&](int y) { return __uint_as_float(u[y]); };
                     if (whole) {
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(A.out) + row * A.C.D + d0;
                         uint32_t w[16];
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) w[y] = pack_bf16(f[2 * y] * inv, f[2 * y + 1] * inv);
+                        for (int y = 0; y < 16; ++y) w[y] = pack_bf16(f(2 * y) * inv, f(2 * y + 1) * inv);
                         if (wide && dims == 32) {
                             store32(out, w);
                             store32(out + 16, w + 8);
@@ -945,7 +946,7 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
                         float4 *po = A.part_o + (part * (A.C.D / 4) + d0 / 4) * A.MT + my_row;
 #pragma unroll
                         for (int y = 0; y < 32; y += 4)
-                            if (y < dims) po[(int64_t)(y / 4) * A.MT] = make_float4(f[y], f[y + 1], f[y + 2], f[y + 3]);
+                            if (y < dims) po[(int64_t)(y / 4) * A.MT] = make_float4(f(y), f(y + 1), f(y + 2), f(y + 3));
                     }
                 }
             }

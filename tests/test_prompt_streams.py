@@ -45,3 +45,14 @@ def test_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(binding, "_current_device", lambda: 0)
     with pytest.raises(binding.GdnSpecError, match="x is on cuda:1"):
         binding._here(x=Elsewhere())
+
+
+def test_a_norms_weights_may_move(monkeypatch):
+    """A parameter whose memory is replaced (as by loading or moving a model): the next call reads the new one."""
+    plan = binding.RopePlan(64)
+    Watch(monkeypatch)
+    w = torch.zeros(64)
+    norm = binding.HeadNorm(w)
+    w.data = torch.ones(64)
+    binding._norm_of(norm, plan, "norm")
+    assert norm.desc().weight == w.data_ptr()
