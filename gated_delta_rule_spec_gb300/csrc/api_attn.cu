@@ -2,6 +2,7 @@
 // step (declared and documented in include/gdn_spec.h): host-side checks, the rotary
 // plan, kernel selection and stream-ordered launches.  Nothing here allocates,
 // frees or synchronises, except gdn_spec_kv_read_status.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -112,7 +113,8 @@ int check_plan(const gdn_spec_rope_plan *p) {
 }
 
 int check_norm(const gdn_spec_head_norm *n) {
-    if (!n || !n->weight || !(n->eps > 0.0f) || !std::isfinite(n->eps) || !std::isfinite(n->offset)) return GDN_SPEC_EINVAL;
+    // a smaller eps has a reciprocal that is infinite in fp32, and the gradient forms it
+    if (!n || !n->weight || !(n->eps >= FLT_MIN) || !std::isfinite(n->eps) || !std::isfinite(n->offset)) return GDN_SPEC_EINVAL;
     return (reinterpret_cast<uintptr_t>(n->weight) & 3u) ? GDN_SPEC_EALIGN : GDN_SPEC_OK;
 }
 

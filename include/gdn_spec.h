@@ -567,7 +567,7 @@ const char *gdn_spec_tree_attn_path(const gdn_spec_kv_cache *cache, int32_t T, i
 /* The norm of a head x of D dims: x / sqrt(mean(x^2) + eps) * (weight + offset). */
 typedef struct {
     const float *weight;  /* fp32 [D], device                                          */
-    float eps;            /* > 0                                                       */
+    float eps;            /* >= 2^-126, finite                                         */
     float offset;         /* 0; 1 where a model keeps weights around zero              */
 } gdn_spec_head_norm;
 

@@ -92,6 +92,17 @@ def test_norm(lib):
     assert lib.gdn_spec_norm_rope(ref(plan()), None, 0, 4, 0, FAKE, FAKE, 512, FAKE, 512, None) == EINVAL
 
 
+def test_the_smallest_eps(lib):
+    """The gradient forms 1 / (mean(x^2) + eps): for a head of zeros and a small eps that is infinite in fp32, and times zero NaN."""
+    least = 2.0 ** -126
+    assert "eps;            /* >= 2^-126, finite" in open(HEADER).read()
+    assert rotate(lib, w=norm(eps=least)) == OK
+    below = norm(eps=least / 2)
+    assert 0.0 < below.eps < least
+    assert rotate(lib, w=below) == EINVAL and gradient(lib, w=below, N=0) == EINVAL
+    assert append(lib, qn=below) == EINVAL and append(lib, kn=below) == EINVAL
+
+
 def test_rotate_call(lib):
     assert rotate(lib) == OK
     for kw, want in ((dict(N=-1), EINVAL), (dict(heads=0), EINVAL), (dict(io=2), EDTYPE), (dict(xs=511), EINVAL),
