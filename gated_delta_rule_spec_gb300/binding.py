@@ -820,7 +820,8 @@ def _norm_of(norm: HeadNorm | None, plan: RopePlan, name: str):
         return None
     if norm._D != plan._desc.D:
         raise GdnSpecError(f"{name}: weights of {norm.D} dims for heads of {plan.D}")
-    norm._desc.weight = norm._weight.data_ptr()          # a parameter's memory may have been replaced
+    _need(norm._weight, name, torch.float32, (norm._D,))  # a parameter's memory may have been replaced, by another type's too
+    norm._desc.weight = norm._weight.data_ptr()
     return norm._ref
 
 

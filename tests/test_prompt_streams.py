@@ -47,6 +47,22 @@ def test_another_device_is_refused(monkeypatch):
         binding._here(x=Elsewhere())
 
 
+@pytest.mark.parametrize("change", [lambda w: w.to(torch.bfloat16), lambda w: w[:32], lambda w: w.double(), lambda w: w])
+def test_a_norms_weights_are_checked_again(change):
+    """Converting a model replaces a parameter's memory under the norm that holds it."""
+    class Weight(torch.Tensor):
+        is_cuda = True
+
+    plan, w = binding.RopePlan(64), torch.zeros(64).as_subclass(Weight)
+    norm = binding.HeadNorm(w)
+    binding._norm_of(norm, plan, "norm")
+    w.data = change(w.data)
+    if w.dtype == torch.float32 and w.shape == (64,):
+        w.is_cuda = False                                                   # moved to the host
+    with pytest.raises(binding.GdnSpecError, match="norm: want contiguous CUDA torch.float32 \\(64,\\)"):
+        binding._norm_of(norm, plan, "norm")
+
+
 def test_a_norms_weights_may_move(monkeypatch):
     """A parameter whose memory is replaced (as by loading or moving a model): the next call reads the new one."""
     plan = binding.RopePlan(64)
