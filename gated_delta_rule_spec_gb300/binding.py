@@ -780,10 +780,10 @@ def tree_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, q: torch.Tenso
 # ------------------------------------------------ prompts, packed
 
 def _here(**tensors) -> None:
-    """The calls launch on the current device: tensors of another one are refused."""
+    """The calls launch on the current device: tensors of another one are refused (None: not given)."""
     now = None
     for name, t in tensors.items():
-        if t.is_cuda:
+        if t is not None and t.is_cuda:
             now = _current_device() if now is None else now
             if t.get_device() != now:
                 raise GdnSpecError(f"{name} is on {t.device}, the current device is cuda:{now}")
@@ -834,7 +834,7 @@ def norm_rope(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.Tensor
         raise GdnSpecError(f"x: want bf16 or fp32 [N, heads, {plan.D}], got {x.dtype} {tuple(x.shape)}")
     _need(pos, "pos", torch.int32, (N,))
     xs = _token_stride(x, "x", x.dtype, (N, heads, D))
-    _here(x=x, norm=norm._weight)
+    _here(x=x, norm=norm._weight, pos=pos, out=out)
     if out is None:
         out, os_ = _result((N, heads, D), x.dtype, x.device, stream), heads * D
     else:
@@ -867,7 +867,7 @@ def norm_rope_grad(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.T
     _need(pos, "pos", torch.int32, (N,))
     xs = _token_stride(x, "x", x.dtype, (N, heads, D))
     ys = _token_stride(dy, "dy", x.dtype, (N, heads, D))
-    _here(x=x, norm=norm._weight)
+    _here(x=x, norm=norm._weight, pos=pos, dy=dy, dx=dx, dw=dw, workspace=workspace)
     if dx is None:
         dx, ds = _result((N, heads, D), x.dtype, x.device, stream), heads * D
     else:
@@ -905,8 +905,8 @@ def norm_rope_append(plan: RopePlan, cache: KvCache, layer: int, slot_idx: torch
     qs = _token_stride(q, "q", io, (N, HQ, cache.D))
     ks = _token_stride(k, "k", io, kv_shape)
     vs = _token_stride(v, "v", io, kv_shape)
-    _here(q=q, cache=cache.k, **{} if q_norm is None else {"q_norm": q_norm._weight},
-          **{} if k_norm is None else {"k_norm": k_norm._weight})
+    _here(q=q, cache=cache.k, q_norm=None if q_norm is None else q_norm._weight,
+          k_norm=None if k_norm is None else k_norm._weight, slot_idx=slot_idx, starts=starts, k=k, v=v, pos=pos, q_out=q_out)
     if pos is not None:
         _need(pos, "pos", torch.int32, (N,))
     if q_out is None:
@@ -948,7 +948,7 @@ def prompt_attn(cache: KvCache, layer: int, slot_idx: torch.Tensor, starts: torc
         raise GdnSpecError(f"q: want [N, HQ, D], got {tuple(q.shape)}")
     N, HQ, _ = q.shape
     _need(q, "q", cache.io_torch, (N, HQ, cache.D))
-    _here(q=q, cache=cache.k)
+    _here(q=q, cache=cache.k, slot_idx=slot_idx, starts=starts, out=out, lse=lse, workspace=workspace)
     if out is None:
         out = _result(q.shape, q.dtype, q.device, stream)
     else:

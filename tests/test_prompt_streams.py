@@ -47,6 +47,38 @@ def test_another_device_is_refused(monkeypatch):
         binding._here(x=Elsewhere())
 
 
+def test_every_tensor_of_a_call_is_looked_at(monkeypatch):
+    """Each tensor that a call takes, on another device than the current one in turn."""
+    class Somewhere(torch.Tensor):
+        is_cuda, at = True, 0
+
+        def get_device(self):
+            return self.at
+
+    plan, w = binding.RopePlan(64), Watch(monkeypatch)
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    t = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype).as_subclass(Somewhere)  # noqa: E731
+    i32, f32 = torch.int32, torch.float32
+    norm, k_norm = binding.HeadNorm(t(64, dtype=f32)), binding.HeadNorm(t(64, dtype=f32))
+    x, dy, dx, k, v, out = (t(3, 4, 64) for _ in range(6))
+    pos, starts, slots = t(3, dtype=i32), t(3, dtype=i32), t(2, dtype=i32)
+    dw, lse, work = t(64, dtype=f32), t(3, 4, dtype=f32), t(64, dtype=torch.uint8)
+    w.cache.k = t(1)
+    for call, tensors in (
+            (lambda: binding.norm_rope(plan, norm, pos, x, out=out), (norm._weight, pos, x, out)),
+            (lambda: binding.norm_rope_grad(plan, norm, pos, x, dy, dx, dw, work), (norm._weight, pos, x, dy, dx, dw, work)),
+            (lambda: binding.norm_rope_append(plan, w.cache, 0, slots, starts, x, k, v, norm, k_norm, pos, out),
+             (w.cache.k, slots, starts, x, k, v, norm._weight, k_norm._weight, pos, out)),
+            (lambda: binding.prompt_attn(w.cache, 0, slots, starts, x, out=out, lse=lse, workspace=work),
+             (w.cache.k, slots, starts, x, out, lse, work))):
+        call()
+        for one in tensors:
+            one.at = 1
+            with pytest.raises(binding.GdnSpecError, match="the current device is cuda:0"):
+                call()
+            one.at = 0
+
+
 @pytest.mark.parametrize("change", [lambda w: w.to(torch.bfloat16), lambda w: w[:32], lambda w: w.double(), lambda w: w])
 def test_a_norms_weights_are_checked_again(change):
     """Converting a model replaces a parameter's memory under the norm that holds it."""
