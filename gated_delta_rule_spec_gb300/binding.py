@@ -847,7 +847,7 @@ def norm_rope(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.Tensor
 
 
 def norm_rope_grad_workspace(N: int, heads: int, D: int) -> int:
-    """gdn_spec_norm_rope_grad_workspace: bytes that a call of this size needs on the current device."""
+    """gdn_spec_norm_rope_grad_workspace: bytes for a call of at most this many tokens on the current device."""
     n = load().gdn_spec_norm_rope_grad_workspace(N, heads, D)
     if n < 0:
         _check(n, "gdn_spec_norm_rope_grad_workspace")
@@ -928,7 +928,7 @@ def prompt_attn_path(cache: KvCache, HQ: int) -> str:
 
 
 def prompt_attn_workspace(cache: KvCache, B: int, N: int, HQ: int) -> int:
-    """gdn_spec_prompt_attn_workspace: bytes that a call of this size needs on the current device."""
+    """gdn_spec_prompt_attn_workspace: bytes for a call of at most this many rows and tokens on the current device."""
     n = load().gdn_spec_prompt_attn_workspace(cache._ref, B, N, HQ)
     if n < 0:
         _check(n, "gdn_spec_prompt_attn_workspace")

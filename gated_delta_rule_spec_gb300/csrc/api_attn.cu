@@ -417,8 +417,9 @@ const char *gdn_spec_prompt_attn_path(const gdn_spec_kv_cache *cache, int32_t HQ
 int64_t gdn_spec_prompt_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, int32_t N, int32_t HQ) {
     int rc = check_prompt(cache, B, N, HQ);
     if (rc) return rc;
+    // as for one row, which may be cut the finest: so that it does for fewer rows and tokens too
     PromptArgs A = {};
-    if ((rc = prompt_args(cache, B, N, HQ, &A))) return rc;
+    if ((rc = prompt_args(cache, B < 1 ? B : 1, N, HQ, &A))) return rc;
     return workspace_bytes_of(A);
 }
 

@@ -598,7 +598,8 @@ int gdn_spec_norm_rope_grad(const gdn_spec_rope_plan *plan, const gdn_spec_head_
                             int64_t dx_stride, float *dw, void *workspace, int64_t workspace_bytes,
                             void *stream);
 
-/* Bytes of workspace for such a call on the current device, or a negative GDN_SPEC_E* code. */
+/* Bytes of workspace for such a call on the current device, and for every one with at most as many tokens, or a
+ * negative GDN_SPEC_E* code. */
 int64_t gdn_spec_norm_rope_grad_workspace(int32_t N, int32_t heads, int32_t D);
 
 /*
@@ -650,7 +651,8 @@ int gdn_spec_prompt_attn(const gdn_spec_kv_cache *cache, int32_t layer, const in
                          float scale, void *out, float *lse, void *workspace, int64_t workspace_bytes,
                          void *stream);
 
-/* Bytes of workspace for such a call on the current device, or a negative GDN_SPEC_E* code. */
+/* Bytes of workspace for such a call on the current device, and for every one with at most as many rows and
+ * tokens, or a negative GDN_SPEC_E* code. */
 int64_t gdn_spec_prompt_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, int32_t N, int32_t HQ);
 
 /* Name of the kernel gdn_spec_prompt_attn would launch ("tc", "generic"), or NULL if the

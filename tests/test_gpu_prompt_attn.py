@@ -196,6 +196,28 @@ def test_another_stream_and_a_graph(io):
 
 
 @pytest.mark.parametrize("io", ["fp32", "bf16"])
+def test_a_workspace_does_for_fewer_rows_and_tokens(io):
+    """One that was made for 64 rows and 1200 tokens takes one row of 1100 (its part of the line may be cut finer), and
+    the gradient's every smaller count."""
+    c = Prompts(30, io, 2, 2, 64, 64, counts=[1100], lens=[40])
+    cache = c.upload()
+    large = binding.KvCache(1, 8192, 2, 64, 64, 1, 4, io)                # more pages than L2 holds
+    for kv in (cache, large):
+        most = binding.prompt_attn_workspace(kv, 64, 1200, 2)
+        for B, N in ((1, 0), (1, 1), (1, 1100), (1, 1200), (2, 700), (63, 1199), (64, 64), (0, 0)):
+            assert binding.prompt_attn_workspace(kv, B, N, 2) <= most, (B, N)
+    slots, starts = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    binding.prompt_attn(large, 0, slots, starts, c.q.cuda(),
+                        workspace=torch.empty(binding.prompt_attn_workspace(large, 64, 1200, 2), dtype=torch.uint8, device="cuda"))
+    c.check(workspace=torch.empty(binding.prompt_attn_workspace(cache, 64, 1200, 2), dtype=torch.uint8, device="cuda"))
+    before = 0
+    for n in (0, 1, 2, 100, 303, 304, 305, 1023, 1024, 1025, 2047, 2048, 4096, 8192, 16384, 100000):
+        now = binding.norm_rope_grad_workspace(n, 4, 128)
+        assert now >= before, n
+        before = now
+
+
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
 def test_refused_rows_report_and_give_zeros(io):
     c = Prompts(15, io, 4, 2, 128, 32, counts=[4, 4, 5, 70, 4], lens=[40, 50, 60, 70], slots=[0, 9, 1, 2, 3])
     cache = c.upload()
