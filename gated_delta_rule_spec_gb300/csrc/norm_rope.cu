@@ -225,7 +225,7 @@ norm_append_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ N
     extern __shared__ __align__(16) float2 cs[];   // [tokens][pairs], see turn_place; then both weights
     __shared__ int64_t row_s[kRopeTokens];   // the token's row in the pool; kDead: its q is zero and nothing else is written
     __shared__ int pos_s[kRopeTokens];
-    constexpr int64_t kDead = -1, kNobodys = -2;
+    constexpr int64_t kDead = -1, kNobodys = -2, kNoPage = -3;   // (of a page that is none: as kDead, and reported)
     float *const wq = reinterpret_cast<float *>(cs + tokens * R.pairs + (tokens * R.pairs & 1)), *const wk = wq + R.D;
     const KvArgs &C = A.C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -257,27 +257,41 @@ norm_append_kernel(const __grid_constant__ RopeArgs R, const __grid_constant__ N
     load();
     stage_weights<HALF, UNITS>(wq, WQ, R);
     stage_weights<HALF, UNITS>(wk, WK, R);
-    for (int64_t b = (int64_t)blockIdx.x * kNormThreads + tid; b < A.B; b += (int64_t)gridDim.x * kNormThreads) {
-        uint32_t bits;
-        prompt_row(A, (int)b, &bits);
-        if (bits) atomicOr(C.status, bits);
-    }
-    for (int t = warp; t < live; t += kNormThreads / 32) {
-        const int token = (int)(n0 + t), b = prompt_owner(A.starts, A.B, token);
-        if (lane == 0) {
-            uint32_t bits;
-            const PromptRow r = prompt_row(A, b, &bits);
-            const int at = token - r.first;
-            int64_t row = at >= 0 && at < r.owned ? kDead : kNobodys;
-            if (at >= 0 && at < r.cnt) {
-                row = kv_token_row(C, r.slot, r.len + at);
-                if (row < 0) atomicOr(C.status, GDN_SPEC_ST_PAGE_OOR);
-            }
-            row_s[t] = row;
-            pos_s[t] = pos ? pos[token] : r.len + at;
+    const int s0 = tid < A.B ? A.starts[tid] : 0, s1 = tid < A.B ? A.starts[tid + 1] : 0;   // (on their way during what follows)
+    uint32_t bits;         // of the rows whose status is this thread's
+    const auto look_up = [&](bool all_ascend) {
+        bits = 0;
+        for (int64_t b = (int64_t)blockIdx.x * kNormThreads + tid; b < A.B; b += (int64_t)gridDim.x * kNormThreads) {
+            uint32_t row_bits;
+            prompt_row(A, (int)b, all_ascend, &row_bits);
+            bits |= row_bits;
         }
+        for (int t = warp; t < live; t += kNormThreads / 32) {
+            const int token = (int)(n0 + t), b = prompt_owner(A, token, all_ascend);
+            if (lane == 0) {
+                uint32_t row_bits;
+                const PromptRow r = prompt_row(A, b, all_ascend, &row_bits);
+                const int at = token - r.first;
+                int64_t row = at >= 0 && at < r.owned ? kDead : kNobodys;
+                if (at >= 0 && at < r.cnt) {
+                    row = kv_token_row(C, r.slot, r.len + at);
+                    if (row < 0) row = kNoPage;
+                }
+                row_s[t] = row;
+                pos_s[t] = pos ? pos[token] : r.len + at;
+            }
+        }
+    };
+    look_up(true);
+    bool ascends = prompt_range(A, s0, s1);   // starts does, as far as the thread sees
+    for (int b = tid + kNormThreads; b < A.B; b += kNormThreads) ascends &= prompt_range(A, A.starts[b], A.starts[b + 1]);
+    ascends = __syncthreads_and(ascends);
+    if (!ascends) {   // the rows that were found need not be the tokens'
+        look_up(false);
+        __syncthreads();
     }
-    __syncthreads();
+    if (tid < live && row_s[tid] == kNoPage) bits |= GDN_SPEC_ST_PAGE_OOR;
+    if (bits) atomicOr(C.status, bits);
     for (int j = tid; j < live * R.pairs; j += kNormThreads) {
         const int t = j / R.pairs, i = j - t * R.pairs;
         cs[t * R.pairs + turn_place<UNITS>(i, R.pairs)] = rope_turn(R, pos_s[t], i);

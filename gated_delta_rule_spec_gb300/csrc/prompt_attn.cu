@@ -48,12 +48,12 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
     const float *const qg = static_cast<const float *>(A.q);
     grid_dep_wait();
 
-    prompt_dead_tokens<float>(A, tid, kPromptThreads);
     const PromptPlan plan = prompt_plan<kPromptThreads>(A, &scratch);
+    prompt_dead_tokens<float>(A, plan.ascends(), tid, kPromptThreads);
     PromptWalk walk(A, plan, 0);   // (one wave: the keys and values are not what bounds it)
     if (tid == 0) prompt_note(A, walk, plan.chunk, 0);
     PromptPiece pc;
-    while (walk.next(A, &pc)) {
+    while (walk.next(A, plan, &pc)) {
         const PromptItem &it = pc.it;
         __syncthreads();   // the piece before is done with shared memory
         for (int x = tid; x < kPromptRows * (DP / 4); x += kPromptThreads) {

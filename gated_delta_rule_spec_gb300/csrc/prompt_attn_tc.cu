@@ -285,12 +285,12 @@ __device__ __forceinline__ void produce(const PromptArgs &A, const CUtensorMap *
         PieceInfo sp;
         bool any;
         if (KEYS) {
-            any = walk.next(A, &pc);
+            any = walk.next(A, plan, &pc);
             while (!any && wave + 1 < A.waves) {   // the block's next chunk
                 walk = PromptWalk(A, plan, ++wave);
                 if (ptx::elect_one()) prompt_note(A, walk, plan.chunk, wave);
                 __syncwarp();
-                any = walk.next(A, &pc);
+                any = walk.next(A, plan, &pc);
             }
             ok = describe(any, &sp);
         } else {
@@ -1024,7 +1024,7 @@ prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 
     if (warp < L::NS * 4) {
         // while the first tile is on its way
-        prompt_dead_tokens<__nv_bfloat16>(A, tid, L::NS * 128);
+        prompt_dead_tokens<__nv_bfloat16>(A, plan.ascends(), tid, L::NS * 128);
         soften<D>(A, ms, tmem, tid);
     } else {
         const int role = warp - L::NS * 4;

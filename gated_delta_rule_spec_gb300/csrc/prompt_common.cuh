@@ -49,13 +49,28 @@ struct PromptRow {
     int first, owned;          // its tokens in the packed tensors
 };
 
-__device__ __forceinline__ PromptRow prompt_row(const PromptArgs &A, int b, uint32_t *bits) {
+__device__ __forceinline__ bool prompt_range(const PromptArgs &A, int first, int end) { return first >= 0 && end >= first && end <= A.N; }
+
+// Whether a row before row b that is a range reaches past b's first token.  Only where some row is no range: if all are,
+// starts ascends.
+__device__ __forceinline__ bool prompt_overlaps(const PromptArgs &A, int b, int first) {
+#pragma unroll 1
+    for (int e = 0; e < b; ++e) {
+        const int end = A.starts[e + 1];
+        if (end > first && prompt_range(A, A.starts[e], end)) return true;
+    }
+    return false;
+}
+
+// ascends: every row is a range.
+__device__ __forceinline__ PromptRow prompt_row(const PromptArgs &A, int b, bool ascends, uint32_t *bits) {
     PromptRow r;
     r.slot = A.slot_idx[b];
     r.first = A.starts[b];
     const int end = A.starts[b + 1];
     *bits = 0;
-    if (r.first < 0 || end < r.first || end > A.N) {   // no range of tokens: there is nothing that could be written
+    // no range of tokens, or tokens that are another's: there is nothing that could be written
+    if (!prompt_range(A, r.first, end) || (!ascends && prompt_overlaps(A, b, r.first))) {
         *bits = GDN_SPEC_ST_ACCEPT_RANGE;
         r.first = r.owned = r.len = r.cnt = 0;
         return r;
@@ -120,11 +135,13 @@ struct PromptScratch {
     int64_t sums[32];
     int64_t off[kPromptWaves];   // where the block's chunks start: the place in the row's part
     int b[kPromptWaves];         // and the row (-1: past the end)
+    int ascends;                 // whether the entries of starts do
 };
 
 struct PromptPlan {
     int64_t total, chunk;      // length of the line and of a chunk
     const PromptScratch *at;   // the chunks' starts
+    __device__ __forceinline__ bool ascends() const { return at->ascends != 0; }
 };
 
 // Sum over the block of x; *before: of the threads below.
@@ -151,22 +168,23 @@ __device__ __forceinline__ int64_t prompt_scan(int64_t x, PromptScratch *sc, int
     return sum;
 }
 
-// By all threads of a block: the line's length, and the rows at which its chunks start.
+// By all threads of a block: the line's length, and the rows at which its chunks start; false: ASCENDS is not so.
 // The grid's first block records the rows' status bits.
-template <int THREADS>
-__device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScratch *sc) {
-    PromptPlan p;
+template <int THREADS, bool ASCENDS>
+__device__ __forceinline__ bool prompt_lay_out(const PromptArgs &A, PromptScratch *sc, PromptPlan *plan) {
+    PromptPlan &p = *plan;
     const int tid = threadIdx.x;
     p.total = 0;
     p.at = sc;
     int64_t mine = 0, before = 0, keys = 0;   // of the first THREADS rows; of this thread's rows
+    uint32_t all = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < A.B; b0 += THREADS) {
         int64_t x = 0, ex;
         if (b0 + tid < A.B) {
             uint32_t bits;
-            const PromptRow r = prompt_row(A, b0 + tid, &bits);
-            if (bits && blockIdx.x == 0) atomicOr(A.C.status, bits);
+            const PromptRow r = prompt_row(A, b0 + tid, ASCENDS, &bits);
+            all |= bits;
             x = prompt_span(A, r);
             if (r.cnt > 2 * A.tokens) keys += r.len + r.cnt;
         }
@@ -174,6 +192,9 @@ __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScr
         if (b0 == 0) { mine = x; before = ex; }
         p.total += sum;
     }
+    if (ASCENDS && __syncthreads_or(all & GDN_SPEC_ST_ACCEPT_RANGE)) return false;
+    if (all && blockIdx.x == 0) atomicOr(A.C.status, all);
+    if (tid == 0) sc->ascends = ASCENDS;
     int64_t waves = 1;
     if (A.waves > 1) {
         int64_t ex;
@@ -194,7 +215,7 @@ __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScr
             x = 0;
             if (b0 + tid < A.B) {
                 uint32_t bits;
-                x = prompt_span(A, prompt_row(A, b0 + tid, &bits));
+                x = prompt_span(A, prompt_row(A, b0 + tid, ASCENDS, &bits));
             }
         }
         int64_t sum = 0;
@@ -214,7 +235,20 @@ __device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScr
         base += sum;
     }
     __syncthreads();
+    return true;
+}
+
+template <int THREADS>
+__device__ __noinline__ PromptPlan prompt_plan_no_order(const PromptArgs &A, PromptScratch *sc) {
+    PromptPlan p;
+    prompt_lay_out<THREADS, false>(A, sc, &p);
     return p;
+}
+
+template <int THREADS>
+__device__ __forceinline__ PromptPlan prompt_plan(const PromptArgs &A, PromptScratch *sc) {
+    PromptPlan p;
+    return prompt_lay_out<THREADS, true>(A, sc, &p) ? p : prompt_plan_no_order<THREADS>(A, sc);
 }
 
 // The pieces of a block's chunk, one after another, for whoever walks.
@@ -234,9 +268,9 @@ struct PromptWalk {
     int64_t start, end;        // the chunk
     bool live;
 
-    __device__ __forceinline__ void load(const PromptArgs &A) {
+    __device__ __forceinline__ void load(const PromptArgs &A, const PromptPlan &p) {
         uint32_t bits;
-        const PromptRow r = prompt_row(A, it.b, &bits);
+        const PromptRow r = prompt_row(A, it.b, p.ascends(), &bits);
         it.slot = r.slot, it.len = r.len, it.cnt = r.cnt, it.first = r.first;
         blocks = (r.cnt + A.tokens - 1) / A.tokens;
     }
@@ -256,7 +290,7 @@ struct PromptWalk {
         end = min(p.total, start + p.chunk);
         it.b = p.at->b[w];
         uint32_t bits;
-        const PromptRow r = prompt_row(A, it.b, &bits);
+        const PromptRow r = prompt_row(A, it.b, true, &bits);   // (a row that has items)
         it.slot = r.slot, it.len = r.len, it.cnt = r.cnt, it.first = r.first;
         const PromptLine line(A, r);
         const int64_t off = p.at->off[w];
@@ -267,7 +301,7 @@ struct PromptWalk {
         it.pos = start - (in - line.before(i));
         set(A);
     }
-    __device__ __forceinline__ bool next(const PromptArgs &A, PromptPiece *pc) {
+    __device__ __forceinline__ bool next(const PromptArgs &A, const PromptPlan &p, PromptPiece *pc) {
         while (live) {
             pc->it = it;
             pc->t0 = it.tile_at(A, start);
@@ -285,7 +319,7 @@ struct PromptWalk {
                                 live = false;
                                 break;
                             }
-                            load(A);
+                            load(A, p);
                         } while (it.cnt == 0);
                     }
                 }
@@ -313,10 +347,21 @@ __device__ __forceinline__ int64_t prompt_out_row(const PromptArgs &A, const Pro
     return ((int64_t)it.first + it.q0 + t) * A.HQ + it.h * A.G + g;
 }
 
-// The row that owns `token` where starts ascends: the last one that starts at or before it; by a whole warp, 32 rows looked
-// at in one step.  In [0, B) always.
-__device__ __forceinline__ int prompt_owner(const int32_t *starts, int B, int token) {
-    const int lane = threadIdx.x & 31;
+// The row that owns `token`, if one does; by a whole warp.  In [0, B) always.  Where starts ascends: the last one that
+// starts at or before it, 32 rows looked at in one step.  Else the first row that is a range with it inside (a later one
+// overlaps that row).
+__device__ __forceinline__ int prompt_owner(const PromptArgs &A, int token, bool ascends) {
+    const int lane = threadIdx.x & 31, B = A.B;
+    const int32_t *const starts = A.starts;
+    if (!ascends) {
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            const int b = b0 + lane;
+            const bool in = b < B && starts[b] <= token && token < starts[b + 1] && prompt_range(A, starts[b], starts[b + 1]);
+            const unsigned some = __ballot_sync(0xffffffffu, in);
+            if (some) return b0 + __ffs(some) - 1;
+        }
+        return 0;
+    }
     int lo = 0, n = B;   // the answer is in [lo, lo + n)
     while (n > 1) {
         const int step = (n + 31) / 32;
@@ -333,12 +378,16 @@ __device__ __forceinline__ int prompt_owner(const int32_t *starts, int B, int to
 // Tokens of rows that nothing computes (padding rows, rows that were refused): zeros, and an lse of -inf.  By `threads`
 // threads (whole warps) of each block; every block takes an equal share of the packed tokens.
 template <typename IO>
-__device__ __noinline__ void prompt_dead_tokens(const PromptArgs &A, int thread, int threads) {
+__device__ __noinline__ void prompt_dead_tokens(const PromptArgs &A, bool ascends, int thread, int threads) {
     const int n0 = (int)((int64_t)A.N * blockIdx.x / gridDim.x), n1 = (int)((int64_t)A.N * (blockIdx.x + 1) / gridDim.x);
     if (n0 >= n1) return;
-    for (int b = prompt_owner(A.starts, A.B, n0); b < A.B && A.starts[b] < n1; ++b) {
+    for (int b = ascends ? prompt_owner(A, n0, true) : 0; b < A.B; ++b) {
+        if (A.starts[b] >= n1 || A.starts[b + 1] <= n0) {   // none of its tokens are this block's
+            if (ascends && A.starts[b] >= n1) break;
+            continue;
+        }
         uint32_t bits;
-        const PromptRow r = prompt_row(A, b, &bits);
+        const PromptRow r = prompt_row(A, b, ascends, &bits);
         if (r.cnt || !r.owned) continue;
         const int64_t t0 = max(n0, r.first), t1 = min(n1, r.first + r.owned);
         float4 *o = reinterpret_cast<float4 *>(static_cast<IO *>(A.out) + t0 * A.HQ * A.C.D);

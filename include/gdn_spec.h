@@ -559,8 +559,10 @@ const char *gdn_spec_tree_attn_path(const gdn_spec_kv_cache *cache, int32_t T, i
  * both with the rows' counts.  Rows of one token (decode) go beside prompts in the
  * same call.
  *   starts  int32 [B + 1], device: ascending, 0 <= starts[b] <= starts[b + 1] <= N.
- *           A row whose two entries are not so owns nothing (ACCEPT_RANGE).  What
- *           belongs to tokens that no row owns is left as it was.
+ *           A row whose two entries are not so owns nothing (ACCEPT_RANGE), nor does a
+ *           row whose first token a row before it, whose entries are so, reaches past;
+ *           the other rows are served.  What belongs to tokens that no row owns is left
+ *           as it was.
  * Rows with slot_idx < 0, and rows refused with a status bit, get zeros.
  * ---------------------------------------------------------------------- */
 
