@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(prompt_threads(DP), prompt_blocks(DP)) prompt_
             bool on;
             const int64_t row = prompt_out_row(A, it, r0 + i, &on);
             if (!on) continue;
-            const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+            const float inv = 1.0f / l[i];   // (no weight at all, every score -inf: infinite, and zeros times it are NaN)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const int d = g * 64 + tx * 4;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kPromptJoinThreads) prompt_join_kernel(const _
             o.w = o.w * wa + po.w * wb;
             m = mn;
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = 1.0f / l;   // (as in the kernels: NaN where every score is -inf)
         IO out[4] = {from_f32<IO>(o.x * inv), from_f32<IO>(o.y * inv), from_f32<IO>(o.z * inv), from_f32<IO>(o.w * inv)};
         IO *op = static_cast<IO *>(A.out) + row * A.C.D + 4 * d4;
         if (sizeof(IO) == 2) *reinterpret_cast<uint2 *>(op) = *reinterpret_cast<const uint2 *>(out);

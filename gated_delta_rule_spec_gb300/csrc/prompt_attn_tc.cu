@@ -911,7 +911,7 @@ __device__ __forceinline__ void soften(const PromptArgs &A, Misc *ms, uint32_t t
             ptx::tc_fence_after_sync();
             if (warp_on) {
                 const bool removed = *(volatile int *)&ms->notes[piece % kNotes].piece == piece;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const float inv = 1.0f / l;   // (no weight at all, every score -inf: infinite, and zeros times it are NaN)
 #pragma unroll 1
                 for (int d0 = 0; d0 < A.C.D; d0 += 32) {
                     uint32_t u[32];

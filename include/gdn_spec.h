@@ -632,6 +632,7 @@ int gdn_spec_norm_rope_append(const gdn_spec_rope_plan *plan, const gdn_spec_hea
  * row's tokens 0..t (cache positions length ..  length + t, written before):
  *   out = sum_j p_j v_j,  p = softmax_j(scale <q, k_j>)
  * What a token does not attend to has no effect on it, whatever its bits.
+ * Where all of a token's scores are -inf its softmax has no value: NaN, with an lse of -inf.
  *   q          io_dtype [N, HQ, D], dense; HKV divides HQ, head h reads kv head h / (HQ / HKV);
  *              out does not overlap it
  *   starts     int32 [B + 1], above
