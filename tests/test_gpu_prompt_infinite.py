@@ -1,4 +1,5 @@
-"""Prompt attention where scores are minus infinity: what the definition gives there (bounds: prompt_case.py)."""
+"""Prompt attention where scores are minus infinity and where a weight vanishes beside an infinite value: what the definition
+gives there (bounds: prompt_case.py)."""
 import math
 
 import numpy as np
@@ -41,3 +42,26 @@ def test_a_token_whose_scores_are_all_minus_infinity(io, HQ, HKV, D, P):
                 want, score = v[page, g, off], float(q[n, h] @ k[page, g, off]) * c.scale
                 assert (np.abs(got[n, h] - want) <= c.bound(want, np.abs(want))).all(), (s, t, h)
                 assert abs(gl[n, h] - score) <= 2e-5, (s, t, h)
+
+
+@pytest.mark.parametrize("io,HQ,HKV,D,P", SHAPES)
+@pytest.mark.parametrize("at", [0, 3, 130, 200])
+def test_an_infinite_value_beside_a_weight_that_vanishes(io, HQ, HKV, D, P, at):
+    """A weight of e^-200 is zero in 32 bits, and times infinity it is not finite, in whichever tile the key lies: the tokens
+    that see it are not finite in that dim, whether others of their block see it or not; the rest are as ever."""
+    c, clean = (Prompts(52, io, HQ, HKV, D, P, counts=[260], lens=[0], poison=False, scale=1.0) for _ in range(2))
+    for x in (c, clean):
+        x.q.zero_()
+        x.q[..., 0] = 1.0
+        x.k[..., 0] = 0.0
+        page, off = x.row(0, at)
+        if at:
+            x.k[0, page, :, off, 0] = -200.0
+        else:                                             # the first token sees nothing else: its weight is one
+            x.k[..., 0] = 200.0
+            x.k[0, page, :, off, 0] = 0.0
+    c.v[0, page, :, off, 1] = math.inf
+    got, want = c.call()[0].float().cpu().numpy(), clean.call()[0].float().cpu().numpy()
+    assert np.array_equal(got[:at], want[:at]) and np.isfinite(want).all()
+    assert not np.isfinite(got[at:, :, 1]).any()
+    assert np.array_equal(np.delete(got, 1, 2), np.delete(want, 1, 2))
