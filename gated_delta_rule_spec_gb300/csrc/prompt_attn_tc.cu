@@ -630,8 +630,11 @@ __device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, i
                 __nanosleep(100);
             }
         __syncwarp();
+        // the rows first: a stream that takes fewer tiles than the piece has may be looking at the piece's number
         if (lane < 4) note->rows[lane] = 0;
-        if (lane == 0) note->piece = piece;
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) *(volatile int *)&note->piece = piece;
         __syncwarp();
     }
 #pragma unroll 1
@@ -704,6 +707,7 @@ __device__ __forceinline__ void clean(const PromptArgs &A, Misc *ms, uint8_t *sm
 __device__ __noinline__ void add_removed(const PromptArgs &A, const Misc *ms, int piece, const PieceInfo &it, int all, int own,
                                          int64_t qrow, float m, int d0, int dims, float *o) {
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(A.q) + qrow * A.C.D;
+    __threadfence_block();   // the piece's number was read, its rows are read behind it
     for (int i = 0; i < own; ++i) {
         const Note &note = ms->notes[piece % kNotes];
         const bool there = note.piece == piece && ((note.rows[i >> 6] >> (i & 63)) & 1);
