@@ -621,14 +621,14 @@ __device__ __noinline__ bool remove(Misc *ms, uint8_t *tile, int row, int key, i
     Note *const note = &ms->notes[piece % kNotes];
     if (note->piece != piece) {   // the place held an earlier piece's: all are done with it
         const volatile int *done = ms->done;
-        for (int w = 0; w < L::NS * 4; ++w)
-            for (uint32_t it = 0; done[w] < piece - kNotes + 1; ++it) {
-                if (it == tat::kPolls || *(volatile int *)&ms->abort) {
-                    ms->abort = 1;
-                    return false;
-                }
-                __nanosleep(100);
+        for (uint32_t it = 0;; ++it) {   // one answer for all lanes, as in wait()
+            if (__all_sync(0xffffffffu, lane >= L::NS * 4 || done[lane] > piece - kNotes)) break;
+            if (__any_sync(0xffffffffu, it == tat::kPolls || *(volatile int *)&ms->abort)) {
+                ms->abort = 1;
+                return false;
             }
+            __nanosleep(100);
+        }
         __syncwarp();
         // the rows first: a stream that takes fewer tiles than the piece has may be looking at the piece's number
         if (lane < 4) note->rows[lane] = 0;

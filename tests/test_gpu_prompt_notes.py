@@ -40,3 +40,20 @@ def test_a_later_tile_opens_a_note_that_an_earlier_piece_used(D, HKV):
         a, b = out[~free][:, rest].float(), want[~free][:, rest].float()
         assert torch.isfinite(a).all()
         assert ((a - b).abs() <= 2.0 ** -7 * (b.abs() + float(c.v.abs().max()))).all()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_a_call_that_gives_up_beside_notes(D):
+    """The wait limit at zero where every piece has values that are not finite: TIMEOUT, and the next call is right."""
+    c = Prompts(62, "bf16", 8, 4, D, 64, counts=[128] * 40, lens=[64] * 40, poison=False)
+    cache = c.upload()
+    cache.v[:, :, :, 40, 1] = math.inf
+    binding.set_wait_limit(0)
+    try:
+        c.call()
+        st = binding.kv_read_status(cache)
+    finally:
+        binding.set_wait_limit(binding.WAIT_LIMIT_DEFAULT)
+    assert st == binding.ST_TIMEOUT
+    cache.v.copy_(c.v)
+    c.check()
