@@ -815,6 +815,11 @@ class HeadNorm:
         return self._desc
 
 
+def _is_norm(norm, name: str, none: bool = False) -> None:
+    if not (isinstance(norm, HeadNorm) or (none and norm is None)):
+        raise GdnSpecError(f"{name}: want a HeadNorm{' or None' if none else ''}, got {type(norm).__name__}")
+
+
 def _norm_of(norm: HeadNorm | None, plan: RopePlan, name: str):
     if norm is None:
         return None
@@ -828,7 +833,9 @@ def _norm_of(norm: HeadNorm | None, plan: RopePlan, name: str):
 def norm_rope(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.Tensor,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """gdn_spec_norm_rope: every head of x [N, heads, D] (tokens may be strided) normed and turned
-    to positions pos [N].  out may be x."""
+    to positions pos [N].  out may be x.  The result carries no autograd history, whatever x or the
+    weight do: ``norm_rope_grad`` is its gradient."""
+    _is_norm(norm, "norm")
     N, heads, D = x.shape if x.dim() == 3 else (0, 0, 0)
     if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float32) or D != plan.D:
         raise GdnSpecError(f"x: want bf16 or fp32 [N, heads, {plan.D}], got {x.dtype} {tuple(x.shape)}")
@@ -861,6 +868,7 @@ def norm_rope_grad(plan: RopePlan, norm: HeadNorm, pos: torch.Tensor, x: torch.T
     norm's weight (fp32 [D]) from dy, that of its result.  Tokens of x, dy and dx may be strided;
     dx may be x or dy; workspace: uint8, at least ``norm_rope_grad_workspace`` bytes (None:
     allocated for the call on its stream)."""
+    _is_norm(norm, "norm")
     N, heads, D = x.shape if x.dim() == 3 else (0, 0, 0)
     if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float32) or D != plan.D:
         raise GdnSpecError(f"x: want bf16 or fp32 [N, heads, {plan.D}], got {x.dtype} {tuple(x.shape)}")
@@ -896,6 +904,8 @@ def norm_rope_append(plan: RopePlan, cache: KvCache, layer: int, slot_idx: torch
     q [N, HQ, D], k and v [N, HKV, D] (slices of one projection's output, say).  Normed and rotated
     q [N, HQ, D]; normed and rotated k, and v, go behind the slots' committed tokens in ``layer`` of
     the cache.  A norm of None leaves that side as it is; pos int32 [N]: length + t where None."""
+    _is_norm(q_norm, "q_norm", none=True)
+    _is_norm(k_norm, "k_norm", none=True)
     B = _rows(slot_idx, "slot_idx")
     _need(starts, "starts", torch.int32, (B + 1,))
     if q.dim() != 3:
