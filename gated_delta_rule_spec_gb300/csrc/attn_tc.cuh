@@ -14,7 +14,6 @@ namespace tat {
 
 constexpr float kGrow = 8.0f;            // log2 of what the maximum may grow by before it is moved
 constexpr uint32_t kPolls = 1u << 18;    // of a wait, before it gives up (half a second)
-constexpr uint32_t kLooks = 1;          // at a barrier, before the polls
 
 // Bounded wait of a whole warp, which also ends when another role has given up; one
 // answer for all lanes.  It looks first: a phase that has passed costs some 50 cycles so,

@@ -1,4 +1,4 @@
-// ptx_attn.cuh -- more inline-PTX wrappers, for the tree attention's kernel: an
+// ptx_attn.cuh -- more inline-PTX wrappers, for the tensor-core attention kernels: an
 // arrive and a poll of an mbarrier, TMEM moves of raw bits, the MN-major operand
 // descriptor, the bf16 MMA with A in tensor memory, and the elected lane.
 #pragma once
