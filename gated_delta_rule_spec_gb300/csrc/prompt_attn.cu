@@ -10,10 +10,13 @@
 // (four where D > 128) with four keys, then, with the probabilities in shared memory where the keys
 // were, the sums of the same rows over DP / 16 columns; sixteen threads share the rows.  The
 // values are copied while the scores are formed, two blocks an SM cover the rest.  2 prompts of
-// 1000 tokens behind 1000, 8 heads on 2 of 128: 313 us, 36 TFLOP/s, nearly half of the fp32 rate (345
-// us with four rows a thread); heads of 256, 600 tokens: 339 us, 34 TFLOP/s.  A wide read of shared
-// memory feeds 10 to 16 multiply-adds, which bounds it.  Sums are of 64 terms, and of such sums: with one
-// chain a row of 8267 keys was off by 1.1e-6 of itself, by 3.7e-7 so.
+// 1000 tokens behind 753 and 1000, 8 heads on 2 of 128: 321 us, 35 TFLOP/s, nearly half of the fp32 rate
+// (with four rows a thread a tenth slower); heads of 256, 600 tokens: 347 us, 33 TFLOP/s.  What bounds it is latency: two
+// warps a scheduler (248 to 255 registers), four block barriers a tile, one buffer each of keys and values.  7 prompts of
+// up to 523 tokens behind up to 777, 6 heads on 2 of 64 (91 us): instructions issue in 61% of the active cycles, the
+// multiply-adds' pipe is 47% and shared memory's 45% busy; a warp waits for shared memory first, then for what it has
+// issued itself, then for instructions and barriers.  Sums are of 64 terms, and of such sums: with one chain a row of 8267
+// keys was off by 1.1e-6 of itself, by 3.7e-7 so.
 #include "launch_setup.cuh"
 #include "prompt_common.cuh"
 

@@ -20,16 +20,16 @@
 //
 // What bounds it is a stream's round: softmax, 950 cycles at best (MUFU: 512 for the
 // exponentials), sums and scores, 1024, and four hand-overs through barriers.  Two streams
-// fill the tensor core to 72% that way (4 x 1024 tokens behind 30000, 16 heads on 2 of 128: 525 us,
-// 1.6 PFLOP/s; 8192 tokens, 32 on 8 of 128: 374 us, 1.47; heads of 64, where a round
-// multiplies half as much: 456 us, 0.93 PFLOP/s).  What led there, first case: 770 us; scores in quarters
+// fill the tensor core to 72% that way (4 x 1024 tokens behind 19751 to 30000, 16 heads on 2 of 128: 525 to 545 us,
+// 1.56 to 1.62 PFLOP/s; 8192 tokens, 32 on 8 of 128: 371 to 394 us, 1.40 to 1.48; heads of 64, where a round
+// multiplies half as much: the first case in 447 us, 0.95 PFLOP/s).  What led there, first case: 770 us; scores in quarters
 // and walkers out of line, so that the loops stay in the instruction cache (a kernel of 170 KB
 // of code waited for instructions a third of the softmax's time): 600; pieces described once: 554;
 // probabilities in one pass against the maximum so far: 525.  Not faster: waiting by looking
 // at a barrier in a loop (13% slower: it takes the softmax's issue slots); one warp for both
 // streams' products (600 us as it stood then); both streams issuing at will (607); for D = 256 pairs of
 // blocks that share tiles by multicast.  D = 256: 16384 + 10308 tokens, 16 heads on 2: 1960 to
-// 2010 us, 1.55 PFLOP/s.
+// 2170 us over several GB300s, 1.41 to 1.57 PFLOP/s.
 //
 // The running maximum is only moved when a row's maximum has grown by more than 2^8 over
 // it, an idea published for attention kernels of this generation: until then the
@@ -178,7 +178,7 @@ struct Ring {
 
 // One lane issues: a copy's operands are uniform registers.  The lanes look up the pages of a tile's boxes side by side.
 // With two streams one warp copies keys and values of each tile in turn; with one, whose rings hold little more than a
-// tile, keys and values have a warp each, so that neither waits for the other's stage (4 x 1024 tokens behind 30000, 16
+// tile, keys and values have a warp each, so that neither waits for the other's stage (4 x 1024 tokens behind 19751 to 30000, 16
 // heads on 2 of 256: 1266 us with one warp, 1227 with two).  The keys' warp walks, describes the pieces and
 // copies the queries.
 template <int D, bool KEYS, bool VALUES>
@@ -518,7 +518,7 @@ __device__ __forceinline__ void multiply_stream(const PromptArgs &A, Misc *ms, u
 }
 
 // One stream: its scores by one warp, a tile ahead, its sums by another.  (In turns, as above, they are no faster: 1234 us
-// against 1227 for 4 x 1024 tokens behind 30000, 16 heads on 2 of 256.)
+// against 1227 for 4 x 1024 tokens behind 19751 to 30000, 16 heads on 2 of 256.)
 template <int D>
 __device__ __forceinline__ void multiply_scores(const PromptArgs &A, Misc *ms, uint32_t base, uint32_t tmem) {
     using L = Lay<D>;

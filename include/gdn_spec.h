@@ -655,7 +655,9 @@ int gdn_spec_prompt_attn(const gdn_spec_kv_cache *cache, int32_t layer, const in
                          void *stream);
 
 /* Bytes of workspace for such a call on the current device, and for every one with at most as many rows and
- * tokens, or a negative GDN_SPEC_E* code. */
+ * tokens, or a negative GDN_SPEC_E* code.  At most: bf16 some 21 MB for heads of up to 64 dims and 41 MB above, where
+ * a layer of the pool (its num_pages) is below 96 MB or the tokens are few, else up to four times as much as the pool is larger;
+ * fp32 some 20 MB. */
 int64_t gdn_spec_prompt_attn_workspace(const gdn_spec_kv_cache *cache, int32_t B, int32_t N, int32_t HQ);
 
 /* Name of the kernel gdn_spec_prompt_attn would launch ("tc", "generic"), or NULL if the
